@@ -64,10 +64,17 @@ MOE_INFO_SPLIT_K = 25
 MOE_INFO_PREDICTED = 32
 STATIC_SCRATCH_BYTES = 4 << 20
 
+MOE_BF16 = 0
+MOE_F32 = 1
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+
 EXPORTS = ("moe_decode_config_check", "moe_decode_plan", "moe_decode_create", "moe_decode_run", "moe_decode_run_host",
            "moe_decode_run_static",
            "moe_decode_get_status", "moe_decode_set_option", "moe_decode_get_info",
-           "moe_decode_destroy", "moe_decode_status_string", "moe_decode_abi_version")
+           "moe_decode_destroy", "moe_decode_status_string", "moe_decode_abi_version",
+           "moe_decode_route_check", "moe_decode_route", "moe_decode_experts_check",
+           "moe_decode_experts_workspace", "moe_decode_experts", "moe_decode_project_check",
+           "moe_decode_project_workspace", "moe_decode_project", "moe_decode_rows_status")
 
 
 class Config(ctypes.Structure):
@@ -91,6 +98,25 @@ class PlanInfo(ctypes.Structure):
         "smem_bytes", "ring_slots", "slot_bytes", "extra_slots", "down_slot_in_x", "pairs_per_stage",
         "router_pairs_per_stage", "down_rows_per_stage", "h_pairs", "h_buffers", "h_per_slot", "slots_max",
         "pairs_max", "lag", "down_h_offset", "threads", "h_rows_max", "down_t_rows_per_stage")]
+
+
+class RouteConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_experts", "top_k", "score", "num_groups", "top_groups", "group_best", "renormalise",
+        "logits_dtype")] + [("scale", ctypes.c_float)]
+
+
+class ExpertsConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "num_experts", "top_k", "num_shared", "wdtype")]
+
+
+class ProjectConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("inner", "outer", "swiglu", "wdtype", "rank", "num_adapters",
+                                              "out_dtype")]
+
+
+class ProjectWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w", "w_scale", "w_gscale", "a", "b", "scale")]
 
 
 class MoEDecodeError(RuntimeError):
@@ -131,6 +157,18 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
         lib.moe_decode_status_string.argtypes = [i32]
         lib.moe_decode_status_string.restype = ctypes.c_char_p
         lib.moe_decode_abi_version.argtypes = []
+        sz = ctypes.c_size_t
+        route, experts, project = (ctypes.POINTER(c) for c in (RouteConfig, ExpertsConfig, ProjectConfig))
+        lib.moe_decode_route_check.argtypes = [route]
+        lib.moe_decode_route.argtypes = [route, vp, i64, vp, i64, vp, vp, vp]
+        lib.moe_decode_experts_check.argtypes = [experts]
+        lib.moe_decode_experts_workspace.argtypes = [experts, i64, ctypes.POINTER(sz)]
+        lib.moe_decode_experts.argtypes = [experts, ctypes.POINTER(Weights), vp, i64, vp, vp, vp, vp, i64, vp, sz, vp]
+        lib.moe_decode_project_check.argtypes = [project]
+        lib.moe_decode_project_workspace.argtypes = [project, i64, ctypes.POINTER(sz)]
+        lib.moe_decode_project.argtypes = [project, ctypes.POINTER(ProjectWeights), vp, i64, vp, vp, vp, i64, vp, sz,
+                                           vp]
+        lib.moe_decode_rows_status.argtypes = [vp, vp]
         for name in EXPORTS:
             if name != "moe_decode_status_string":
                 getattr(lib, name).restype = i32

@@ -1,0 +1,264 @@
+"""The MoE layer's operators for any number of rows, over torch tensors.
+
+``route``, ``experts`` and ``project`` marshal tensors into the C entry points of
+include/moe_decode_rows.h, which document what is computed. They check shapes,
+types and devices, allocate results (and a workspace, unless one is given) with
+torch's allocator on the stream they run on, and enqueue their work on the current
+stream (or ``stream``) without waiting. No arithmetic happens here.
+
+A workspace that is handed in must not be in use by another call at the same time,
+and must stay alive while a CUDA graph that captured a call with it is replayed.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import _lib
+from .synth import LayerShape
+
+_DTYPES = {torch.bfloat16: _lib.MOE_BF16, torch.float32: _lib.MOE_F32}
+
+
+class Adapters(NamedTuple):
+    """Low-rank adapters: a bf16 [L, r, K], b bf16 [L, O, r] ([L, 2 O, r] beside a
+    gate/up projection), scale fp32 [L] or None (1). r % 8 == 0."""
+
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: torch.Tensor | None = None
+
+
+def _need(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def _tensor(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """The address of a contiguous tensor of this type, shape and device."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}: got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, cols: int, device) -> tuple[int, int]:
+    """(address, row stride) of a bf16 [T, cols] tensor whose rows are contiguous."""
+    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 2 or t.shape[1] != cols or \
+            (t.shape[0] and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a bf16 [rows, {cols}] tensor on {device} with contiguous rows: got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    # one row, or none, has no stride of its own
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
+
+
+class _On:
+    """Makes a tensor's device the current one while the library is called; the stream to run on."""
+
+    def __init__(self, device: torch.device, stream):
+        _need(device.type == "cuda", "tensors must be on a CUDA device")
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.stream = stream
+        self.device = device
+
+    def __enter__(self):
+        if self.guard:
+            self.guard.__enter__()
+        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
+        # results and workspaces are allocated for the stream that the kernels run on
+        self.on = None if self.stream is None else torch.cuda.stream(s)
+        if self.on:
+            self.on.__enter__()
+        return s.cuda_stream
+
+    def __exit__(self, *e):
+        if self.on:
+            self.on.__exit__(*e)
+        if self.guard:
+            self.guard.__exit__(*e)
+
+
+def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
+          num_groups: int = 1, top_groups: int = 1, group_best: int = 1, renormalise: bool = True, scale: float = 1.0,
+          idx: torch.Tensor | None = None, w: torch.Tensor | None = None, stream=None):
+    """The chosen experts of each row of ``logits`` (bf16 or fp32 [T, E], any row
+    stride) and their weights: (int32 [T, k], fp32 [T, k]), as moe_decode_route
+    documents. ``score``: "softmax" or "sigmoid"; ``bias`` fp32 [E]."""
+    _need(logits.dim() == 2 and logits.dtype in _DTYPES, "logits must be a bf16 or fp32 [rows, experts] tensor")
+    t, e = logits.shape
+    _need(t == 0 or e == 1 or logits.stride(1) == 1, "a row of logits must be contiguous")
+    _need(score in _lib.ROUTE_SCORES, f"unknown score {score!r}")
+    lib = _lib.load()
+    cfg = _lib.RouteConfig(e, top_k, _lib.ROUTE_SCORES[score], num_groups, top_groups, group_best, renormalise,
+                           _DTYPES[logits.dtype], scale)
+    _lib.check(lib.moe_decode_route_check(cfg), "moe_decode_route_check")
+    dev = logits.device
+    b = None if bias is None else _tensor(bias, "bias", torch.float32, (e,), dev)
+    with _On(dev, stream) as s:
+        if idx is None:
+            idx = torch.empty((t, top_k), dtype=torch.int32, device=dev)
+        if w is None:
+            w = torch.empty((t, top_k), dtype=torch.float32, device=dev)
+        _lib.check(lib.moe_decode_route(cfg, logits.data_ptr(), logits.stride(0) if t > 1 else e, b, t,
+                                        _tensor(idx, "idx", torch.int32, (t, top_k), dev),
+                                        _tensor(w, "w", torch.float32, (t, top_k), dev), s), "moe_decode_route")
+    return idx, w
+
+
+def _quantised(wdtype: str, n: tuple, rows: int, cols: int, halves: int):
+    """(dtype, shape) of a matrix's codes, block scales and tensor scale; leading dims n."""
+    if wdtype == "bf16":
+        return ((torch.bfloat16, (*n, rows, cols)),)
+    if wdtype == "fp8":
+        return (torch.uint8, (*n, rows, cols)), (torch.float32, (*n, rows // 128, cols // 128))
+    return ((torch.uint8, (*n, rows, cols // 2)), (torch.uint8, (*n, rows, cols // 16)),
+            (torch.float32, (*n, 2) if halves == 2 else n))
+
+
+_SUFFIX = {"bf16": ("",), "fp8": ("_q", "_s"), "nvfp4": ("_q", "_s", "_gs")}
+_FIELDS = {"": "", "_q": "", "_s": "_scale", "_gs": "_gscale"}
+
+
+def expert_weights(shape: LayerShape, weights: dict, device) -> _lib.Weights:
+    """The C struct of a layer's routed and shared expert weights (dict layout of synth.make_layer)."""
+    _need(weights.get("w2_layout", "h_i") == "h_i", "down matrices must be stored [E, H, I] (w2_layout h_i)")
+    h, i = shape.hidden, shape.inter
+    out = _lib.Weights()
+    for prefix, n in (("", shape.num_experts), ("sh_", shape.num_shared)):
+        if n == 0:
+            continue
+        for name, rows, cols, halves in (("w13", 2 * i, h, 2), ("w2", h, i, 1)):
+            for sfx, (dtype, size) in zip(_SUFFIX[shape.wdtype], _quantised(shape.wdtype, (n,), rows, cols, halves)):
+                key = prefix + name + sfx
+                _need(key in weights, f"weights lack {key}")
+                setattr(out, prefix + name + _FIELDS[sfx], _tensor(weights[key], key, dtype, size, device))
+    return out
+
+
+def _workspace(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.device == device and
+          workspace.numel() >= need, f"the workspace must be a contiguous uint8 tensor of at least {need} bytes on {device}")
+    return workspace
+
+
+def experts_workspace(shape: LayerShape, rows: int) -> int:
+    """Bytes of workspace that :func:`experts` needs for at most ``rows`` rows."""
+    n = ctypes.c_size_t()
+    _lib.check(_lib.load().moe_decode_experts_workspace(_experts_config(shape), rows, n),
+               "moe_decode_experts_workspace")
+    return n.value
+
+
+def _experts_config(shape: LayerShape) -> _lib.ExpertsConfig:
+    _need(shape.wdtype in _lib.WDTYPE, f"unknown weight type {shape.wdtype!r}")
+    return _lib.ExpertsConfig(shape.hidden, shape.inter, shape.num_experts, shape.top_k, shape.num_shared,
+                              _lib.WDTYPE[shape.wdtype])
+
+
+def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, *,
+            residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """bf16 [T, H]: residual + the weighted sum of the chosen experts' MLPs of x (and
+    the shared experts'), as moe_decode_experts documents. ``weights``: the dict
+    layout of synth.make_layer, or what :func:`expert_weights` made of it; ``x`` bf16
+    [T, H], any row stride of a multiple of 8; ``idx`` int32 and ``w`` fp32 [T, k];
+    an index outside the experts (-1) takes no part."""
+    lib = _lib.load()
+    cfg = _experts_config(shape)
+    _lib.check(lib.moe_decode_experts_check(cfg), "moe_decode_experts_check")
+    dev = x.device
+    px, sx = _rows(x, "x", shape.hidden, dev)
+    t = x.shape[0]
+    cw = weights if isinstance(weights, _lib.Weights) else expert_weights(shape, weights, dev)
+    pi = _tensor(idx, "idx", torch.int32, (t, shape.top_k), dev)
+    pw = _tensor(w, "w", torch.float32, (t, shape.top_k), dev)
+    pr = None if residual is None else _tensor(residual, "residual", torch.bfloat16, (t, shape.hidden), dev)
+    n = ctypes.c_size_t()
+    _lib.check(lib.moe_decode_experts_workspace(cfg, t, n), "moe_decode_experts_workspace")
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty((t, shape.hidden), dtype=torch.bfloat16, device=dev)
+        ws = _workspace(workspace, n.value, dev)
+        _lib.check(lib.moe_decode_experts(cfg, cw, px, sx, pi, pw, pr,
+                                          _tensor(out, "out", torch.bfloat16, (t, shape.hidden), dev), t,
+                                          ws.data_ptr(), ws.numel(), s), "moe_decode_experts")
+    return out
+
+
+def _project_config(wdtype: str, inner: int, outer: int, swiglu: bool, adapters: Adapters | None, out_dtype):
+    _need(wdtype in _lib.WDTYPE, f"unknown weight type {wdtype!r}")
+    _need(out_dtype in _DTYPES, "the result is bf16 or fp32")
+    count, rank = (0, 0) if adapters is None else adapters.a.shape[:2]
+    return _lib.ProjectConfig(inner, outer, swiglu, _lib.WDTYPE[wdtype], rank, count, _DTYPES[out_dtype])
+
+
+def project_workspace(inner: int, outer: int, rows: int, *, wdtype: str = "bf16", swiglu: bool = False, rank: int = 0,
+                      num_adapters: int = 0, out_dtype=torch.bfloat16) -> int:
+    """Bytes of workspace that :func:`project` needs for at most ``rows`` rows."""
+    n = ctypes.c_size_t()
+    cfg = _lib.ProjectConfig(inner, outer, swiglu, _lib.WDTYPE[wdtype], rank, num_adapters, _DTYPES[out_dtype])
+    _lib.check(_lib.load().moe_decode_project_workspace(cfg, rows, n), "moe_decode_project_workspace")
+    return n.value
+
+
+def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters | None = None,
+            adapter_ids: torch.Tensor | None = None, addend: torch.Tensor | None = None, swiglu: bool = False,
+            out: torch.Tensor | None = None, out_dtype=torch.bfloat16, workspace: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """[T, O]: W x + the low-rank product of each row's adapter (+ addend), or with
+    ``swiglu`` silu(gate) * up of its two halves, as moe_decode_project documents.
+    ``x`` bf16 [T, K], any row stride of a multiple of 8. ``weight``: bf16 [O, K]
+    ([2 O, K] with swiglu), or for ``wdtype`` "fp8" / "nvfp4" the tuple (codes, block
+    scales) / (codes, block scales, tensor scale [] or [2]). ``adapter_ids`` int32 [T]: the
+    adapter of each row, outside 0..L-1 (-1) none."""
+    lib = _lib.load()
+    dev = x.device
+    parts = weight if isinstance(weight, (tuple, list)) else (weight,)
+    _need(x.dim() == 2, "x must be [rows, inner]")
+    halves = 2 if swiglu else 1
+    t, k = x.shape
+    rows = parts[0].shape[0]
+    _need(rows % halves == 0, "a gate/up weight has an even number of rows")
+    o = rows // halves
+    _need((adapters is None) == (adapter_ids is None), "adapters and adapter_ids come together")
+    if adapters is not None:
+        _need(adapters.a.dim() == 3 and adapters.a.shape[0] > 0 and adapters.a.shape[1] > 0, "adapters.a must be [L, r, K]")
+    if out is not None:
+        out_dtype = out.dtype
+    cfg = _project_config(wdtype, k, o, swiglu, adapters, out_dtype)
+    _lib.check(lib.moe_decode_project_check(cfg), "moe_decode_project_check")
+    px, sx = _rows(x, "x", k, dev)
+    want = _quantised(wdtype, (), rows, k, halves)
+    _need(len(parts) == len(want), f"a {wdtype} weight comes in {len(want)} tensors")
+    cw = _lib.ProjectWeights()
+    for field, t_, (dtype, size) in zip(("w", "w_scale", "w_gscale"), parts, want):
+        setattr(cw, field, _tensor(t_, field, dtype, size, dev))
+    ids = None
+    if adapters is not None:
+        n, r = cfg.num_adapters, cfg.rank
+        cw.a = _tensor(adapters.a, "adapters.a", torch.bfloat16, (n, r, k), dev)
+        cw.b = _tensor(adapters.b, "adapters.b", torch.bfloat16, (n, rows, r), dev)
+        if adapters.scale is not None:
+            cw.scale = _tensor(adapters.scale, "adapters.scale", torch.float32, (n,), dev)
+        ids = _tensor(adapter_ids, "adapter_ids", torch.int32, (t,), dev)
+    pa = None if addend is None else _tensor(addend, "addend", torch.bfloat16, (t, o), dev)
+    need = ctypes.c_size_t()
+    _lib.check(lib.moe_decode_project_workspace(cfg, t, need), "moe_decode_project_workspace")
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty((t, o), dtype=out_dtype, device=dev)
+        ws = _workspace(workspace, need.value, dev)
+        _lib.check(lib.moe_decode_project(cfg, cw, px, sx, ids, pa, _tensor(out, "out", out_dtype, (t, o), dev), t,
+                                          ws.data_ptr(), ws.numel(), s), "moe_decode_project")
+    return out
+
+
+def status(workspace: torch.Tensor, stream=None) -> int:
+    """Synchronise and return the status code of the last call that used ``workspace``."""
+    with _On(workspace.device, stream) as s:
+        return _lib.load().moe_decode_rows_status(workspace.data_ptr(), s)

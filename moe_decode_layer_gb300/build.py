@@ -25,7 +25,8 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_decode.so")
 
-SOURCES = ["api.cu", "kernels_bf16.cu", "kernels_nvfp4.cu", "kernels_fp8.cu", "kernels_flat.cu", "kernels_sk.cu", "static_run.cu"]
+SOURCES = ["api.cu", "kernels_bf16.cu", "kernels_nvfp4.cu", "kernels_fp8.cu", "kernels_flat.cu", "kernels_sk.cu", "static_run.cu",
+           "rows_api.cu", "rows_kernels.cu", "rows_route.cu", "rows_gemm.cu", "rows_gemm_fp8.cu", "rows_gemm_nvfp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
          "--expt-relaxed-constexpr"]
@@ -40,7 +41,7 @@ def nvcc() -> str:
 
 def _deps() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "moe_decode.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

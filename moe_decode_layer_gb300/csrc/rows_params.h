@@ -1,0 +1,92 @@
+// Launch parameters and constants of the many-row operators, shared by the host
+// code (rows_api.cu) and the kernels.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "moe_params.h"
+
+namespace moe {
+namespace rows {
+
+constexpr int kMaxN = 256;        // rows of x per tile
+constexpr int kMaxStages = 48;    // operand stages in shared memory
+constexpr int kMaxRaw = 8;        // slots of quantised codes
+constexpr int kGatherThreads = 128;
+constexpr int kWidenThreads = 256;
+constexpr int kMaxGroups = 1024 + 8;  // experts and shared experts, or adapters
+constexpr int kMaxAdapters = 1024;
+constexpr int kMaxSms = 512;      // status words of a launch
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+constexpr unsigned long long kDrainNs = 1000000ull;
+
+// What the epilogue makes of the accumulators.
+enum Epi {
+  EPI_SWIGLU = 0,  // bf16 silu(gate) * up
+  EPI_F32 = 1,     // fp32
+  EPI_BF16 = 2     // bf16, with a scale per group
+};
+
+// How the rows' adapters join the sum.
+enum AdMode {
+  AD_NONE = 0,
+  AD_STEPS = 1,    // more K steps on the tensor core, each over one adapter's rows
+  AD_EPILOGUE = 2  // fp32 products of few rows, added in the epilogue
+};
+
+constexpr int threads_of(int fmt) { return fmt == FMT_BF16 ? 320 : 320 + kWidenThreads; }
+// k's in 128 bytes of codes
+constexpr int kmath(int fmt) { return fmt == FMT_FP8 ? 128 : 256; }
+
+struct GemmParams {
+  // weights
+  int R;            // output rows per group (EPI_SWIGLU: gate rows)
+  int K;
+  int rt;           // weight rows per sub-tile (multiple of 8, <= 128)
+  int nrb;          // tiles along R
+  int groups_main;  // groups of map_w; later ones are map_s's
+  const void* wscale;    // FP8 / NVFP4 block scales
+  const void* wscale_s;
+  const float* gscale;   // NVFP4 tensor scales; EPI_BF16: a scale per group
+  const float* gscale_s;
+  // rows of x
+  const __nv_bfloat16* src;
+  int64_t src_stride;
+  const int* src_row;  // row of x at each sorted position (NULL: the position)
+  int rows;            // uniform tiles: rows in all
+  int nmax;            // rows per tile at most
+  const int4* ents;    // {group, first position, rows, block | blocks << 16}, or NULL: uniform tiles
+  const int* nent;
+  // adapters
+  int ad_mode;         // AdMode
+  int num_adapters;
+  int rank;
+  // AD_STEPS: positions off[a] .. off[a + 1] (multiples of 16) belong to adapter a,
+  // off[num_adapters] .. off[num_adapters + 1] to none; B is map_s
+  const int* adapter_off;
+  const __nv_bfloat16* u;  // [positions, rank]
+  // AD_EPILOGUE: rows in their own order
+  const int* ids;
+  const float* u32;        // [rows, rank]
+  const __nv_bfloat16* b;  // [num_adapters][halves * R][rank]
+  int ad_off;              // shared memory of the tile's adapter products
+  // results
+  void* out;
+  int64_t out_stride;
+  const int* out_row;  // row of out at each sorted position (NULL: the position)
+  const __nv_bfloat16* addend;  // laid out as out
+  int* status;         // [kMaxSms] one word per CTA: 1 = a wait ran into its limit
+  int* status_clear;   // [kMaxSms] another launch's words when that launch is left out, or NULL
+  int status_keep;     // 1: a later round of the same call; words are only set
+  // shared memory
+  int stages;
+  int stage_bytes;
+  int raw_off;
+  int raw_slots;
+  int pdl;
+};
+
+const void* gemm_kernel(int epi, int fmt);
+}  // namespace rows
+}  // namespace moe

@@ -1,0 +1,469 @@
+// Routing of any number of rows: one warp per row, the row's logits in registers.
+//
+// The choice is made on 32-bit keys and costs few instructions:
+//   1. each lane's largest key; K rounds of a warp maximum over the 32 lane maxima
+//      (each round retires the lanes that hold it) give a lower bound on the K-th
+//      largest key;
+//   2. the keys at or above the bound (about K of them) are listed in shared
+//      memory; each is ranked against the others, one lane per candidate.
+// Where the keys are rounded values (a bias, sums over groups), neighbours in the
+// order that are closer than their rounding errors, and not equal inputs, make the
+// row's choice anew in fp64, by the definition: rare, and needed for an order
+// that does not depend on how the scores were computed.
+//
+// Bound by the logits' bytes for many rows, by launch latency for few.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "ptx.cuh"
+#include "rows_kernels.h"
+
+namespace moe {
+namespace rows {
+namespace {
+
+constexpr int kWarps = 4;     // rows per CTA
+constexpr int kCand = 64;     // candidates listed per row
+constexpr float kMasked = -0x1.2ced34p+126f;  // the first fp32 at or below -1e38
+constexpr float kLargest = 3e38f;
+
+struct RouteParams {
+  const void* logits;
+  int64_t stride;
+  const float* bias;
+  int64_t rows;
+  int32_t* idx;
+  float* w;
+  int E, K;
+  int softmax;     // else sigmoid
+  int groups, kept, best, group_size;
+  int renormalise;
+  float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+  if constexpr (sizeof(T) == 2) return __bfloat162float(v);
+  else return v;
+}
+
+// NaN and masks -> -inf; +inf and the like -> a finite value, so that no sum is NaN.
+__device__ __forceinline__ float clean(float l) { return l > kMasked ? fminf(l, kLargest) : -INFINITY; }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  return order_key_f32(warp_max_u32(f32_order_key(v)));
+}
+
+__device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+// The row's choice by the definition, in fp64. src: the row's logits; key: E
+// doubles of shared memory. Lane j < K returns its expert or -1.
+template <typename T>
+__device__ __noinline__ int choose64(const RouteParams& p, const T* src, double* key, int lane) {
+  const int E = p.E;
+  auto l = [&](int e) { return clean(to_f32(src[e])); };
+  double norm = 1.0, top = 0.0;
+  if (p.softmax) {
+    float m = -INFINITY;
+    for (int e = lane; e < E; e += 32) m = fmaxf(m, l(e));
+    top = (double)warp_max(m);
+    double s = 0.0;
+    for (int e = lane; e < E; e += 32)
+      if (l(e) > kMasked) s += exp((double)l(e) - top);
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    norm = s;
+  }
+  for (int e = lane; e < E; e += 32) {
+    double v = -INFINITY;
+    if (l(e) > kMasked) {
+      v = p.softmax ? exp((double)l(e) - top) / norm : sigmoid64((double)l(e));
+      if (p.bias) v += (double)__ldg(p.bias + e);
+    }
+    key[e] = v;
+  }
+  __syncwarp();
+  uint32_t keep = 0xffffffffu;
+  if (p.kept < p.groups) {
+    double v = -INFINITY;
+    if (lane < p.groups) {
+      double b1 = -INFINITY, b2 = -INFINITY;
+      for (int i = 0; i < p.group_size; i++) {
+        const double x = key[lane * p.group_size + i];
+        if (x > b1) {
+          b2 = b1;
+          b1 = x;
+        } else if (x > b2) {
+          b2 = x;
+        }
+      }
+      v = b1;
+      if (p.best == 2 && b2 > -INFINITY) v += b2;
+    }
+    int rank = 0;
+    for (int g = 0; g < p.groups; g++) {
+      const double o = __shfl_sync(0xffffffffu, v, g);
+      rank += o > v || (o == v && g < lane);
+    }
+    keep = __ballot_sync(0xffffffffu, lane < p.groups && rank < p.kept);
+  }
+  if (!p.bias) {  // inside the kept groups the logits' order is the scores', also where fp64 holds them as equal
+    __syncwarp();
+    for (int e = lane; e < E; e += 32) key[e] = (double)l(e);
+    __syncwarp();
+  }
+  int mine = -1;
+  for (int j = 0; j < p.K; j++) {
+    double b = -INFINITY;
+    int at = E;
+    for (int e = lane; e < E; e += 32) {
+      const double x = key[e];
+      if (x > b && (keep >> (e / p.group_size) & 1)) {
+        b = x;
+        at = e;
+      }
+    }
+    for (int d = 16; d; d >>= 1) {
+      const double ob = __shfl_xor_sync(0xffffffffu, b, d);
+      const int oa = __shfl_xor_sync(0xffffffffu, at, d);
+      if (ob > b || (ob == b && oa < at)) {
+        b = ob;
+        at = oa;
+      }
+    }
+    if (lane == j && at < E) mine = at;
+    __syncwarp();
+    if (at < E && lane == 0) key[at] = -INFINITY;
+    __syncwarp();
+  }
+  return mine;
+}
+
+// The row's choice by K warp maxima over the exact keys: when so many keys tie
+// at the bound that they cannot all be listed.
+template <int N, typename At>
+__device__ __noinline__ int choose_rounds(const uint32_t (&k0)[N], int K, int lane, At at) {
+  uint32_t k[N];
+#pragma unroll
+  for (int j = 0; j < N; j++) k[j] = k0[j];
+  int mine = -1;
+  for (int r = 0; r < K; r++) {
+    uint32_t b = 0;
+    int e = 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < N; j++)
+      if (k[j] > b) {
+        b = k[j];
+        e = at(j);
+      }
+    const uint32_t m = warp_max_u32(b);
+    if (m == 0) break;
+    const int first = __reduce_min_sync(0xffffffffu, b == m ? e : 0x7fffffff);
+    if (lane == r) mine = first;
+#pragma unroll
+    for (int j = 0; j < N; j++)
+      if (at(j) == first) k[j] = 0;
+  }
+  return mine;
+}
+
+struct Cand {
+  uint32_t key;
+  int e;
+  float l;
+};
+
+// N: logits per lane (32 N >= E). VEC: 4 consecutive logits per lane and load.
+// KEYS: there is a bias, or groups (else the choice is by the logits alone, whose
+// order is the scores').
+template <typename T, int N, bool VEC, bool KEYS>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // KEYS: per warp E doubles
+  __shared__ Cand s_cand[kWarps][kCand];
+  __shared__ Cand s_sorted[kWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
+  if (row >= p.rows) return;
+  const int E = p.E, K = p.K;
+  auto at = [&](int j) { return VEC ? (j >> 2) * 128 + lane * 4 + (j & 3) : j * 32 + lane; };
+
+  float l[N];
+  const T* src = reinterpret_cast<const T*>(p.logits) + row * p.stride;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const int e = at(j);
+      if (e < E) {  // E % 4 == 0
+        if constexpr (sizeof(T) == 4) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(src + e));
+          l[j] = v.x;
+          l[j + 1] = v.y;
+          l[j + 2] = v.z;
+          l[j + 3] = v.w;
+        } else {
+          const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + e));
+          l[j] = bf16lo(v.x);
+          l[j + 1] = bf16hi(v.x);
+          l[j + 2] = bf16lo(v.y);
+          l[j + 3] = bf16hi(v.y);
+        }
+      } else {
+        l[j] = l[j + 1] = l[j + 2] = l[j + 3] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j++) l[j] = at(j) < E ? to_f32(src[at(j)]) : -INFINITY;
+  }
+  float lmax = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < N; j++) {
+    l[j] = clean(l[j]);
+    lmax = fmaxf(lmax, l[j]);
+  }
+
+  // sum over the row's softmax (its weights unnormalised over the chosen, or its keys)
+  float top = 0.0f, norm = 1.0f;
+  const bool whole = p.softmax && (KEYS || !p.renormalise);
+  if (whole) {
+    top = warp_max(lmax);
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; j++) s += l[j] > kMasked ? expf(l[j] - top) : 0.0f;
+    norm = warp_sum(s);
+  }
+
+  // 32-bit keys, order-preserving; 0: not to be chosen
+  uint32_t key[N];
+  float smax = 0.0f;  // KEYS: a bound on the row's scores, for the rounding errors
+  bool close = false;
+  float* s_key = nullptr;
+  if constexpr (KEYS) {
+    s_key = reinterpret_cast<float*>(s_dyn + (size_t)warp * E * 8);
+    float f[N];
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const int e = at(j);
+      const float s = p.softmax ? expf(l[j] - top) / norm : 1.0f / (1.0f + expf(-l[j]));
+      const bool ok = l[j] > kMasked;
+      smax = fmaxf(smax, ok ? s : 0.0f);
+      f[j] = ok ? (p.bias ? s + __ldg(p.bias + e) : s) : -INFINITY;
+      if (e < E) s_key[e] = f[j];
+    }
+    smax = warp_max(smax);
+    uint32_t keep = 0xffffffffu;
+    __syncwarp();
+    if (p.kept < p.groups) {
+      // lanes share a group's keys: sub lanes each (a power of two), merged by shuffles
+      int sub = 32;
+      while (sub * p.groups > 32) sub >>= 1;
+      const int g = lane / sub, u = lane % sub;
+      float b1 = -INFINITY, b2 = -INFINITY;
+      if (g < p.groups) {
+        const int n = (p.group_size + sub - 1) / sub;
+        int i = g % n;  // groups start at different steps: their lanes hit different banks
+        for (int q = 0; q < n; q++) {
+          const int o = i * sub + u;
+          if (o < p.group_size) {
+            const float x = s_key[g * p.group_size + o];
+            b2 = fmaxf(b2, fminf(b1, x));
+            b1 = fmaxf(b1, x);
+          }
+          i = i + 1 == n ? 0 : i + 1;
+        }
+      }
+      for (int d = 1; d < sub; d <<= 1) {
+        const float o1 = __shfl_xor_sync(0xffffffffu, b1, d), o2 = __shfl_xor_sync(0xffffffffu, b2, d);
+        b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+        b1 = fmaxf(b1, o1);
+      }
+      float v = b1;
+      if (p.best == 2 && b2 > -INFINITY) v += b2;
+      int rank = 0;
+      for (int o = 0; o < p.groups; o++) {
+        const float x = __shfl_sync(0xffffffffu, v, o * sub);
+        rank += x > v || (x == v && o < g);
+      }
+      const bool lead = u == 0 && g < p.groups;
+      const uint32_t in = __ballot_sync(0xffffffffu, lead && rank < p.kept);
+      // groups -> bits
+      keep = 0;
+      for (int o = 0; o < p.groups; o++) keep |= (in >> (o * sub) & 1u) << o;
+      // the last kept and the first dropped group: too close to tell in fp32?
+      const uint32_t l0 = __ballot_sync(0xffffffffu, lead && rank == p.kept - 1);
+      const uint32_t l1 = __ballot_sync(0xffffffffu, lead && rank == p.kept);
+      const float v0 = __shfl_sync(0xffffffffu, v, __ffs(l0) - 1), v1 = __shfl_sync(0xffffffffu, v, __ffs(l1) - 1);
+      if (v1 > -INFINITY) close = v0 - v1 <= 0x1p-17f * smax + 0x1p-20f * fmaxf(fabsf(v0), fabsf(v1));
+    }
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const int e = at(j);
+      const bool in = p.kept >= p.groups || (e < E && (keep >> (e / p.group_size) & 1u));
+      key[j] = in && f[j] > -INFINITY ? f32_order_key(p.bias ? f[j] : l[j] + 0.0f) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j++) key[j] = l[j] > kMasked ? f32_order_key(l[j] + 0.0f) : 0u;
+  }
+
+  // 1. a lower bound on the K-th largest key
+  uint32_t lane_max = 0;
+#pragma unroll
+  for (int j = 0; j < N; j++) lane_max = max(lane_max, key[j]);
+  uint32_t bound = 0, rest = lane_max;
+  for (int r = 0; r < K; r++) {
+    const uint32_t m = warp_max_u32(rest);
+    if (m == 0) break;
+    bound = m;
+    if (rest == m) rest = 0;
+  }
+  if (K > 1 && __popc(__ballot_sync(0xffffffffu, lane_max >= bound && lane_max)) < K) bound = 1;  // fewer lanes than K
+  if constexpr (KEYS) {
+    // a key below the bound by less than its rounding error is a candidate too
+    if (bound > 1 && p.bias) {
+      const float f = order_key_f32(bound);
+      bound = f32_order_key(f - (0x1p-18f * smax + 0x1p-21f * fabsf(f)));
+    }
+  }
+  bound = max(bound, 1u);
+
+  // 2. list and rank the candidates
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < N; j++) n += key[j] >= bound;
+  int before = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += o;
+  }
+  const int count = __shfl_sync(0xffffffffu, before, 31);
+  before -= n;
+  int mine = -1;       // lane j: the j-th chosen expert
+  float mine_l = 0.0f;
+  if (count <= kCand) {
+#pragma unroll
+    for (int j = 0; j < N; j++)
+      if (key[j] >= bound) s_cand[warp][before++] = Cand{key[j], at(j), l[j]};
+    __syncwarp();
+    for (int c = lane; c < count; c += 32) {
+      const Cand x = s_cand[warp][c];
+      int rank = 0;
+      for (int o = 0; o < count; o++) {
+        const uint32_t k = s_cand[warp][o].key;
+        rank += k > x.key || (k == x.key && s_cand[warp][o].e < x.e);
+      }
+      if (rank <= K && rank < 32) s_sorted[warp][rank] = x;
+    }
+    __syncwarp();
+    const int have = min(count, K);
+    if (lane < have) {
+      const Cand x = s_sorted[warp][lane];
+      mine = x.e;
+      mine_l = x.l;
+      if constexpr (KEYS) {
+        if (p.bias && lane + 1 < min(count, K + 1)) {
+          const Cand y = s_sorted[warp][lane + 1];
+          const float a = order_key_f32(x.key), b = order_key_f32(y.key);
+          const bool same = x.l == y.l && __ldg(p.bias + x.e) == __ldg(p.bias + y.e);
+          if (!same && a - b <= 0x1p-18f * smax + 0x1p-21f * fmaxf(fabsf(a), fabsf(b))) close = true;
+        }
+      }
+    }
+  } else {
+    if constexpr (KEYS) close = true;  // too many to rank: decide them in fp64
+    else mine = choose_rounds<N>(key, K, lane, at);
+    if (mine >= 0) mine_l = clean(to_f32(src[mine]));
+  }
+  if constexpr (KEYS) {
+    if (__any_sync(0xffffffffu, close)) {
+      __syncwarp();
+      mine = choose64<T>(p, src, reinterpret_cast<double*>(s_key), lane);
+      mine_l = mine >= 0 ? clean(to_f32(src[mine])) : 0.0f;
+    }
+  }
+
+  // weights
+  const bool there = lane < K && mine >= 0;
+  float s;
+  if (p.softmax) {
+    const float m = whole ? top : warp_max(there ? mine_l : -INFINITY);
+    s = there ? expf(mine_l - m) : 0.0f;
+    if (!p.renormalise) s /= norm;
+  } else {
+    // far below 0 a sigmoid is exp(l): common factors are taken out before fp32 loses them
+    const float m = warp_max(there ? mine_l : -INFINITY);
+    if (p.renormalise && m < -30.0f) s = there ? expf(mine_l - m) : 0.0f;
+    else s = there ? 1.0f / (1.0f + expf(-mine_l)) : 0.0f;
+  }
+  if (p.renormalise) {
+    const float sum = warp_sum(s);
+    s = sum > 0.0f ? s / sum : 0.0f;
+  }
+  if (lane < K) {
+    p.idx[row * K + lane] = there ? mine : -1;
+    p.w[row * K + lane] = there ? p.scale * s : 0.0f;
+  }
+}
+
+template <typename T, int N, bool VEC>
+cudaError_t launch_n(const RouteParams& p, bool keys, cudaStream_t s) {
+  const unsigned grid = (unsigned)((p.rows + kWarps - 1) / kWarps);
+  if (keys) {
+    const size_t smem = (size_t)kWarps * p.E * 8;  // at most 32 KB (E = 1024)
+    route_kernel<T, N, VEC, true><<<grid, kWarps * 32, smem, s>>>(p);
+  } else {
+    route_kernel<T, N, VEC, false><<<grid, kWarps * 32, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const RouteParams& p, bool keys, cudaStream_t s) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p.logits);
+  // four consecutive logits in one load: every row starts on a multiple of it
+  const bool vec = p.E % 4 == 0 && p.stride % 4 == 0 && a % (4 * sizeof(T)) == 0 && p.E > 64;
+  if (vec) {
+    if (p.E <= 128) return launch_n<T, 4, true>(p, keys, s);
+    if (p.E <= 256) return launch_n<T, 8, true>(p, keys, s);
+    if (p.E <= 512) return launch_n<T, 16, true>(p, keys, s);
+    return launch_n<T, 32, true>(p, keys, s);
+  }
+  if (p.E <= 64) return launch_n<T, 2, false>(p, keys, s);
+  if (p.E <= 128) return launch_n<T, 4, false>(p, keys, s);
+  if (p.E <= 256) return launch_n<T, 8, false>(p, keys, s);
+  if (p.E <= 512) return launch_n<T, 16, false>(p, keys, s);
+  return launch_n<T, 32, false>(p, keys, s);
+}
+
+}  // namespace
+
+cudaError_t launch_route(const moe_route_config& c, const void* logits, int64_t stride, const float* bias,
+                         int64_t rows, int32_t* idx, float* w, cudaStream_t s) {
+  RouteParams p;
+  p.logits = logits;
+  p.stride = stride;
+  p.bias = bias;
+  p.rows = rows;
+  p.idx = idx;
+  p.w = w;
+  p.E = c.num_experts;
+  p.K = c.top_k;
+  p.softmax = c.score == MOE_ROUTE_SOFTMAX;
+  p.groups = c.num_groups;
+  p.kept = c.top_groups;
+  p.best = c.group_best;
+  p.group_size = c.num_experts / c.num_groups;
+  p.renormalise = c.renormalise != 0;
+  p.scale = c.scale;
+  const bool keys = bias || c.top_groups < c.num_groups;
+  return c.logits_dtype == MOE_F32 ? launch_t<float>(p, keys, s) : launch_t<__nv_bfloat16>(p, keys, s);
+}
+
+}  // namespace rows
+}  // namespace moe

@@ -5,10 +5,11 @@ moe_decode_create / moe_decode_run. No arithmetic happens here.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 
 import torch
 
-from . import _lib
+from . import _lib, batch
 from .synth import LayerShape
 
 
@@ -111,6 +112,44 @@ class MoEDecodeLayer:
                                                 _ptr(topk_idx), _ptr(topk_w), _stream_ptr(stream)),
                    "moe_decode_run_host")
         return out
+
+    def run_rows(self, x: torch.Tensor, residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 topk_idx: torch.Tensor | None = None, topk_w: torch.Tensor | None = None, *,
+                 num_groups: int = 1, top_groups: int = 1, group_best: int = 1,
+                 adapters: tuple[batch.Adapters, batch.Adapters] | None = None,
+                 adapter_ids: torch.Tensor | None = None, stream=None):
+        """The same layer for any number of rows (a chunk of a prompt, many requests):
+        router logits, batch.route and batch.experts one after another, with this
+        layer's weights, scoring rule and routed scale. Nothing of the handle is
+        used, so runs on different streams may overlap. ``num_groups``,
+        ``top_groups`` and ``group_best`` limit the choice to the best groups of
+        experts. ``adapters``: the low-rank adapters of the one shared expert's
+        gate/up and down projections, and ``adapter_ids`` int32 [T] each row's; the
+        shared expert's output is then added to the residual in a rounding to
+        bf16 of its own. Not for layers with pre_rmsnorm or transposed down matrices."""
+        if self._cfg.pre_rmsnorm:
+            raise ValueError("run_rows takes the layer's normalised input: pre_rmsnorm is not computed")
+        residual = x if residual is None else residual
+        sig = self._cfg.score == _lib.MOE_SCORE_SIGMOID_BIAS
+        logits = batch.project(x, self._weights["router_w"], out_dtype=torch.float32, stream=stream)
+        idx, w = batch.route(logits, self.shape.top_k, score="sigmoid" if sig else "softmax",
+                             bias=self._weights["router_bias"] if sig else None, num_groups=num_groups,
+                             top_groups=top_groups, group_best=group_best, scale=self._cfg.routed_scale,
+                             idx=topk_idx, w=topk_w, stream=stream)
+        shape = self.shape
+        if adapters is not None:
+            if shape.num_shared != 1:
+                raise ValueError("adapters belong to the one shared expert of a layer")
+            sfx = batch._SUFFIX[shape.wdtype]
+            w13, w2 = (tuple(self._weights["sh_" + n + f][0] for f in sfx) for n in ("w13", "w2"))
+            h = batch.project(x, w13, wdtype=shape.wdtype, swiglu=True, adapters=adapters[0], adapter_ids=adapter_ids,
+                              stream=stream)
+            residual = batch.project(h, w2, wdtype=shape.wdtype, adapters=adapters[1], adapter_ids=adapter_ids,
+                                     addend=residual, stream=stream)
+            shape = dataclasses.replace(shape, num_shared=0)
+        elif adapter_ids is not None:
+            raise ValueError("adapters and adapter_ids come together")
+        return batch.experts(shape, self._weights, x, idx, w, residual=residual, out=out, stream=stream)
 
     def host_copy_bytes(self, m: int) -> tuple[int, int]:
         """Bytes run_host copies per call with m rows and x as the residual: (in, out).
