@@ -63,6 +63,19 @@ bool make_map(CUtensorMap* m, const void* ptr, int fmt, int64_t cols, int64_t ro
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [rows][cols] bf16, row r at ptr + r * stride elements, copied 64 columns x box rows.
+bool make_rows_map(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64_t stride, int box) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(stride * 2)};
+  const cuuint32_t b[2] = {64, (cuuint32_t)box};
+  const cuuint32_t one[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, b, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Device {
   int sms = 0, smem = 0, id = 0;
 };
@@ -99,20 +112,24 @@ bool layout(int rt, int nmax, int fmt, int ksteps, int ad_mode, int smem_max, La
 }
 
 // Rows of a sub-tile. A tile costs, per 64 k, the larger of its weight bytes (an
-// SM's share of the HBM rate is about 23 bytes a clock) and its tensor time (a
-// sub-tile takes 2 n16 clocks whatever rt is), and a fixed share for its start and
-// epilogue. The tiles go round the SMs in waves: rt is what makes the sum least.
-int choose_rt(int64_t R, bool swiglu, double entries, int n, int fmt, int nmax, int ksteps, int ad_mode,
+// SM's share of the HBM rate is about 23 bytes a clock), its operand bytes (about 45
+// a clock from L2) and its tensor time (a sub-tile takes 2 n16 clocks whatever rt
+// is), and a fixed share for its start and epilogue. The tiles go round the SMs in
+// waves: rt is what makes the sum least. It is a multiple of 16 (or 8, when that
+// little is wanted): a warp's results then start on a 32-byte sector, and stores of
+// part of a sector cost more than the product (rt = 104 against 112: 575 against ...).
+// reuse: tiles that read the same weights.
+int choose_rt(int64_t R, bool swiglu, double entries, double reuse, int n, int fmt, int nmax, int ksteps, int ad_mode,
               const Device& d) {
   int best = 128;
   double least = 1e300;
   const double bytes = fmt == FMT_BF16 ? 256.0 : fmt == FMT_FP8 ? 128.0 : 72.0;
-  for (int rt = 128; rt >= 8; rt -= 8) {
+  for (int rt = 128; rt >= 8; rt -= rt > 16 ? 16 : 8) {
     Layout l;
     if (!layout(rt, nmax, fmt, ksteps, ad_mode, d.smem, &l)) continue;
     const int64_t nrb = cdiv(R, swiglu ? rt : 2 * rt);
     const double waves = std::ceil(entries * (double)nrb / d.sms);
-    const double step = std::max(rt * bytes / 23.0, 4.0 * n);
+    const double step = std::max({rt * bytes / (23.0 * reuse), (rt * 256.0 + n * 128.0) / 45.0, 4.0 * n});
     const double cost = waves * (ksteps * step + 2500.0);
     if (cost < least * 0.999) {
       least = cost;
@@ -122,8 +139,11 @@ int choose_rt(int64_t R, bool swiglu, double entries, int n, int fmt, int nmax, 
   return best;
 }
 
-cudaError_t launch_gemm(GemmParams& p, int epi, int fmt, const CUtensorMap& w, const CUtensorMap& s, int64_t tiles,
-                        const Layout& l, const Device& d, bool pdl, cudaStream_t st) {
+struct Maps {
+  CUtensorMap w, s, x, u;  // weights, the shared experts' or the adapters', rows, the rows' adapter products
+};
+
+cudaError_t launch_gemm(GemmParams& p, int epi, int fmt, Maps& m, int64_t tiles, const Layout& l, const Device& d, bool pdl, cudaStream_t st) {
   const void* k = gemm_kernel(epi, fmt);
   static std::atomic<uint64_t> ready[3][3];  // per kernel: devices whose limit is set
   if (d.id >= 64 || !(ready[epi][fmt].load() >> d.id & 1)) {
@@ -147,7 +167,7 @@ cudaError_t launch_gemm(GemmParams& p, int epi, int fmt, const CUtensorMap& w, c
   a[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   c.attrs = a;
   c.numAttrs = 1;
-  void* args[] = {&p, const_cast<CUtensorMap*>(&w), const_cast<CUtensorMap*>(&s)};
+  void* args[] = {&p, &m.w, &m.s, &m.x, &m.u};
   return cudaLaunchKernelExC(&c, k, args);
 }
 
@@ -165,6 +185,7 @@ struct ExpertsPlan {
   int64_t rows = 0;  // rows of a round
   int64_t positions = 0;
   int nmax = 0;
+  bool spread = false;  // x is copied into the groups' order first (into y's place)
   size_t status = 0, off = 0, nent = 0, ents = 0, src_row = 0, pos = 0, h = 0, y = 0, bytes = 0;
   double touched = 0;
 };
@@ -178,6 +199,10 @@ ExpertsPlan experts_plan(const moe_experts_config& c, int64_t rows) {
   // quantised formats keep half of the shared memory for their codes
   const double avg = pairs / std::max(1.0, p.touched);
   p.nmax = std::max(kMinN, round16(2.0 * avg + 8.0));
+  // Listed rows come four to a copy, about 43 clocks each: up to 128 rows a tile that
+  // hides behind the weights' copies (1400 clocks a step), with 256 it is the longest
+  // part (2800 clocks against the tensor core's 1024); then a pass over x pays.
+  p.spread = p.nmax > 128;
   if (p.nmax > 128) p.nmax = fmt_of(c.wdtype) == FMT_BF16 ? kMaxN : 128;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -189,7 +214,7 @@ ExpertsPlan experts_plan(const moe_experts_config& c, int64_t rows) {
   p.off = take((size_t)(c.num_experts + 1) * 4);
   p.nent = take(4);
   p.ents = take((size_t)(cdiv(pairs, kMinN) + c.num_experts + c.num_shared * cdiv(p.rows, kMinN)) * sizeof(int4));
-  p.src_row = take((size_t)p.positions * 4);
+  p.src_row = take((size_t)pairs * 4);
   p.pos = take((size_t)pairs * 4);
   p.h = take((size_t)p.positions * c.inter * 2);
   p.y = take((size_t)p.positions * c.hidden * 4);
@@ -212,7 +237,7 @@ struct ProjectPlan {
   int mode = AD_NONE;
   int nmax = 0, nmax_a = 0;
   int64_t positions = 0;  // rows, with AD_STEPS those of each adapter padded to 16
-  size_t status = 0, off = 0, nent = 0, ents = 0, src_row = 0, u = 0, bytes = 0;
+  size_t status = 0, off = 0, nent = 0, ents = 0, src_row = 0, u = 0, x = 0, bytes = 0;
 };
 // Adapters' rows go through the tensor core, 16 columns at least for each adapter,
 // when that pads little or there are many rows; else (decoding, where every row may
@@ -238,6 +263,7 @@ ProjectPlan project_plan(const moe_project_config& c, int64_t rows) {
     p.ents = take((size_t)(cdiv(rows, 16) + c.num_adapters) * sizeof(int4));
     p.src_row = take((size_t)p.positions * 4);
     p.u = take((size_t)p.positions * c.rank * 2);
+    p.x = take((size_t)p.positions * c.inner * 2);  // x in the adapters' order
   } else if (p.mode == AD_EPILOGUE) {
     p.u = take((size_t)rows * c.rank * 4);
   }
@@ -374,15 +400,16 @@ moe_status moe_decode_experts(const moe_experts_config* c, const moe_decode_weig
     GemmParams g1 = g;
     g1.R = c->inter;
     g1.K = c->hidden;
-    g1.rt = choose_rt(c->inter, true, entries, n_avg, fmt, p.nmax, (c->hidden + 63) / 64, AD_NONE, d);
+    g1.rt = choose_rt(c->inter, true, entries, blocks, n_avg, fmt, p.nmax, (c->hidden + 63) / 64, AD_NONE, d);
     g1.nrb = (int)cdiv(c->inter, g1.rt);
     g1.wscale = wt->w13_scale;
     g1.wscale_s = wt->sh_w13_scale;
     g1.gscale = wt->w13_gscale;
     g1.gscale_s = wt->sh_w13_gscale;
-    g1.src = static_cast<const __nv_bfloat16*>(x) + r0 * x_stride;
-    g1.src_stride = x_stride;
-    g1.src_row = pl.src_row;
+    g1.src_row = p.spread ? nullptr : pl.src_row;
+    g1.box_rows = p.nmax % 32 ? 16 : 32;
+    g1.all_rows = sh ? (int)n : 0;
+    g1.all_first = (int)pairs;
     g1.out = h;
     g1.out_stride = c->inter;
     g1.status = status;
@@ -391,35 +418,42 @@ moe_status moe_decode_experts(const moe_experts_config* c, const moe_decode_weig
     GemmParams g2 = g;
     g2.R = c->hidden;
     g2.K = c->inter;
-    g2.rt = choose_rt(c->hidden, false, entries, n_avg, fmt, p.nmax, (c->inter + 63) / 64, AD_NONE, d);
+    g2.rt = choose_rt(c->hidden, false, entries, blocks, n_avg, fmt, p.nmax, (c->inter + 63) / 64, AD_NONE, d);
     g2.nrb = (int)cdiv(c->hidden, 2 * g2.rt);
     g2.wscale = wt->w2_scale;
     g2.wscale_s = wt->sh_w2_scale;
     g2.gscale = wt->w2_gscale;
     g2.gscale_s = wt->sh_w2_gscale;
-    g2.src = h;
-    g2.src_stride = c->inter;
+    g2.box_rows = p.nmax % 32 ? 16 : 32;
     g2.out = y;
     g2.out_stride = c->hidden;
     g2.status = status + kMaxSms;
     g2.status_keep = r0 > 0;
 
-    CUtensorMap m1, m1s, m2, m2s;
-    if (!make_map(&m1, wt->w13, fmt, c->hidden, c->inter, 2, c->num_experts, g1.rt) ||
-        !make_map(&m2, wt->w2, fmt, c->inter, c->hidden, 1, c->num_experts, g2.rt))
+    Maps m1, m2;
+    const __nv_bfloat16* xr = static_cast<const __nv_bfloat16*>(x) + r0 * x_stride;
+    if (!make_map(&m1.w, wt->w13, fmt, c->hidden, c->inter, 2, c->num_experts, g1.rt) ||
+        !make_map(&m2.w, wt->w2, fmt, c->inter, c->hidden, 1, c->num_experts, g2.rt) ||
+        !(p.spread ? make_rows_map(&m1.x, y, c->hidden, pairs, c->hidden, g1.box_rows)
+                   : make_rows_map(&m1.x, xr, c->hidden, n, x_stride, 1)) ||
+        !make_rows_map(&m1.u, xr, c->hidden, n, x_stride, g1.box_rows) ||
+        !make_rows_map(&m2.x, h, c->inter, p.positions, c->inter, g2.box_rows))
       return MOE_ERR_CUDA;
-    m1s = m1;
-    m2s = m2;
-    if (sh && (!make_map(&m1s, wt->sh_w13, fmt, c->hidden, c->inter, 2, c->num_shared, g1.rt) ||
-               !make_map(&m2s, wt->sh_w2, fmt, c->inter, c->hidden, 1, c->num_shared, g2.rt)))
+    m1.s = m1.w;
+    m2.s = m2.u = m2.w;
+    if (sh && (!make_map(&m1.s, wt->sh_w13, fmt, c->hidden, c->inter, 2, c->num_shared, g1.rt) ||
+               !make_map(&m2.s, wt->sh_w2, fmt, c->inter, c->hidden, 1, c->num_shared, g2.rt)))
       return MOE_ERR_CUDA;
     Layout l1, l2;
     if (!layout(g1.rt, p.nmax, fmt, (c->hidden + 63) / 64, AD_NONE, d.smem, &l1) ||
         !layout(g2.rt, p.nmax, fmt, (c->inter + 63) / 64, AD_NONE, d.smem, &l2))
       return MOE_ERR_UNSUPPORTED;
     cudaError_t e = launch_plan(pl, s);
-    if (e == cudaSuccess) e = launch_gemm(g1, EPI_SWIGLU, fmt, m1, m1s, ents_max * g1.nrb, l1, d, true, s);
-    if (e == cudaSuccess) e = launch_gemm(g2, EPI_F32, fmt, m2, m2s, ents_max * g2.nrb, l2, d, true, s);
+    if (e == cudaSuccess && p.spread)
+      e = launch_spread(xr, x_stride, pl.src_row, pl.off + c->num_experts, pairs, c->hidden,
+                        reinterpret_cast<__nv_bfloat16*>(y), s);
+    if (e == cudaSuccess) e = launch_gemm(g1, EPI_SWIGLU, fmt, m1, ents_max * g1.nrb, l1, d, true, s);
+    if (e == cudaSuccess) e = launch_gemm(g2, EPI_F32, fmt, m2, ents_max * g2.nrb, l2, d, true, s);
     if (e == cudaSuccess)
       e = launch_combine(y, pl.pos, w + r0 * c->top_k,
                          residual ? static_cast<const __nv_bfloat16*>(residual) + r0 * c->hidden : nullptr,
@@ -484,13 +518,12 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
   g.R = c->outer;
   g.K = c->inner;
   const double entries = (double)cdiv(p.positions, p.nmax);
-  g.rt = choose_rt(c->outer, swiglu, entries, p.nmax, fmt, p.nmax, ksteps, p.mode, d);
+  g.rt = choose_rt(c->outer, swiglu, entries, entries, p.nmax, fmt, p.nmax, ksteps, p.mode, d);
   g.nrb = (int)cdiv(c->outer, swiglu ? g.rt : 2 * g.rt);
   g.groups_main = 1;
   g.wscale = wt->w_scale;
   g.gscale = fmt == FMT_NVFP4 ? wt->w_gscale : nullptr;
-  g.src = static_cast<const __nv_bfloat16*>(x);
-  g.src_stride = x_stride;
+  g.box_rows = p.nmax % 32 ? 16 : 32;
   g.rows = (int)rows;
   g.nmax = p.nmax;
   g.out = out;
@@ -498,9 +531,12 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
   g.addend = static_cast<const __nv_bfloat16*>(addend);
   g.status = status + kMaxSms;
   g.status_clear = p.mode == AD_STEPS ? nullptr : status;
-  CUtensorMap m, ma, mb;
-  if (!make_map(&m, wt->w, fmt, c->inner, c->outer, swiglu ? 2 : 1, 1, g.rt)) return MOE_ERR_CUDA;
-  mb = m;
+  Maps m, ma;
+  if (!make_map(&m.w, wt->w, fmt, c->inner, c->outer, swiglu ? 2 : 1, 1, g.rt) ||
+      !(p.mode == AD_STEPS ? make_rows_map(&m.x, ws + p.x, c->inner, p.positions, c->inner, g.box_rows)
+                           : make_rows_map(&m.x, x, c->inner, rows, x_stride, g.box_rows)))
+    return MOE_ERR_CUDA;
+  m.s = m.u = m.w;
   Layout l, la;
   if (!layout(g.rt, p.nmax, fmt, ksteps, p.mode, d.smem, &l)) return MOE_ERR_UNSUPPORTED;
 
@@ -512,7 +548,7 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
     g.ids = ids;
     g.u32 = reinterpret_cast<const float*>(ws + p.u);
     g.b = static_cast<const __nv_bfloat16*>(wt->b);
-    e = launch_shrink(g.src, x_stride, static_cast<const __nv_bfloat16*>(wt->a), wt->scale, ids,
+    e = launch_shrink(static_cast<const __nv_bfloat16*>(x), x_stride, static_cast<const __nv_bfloat16*>(wt->a), wt->scale, ids,
                       reinterpret_cast<float*>(ws + p.u), (int)rows, c->inner, c->rank, c->num_adapters, s);
   } else if (p.mode == AD_STEPS) {
     PlanParams pl = {};
@@ -533,34 +569,36 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
     ga.R = c->rank;
     ga.K = c->inner;
     const double groups = std::min<double>(c->num_adapters, (double)rows);
-    ga.rt = choose_rt(c->rank, false, groups * std::ceil(rows / groups / p.nmax_a), p.nmax_a, FMT_BF16, p.nmax_a,
+    ga.rt = choose_rt(c->rank, false, groups * std::ceil(rows / groups / p.nmax_a), 1.0, p.nmax_a, FMT_BF16, p.nmax_a,
                       ksteps, AD_NONE, d);
     ga.nrb = (int)cdiv(c->rank, 2 * ga.rt);
     ga.groups_main = c->num_adapters;
     ga.gscale = wt->scale;
-    ga.src = g.src;
-    ga.src_stride = x_stride;
-    ga.src_row = pl.src_row;
+    ga.box_rows = p.nmax_a % 32 ? 16 : 32;
     ga.nmax = p.nmax_a;
     ga.ents = pl.ents;
     ga.nent = pl.nent;
     ga.out = ws + p.u;
     ga.out_stride = c->rank;
     ga.status = status;
-    if (!make_map(&ma, wt->a, FMT_BF16, c->inner, c->rank, 1, c->num_adapters, ga.rt) ||
-        !make_map(&mb, wt->b, FMT_BF16, c->rank, c->outer, swiglu ? 2 : 1, c->num_adapters, g.rt))
+    if (!make_map(&ma.w, wt->a, FMT_BF16, c->inner, c->rank, 1, c->num_adapters, ga.rt) ||
+        !make_map(&m.s, wt->b, FMT_BF16, c->rank, c->outer, swiglu ? 2 : 1, c->num_adapters, g.rt) ||
+        !make_rows_map(&m.u, ws + p.u, c->rank, p.positions, c->rank, 16))
       return MOE_ERR_CUDA;
+    if (!make_rows_map(&ma.x, ws + p.x, c->inner, p.positions, c->inner, ga.box_rows)) return MOE_ERR_CUDA;
+    ma.s = ma.u = ma.w;
     if (!layout(ga.rt, p.nmax_a, FMT_BF16, ksteps, AD_NONE, d.smem, &la)) return MOE_ERR_UNSUPPORTED;
     const int64_t tiles = (cdiv(rows, p.nmax_a) + std::min<int64_t>(c->num_adapters, rows)) * ga.nrb;
     e = launch_plan(pl, s);
-    if (e == cudaSuccess) e = launch_gemm(ga, EPI_BF16, FMT_BF16, ma, ma, tiles, la, d, true, s);
+    if (e == cudaSuccess)
+      e = launch_spread(static_cast<const __nv_bfloat16*>(x), x_stride, pl.src_row, pl.off + c->num_adapters + 1,
+                        p.positions, c->inner, reinterpret_cast<__nv_bfloat16*>(ws + p.x), s);
+    if (e == cudaSuccess) e = launch_gemm(ga, EPI_BF16, FMT_BF16, ma, tiles, la, d, true, s);
     g.adapter_off = pl.off;
-    g.u = reinterpret_cast<const __nv_bfloat16*>(ws + p.u);
-    g.src_row = pl.src_row;
     g.out_row = pl.src_row;
   }
   if (e == cudaSuccess)
-    e = launch_gemm(g, epi, fmt, m, mb, cdiv(p.positions, p.nmax) * g.nrb, l, d, p.mode != AD_NONE, s);
+    e = launch_gemm(g, epi, fmt, m, cdiv(p.positions, p.nmax) * g.nrb, l, d, p.mode != AD_NONE, s);
   return cuda_status(e);
 }
 

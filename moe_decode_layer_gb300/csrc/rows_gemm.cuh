@@ -16,9 +16,12 @@
 // rt is a run-time multiple of 8: a small matrix is cut into as many tiles as
 // there are SMs; TMEM lanes past rt hold leftovers that nothing reads.
 //
-// Warps: 0 weight copies (TMA, 128-byte swizzle), 1 tensor-core issue, 2..5
-// gather the x rows (16-byte cp.async, zero-filled past K), 6..9 epilogue; the
-// quantised formats add 8 warps that widen the codes into the bf16 stage.
+// Warps: 0 weight copies, 1 tensor-core issue, 2 copies of the rows of x (listed
+// rows four to a copy, neighbouring ones as a box), 4..11 epilogue; the quantised
+// formats add 8 warps that widen the codes into the bf16 stage. All copies are TMA
+// with the 128-byte swizzle of the operands, zero-filled past K. (A first version
+// gathered rows with 16-byte cp.async from four warps: with 256 rows a stage its
+// loop took 5900 clocks where the tensor core needs 1024.)
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -44,12 +47,19 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
-// Arrives on bar when all earlier cp.async of this thread have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+// Four rows of a map whose box is one row.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
@@ -92,19 +102,16 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
          ((uint64_t)2 << 61);
 }
 
-// Waits for a phase of an mbarrier, at most ~2 s; false when the limit or
-// another warp's limit (*abort) ended the wait.
+// Waits for a phase of an mbarrier, at most kWaitLimit probes of up to a
+// microsecond each; false when the limit or another warp's (*abort) ended the wait.
+// (Probes are counted: reading the global timer in this loop cost more than a stage.)
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (;;) {
+  for (uint32_t i = 0; i < kWaitLimit; i++) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      *abort = 1;
-      return false;
-    }
+    if ((i & 63) == 63 && *abort) return false;
   }
+  *abort = 1;
+  return false;
 }
 
 // The same for a whole warp, whose lanes all get the same answer.
@@ -172,7 +179,8 @@ __device__ __forceinline__ int adapter_next(const GemmParams& p, int a, int p0, 
   return p.num_adapters;
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// exp(-g) past fp32's range makes the quotient 0, as it should be.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // Widening of quantised codes to the bf16 operand.
 // FP8: w = bf16(e4m3 * block scale): one rounding of the product (2^-9 relative,
@@ -207,11 +215,11 @@ __device__ __forceinline__ uint32_t fp4x2_bf16x2_folded(uint32_t byte, float s) 
 template <int EPI, int FMT>
 __global__ void __launch_bounds__(threads_of(FMT), 1)
     rows_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap map_w,
-                     const __grid_constant__ CUtensorMap map_s) {
+                     const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_u) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_row[kMaxN];
   // full, empty [kMaxStages], tmem full / empty [2], raw full / empty [kMaxRaw], drain,
   // adapter products full / empty
   __shared__ __align__(8) uint64_t s_bar[2 * kMaxStages + 4 + 2 * kMaxRaw + 3];
@@ -230,16 +238,16 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 
   if (tid == 0) {
     s_abort = 0;
-    // a stage is full when its weights (TMA bytes, or every widening thread) and
-    // every gathering thread's rows are there
-    const uint32_t nfull = kGatherThreads + (FMT == FMT_BF16 ? 1 : kWidenThreads + 1);
+    // a stage is full when its weights (TMA bytes, or every widening thread and one
+    // arrival in the copies' place) and its rows of x (TMA bytes) are there
+    const uint32_t nfull = 1 + (FMT == FMT_BF16 ? 1 : kWidenThreads + 1);
     for (int s = 0; s < p.stages; s++) {
       mbar_init(full(s), nfull);
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), 4);
+      mbar_init(tempty(b), kEpilogueWarps);
     }
     if (FMT != FMT_BF16)
       for (int s = 0; s < p.raw_slots; s++) {
@@ -247,11 +255,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         mbar_init(rempty(s), kWidenThreads / 32);
       }
     mbar_init(drain, 1);
-    mbar_init(ad_full, 4);
-    mbar_init(ad_empty, 4);
+    mbar_init(ad_full, kEpilogueWarps);
+    mbar_init(ad_empty, kEpilogueWarps);
     mbar_init_fence();
     tma_prefetch_map(&map_w);
     tma_prefetch_map(&map_s);
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_u);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&s_tmem), 512);
@@ -263,7 +273,10 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   const uint32_t tmem = s_tmem;
   // With AD_EPILOGUE the launch before this one makes u32 alone, which the epilogue
   // warps wait for; the others start on the weights and rows at once.
-  if (p.pdl && (p.ad_mode != AD_EPILOGUE || (warp >= 6 && warp < 10))) pdl_wait();
+  if (p.pdl && (p.ad_mode != AD_EPILOGUE || (warp >= 4 && warp < 12))) {
+    pdl_wait();
+    fence_proxy_async_global();  // rows that the launch before wrote are read by TMA
+  }
   pdl_launch_dependents();
 
   const int ntiles = num_tiles(p);
@@ -348,7 +361,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           const int s = it % p.stages;
           if (!wait_phase(full(s), (it / p.stages) & 1, &s_abort)) return false;
           tc_fence_after();
-          fence_proxy_async_shared();  // the gathered rows were written by cp.async
           const uint32_t idesc = kDesc | ((uint32_t)((n + 15) >> 4) << 18);
           const uint32_t a = base + s * stage_bytes, bb = a + 2 * a_half + c * 128;
           const uint64_t da = smem_desc(a), db = smem_desc(bb), da1 = smem_desc(a + a_half);
@@ -379,54 +391,68 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
       }
     }
-  } else if (warp < 6) {
+  } else if (warp == 2) {
     // ---------------------------------------------------------------- rows of x
-    const int gt = tid - 64;             // 0..127
-    const int c = gt & 7, r0 = gt >> 3;  // 16-byte chunk, first row; 16 rows apart
     uint32_t it = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
       const Tile tl = tile_at(p, t);
-      // each warp lists the rows that it gathers: four of every 16
-      __syncwarp();
-      for (int i = 16 * (lane >> 2) + 4 * (warp - 2) + (lane & 3); i < tl.n; i += 128)
-        s_row[i] = p.src_row ? __ldg(p.src_row + tl.p0 + i) : tl.p0 + i;
-      __syncwarp();
+      // a group that every row belongs to has its rows in x's own order (map_u)
+      const bool all = p.all_rows && tl.g >= p.groups_main;
+      const bool listed = !all && p.src_row != nullptr;
+      const CUtensorMap* mx = all ? &map_u : &map_x;
+      const int y_box = all ? tl.p0 - p.all_first - (tl.g - p.groups_main) * p.all_rows : tl.p0;
+      // listed: lane i copies rows 4 i .. 4 i + 3 and those 128 further on; the last
+      // copy repeats a row, and padding takes row 0 (their columns are not read)
+      int4 y[2];
+      const int copies = listed ? (tl.n + 3) / 4 : (tl.n + p.box_rows - 1) / p.box_rows;
+      if (listed) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          int v[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) v[j] = max(__ldg(p.src_row + tl.p0 + min(4 * (lane + 32 * h) + j, tl.n - 1)), 0);
+          y[h] = make_int4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      const uint32_t bytes = copies * (listed ? 512u : p.box_rows * 128u);
       for (int k = 0; k < main_steps; k++, it++) {
         const int s = it % p.stages;
         if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
+        if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
+        __syncwarp();
         const uint32_t dst = base + s * stage_bytes + 2 * a_half;
-        const int k0 = k * 64 + c * 8;
-        const uint32_t bytes = k0 < p.K ? 16u : 0u;
-        const __nv_bfloat16* src = p.src + (bytes ? k0 : 0);
-        for (int r = r0; r < tl.n; r += 16) {
-          const int row = s_row[r];
-          if (row >= 0) cp_async16(dst + r * 128 + ((c ^ (r & 7)) << 4), src + (size_t)row * p.src_stride, bytes);
+        if (listed) {
+          if (lane < copies) tma_gather4(dst + lane * 512, &map_x, k * 64, y[0], full(s));
+          if (lane + 32 < copies) tma_gather4(dst + (lane + 32) * 512, &map_x, k * 64, y[1], full(s));
+        } else if (lane < copies) {
+          tma_load_2d(dst + lane * p.box_rows * 128, mx, k * 64, y_box + lane * p.box_rows, full(s));
         }
-        cp_async_arrive(full(s));
       }
       if (ok && ad_steps) {
         for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
              a = adapter_next(p, a + 1, tl.p0, tl.n)) {
           const int b = max(__ldg(p.adapter_off + a) - tl.p0, 0), e = min(__ldg(p.adapter_off + a + 1) - tl.p0, tl.n);
+          const int boxes = (e - b + 15) / 16;  // 16 rows each, as the adapter's are padded
           for (int k = 0; k < per_adapter; k++, it++) {
             const int s = it % p.stages;
             if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
-            const uint32_t dst = base + s * stage_bytes + 2 * a_half;
-            const int k0 = k * 64 + c * 8;
-            const uint32_t bytes = k0 < p.rank ? 16u : 0u;
-            for (int r = b + r0; r < e; r += 16)  // b is a multiple of 16
-              cp_async16(dst + r * 128 + ((c ^ (r & 7)) << 4), p.u + (size_t)(tl.p0 + r) * p.rank + (bytes ? k0 : 0),
-                         bytes);
-            cp_async_arrive(full(s));
+            if (lane == 0) mbar_arrive_expect_tx(full(s), boxes * 2048u);
+            __syncwarp();
+            const uint32_t dst = base + s * stage_bytes + 2 * a_half + b * 128;
+            if (lane < boxes) tma_load_2d(dst + lane * 2048, &map_u, k * 64, tl.p0 + b + lane * 16, full(s));
           }
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp < 10) {
+    if (!ok && lane == 0) {
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
+    }
+  } else if (warp >= 4 && warp < 12) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;  // this warp's 32 TMEM lanes
+    const int q = warp & 3;  // this warp's 32 TMEM lanes; two warps share them, 16 columns in turn
+    const int c0 = warp >= 8 ? 16 : 0;
     float* s_ad = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + p.ad_off);
     const int r = q * 32 + lane;
     uint32_t tcount = 0;
@@ -438,7 +464,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         // the tile's adapter products, while the tensor core works on the rest: one
         // thread per (weight row, row of x), weight rows of one sub-tile after another
         if (!(ok = warp_wait(ad_empty, (tcount + 1) & 1, &s_abort))) break;
-        for (int i = tid - 192; i < tl.n * 2 * p.rt; i += 128) {
+        for (int i = tid - 128; i < tl.n * 2 * p.rt; i += 32 * kEpilogueWarps) {
           const int c = i / (2 * p.rt), wr = i % (2 * p.rt);
           const int sub = wr >= p.rt;
           const int y = tl.rb * sub_rows + (EPI == EPI_SWIGLU ? wr - sub * p.rt : wr);
@@ -482,43 +508,62 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const int y0 = tl.rb * sub_rows + r;
         const int y1 = y0 + p.rt;
         const bool ok0 = r < p.rt && y0 < p.R, ok1 = EPI != EPI_SWIGLU && r < p.rt && y1 < p.R;
-        for (int c = 0; c < tl.n; c += 16) {
+        for (int c = c0; c < tl.n; c += 32) {
+          // Everything that is loaded is on its way before the first sum is used, and
+          // all 16 columns' results are made before the first is stored, without
+          // branches: with them each column waited for the one before (225 clocks).
           uint32_t v0[16], v1[16];
+          const int m = min(16, tl.n - c);
+          int row_l = tl.p0 + c + (lane & 15);  // lane j: the row of out of column j
+          if (p.out_row) row_l = (lane & 15) < m ? __ldg(p.out_row + row_l) : -1;
+          row_l = (lane & 15) < m ? row_l : -1;
           __syncwarp();
           tmem_ld16(d0 + c, v0);
           tmem_ld16(d1 + c, v1);
+          float e0[16], e1[16];
+          if (EPI != EPI_SWIGLU && p.addend) {
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+              const __nv_bfloat16* a = p.addend + (size_t)max(__shfl_sync(0xffffffffu, row_l, j), 0) * p.out_stride;
+              e0[j] = __bfloat162float(a[ok0 ? y0 : 0]);
+              e1[j] = __bfloat162float(a[ok1 ? y1 : 0]);
+            }
+          }
+          if (p.ad_mode == AD_EPILOGUE) {
+            const float* ad = s_ad + c * 2 * p.rt + min(r, p.rt - 1);
+            const bool add = EPI != EPI_SWIGLU && p.addend;
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+              const int at = j < m ? j * 2 * p.rt : 0;
+              e0[j] = (add ? e0[j] : 0.0f) + ad[at];
+              e1[j] = (add ? e1[j] : 0.0f) + ad[at + p.rt];
+            }
+          }
+          const bool extra = p.ad_mode == AD_EPILOGUE || (EPI != EPI_SWIGLU && p.addend);
           tmem_ld_wait();
-          const int m = min(16, tl.n - c);
+          float a0[16], a1[16];
 #pragma unroll
           for (int j = 0; j < 16; j++) {
-            if (j >= m) break;
-            const int pos = tl.p0 + c + j;
-            const int row = p.out_row ? __ldg(p.out_row + pos) : pos;
-            if (row < 0) continue;  // padding
-            const size_t o = (size_t)row * p.out_stride;
-            float a0 = __uint_as_float(v0[j]) * g0, a1 = __uint_as_float(v1[j]) * g1;
-            if (p.ad_mode == AD_EPILOGUE && r < p.rt) {
-              a0 += s_ad[(c + j) * 2 * p.rt + r];
-              a1 += s_ad[(c + j) * 2 * p.rt + p.rt + r];
+            a0[j] = __uint_as_float(v0[j]) * g0;
+            a1[j] = __uint_as_float(v1[j]) * g1;
+            if (extra) {
+              a0[j] += e0[j];
+              a1[j] += e1[j];
             }
-            if (EPI == EPI_SWIGLU) {
-              if (ok0) reinterpret_cast<__nv_bfloat16*>(p.out)[o + y0] = __float2bfloat16_rn(silu_mul(a0, a1));
-            } else if (EPI == EPI_F32) {
-              float* out = reinterpret_cast<float*>(p.out);
-              if (p.addend) {
-                if (ok0) a0 += __bfloat162float(p.addend[o + y0]);
-                if (ok1) a1 += __bfloat162float(p.addend[o + y1]);
-              }
-              if (ok0) out[o + y0] = a0;
-              if (ok1) out[o + y1] = a1;
+            if (EPI == EPI_SWIGLU) a0[j] = silu_mul(a0[j], a1[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j++) {
+            const int row = __shfl_sync(0xffffffffu, row_l, j);
+            const size_t o = (size_t)row * p.out_stride;
+            if (EPI == EPI_F32) {
+              float* out = reinterpret_cast<float*>(p.out) + o;
+              if (ok0 && row >= 0) out[y0] = a0[j];
+              if (ok1 && row >= 0) out[y1] = a1[j];
             } else {
-              __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
-              if (p.addend) {
-                if (ok0) a0 += __bfloat162float(p.addend[o + y0]);
-                if (ok1) a1 += __bfloat162float(p.addend[o + y1]);
-              }
-              if (ok0) out[o + y0] = __float2bfloat16_rn(a0);
-              if (ok1) out[o + y1] = __float2bfloat16_rn(a1);
+              __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + o;
+              if (ok0 && row >= 0) out[y0] = __float2bfloat16_rn(a0[j]);
+              if (EPI == EPI_BF16 && ok1 && row >= 0) out[y1] = __float2bfloat16_rn(a1[j]);
             }
           }
         }
@@ -530,9 +575,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         if (p.ad_mode == AD_EPILOGUE) mbar_arrive(ad_empty, 1);
       }
     }
-  } else if (FMT != FMT_BF16) {
+  } else if (FMT != FMT_BF16 && warp >= 12) {
     // ---------------------------------------------------------------- widening
-    const int wt = tid - 320;  // 0..kWidenThreads - 1
+    const int wt = tid - 384;  // 0..kWidenThreads - 1
     const int nrow = 2 * p.rt;
     uint32_t it = 0, rit = 0;
     bool ok = true;

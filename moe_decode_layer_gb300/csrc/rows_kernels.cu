@@ -93,8 +93,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
     if (p.pos) p.pos[i] = at;
   }
-  for (int i = me * kPlanThreads + tid; i < p.shared * p.rows; i += nc * kPlanThreads)
-    p.src_row[p.pairs + i] = i % p.rows;
   if (me == 0) {
     if (tid < p.groups) {
       p.off[tid] = start;
@@ -126,6 +124,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
   }
   if (nc > 1) cl.sync();  // no CTA leaves while another reads its counts
+}
+
+constexpr int kSpreadWarps = 8;
+
+// One warp per position; the grouped product then copies its rows in boxes.
+__global__ void __launch_bounds__(kSpreadWarps * 32)
+    spread_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, const int* src_row, const int* count,
+                  int inner, __nv_bfloat16* __restrict__ dst) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t at = (int64_t)blockIdx.x * kSpreadWarps + (threadIdx.x >> 5);
+  if (at >= *count) return;
+  const int row = src_row[at];
+  if (row < 0) return;
+  const uint4* s = reinterpret_cast<const uint4*>(x + (int64_t)row * x_stride);
+  uint4* d = reinterpret_cast<uint4*>(dst + at * inner);
+  const int n = inner / 8;
+  int i = threadIdx.x & 31;
+  for (; i + 96 < n; i += 128) {
+    const uint4 a = __ldg(s + i), b = __ldg(s + i + 32), c = __ldg(s + i + 64), e = __ldg(s + i + 96);
+    d[i] = a;
+    d[i + 32] = b;
+    d[i + 64] = c;
+    d[i + 96] = e;
+  }
+  for (; i < n; i += 32) d[i] = __ldg(s + i);
 }
 
 constexpr int kShrinkWarps = 8;
@@ -216,6 +240,20 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
   c.attrs = a;
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, plan_kernel, p);
+}
+
+cudaError_t launch_spread(const __nv_bfloat16* x, int64_t x_stride, const int* src_row, const int* count,
+                          int64_t positions, int inner, __nv_bfloat16* dst, cudaStream_t s) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)((positions + kSpreadWarps - 1) / kSpreadWarps));
+  c.blockDim = dim3(kSpreadWarps * 32);
+  c.stream = s;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, spread_kernel, x, x_stride, src_row, count, inner, dst);
 }
 
 cudaError_t launch_shrink(const __nv_bfloat16* x, int64_t x_stride, const __nv_bfloat16* a, const float* scale,

@@ -20,12 +20,16 @@ struct PlanParams {
   int keep_none;     // 1: pairs without a group get the positions after all groups'
   int align;         // groups start at multiples of it (a power of two)
   int* off;          // [groups + 1] first position of each group; keep_none: [groups + 2] and the end
-  int* src_row;      // [pairs + shared * rows] row at each position, -1 between groups
+  int* src_row;      // [pairs] row at each position, -1 between groups
   int* pos;          // [pairs] position of each pair or -1 (may be NULL)
   int4* ents;        // tiles: {group, first position, rows, block | blocks << 16}
   int* nent;
 };
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);
+
+// dst[p] = x[src_row[p]] for the positions p < *count that have a row
+cudaError_t launch_spread(const __nv_bfloat16* x, int64_t x_stride, const int* src_row, const int* count,
+                          int64_t positions, int inner, __nv_bfloat16* dst, cudaStream_t s);
 
 // out = bf16(residual + sum_j w_j y[pos_j] + sum_s y[pairs + s * rows + row])
 cudaError_t launch_combine(const float* y, const int* pos, const float* w, const __nv_bfloat16* residual,

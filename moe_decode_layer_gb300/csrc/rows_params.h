@@ -13,12 +13,12 @@ namespace rows {
 constexpr int kMaxN = 256;        // rows of x per tile
 constexpr int kMaxStages = 48;    // operand stages in shared memory
 constexpr int kMaxRaw = 8;        // slots of quantised codes
-constexpr int kGatherThreads = 128;
+constexpr int kEpilogueWarps = 8;
 constexpr int kWidenThreads = 256;
 constexpr int kMaxGroups = 1024 + 8;  // experts and shared experts, or adapters
 constexpr int kMaxAdapters = 1024;
 constexpr int kMaxSms = 512;      // status words of a launch
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+constexpr uint32_t kWaitLimit = 1u << 21;
 constexpr unsigned long long kDrainNs = 1000000ull;
 
 // What the epilogue makes of the accumulators.
@@ -35,7 +35,7 @@ enum AdMode {
   AD_EPILOGUE = 2  // fp32 products of few rows, added in the epilogue
 };
 
-constexpr int threads_of(int fmt) { return fmt == FMT_BF16 ? 320 : 320 + kWidenThreads; }
+constexpr int threads_of(int fmt) { return fmt == FMT_BF16 ? 384 : 384 + kWidenThreads; }
 // k's in 128 bytes of codes
 constexpr int kmath(int fmt) { return fmt == FMT_FP8 ? 128 : 256; }
 
@@ -50,10 +50,11 @@ struct GemmParams {
   const void* wscale_s;
   const float* gscale;   // NVFP4 tensor scales; EPI_BF16: a scale per group
   const float* gscale_s;
-  // rows of x
-  const __nv_bfloat16* src;
-  int64_t src_stride;
-  const int* src_row;  // row of x at each sorted position (NULL: the position)
+  // rows of x (map_x)
+  const int* src_row;  // row at each sorted position (NULL: the position)
+  int box_rows;        // without a list: rows of a copy (map_x's box)
+  int all_rows;        // rows of each group from groups_main on, read through map_u; 0: as the others
+  int all_first;       // the first such group's first position
   int rows;            // uniform tiles: rows in all
   int nmax;            // rows per tile at most
   const int4* ents;    // {group, first position, rows, block | blocks << 16}, or NULL: uniform tiles
@@ -65,7 +66,7 @@ struct GemmParams {
   // AD_STEPS: positions off[a] .. off[a + 1] (multiples of 16) belong to adapter a,
   // off[num_adapters] .. off[num_adapters + 1] to none; B is map_s
   const int* adapter_off;
-  const __nv_bfloat16* u;  // [positions, rank]
+  // and the rows' products A x are map_u's, [positions, rank]
   // AD_EPILOGUE: rows in their own order
   const int* ids;
   const float* u32;        // [rows, rank]
