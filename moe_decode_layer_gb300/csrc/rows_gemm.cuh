@@ -18,7 +18,10 @@
 //
 // Warps: 0 weight copies, 1 tensor-core issue, 2 copies of the rows of x (listed
 // rows four to a copy, neighbouring ones as a box), 4..11 epilogue; the quantised
-// formats add 8 warps that widen the codes into the bf16 stage. All copies are TMA
+// formats add 8 warps that widen the codes to bf16, into tensor memory, from where the
+// tensor core takes them as its A operand. (Through shared memory a step moved
+// 92 to 108 KB there, 720 to 845 clocks at its 128 bytes a clock, and FP8 weights
+// streamed at 59 % of the HBM rate, NVFP4 at 22 %.) All copies are TMA
 // with the 128-byte swizzle of the operands, zero-filled past K. (A first version
 // gathered rows with 16-byte cp.async from four warps: with 256 rows a stage its
 // loop took 5900 clocks where the tensor core needs 1024.)
@@ -80,6 +83,27 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same with A in tensor memory: lane = row, two k's a column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Stores 32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Arrives on bar when all earlier tcgen05.mma of this thread have completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -193,14 +217,23 @@ __device__ __forceinline__ uint32_t fp8x2_bf16x2(uint32_t two, float s) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
-// NVFP4: e2m1 * e4m3 has at most 6 significant bits: the bf16 operand is exact
-// (as is the f16 product on the way: 2^-10 <= |v| <= 2688); the tensor scale
-// multiplies the fp32 sum.
-__device__ __forceinline__ uint32_t fp4x2_bf16x2(uint32_t byte, __half2 s) {
-  const uint32_t h = e2m1x2_to_f16x2(byte);
-  const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&h), s));
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t*>(&b);
+// NVFP4: e2m1 * e4m3 has at most 6 significant bits: the bf16 operand is exact; the
+// tensor scale multiplies the fp32 sum.
+// Four codes (the low 16 bits of w): the bytes of the bf16 values of 0, 0.5, 1, 1.5,
+// 2, 3, 4, 6 come out of byte permutes with the codes as selectors; a permute's
+// selector with its top bit set replicates the byte's sign, which gives the signs.
+__device__ __forceinline__ void fp4x4_bf16x4(uint32_t w, __nv_bfloat162 s, uint32_t& o0, uint32_t& o1) {
+  const uint32_t m = w & 0x7777u;
+  const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, m);
+  const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, m);
+  uint32_t sg;  // __byte_perm takes three bits of a selector only
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sg) : "r"(0x80808080u), "r"(w));  // 0xff: negative, 0x80: not
+  const uint32_t h = hi | ((sg << 7) & 0x80808080u);
+  const uint32_t p0 = __byte_perm(lo, h, 0x5140), p1 = __byte_perm(lo, h, 0x7362);
+  const __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&p0), s);
+  const __nv_bfloat162 b = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&p1), s);
+  o0 = *reinterpret_cast<const uint32_t*>(&a);
+  o1 = *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // The same with the tensor scale in the weights, where adapters share the sum:
@@ -238,16 +271,16 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 
   if (tid == 0) {
     s_abort = 0;
-    // a stage is full when its weights (TMA bytes, or every widening thread and one
+    // a stage is full when its weights (TMA bytes, or every widening warp and one
     // arrival in the copies' place) and its rows of x (TMA bytes) are there
-    const uint32_t nfull = 1 + (FMT == FMT_BF16 ? 1 : kWidenThreads + 1);
+    const uint32_t nfull = 1 + (FMT == FMT_BF16 ? 1 : kWidenThreads / 32 + 1);
     for (int s = 0; s < p.stages; s++) {
       mbar_init(full(s), nfull);
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), kEpilogueWarps);
+      mbar_init(tempty(b), epilogue_warps(FMT));
     }
     if (FMT != FMT_BF16)
       for (int s = 0; s < p.raw_slots; s++) {
@@ -255,8 +288,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         mbar_init(rempty(s), kWidenThreads / 32);
       }
     mbar_init(drain, 1);
-    mbar_init(ad_full, kEpilogueWarps);
-    mbar_init(ad_empty, kEpilogueWarps);
+    mbar_init(ad_full, epilogue_warps(FMT));
+    mbar_init(ad_empty, epilogue_warps(FMT));
     mbar_init_fence();
     tma_prefetch_map(&map_w);
     tma_prefetch_map(&map_s);
@@ -273,7 +306,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   const uint32_t tmem = s_tmem;
   // With AD_EPILOGUE the launch before this one makes u32 alone, which the epilogue
   // warps wait for; the others start on the weights and rows at once.
-  if (p.pdl && (p.ad_mode != AD_EPILOGUE || (warp >= 4 && warp < 12))) {
+  if (p.pdl && (p.ad_mode != AD_EPILOGUE || (warp >= 4 && warp < 4 + epilogue_warps(FMT)))) {
     pdl_wait();
     fence_proxy_async_global();  // rows that the launch before wrote are read by TMA
   }
@@ -285,8 +318,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   const uint32_t stage_bytes = p.stage_bytes;
   const bool ad_steps = p.ad_mode == AD_STEPS;
   const int per_adapter = ad_steps ? (p.rank + 63) / 64 : 0;
-  // accumulator columns: [buffer][sub-tile][nmax]
-  const int nbuf = 4 * p.nmax <= 512 ? 2 : 1;
+  // tensor memory: accumulators [buffer][sub-tile][nmax], then the quantised formats'
+  // widened weights [stage][sub-tile][32]
+  const int nbuf = acc_buffers(FMT, p.nmax);
+  const uint32_t a_tmem = tmem + nbuf * 2 * p.nmax;
+  const int b_off = FMT == FMT_BF16 || ad_steps ? 2 * a_half : 0;  // the rows of x in a stage
   const int sub_rows = EPI == EPI_SWIGLU ? p.rt : 2 * p.rt;  // output rows per tile
 
   if (warp == 0) {
@@ -357,30 +393,40 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
         const uint32_t d0 = tmem + b * 2 * p.nmax, d1 = d0 + p.nmax;
         // one stage into the accumulators of n rows from the tile's row c on
-        auto step = [&](int c, int n, bool first) {
+        auto step = [&](int c, int n, bool first, bool main) {
           const int s = it % p.stages;
           if (!wait_phase(full(s), (it / p.stages) & 1, &s_abort)) return false;
           tc_fence_after();
           const uint32_t idesc = kDesc | ((uint32_t)((n + 15) >> 4) << 18);
-          const uint32_t a = base + s * stage_bytes, bb = a + 2 * a_half + c * 128;
+          const uint32_t a = base + s * stage_bytes, bb = a + b_off + c * 128;
           const uint64_t da = smem_desc(a), db = smem_desc(bb), da1 = smem_desc(a + a_half);
+          if (FMT != FMT_BF16 && main) {
+            const uint32_t ta = a_tmem + s * 64;
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const uint32_t acc = !first || j != 0;
-            mma_bf16(d0 + c, da + 2 * j, db + 2 * j, idesc, acc);
-            mma_bf16(d1 + c, da1 + 2 * j, db + 2 * j, idesc, acc);
+            for (int j = 0; j < 4; j++) {
+              const uint32_t acc = !first || j != 0;
+              mma_bf16_ta(d0, ta + 8 * j, db + 2 * j, idesc, acc);
+              mma_bf16_ta(d1, ta + 32 + 8 * j, db + 2 * j, idesc, acc);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+              const uint32_t acc = !first || j != 0;
+              mma_bf16(d0 + c, da + 2 * j, db + 2 * j, idesc, acc);
+              mma_bf16(d1 + c, da1 + 2 * j, db + 2 * j, idesc, acc);
+            }
           }
           mma_commit(empty(s));
           it++;
           return true;
         };
-        for (int k = 0; ok && k < main_steps; k++) ok = step(0, tl.n, k == 0);
+        for (int k = 0; ok && k < main_steps; k++) ok = step(0, tl.n, k == 0, true);
         if (ok && ad_steps)
           for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
                a = adapter_next(p, a + 1, tl.p0, tl.n)) {
             const int c0 = max(__ldg(p.adapter_off + a) - tl.p0, 0);
             const int c1 = min(__ldg(p.adapter_off + a + 1) - tl.p0, tl.n);
-            for (int k = 0; ok && k < per_adapter; k++) ok = step(c0, c1 - c0, false);
+            for (int k = 0; ok && k < per_adapter; k++) ok = step(c0, c1 - c0, false, false);
           }
         if (ok) mma_commit(tfull(b));
       }
@@ -421,7 +467,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
         if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
         __syncwarp();
-        const uint32_t dst = base + s * stage_bytes + 2 * a_half;
+        const uint32_t dst = base + s * stage_bytes + b_off;
         if (listed) {
           if (lane < copies) tma_gather4(dst + lane * 512, &map_x, k * 64, y[0], full(s));
           if (lane + 32 < copies) tma_gather4(dst + (lane + 32) * 512, &map_x, k * 64, y[1], full(s));
@@ -439,7 +485,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
             if (lane == 0) mbar_arrive_expect_tx(full(s), boxes * 2048u);
             __syncwarp();
-            const uint32_t dst = base + s * stage_bytes + 2 * a_half + b * 128;
+            const uint32_t dst = base + s * stage_bytes + b_off + b * 128;
             if (lane < boxes) tma_load_2d(dst + lane * 2048, &map_u, k * 64, tl.p0 + b + lane * 16, full(s));
           }
         }
@@ -449,9 +495,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       const uint64_t t0 = global_ns();
       while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4 && warp < 4 + epilogue_warps(FMT)) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;  // this warp's 32 TMEM lanes; two warps share them, 16 columns in turn
+    const int q = warp & 3;  // this warp's 32 TMEM lanes; two warps (bf16) share them, 16 columns in turn
     const int c0 = warp >= 8 ? 16 : 0;
     float* s_ad = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + p.ad_off);
     const int r = q * 32 + lane;
@@ -464,7 +510,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         // the tile's adapter products, while the tensor core works on the rest: one
         // thread per (weight row, row of x), weight rows of one sub-tile after another
         if (!(ok = warp_wait(ad_empty, (tcount + 1) & 1, &s_abort))) break;
-        for (int i = tid - 128; i < tl.n * 2 * p.rt; i += 32 * kEpilogueWarps) {
+        for (int i = tid - 128; i < tl.n * 2 * p.rt; i += 32 * epilogue_warps(FMT)) {
           const int c = i / (2 * p.rt), wr = i % (2 * p.rt);
           const int sub = wr >= p.rt;
           const int y = tl.rb * sub_rows + (EPI == EPI_SWIGLU ? wr - sub * p.rt : wr);
@@ -508,44 +554,55 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const int y0 = tl.rb * sub_rows + r;
         const int y1 = y0 + p.rt;
         const bool ok0 = r < p.rt && y0 < p.R, ok1 = EPI != EPI_SWIGLU && r < p.rt && y1 < p.R;
-        for (int c = c0; c < tl.n; c += 32) {
+        // Two lanes exchange a value of each pair of columns, so that a store takes two
+        // neighbouring results of one column: lane 2 i those of the even column.
+        const bool odd = lane & 1;
+        const int yp0 = y0 & ~1, yp1 = y1 & ~1;
+        const bool extra = p.ad_mode == AD_EPILOGUE || (EPI != EPI_SWIGLU && p.addend);
+        for (int c = c0; c < tl.n; c += 4 * epilogue_warps(FMT)) {
           // Everything that is loaded is on its way before the first sum is used, and
           // all 16 columns' results are made before the first is stored, without
           // branches: with them each column waited for the one before (225 clocks).
           uint32_t v0[16], v1[16];
           const int m = min(16, tl.n - c);
-          int row_l = tl.p0 + c + (lane & 15);  // lane j: the row of out of column j
-          if (p.out_row) row_l = (lane & 15) < m ? __ldg(p.out_row + row_l) : -1;
-          row_l = (lane & 15) < m ? row_l : -1;
           __syncwarp();
           tmem_ld16(d0 + c, v0);
           tmem_ld16(d1 + c, v1);
+          int row_l = tl.p0 + c + (lane & 15);  // lane j: the row of out of column j
+          if (p.out_row) row_l = __ldg(p.out_row + min(row_l, tl.p0 + tl.n - 1));
+          row_l = (lane & 15) < m ? row_l : -1;
           float e0[16], e1[16];
-          if (EPI != EPI_SWIGLU && p.addend) {
+          if (extra) {
 #pragma unroll
-            for (int j = 0; j < 16; j++) {
-              const __nv_bfloat16* a = p.addend + (size_t)max(__shfl_sync(0xffffffffu, row_l, j), 0) * p.out_stride;
-              e0[j] = __bfloat162float(a[ok0 ? y0 : 0]);
-              e1[j] = __bfloat162float(a[ok1 ? y1 : 0]);
+            for (int j = 0; j < 16; j++) e0[j] = e1[j] = 0.0f;
+            if (EPI != EPI_SWIGLU && p.addend) {
+#pragma unroll
+              for (int j = 0; j < 16; j++) {
+                const __nv_bfloat16* a = p.addend + (size_t)max(__shfl_sync(0xffffffffu, row_l, j), 0) * p.out_stride;
+                e0[j] = __bfloat162float(a[ok0 ? y0 : 0]);
+                e1[j] = __bfloat162float(a[ok1 ? y1 : 0]);
+              }
+            }
+            if (p.ad_mode == AD_EPILOGUE) {
+              const float* ad = s_ad + c * 2 * p.rt + min(r, p.rt - 1);
+#pragma unroll
+              for (int j = 0; j < 16; j++) {
+                const int at = j < m ? j * 2 * p.rt : 0;
+                e0[j] += ad[at];
+                e1[j] += ad[at + p.rt];
+              }
             }
           }
-          if (p.ad_mode == AD_EPILOGUE) {
-            const float* ad = s_ad + c * 2 * p.rt + min(r, p.rt - 1);
-            const bool add = EPI != EPI_SWIGLU && p.addend;
-#pragma unroll
-            for (int j = 0; j < 16; j++) {
-              const int at = j < m ? j * 2 * p.rt : 0;
-              e0[j] = (add ? e0[j] : 0.0f) + ad[at];
-              e1[j] = (add ? e1[j] : 0.0f) + ad[at + p.rt];
-            }
-          }
-          const bool extra = p.ad_mode == AD_EPILOGUE || (EPI != EPI_SWIGLU && p.addend);
           tmem_ld_wait();
           float a0[16], a1[16];
 #pragma unroll
           for (int j = 0; j < 16; j++) {
-            a0[j] = __uint_as_float(v0[j]) * g0;
-            a1[j] = __uint_as_float(v1[j]) * g1;
+            a0[j] = __uint_as_float(v0[j]);
+            a1[j] = __uint_as_float(v1[j]);
+            if (FMT == FMT_NVFP4 || EPI == EPI_BF16) {
+              a0[j] *= g0;
+              a1[j] *= g1;
+            }
             if (extra) {
               a0[j] += e0[j];
               a1[j] += e1[j];
@@ -553,17 +610,26 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             if (EPI == EPI_SWIGLU) a0[j] = silu_mul(a0[j], a1[j]);
           }
 #pragma unroll
-          for (int j = 0; j < 16; j++) {
-            const int row = __shfl_sync(0xffffffffu, row_l, j);
+          for (int j = 0; j < 16; j += 2) {
+            const int row = p.out_row ? __shfl_sync(0xffffffffu, row_l, j + odd) : tl.p0 + c + j + odd;
+            const bool there = j + odd < m && row >= 0;
             const size_t o = (size_t)row * p.out_stride;
+            const float x0 = __shfl_xor_sync(0xffffffffu, odd ? a0[j] : a0[j + 1], 1);
+            const float2 f0 = odd ? make_float2(x0, a0[j + 1]) : make_float2(a0[j], x0);
+            float2 f1 = f0;
+            if (EPI != EPI_SWIGLU) {
+              const float x1 = __shfl_xor_sync(0xffffffffu, odd ? a1[j] : a1[j + 1], 1);
+              f1 = odd ? make_float2(x1, a1[j + 1]) : make_float2(a1[j], x1);
+            }
             if (EPI == EPI_F32) {
               float* out = reinterpret_cast<float*>(p.out) + o;
-              if (ok0 && row >= 0) out[y0] = a0[j];
-              if (ok1 && row >= 0) out[y1] = a1[j];
+              if (ok0 && there) *reinterpret_cast<float2*>(out + yp0) = f0;
+              if (ok1 && there) *reinterpret_cast<float2*>(out + yp1) = f1;
             } else {
               __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + o;
-              if (ok0 && row >= 0) out[y0] = __float2bfloat16_rn(a0[j]);
-              if (EPI == EPI_BF16 && ok1 && row >= 0) out[y1] = __float2bfloat16_rn(a1[j]);
+              if (ok0 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp0) = __floats2bfloat162_rn(f0.x, f0.y);
+              if (EPI == EPI_BF16 && ok1 && there)
+                *reinterpret_cast<__nv_bfloat162*>(out + yp1) = __floats2bfloat162_rn(f1.x, f1.y);
             }
           }
         }
@@ -575,10 +641,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         if (p.ad_mode == AD_EPILOGUE) mbar_arrive(ad_empty, 1);
       }
     }
-  } else if (FMT != FMT_BF16 && warp >= 12) {
+  } else if (FMT != FMT_BF16 && warp >= 4 + epilogue_warps(FMT)) {
     // ---------------------------------------------------------------- widening
-    const int wt = tid - 384;  // 0..kWidenThreads - 1
-    const int nrow = 2 * p.rt;
+    const int wt = tid - (128 + 32 * epilogue_warps(FMT));  // 0..kWidenThreads - 1
+    // A thread has one row of one sub-tile, its warp's tensor-memory lane. Lanes with
+    // neighbouring rows read one chunk each: the swizzle spreads them over all banks.
+    const int sub = wt >> 7;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int rr = min((warp & 3) * 32 + lane, p.rt - 1);  // lanes past the sub-tile repeat its last row
+    const int row = sub * p.rt + rr;
     uint32_t it = 0, rit = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
@@ -587,73 +658,79 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       const int g = sh ? tl.g - p.groups_main : tl.g;
       const int y0 = tl.rb * sub_rows;
       const int nraw = p.K / kmath(FMT);
-      const int parts = kmath(FMT) / 64;  // stages per raw slot
+      constexpr int kParts = kmath(FMT) / 64;          // stages per raw slot
+      constexpr int kChunks = FMT == FMT_FP8 ? 4 : 2;  // 16-byte chunks of codes per row and stage
+      constexpr int kOut = 32 / kChunks;               // columns made of one
+      // The matrix row of this thread's sub-tile row (rows past the matrix hold zero
+      // codes) and where its scales are. The scales of a slot are loaded while the
+      // one before is widened.
+      const int y = min(y0 + (EPI == EPI_SWIGLU ? rr : row), p.R - 1);
+      const int yy = EPI == EPI_SWIGLU ? sub * p.R + y : y;
+      const int rows_all = EPI == EPI_SWIGLU ? 2 * p.R : p.R;
+      const float* sc8 = reinterpret_cast<const float*>(sh ? p.wscale_s : p.wscale) +
+                         ((size_t)g * (rows_all / 128) + yy / 128) * (p.K / 128);
+      const uint4* sc4 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(sh ? p.wscale_s : p.wscale) +
+                                                        ((size_t)g * rows_all + yy) * (p.K / 16));
+      float next8 = 0.0f, ts = 1.0f;
+      uint4 next4 = make_uint4(0, 0, 0, 0);
+      if (FMT == FMT_FP8) next8 = __ldg(sc8); else next4 = __ldg(sc4);
+      if (FMT == FMT_NVFP4 && ad_steps) ts = __ldg((sh ? p.gscale_s : p.gscale) + (EPI == EPI_SWIGLU ? 2 * g + sub : g));
       for (int k = 0; ok && k < nraw; k++, rit++) {
+        const float f8 = next8;
+        const uint32_t f4[4] = {next4.x, next4.y, next4.z, next4.w};
+        if (k + 1 < nraw) {
+          if (FMT == FMT_FP8) next8 = __ldg(sc8 + k + 1); else next4 = __ldg(sc4 + k + 1);
+        }
         const int rs = rit % p.raw_slots;
         if (!(ok = warp_wait(rfull(rs), (rit / p.raw_slots) & 1, &s_abort))) break;
-        const uint32_t raw = base + p.raw_off + rs * (2 * a_half);
-        for (int h = 0; h < parts; h++, it++) {
+        const uint32_t raw = base + p.raw_off + rs * (2 * a_half) + row * 128;
+#pragma unroll
+        for (int h = 0; h < kParts; h++, it++) {
           const int s = it % p.stages;
           if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
-          const uint32_t dst = base + s * stage_bytes;
-          constexpr int kChunks = FMT == FMT_FP8 ? 4 : 2;  // raw 16-byte chunks per row and stage
-          for (int i = wt; i < nrow * kChunks; i += kWidenThreads) {
-            const int row = i % nrow, ch = i / nrow;
-            // the matrix row of this sub-tile row (scales); rows past the matrix hold zero codes
-            const int sub = row >= p.rt;
-            int y = y0 + (EPI == EPI_SWIGLU ? row - sub * p.rt : row);
-            y = min(y, p.R - 1);
-            const int yy = EPI == EPI_SWIGLU ? sub * p.R + y : y;
-            const int rows_all = EPI == EPI_SWIGLU ? 2 * p.R : p.R;
-            uint4 v;
-            const int rc = h * kChunks + ch;
+          tc_fence_after();
+          uint4 codes[kChunks];
+#pragma unroll
+          for (int q = 0; q < kChunks; q++)
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(raw + row * 128 + ((rc ^ (row & 7)) << 4)));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[16];
+                         : "=r"(codes[q].x), "=r"(codes[q].y), "=r"(codes[q].z), "=r"(codes[q].w)
+                         : "r"(raw + (((h * kChunks + q) ^ (row & 7)) << 4)));
+          uint32_t o[32];
+#pragma unroll
+          for (int q = 0; q < kChunks; q++) {
+            const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
             if (FMT == FMT_FP8) {
-              const float* sc = reinterpret_cast<const float*>(sh ? p.wscale_s : p.wscale);
-              const float f = __ldg(sc + ((size_t)g * (rows_all / 128) + yy / 128) * (p.K / 128) + k);
 #pragma unroll
               for (int j = 0; j < 4; j++) {
-                o[2 * j] = fp8x2_bf16x2(w[j] & 0xffffu, f);
-                o[2 * j + 1] = fp8x2_bf16x2(w[j] >> 16, f);
+                o[(kOut * q + 2 * j) & 31] = fp8x2_bf16x2(w[j] & 0xffffu, f8);
+                o[(kOut * q + 2 * j + 1) & 31] = fp8x2_bf16x2(w[j] >> 16, f8);
               }
             } else {
-              const uint8_t* sc = reinterpret_cast<const uint8_t*>(sh ? p.wscale_s : p.wscale);
-              const uint32_t two = __ldg(reinterpret_cast<const uint16_t*>(
-                  sc + ((size_t)g * rows_all + yy) * (p.K / 16) + k * 16 + h * 4 + ch * 2));
-              const uint32_t hs = e4m3x2_to_f16x2(two);
-              const __half2 h2 = *reinterpret_cast<const __half2*>(&hs);
-              const __half2 s0 = __low2half2(h2), s1 = __high2half2(h2);
+              const uint32_t hs = e4m3x2_to_f16x2(q ? f4[h & 3] >> 16 : f4[h & 3] & 0xffffu);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hs));
               if (!ad_steps) {
+                const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x), s1 = __float2bfloat162_rn(f.y);
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-#pragma unroll
-                  for (int b = 0; b < 4; b++) o[4 * j + b] = fp4x2_bf16x2((w[j] >> (8 * b)) & 0xffu, j < 2 ? s0 : s1);
+                for (int j = 0; j < 4; j++) {
+                  const int at = (kOut * q + 4 * j) & 31;
+                  fp4x4_bf16x4(w[j], j < 2 ? s0 : s1, o[at], o[at + 1]);
+                  fp4x4_bf16x4(w[j] >> 16, j < 2 ? s0 : s1, o[at + 2], o[at + 3]);
+                }
               } else {
-                const float ts = __ldg((sh ? p.gscale_s : p.gscale) + (EPI == EPI_SWIGLU ? 2 * g + sub : g));
-                const float f0 = __low2float(h2) * ts, f1 = __high2float(h2) * ts;
 #pragma unroll
                 for (int j = 0; j < 4; j++)
 #pragma unroll
                   for (int b = 0; b < 4; b++)
-                    o[4 * j + b] = fp4x2_bf16x2_folded((w[j] >> (8 * b)) & 0xffu, j < 2 ? f0 : f1);
+                    o[(kOut * q + 4 * j + b) & 31] =
+                        fp4x2_bf16x2_folded((w[j] >> (8 * b)) & 0xffu, (j < 2 ? f.x : f.y) * ts);
               }
             }
-            constexpr int kOut = FMT == FMT_FP8 ? 2 : 4;  // bf16 16-byte chunks written
-#pragma unroll
-            for (int j = 0; j < kOut; j++) {
-              const int oc = ch * kOut + j;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + ((oc ^ (row & 7)) << 4)),
-                           "r"(o[4 * j]), "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
-                           : "memory");
-            }
           }
-          fence_proxy_async_shared();
-          mbar_arrive(full(s), 1);
-          if (wt == 0) mbar_arrive(full(s), 1);  // in the place of the weight copies' arrival
+          tmem_st32(a_tmem + s * 64 + sub * 32 + lanes, o);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full(s), wt == 0 ? 2 : 1);  // thread 0: also in the weight copies' place
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(rempty(rs), 1);
@@ -672,7 +749,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
               tma_load_4d(dst, &map_s, k * 64, y0, 0, a, full(s));
               tma_load_4d(dst + a_half, &map_s, k * 64, y1, z1, a, full(s));
             }
-            mbar_arrive(full(s), 1);
+            if (lane == 0) mbar_arrive(full(s), 1);
           }
         }
       }

@@ -13,7 +13,6 @@ namespace rows {
 constexpr int kMaxN = 256;        // rows of x per tile
 constexpr int kMaxStages = 48;    // operand stages in shared memory
 constexpr int kMaxRaw = 8;        // slots of quantised codes
-constexpr int kEpilogueWarps = 8;
 constexpr int kWidenThreads = 256;
 constexpr int kMaxGroups = 1024 + 8;  // experts and shared experts, or adapters
 constexpr int kMaxAdapters = 1024;
@@ -35,7 +34,15 @@ enum AdMode {
   AD_EPILOGUE = 2  // fp32 products of few rows, added in the epilogue
 };
 
-constexpr int threads_of(int fmt) { return fmt == FMT_BF16 ? 384 : 384 + kWidenThreads; }
+__host__ __device__ constexpr int epilogue_warps(int fmt) { return 8; }
+// Accumulators at once: two while tensor memory (512 columns) has room for them, beside
+// the widened weights of a quantised format.
+__host__ __device__ constexpr int acc_buffers(int fmt, int nmax) {
+  return 4 * nmax <= (fmt == FMT_BF16 ? 512 : 256) ? 2 : 1;
+}
+constexpr int threads_of(int fmt) {
+  return 128 + 32 * epilogue_warps(fmt) + (fmt == FMT_BF16 ? 0 : kWidenThreads);
+}
 // k's in 128 bytes of codes
 constexpr int kmath(int fmt) { return fmt == FMT_FP8 ? 128 : 256; }
 
