@@ -143,6 +143,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, wait_phase(bar, parity, abort));
 }
 
+// A place in a ring of n barriers: the slot, and the parity of its use. (Divisions
+// by the number of slots took a quarter of a widening warp's step.)
+struct Ring {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 struct Tile {
   int g, p0, n, rb;
 };
@@ -210,15 +222,34 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(
 // FP8: w = bf16(e4m3 * block scale): one rounding of the product (2^-9 relative,
 // 1/32 of the codes' own step); the tensor core takes bf16 operands with the bf16
 // rows of x, and a block scale of 128 k cannot be taken out of the sum over all k.
-__device__ __forceinline__ uint32_t fp8x2_bf16x2(uint32_t two, float s) {
-  const uint32_t h = e4m3x2_to_f16x2(two);
-  const __half2 hh = *reinterpret_cast<const __half2*>(&h);
-  const float2 f = __half22float2(hh);
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float s) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
   const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
+__device__ __forceinline__ void fp8x4_bf16x4(uint32_t w, float s, uint32_t& o0, uint32_t& o1) {
+  uint32_t h0, h1;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(h0), "=r"(h1)
+      : "r"(w));
+  o0 = scaled_bf16x2(h0, s);
+  o1 = scaled_bf16x2(h1, s);
+}
+// Eight e2m1 codes -> eight fp16 values.
+__device__ __forceinline__ void fp4x8_f16x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
 // NVFP4: e2m1 * e4m3 has at most 6 significant bits: the bf16 operand is exact; the
-// tensor scale multiplies the fp32 sum.
+// tensor scale multiplies the fp32 sum. (Where adapters share the sum it is
+// multiplied into the weights, which are rounded to bf16 as FP8's are.)
+// Two ways to the same values keep both arithmetic pipes busy: conversions to fp16
+// and on to bf16 (per two codes 4 clocks of the integer pipe, 6 of the
+// floating-point pipe), and byte permutes (7.5 and 2); of four groups of codes one
+// takes the second.
 // Four codes (the low 16 bits of w): the bytes of the bf16 values of 0, 0.5, 1, 1.5,
 // 2, 3, 4, 6 come out of byte permutes with the codes as selectors; a permute's
 // selector with its top bit set replicates the byte's sign, which gives the signs.
@@ -236,15 +267,6 @@ __device__ __forceinline__ void fp4x4_bf16x4(uint32_t w, __nv_bfloat162 s, uint3
   o1 = *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// The same with the tensor scale in the weights, where adapters share the sum:
-// rounded to bf16 as the FP8 weights are.
-__device__ __forceinline__ uint32_t fp4x2_bf16x2_folded(uint32_t byte, float s) {
-  const uint32_t h = e2m1x2_to_f16x2(byte);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
 template <int EPI, int FMT>
 __global__ void __launch_bounds__(threads_of(FMT), 1)
     rows_gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap map_w,
@@ -253,9 +275,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  // full, empty [kMaxStages], tmem full / empty [2], raw full / empty [kMaxRaw], drain,
-  // adapter products full / empty
-  __shared__ __align__(8) uint64_t s_bar[2 * kMaxStages + 4 + 2 * kMaxRaw + 3];
+  __shared__ volatile int s_in[2];  // epilogue: a tile's sums are there (odd and even tiles)
+  // full, empty [kMaxStages], tmem full / empty [2], raw full / empty [kMaxRaw], drain
+  __shared__ __align__(8) uint64_t s_bar[2 * kMaxStages + 4 + 2 * kMaxRaw + 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -267,7 +289,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   auto rfull = [&](int s) { return bar0 + 8u * (2 * kMaxStages + 4 + s); };
   auto rempty = [&](int s) { return bar0 + 8u * (2 * kMaxStages + 4 + kMaxRaw + s); };
   const uint32_t drain = bar0 + 8u * (2 * kMaxStages + 4 + 2 * kMaxRaw);
-  const uint32_t ad_full = drain + 8u, ad_empty = drain + 16u;
 
   if (tid == 0) {
     s_abort = 0;
@@ -288,8 +309,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         mbar_init(rempty(s), kWidenThreads / 32);
       }
     mbar_init(drain, 1);
-    mbar_init(ad_full, epilogue_warps(FMT));
-    mbar_init(ad_empty, epilogue_warps(FMT));
     mbar_init_fence();
     tma_prefetch_map(&map_w);
     tma_prefetch_map(&map_s);
@@ -328,7 +347,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- weights
     if (lane == 0) {
-      uint32_t it = 0, rit = 0;
+      Ring it, rit;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
         const Tile tl = tile_at(p, t);
@@ -338,9 +357,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const int y0 = tl.rb * sub_rows;
         const int y1 = EPI == EPI_SWIGLU ? y0 : y0 + p.rt, z1 = EPI == EPI_SWIGLU ? 1 : 0;
         if (FMT == FMT_BF16) {
-          for (int k = 0; k < main_steps; k++, it++) {
-            const int s = it % p.stages;
-            if (!(ok = wait_phase(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
+          for (int k = 0; k < main_steps; k++, it.next(p.stages)) {
+            const uint32_t s = it.slot;
+            if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
             const uint32_t dst = base + s * stage_bytes;
             mbar_arrive_expect_tx(full(s), 2 * a_half);
             tma_load_4d(dst, m, k * 64, y0, 0, g, full(s));
@@ -349,9 +368,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         } else {
           // raw slots: 128 bytes of codes per row
           const int nraw = p.K / kmath(FMT);
-          for (int k = 0; k < nraw; k++, rit++) {
-            const int s = rit % p.raw_slots;
-            if (!(ok = wait_phase(rempty(s), (rit / p.raw_slots + 1) & 1, &s_abort))) break;
+          for (int k = 0; k < nraw; k++, rit.next(p.raw_slots)) {
+            const uint32_t s = rit.slot;
+            if (!(ok = wait_phase(rempty(s), rit.parity ^ 1, &s_abort))) break;
             const uint32_t dst = base + p.raw_off + s * (2 * a_half);
             mbar_arrive_expect_tx(rfull(s), 2 * a_half);
             tma_load_4d(dst, m, k * 128, y0, 0, g, rfull(s));
@@ -363,9 +382,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         if (FMT == FMT_BF16 && ok && ad_steps) {
           for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
                a = adapter_next(p, a + 1, tl.p0, tl.n)) {
-            for (int k = 0; k < per_adapter; k++, it++) {
-              const int s = it % p.stages;
-              if (!(ok = wait_phase(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
+            for (int k = 0; k < per_adapter; k++, it.next(p.stages)) {
+              const uint32_t s = it.slot;
+              if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
               const uint32_t dst = base + s * stage_bytes;
               mbar_arrive_expect_tx(full(s), 2 * a_half);
               tma_load_4d(dst, &map_s, k * 64, y0, 0, a, full(s));
@@ -382,20 +401,20 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- tensor core
     if (lane == 0) {
-      uint32_t it = 0, tcount = 0;
+      Ring it, acc;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, tcount++) {
+      for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, acc.next(nbuf)) {
         const Tile tl = tile_at(p, t);
-        const int b = tcount % nbuf;
-        if (!(ok = wait_phase(tempty(b), (tcount / nbuf + 1) & 1, &s_abort))) break;
+        const int b = acc.slot;
+        if (!(ok = wait_phase(tempty(b), acc.parity ^ 1, &s_abort))) break;
         tc_fence_after();
         // fp32 accumulators, bf16 x bf16, both K-major, M = 128
         constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
         const uint32_t d0 = tmem + b * 2 * p.nmax, d1 = d0 + p.nmax;
         // one stage into the accumulators of n rows from the tile's row c on
         auto step = [&](int c, int n, bool first, bool main) {
-          const int s = it % p.stages;
-          if (!wait_phase(full(s), (it / p.stages) & 1, &s_abort)) return false;
+          const uint32_t s = it.slot;
+          if (!wait_phase(full(s), it.parity, &s_abort)) return false;
           tc_fence_after();
           const uint32_t idesc = kDesc | ((uint32_t)((n + 15) >> 4) << 18);
           const uint32_t a = base + s * stage_bytes, bb = a + b_off + c * 128;
@@ -417,7 +436,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
           }
           mma_commit(empty(s));
-          it++;
+          it.next(p.stages);
           return true;
         };
         for (int k = 0; ok && k < main_steps; k++) ok = step(0, tl.n, k == 0, true);
@@ -439,7 +458,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- rows of x
-    uint32_t it = 0;
+    Ring it;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
       const Tile tl = tile_at(p, t);
@@ -462,9 +481,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
       }
       const uint32_t bytes = copies * (listed ? 512u : p.box_rows * 128u);
-      for (int k = 0; k < main_steps; k++, it++) {
-        const int s = it % p.stages;
-        if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
+      for (int k = 0; k < main_steps; k++, it.next(p.stages)) {
+        const uint32_t s = it.slot;
+        if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
         if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
         __syncwarp();
         const uint32_t dst = base + s * stage_bytes + b_off;
@@ -480,9 +499,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
              a = adapter_next(p, a + 1, tl.p0, tl.n)) {
           const int b = max(__ldg(p.adapter_off + a) - tl.p0, 0), e = min(__ldg(p.adapter_off + a + 1) - tl.p0, tl.n);
           const int boxes = (e - b + 15) / 16;  // 16 rows each, as the adapter's are padded
-          for (int k = 0; k < per_adapter; k++, it++) {
-            const int s = it % p.stages;
-            if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
+          for (int k = 0; k < per_adapter; k++, it.next(p.stages)) {
+            const uint32_t s = it.slot;
+            if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
             if (lane == 0) mbar_arrive_expect_tx(full(s), boxes * 2048u);
             __syncwarp();
             const uint32_t dst = base + s * stage_bytes + b_off + b * 128;
@@ -501,15 +520,16 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const int c0 = warp >= 8 ? 16 : 0;
     float* s_ad = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + p.ad_off);
     const int r = q * 32 + lane;
+    Ring acc;
     uint32_t tcount = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, tcount++) {
+    for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, tcount++, acc.next(nbuf)) {
       const Tile tl = tile_at(p, t);
-      const int b = tcount % nbuf;
+      const int b = acc.slot;
       if (p.ad_mode == AD_EPILOGUE) {
         // the tile's adapter products, while the tensor core works on the rest: one
         // thread per (weight row, row of x), weight rows of one sub-tile after another
-        if (!(ok = warp_wait(ad_empty, (tcount + 1) & 1, &s_abort))) break;
+        bar_sync(1, 32 * epilogue_warps(FMT));  // the last tile's products are read
         for (int i = tid - 128; i < tl.n * 2 * p.rt; i += 32 * epilogue_warps(FMT)) {
           const int c = i / (2 * p.rt), wr = i % (2 * p.rt);
           const int sub = wr >= p.rt;
@@ -529,11 +549,17 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           }
           s_ad[i] = v;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ad_full, 1);
-        if (!(ok = warp_wait(ad_full, tcount & 1, &s_abort))) break;
       }
-      if (!(ok = warp_wait(tfull(b), (tcount / nbuf) & 1, &s_abort))) break;
+      // one warp polls, the others wait at a barrier that costs no issue slots; all
+      // get the same answer and leave the loop together
+      if (warp == 4) {
+        const bool in = warp_wait(tfull(b), acc.parity, &s_abort);
+        if (lane == 0) s_in[tcount & 1] = in;
+        __syncwarp();
+      }
+      bar_sync(1, 32 * epilogue_warps(FMT));
+      ok = s_in[tcount & 1];
+      if (!ok) break;
       tc_fence_after();
       const uint32_t d0 = tmem + b * 2 * p.nmax + ((uint32_t)(q * 32) << 16), d1 = d0 + p.nmax;
       const bool sh = tl.g >= p.groups_main;
@@ -638,7 +664,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(tempty(b), 1);
-        if (p.ad_mode == AD_EPILOGUE) mbar_arrive(ad_empty, 1);
       }
     }
   } else if (FMT != FMT_BF16 && warp >= 4 + epilogue_warps(FMT)) {
@@ -650,7 +675,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int rr = min((warp & 3) * 32 + lane, p.rt - 1);  // lanes past the sub-tile repeat its last row
     const int row = sub * p.rt + rr;
-    uint32_t it = 0, rit = 0;
+    Ring it, rit;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
       const Tile tl = tile_at(p, t);
@@ -675,19 +700,19 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       uint4 next4 = make_uint4(0, 0, 0, 0);
       if (FMT == FMT_FP8) next8 = __ldg(sc8); else next4 = __ldg(sc4);
       if (FMT == FMT_NVFP4 && ad_steps) ts = __ldg((sh ? p.gscale_s : p.gscale) + (EPI == EPI_SWIGLU ? 2 * g + sub : g));
-      for (int k = 0; ok && k < nraw; k++, rit++) {
+      for (int k = 0; ok && k < nraw; k++, rit.next(p.raw_slots)) {
         const float f8 = next8;
         const uint32_t f4[4] = {next4.x, next4.y, next4.z, next4.w};
         if (k + 1 < nraw) {
           if (FMT == FMT_FP8) next8 = __ldg(sc8 + k + 1); else next4 = __ldg(sc4 + k + 1);
         }
-        const int rs = rit % p.raw_slots;
-        if (!(ok = warp_wait(rfull(rs), (rit / p.raw_slots) & 1, &s_abort))) break;
+        const uint32_t rs = rit.slot;
+        if (!(ok = warp_wait(rfull(rs), rit.parity, &s_abort))) break;
         const uint32_t raw = base + p.raw_off + rs * (2 * a_half) + row * 128;
 #pragma unroll
-        for (int h = 0; h < kParts; h++, it++) {
-          const int s = it % p.stages;
-          if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
+        for (int h = 0; h < kParts; h++, it.next(p.stages)) {
+          const uint32_t s = it.slot;
+          if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
           tc_fence_after();
           uint4 codes[kChunks];
 #pragma unroll
@@ -701,28 +726,35 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
             if (FMT == FMT_FP8) {
 #pragma unroll
-              for (int j = 0; j < 4; j++) {
-                o[(kOut * q + 2 * j) & 31] = fp8x2_bf16x2(w[j] & 0xffffu, f8);
-                o[(kOut * q + 2 * j + 1) & 31] = fp8x2_bf16x2(w[j] >> 16, f8);
-              }
+              for (int j = 0; j < 4; j++)
+                fp8x4_bf16x4(w[j], f8, o[(kOut * q + 2 * j) & 31], o[(kOut * q + 2 * j + 1) & 31]);
             } else {
               const uint32_t hs = e4m3x2_to_f16x2(q ? f4[h & 3] >> 16 : f4[h & 3] & 0xffffu);
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hs));
               if (!ad_steps) {
-                const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x), s1 = __float2bfloat162_rn(f.y);
+                const __nv_bfloat162 s1 = __float2bfloat162_rn(f.y);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                   const int at = (kOut * q + 4 * j) & 31;
-                  fp4x4_bf16x4(w[j], j < 2 ? s0 : s1, o[at], o[at + 1]);
-                  fp4x4_bf16x4(w[j] >> 16, j < 2 ? s0 : s1, o[at + 2], o[at + 3]);
+                  if (j == 3) {
+                    fp4x4_bf16x4(w[j], s1, o[at], o[at + 1]);
+                    fp4x4_bf16x4(w[j] >> 16, s1, o[at + 2], o[at + 3]);
+                  } else {
+                    uint32_t v[4];
+                    fp4x8_f16x8(w[j], v);
+#pragma unroll
+                    for (int b = 0; b < 4; b++) o[at + b] = scaled_bf16x2(v[b], j < 2 ? f.x : f.y);
+                  }
                 }
               } else {
 #pragma unroll
-                for (int j = 0; j < 4; j++)
+                for (int j = 0; j < 4; j++) {
+                  uint32_t v[4];
+                  fp4x8_f16x8(w[j], v);
 #pragma unroll
                   for (int b = 0; b < 4; b++)
-                    o[(kOut * q + 4 * j + b) & 31] =
-                        fp4x2_bf16x2_folded((w[j] >> (8 * b)) & 0xffu, (j < 2 ? f.x : f.y) * ts);
+                    o[(kOut * q + 4 * j + b) & 31] = scaled_bf16x2(v[b], (j < 2 ? f.x : f.y) * ts);
+                }
               }
             }
           }
@@ -740,9 +772,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const int y1 = EPI == EPI_SWIGLU ? y0 : y0 + p.rt, z1 = EPI == EPI_SWIGLU ? 1 : 0;
         for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
              a = adapter_next(p, a + 1, tl.p0, tl.n)) {
-          for (int k = 0; k < per_adapter; k++, it++) {
-            const int s = it % p.stages;
-            if (!(ok = warp_wait(empty(s), (it / p.stages + 1) & 1, &s_abort))) break;
+          for (int k = 0; k < per_adapter; k++, it.next(p.stages)) {
+            const uint32_t s = it.slot;
+            if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
             if (wt == 0) {
               const uint32_t dst = base + s * stage_bytes;
               mbar_arrive_expect_tx(full(s), 2 * a_half);
