@@ -132,6 +132,8 @@ _lib = None
 def load(build_if_stale: bool = True) -> ctypes.CDLL:
     """Open libmoe_decode.so (building it first if sources are newer)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -12,7 +12,9 @@ and must stay alive while a CUDA graph that captured a call with it is replayed.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -39,8 +41,8 @@ def _need(cond: bool, what: str) -> None:
 
 def _tensor(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     """The address of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}: got "
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}: got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -55,30 +57,30 @@ def _rows(t: torch.Tensor, name: str, cols: int, device) -> tuple[int, int]:
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
 
 
-class _On:
-    """Makes a tensor's device the current one while the library is called; the stream to run on."""
+def _enter(device: torch.device, stream):
+    """(stream handle, what to leave): makes ``device`` the current one while the
+    library is called, and ``stream`` the one that results and workspaces are allocated
+    for. The usual call, on the current device and stream, has nothing to leave."""
+    _need(device.type == "cuda", "tensors must be on a CUDA device")
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(device.index), None
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    else:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stream.cuda_stream, stack
 
-    def __init__(self, device: torch.device, stream):
-        _need(device.type == "cuda", "tensors must be on a CUDA device")
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.stream = stream
-        self.device = device
 
-    def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
-        # results and workspaces are allocated for the stream that the kernels run on
-        self.on = None if self.stream is None else torch.cuda.stream(s)
-        if self.on:
-            self.on.__enter__()
-        return s.cuda_stream
-
-    def __exit__(self, *e):
-        if self.on:
-            self.on.__exit__(*e)
-        if self.guard:
-            self.guard.__exit__(*e)
+@functools.lru_cache(maxsize=256)
+def _route_config(e: int, top_k: int, score: str, num_groups: int, top_groups: int, group_best: int,
+                  renormalise: bool, dtype, scale: float) -> _lib.RouteConfig:
+    _need(score in _lib.ROUTE_SCORES, f"unknown score {score!r}")
+    cfg = _lib.RouteConfig(e, top_k, _lib.ROUTE_SCORES[score], num_groups, top_groups, group_best, renormalise,
+                           _DTYPES[dtype], scale)
+    _lib.check(_lib.load().moe_decode_route_check(cfg), "moe_decode_route_check")
+    return cfg
 
 
 def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
@@ -89,22 +91,23 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: tor
     documents. ``score``: "softmax" or "sigmoid"; ``bias`` fp32 [E]."""
     _need(logits.dim() == 2 and logits.dtype in _DTYPES, "logits must be a bf16 or fp32 [rows, experts] tensor")
     t, e = logits.shape
-    _need(t == 0 or e == 1 or logits.stride(1) == 1, "a row of logits must be contiguous")
-    _need(score in _lib.ROUTE_SCORES, f"unknown score {score!r}")
-    lib = _lib.load()
-    cfg = _lib.RouteConfig(e, top_k, _lib.ROUTE_SCORES[score], num_groups, top_groups, group_best, renormalise,
-                           _DTYPES[logits.dtype], scale)
-    _lib.check(lib.moe_decode_route_check(cfg), "moe_decode_route_check")
+    row, col = logits.stride()
+    _need(t == 0 or e == 1 or col == 1, "a row of logits must be contiguous")
+    cfg = _route_config(e, top_k, score, num_groups, top_groups, group_best, bool(renormalise), logits.dtype, scale)
     dev = logits.device
     b = None if bias is None else _tensor(bias, "bias", torch.float32, (e,), dev)
-    with _On(dev, stream) as s:
-        if idx is None:
-            idx = torch.empty((t, top_k), dtype=torch.int32, device=dev)
-        if w is None:
-            w = torch.empty((t, top_k), dtype=torch.float32, device=dev)
-        _lib.check(lib.moe_decode_route(cfg, logits.data_ptr(), logits.stride(0) if t > 1 else e, b, t,
-                                        _tensor(idx, "idx", torch.int32, (t, top_k), dev),
-                                        _tensor(w, "w", torch.float32, (t, top_k), dev), s), "moe_decode_route")
+    s, leave = _enter(dev, stream)
+    try:
+        idx = torch.empty((t, top_k), dtype=torch.int32, device=dev) if idx is None else idx
+        w = torch.empty((t, top_k), dtype=torch.float32, device=dev) if w is None else w
+        st = _lib.load().moe_decode_route(cfg, logits.data_ptr(), row if t > 1 else e, b, t,
+                                          _tensor(idx, "idx", torch.int32, (t, top_k), dev),
+                                          _tensor(w, "w", torch.float32, (t, top_k), dev), s)
+    finally:
+        if leave is not None:
+            leave.close()
+    if st:
+        _lib.check(st, "moe_decode_route")
     return idx, w
 
 
@@ -146,6 +149,7 @@ def _workspace(workspace: torch.Tensor | None, need: int, device) -> torch.Tenso
     return workspace
 
 
+@functools.lru_cache(maxsize=1024)
 def experts_workspace(shape: LayerShape, rows: int) -> int:
     """Bytes of workspace that :func:`experts` needs for at most ``rows`` rows."""
     n = ctypes.c_size_t()
@@ -154,10 +158,13 @@ def experts_workspace(shape: LayerShape, rows: int) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=256)
 def _experts_config(shape: LayerShape) -> _lib.ExpertsConfig:
     _need(shape.wdtype in _lib.WDTYPE, f"unknown weight type {shape.wdtype!r}")
-    return _lib.ExpertsConfig(shape.hidden, shape.inter, shape.num_experts, shape.top_k, shape.num_shared,
-                              _lib.WDTYPE[shape.wdtype])
+    cfg = _lib.ExpertsConfig(shape.hidden, shape.inter, shape.num_experts, shape.top_k, shape.num_shared,
+                             _lib.WDTYPE[shape.wdtype])
+    _lib.check(_lib.load().moe_decode_experts_check(cfg), "moe_decode_experts_check")
+    return cfg
 
 
 def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, *,
@@ -168,9 +175,7 @@ def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: t
     layout of synth.make_layer, or what :func:`expert_weights` made of it; ``x`` bf16
     [T, H], any row stride of a multiple of 8; ``idx`` int32 and ``w`` fp32 [T, k];
     an index outside the experts (-1) takes no part."""
-    lib = _lib.load()
     cfg = _experts_config(shape)
-    _lib.check(lib.moe_decode_experts_check(cfg), "moe_decode_experts_check")
     dev = x.device
     px, sx = _rows(x, "x", shape.hidden, dev)
     t = x.shape[0]
@@ -178,30 +183,37 @@ def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: t
     pi = _tensor(idx, "idx", torch.int32, (t, shape.top_k), dev)
     pw = _tensor(w, "w", torch.float32, (t, shape.top_k), dev)
     pr = None if residual is None else _tensor(residual, "residual", torch.bfloat16, (t, shape.hidden), dev)
-    n = ctypes.c_size_t()
-    _lib.check(lib.moe_decode_experts_workspace(cfg, t, n), "moe_decode_experts_workspace")
-    with _On(dev, stream) as s:
+    s, leave = _enter(dev, stream)
+    try:
         if out is None:
             out = torch.empty((t, shape.hidden), dtype=torch.bfloat16, device=dev)
-        ws = _workspace(workspace, n.value, dev)
-        _lib.check(lib.moe_decode_experts(cfg, cw, px, sx, pi, pw, pr,
-                                          _tensor(out, "out", torch.bfloat16, (t, shape.hidden), dev), t,
-                                          ws.data_ptr(), ws.numel(), s), "moe_decode_experts")
+        ws = _workspace(workspace, experts_workspace(shape, t), dev)
+        st = _lib.load().moe_decode_experts(cfg, cw, px, sx, pi, pw, pr,
+                                            _tensor(out, "out", torch.bfloat16, (t, shape.hidden), dev), t,
+                                            ws.data_ptr(), ws.numel(), s)
+    finally:
+        if leave is not None:
+            leave.close()
+    if st:
+        _lib.check(st, "moe_decode_experts")
     return out
 
 
-def _project_config(wdtype: str, inner: int, outer: int, swiglu: bool, adapters: Adapters | None, out_dtype):
+@functools.lru_cache(maxsize=1024)
+def _project_config(wdtype: str, inner: int, outer: int, swiglu: bool, rank: int, count: int, out_dtype):
     _need(wdtype in _lib.WDTYPE, f"unknown weight type {wdtype!r}")
     _need(out_dtype in _DTYPES, "the result is bf16 or fp32")
-    count, rank = (0, 0) if adapters is None else adapters.a.shape[:2]
-    return _lib.ProjectConfig(inner, outer, swiglu, _lib.WDTYPE[wdtype], rank, count, _DTYPES[out_dtype])
+    cfg = _lib.ProjectConfig(inner, outer, swiglu, _lib.WDTYPE[wdtype], rank, count, _DTYPES[out_dtype])
+    _lib.check(_lib.load().moe_decode_project_check(cfg), "moe_decode_project_check")
+    return cfg
 
 
+@functools.lru_cache(maxsize=1024)
 def project_workspace(inner: int, outer: int, rows: int, *, wdtype: str = "bf16", swiglu: bool = False, rank: int = 0,
                       num_adapters: int = 0, out_dtype=torch.bfloat16) -> int:
     """Bytes of workspace that :func:`project` needs for at most ``rows`` rows."""
     n = ctypes.c_size_t()
-    cfg = _lib.ProjectConfig(inner, outer, swiglu, _lib.WDTYPE[wdtype], rank, num_adapters, _DTYPES[out_dtype])
+    cfg = _project_config(wdtype, inner, outer, bool(swiglu), rank, num_adapters, out_dtype)
     _lib.check(_lib.load().moe_decode_project_workspace(cfg, rows, n), "moe_decode_project_workspace")
     return n.value
 
@@ -216,7 +228,6 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
     ([2 O, K] with swiglu), or for ``wdtype`` "fp8" / "nvfp4" the tuple (codes, block
     scales) / (codes, block scales, tensor scale [] or [2]). ``adapter_ids`` int32 [T]: the
     adapter of each row, outside 0..L-1 (-1) none."""
-    lib = _lib.load()
     dev = x.device
     parts = weight if isinstance(weight, (tuple, list)) else (weight,)
     _need(x.dim() == 2, "x must be [rows, inner]")
@@ -226,12 +237,13 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
     _need(rows % halves == 0, "a gate/up weight has an even number of rows")
     o = rows // halves
     _need((adapters is None) == (adapter_ids is None), "adapters and adapter_ids come together")
+    n = r = 0
     if adapters is not None:
         _need(adapters.a.dim() == 3 and adapters.a.shape[0] > 0 and adapters.a.shape[1] > 0, "adapters.a must be [L, r, K]")
+        n, r = adapters.a.shape[:2]
     if out is not None:
         out_dtype = out.dtype
-    cfg = _project_config(wdtype, k, o, swiglu, adapters, out_dtype)
-    _lib.check(lib.moe_decode_project_check(cfg), "moe_decode_project_check")
+    cfg = _project_config(wdtype, k, o, bool(swiglu), r, n, out_dtype)
     px, sx = _rows(x, "x", k, dev)
     want = _quantised(wdtype, (), rows, k, halves)
     _need(len(parts) == len(want), f"a {wdtype} weight comes in {len(want)} tensors")
@@ -240,25 +252,33 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
         setattr(cw, field, _tensor(t_, field, dtype, size, dev))
     ids = None
     if adapters is not None:
-        n, r = cfg.num_adapters, cfg.rank
         cw.a = _tensor(adapters.a, "adapters.a", torch.bfloat16, (n, r, k), dev)
         cw.b = _tensor(adapters.b, "adapters.b", torch.bfloat16, (n, rows, r), dev)
         if adapters.scale is not None:
             cw.scale = _tensor(adapters.scale, "adapters.scale", torch.float32, (n,), dev)
         ids = _tensor(adapter_ids, "adapter_ids", torch.int32, (t,), dev)
     pa = None if addend is None else _tensor(addend, "addend", torch.bfloat16, (t, o), dev)
-    need = ctypes.c_size_t()
-    _lib.check(lib.moe_decode_project_workspace(cfg, t, need), "moe_decode_project_workspace")
-    with _On(dev, stream) as s:
+    s, leave = _enter(dev, stream)
+    try:
         if out is None:
             out = torch.empty((t, o), dtype=out_dtype, device=dev)
-        ws = _workspace(workspace, need.value, dev)
-        _lib.check(lib.moe_decode_project(cfg, cw, px, sx, ids, pa, _tensor(out, "out", out_dtype, (t, o), dev), t,
-                                          ws.data_ptr(), ws.numel(), s), "moe_decode_project")
+        ws = _workspace(workspace, project_workspace(k, o, t, wdtype=wdtype, swiglu=swiglu, rank=r, num_adapters=n,
+                                                     out_dtype=out_dtype), dev)
+        st = _lib.load().moe_decode_project(cfg, cw, px, sx, ids, pa, _tensor(out, "out", out_dtype, (t, o), dev), t,
+                                            ws.data_ptr(), ws.numel(), s)
+    finally:
+        if leave is not None:
+            leave.close()
+    if st:
+        _lib.check(st, "moe_decode_project")
     return out
 
 
 def status(workspace: torch.Tensor, stream=None) -> int:
     """Synchronise and return the status code of the last call that used ``workspace``."""
-    with _On(workspace.device, stream) as s:
+    s, leave = _enter(workspace.device, stream)
+    try:
         return _lib.load().moe_decode_rows_status(workspace.data_ptr(), s)
+    finally:
+        if leave is not None:
+            leave.close()

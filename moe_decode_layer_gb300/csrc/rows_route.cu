@@ -6,10 +6,13 @@
 //      largest key;
 //   2. the keys at or above the bound (about K of them) are listed in shared
 //      memory; each is ranked against the others, one lane per candidate.
-// Where the keys are rounded values (a bias, sums over groups), neighbours in the
-// order that are closer than their rounding errors, and not equal inputs, make the
-// row's choice anew in fp64, by the definition: rare, and needed for an order
-// that does not depend on how the scores were computed.
+// Without a bias the order is the logits' own and exact. Where the keys are rounded
+// values (a bias, sums over groups), neighbours in the order that are closer than
+// their rounding errors, and not equal inputs, are decided in fp64: sigmoid keys by
+// the candidates' keys alone, else the row's whole choice by the definition. That is
+// rare, and makes the choice independent of how the scores were computed. (fp64 runs
+// at 1/64 of the fp32 rate: one row decided as a whole takes longer than all the
+// others of a 4096-row launch, so the bounds below count each rounding.)
 //
 // Bound by the logits' bytes for many rows, by launch latency for few.
 #include <cuda_bf16.h>
@@ -38,6 +41,7 @@ struct RouteParams {
   int E, K;
   int softmax;     // else sigmoid
   int groups, kept, best, group_size;
+  uint32_t group_magic;  // 2^32 / group_size, rounded up
   int renormalise;
   float scale;
 };
@@ -50,6 +54,10 @@ __device__ __forceinline__ float to_f32(T v) {
 
 // NaN and masks -> -inf; +inf and the like -> a finite value, so that no sum is NaN.
 __device__ __forceinline__ float clean(float l) { return l > kMasked ? fminf(l, kLargest) : -INFINITY; }
+
+__device__ __forceinline__ int group_of(const RouteParams& p, int e) {
+  return p.group_size == 1 ? e : (int)__umulhi((uint32_t)e, p.group_magic);  // e < 1024: exact
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -123,7 +131,7 @@ __device__ __noinline__ int choose64(const RouteParams& p, const T* src, double*
     int at = E;
     for (int e = lane; e < E; e += 32) {
       const double x = key[e];
-      if (x > b && (keep >> (e / p.group_size) & 1)) {
+      if (x > b && (keep >> group_of(p, e) & 1)) {
         b = x;
         at = e;
       }
@@ -144,30 +152,30 @@ __device__ __noinline__ int choose64(const RouteParams& p, const T* src, double*
   return mine;
 }
 
-// The row's choice by K warp maxima over the exact keys: when so many keys tie
-// at the bound that they cannot all be listed.
-template <int N, typename At>
-__device__ __noinline__ int choose_rounds(const uint32_t (&k0)[N], int K, int lane, At at) {
-  uint32_t k[N];
-#pragma unroll
-  for (int j = 0; j < N; j++) k[j] = k0[j];
+// The row's choice by K warp maxima over the logits: when so many tie at the bound
+// that they cannot all be listed. keep: bits of the groups in the choice.
+template <typename T>
+__device__ __noinline__ int choose_rounds(const RouteParams& p, const T* src, uint32_t keep, int lane) {
   int mine = -1;
-  for (int r = 0; r < K; r++) {
+  uint32_t last = 0xffffffffu;  // the key and expert chosen last: later ones come after it
+  int last_e = -1;
+  for (int r = 0; r < p.K; r++) {
     uint32_t b = 0;
-    int e = 0x7fffffff;
-#pragma unroll
-    for (int j = 0; j < N; j++)
-      if (k[j] > b) {
-        b = k[j];
-        e = at(j);
+    int at = 0x7fffffff;
+    for (int e = lane; e < p.E; e += 32) {
+      const float l = clean(to_f32(src[e]));
+      if (!(l > kMasked) || !(keep >> group_of(p, e) & 1u)) continue;
+      const uint32_t k = f32_order_key(l + 0.0f);
+      if ((k < last || (k == last && e > last_e)) && k > b) {
+        b = k;
+        at = e;
       }
+    }
     const uint32_t m = warp_max_u32(b);
     if (m == 0) break;
-    const int first = __reduce_min_sync(0xffffffffu, b == m ? e : 0x7fffffff);
-    if (lane == r) mine = first;
-#pragma unroll
-    for (int j = 0; j < N; j++)
-      if (at(j) == first) k[j] = 0;
+    last = m;
+    last_e = __reduce_min_sync(0xffffffffu, b == m ? at : 0x7fffffff);
+    if (lane == r) mine = last_e;
   }
   return mine;
 }
@@ -182,7 +190,7 @@ struct Cand {
 // KEYS: there is a bias, or groups (else the choice is by the logits alone, whose
 // order is the scores').
 template <typename T, int N, bool VEC, bool KEYS>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ __align__(16) uint8_t s_dyn[];  // KEYS: per warp E doubles
   __shared__ Cand s_cand[kWarps][kCand];
   __shared__ Cand s_sorted[kWarps][32];
@@ -229,9 +237,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
 
   // sum over the row's softmax (its weights unnormalised over the chosen, or its keys)
   float top = 0.0f, norm = 1.0f;
-  const bool whole = p.softmax && (KEYS || !p.renormalise);
+  const bool bias = KEYS && p.bias;
+  const bool whole = p.softmax && (bias || !p.renormalise);
+  if (whole || (KEYS && p.softmax)) top = warp_max(lmax);
   if (whole) {
-    top = warp_max(lmax);
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; j++) s += l[j] > kMasked ? expf(l[j] - top) : 0.0f;
@@ -240,23 +249,29 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
 
   // 32-bit keys, order-preserving; 0: not to be chosen
   uint32_t key[N];
-  float smax = 0.0f;  // KEYS: a bound on the row's scores, for the rounding errors
-  bool close = false;
+  float tol_s = 0.0f;  // with a bias: how far two keys' scores may be off together
+  bool close = false, close_group = false;
+  uint32_t keep = 0xffffffffu;
   float* s_key = nullptr;
   if constexpr (KEYS) {
     s_key = reinterpret_cast<float*>(s_dyn + (size_t)warp * E * 8);
-    float f[N];
+    float f[N];  // key values; without a bias the logits, whose order is the scores'
+    float smax = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; j++) {
       const int e = at(j);
-      const float s = p.softmax ? expf(l[j] - top) / norm : 1.0f / (1.0f + expf(-l[j]));
-      const bool ok = l[j] > kMasked;
-      smax = fmaxf(smax, ok ? s : 0.0f);
-      f[j] = ok ? (p.bias ? s + __ldg(p.bias + e) : s) : -INFINITY;
+      f[j] = l[j];
+      if (bias) {
+        const float s = p.softmax ? expf(l[j] - top) / norm : 1.0f / (1.0f + expf(-l[j]));
+        const bool ok = l[j] > kMasked;
+        smax = fmaxf(smax, ok ? s : 0.0f);
+        f[j] = ok ? s + __ldg(p.bias + e) : -INFINITY;
+      }
       if (e < E) s_key[e] = f[j];
     }
-    smax = warp_max(smax);
-    uint32_t keep = 0xffffffffu;
+    // exp and the quotients are off by 2^-21.4 of a score at most; a softmax's sum by
+    // one step for each addition, and its exponent's rounding weighs 2^-25 of the top score
+    if (bias) tol_s = warp_max(smax) * (p.softmax ? (N + 16) * 0x1p-23f : 0x1p-20f);
     __syncwarp();
     if (p.kept < p.groups) {
       // lanes share a group's keys: sub lanes each (a power of two), merged by shuffles
@@ -282,8 +297,18 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
         b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
         b1 = fmaxf(b1, o1);
       }
+      // a group's value: its best key (by the logit itself, exact), or the two best
+      // keys' sum (softmax: without the row's common factor)
       float v = b1;
-      if (p.best == 2 && b2 > -INFINITY) v += b2;
+      if (p.best == 2) {
+        if (bias) {
+          if (b2 > -INFINITY) v += b2;
+        } else if (b1 > -INFINITY) {
+          const float s1 = p.softmax ? expf(b1 - top) : 1.0f / (1.0f + expf(-b1));
+          const float s2 = p.softmax ? expf(b2 - top) : 1.0f / (1.0f + expf(-b2));  // 0 for none
+          v = s1 + s2;
+        }
+      }
       int rank = 0;
       for (int o = 0; o < p.groups; o++) {
         const float x = __shfl_sync(0xffffffffu, v, o * sub);
@@ -291,20 +316,24 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
       }
       const bool lead = u == 0 && g < p.groups;
       const uint32_t in = __ballot_sync(0xffffffffu, lead && rank < p.kept);
-      // groups -> bits
-      keep = 0;
+      keep = 0;  // groups -> bits
       for (int o = 0; o < p.groups; o++) keep |= (in >> (o * sub) & 1u) << o;
       // the last kept and the first dropped group: too close to tell in fp32?
-      const uint32_t l0 = __ballot_sync(0xffffffffu, lead && rank == p.kept - 1);
-      const uint32_t l1 = __ballot_sync(0xffffffffu, lead && rank == p.kept);
-      const float v0 = __shfl_sync(0xffffffffu, v, __ffs(l0) - 1), v1 = __shfl_sync(0xffffffffu, v, __ffs(l1) - 1);
-      if (v1 > -INFINITY) close = v0 - v1 <= 0x1p-17f * smax + 0x1p-20f * fmaxf(fabsf(v0), fabsf(v1));
+      if (bias || p.best == 2) {
+        const int i0 = __ffs(__ballot_sync(0xffffffffu, lead && rank == p.kept - 1)) - 1;
+        const int i1 = __ffs(__ballot_sync(0xffffffffu, lead && rank == p.kept)) - 1;
+        const float v0 = __shfl_sync(0xffffffffu, v, i0), v1 = __shfl_sync(0xffffffffu, v, i1);
+        const bool same = !bias && __shfl_sync(0xffffffffu, b1, i0) == __shfl_sync(0xffffffffu, b1, i1) &&
+                          __shfl_sync(0xffffffffu, b2, i0) == __shfl_sync(0xffffffffu, b2, i1);
+        const float big = fmaxf(fabsf(v0), fabsf(v1));
+        if (v1 > -INFINITY && !same) close_group = v0 - v1 <= (bias ? 2.0f * tol_s + 0x1p-21f * big : 0x1p-19f * big);
+      }
     }
 #pragma unroll
     for (int j = 0; j < N; j++) {
       const int e = at(j);
-      const bool in = p.kept >= p.groups || (e < E && (keep >> (e / p.group_size) & 1u));
-      key[j] = in && f[j] > -INFINITY ? f32_order_key(p.bias ? f[j] : l[j] + 0.0f) : 0u;
+      const bool in = p.kept >= p.groups || (e < E && (keep >> group_of(p, e) & 1u));
+      key[j] = in && f[j] > kMasked ? f32_order_key(f[j] + 0.0f) : 0u;
     }
   } else {
 #pragma unroll
@@ -325,9 +354,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
   if (K > 1 && __popc(__ballot_sync(0xffffffffu, lane_max >= bound && lane_max)) < K) bound = 1;  // fewer lanes than K
   if constexpr (KEYS) {
     // a key below the bound by less than its rounding error is a candidate too
-    if (bound > 1 && p.bias) {
+    if (bound > 1 && bias) {
       const float f = order_key_f32(bound);
-      bound = f32_order_key(f - (0x1p-18f * smax + 0x1p-21f * fabsf(f)));
+      bound = f32_order_key(f - (tol_s + 0x1p-21f * fabsf(f)));
     }
   }
   bound = max(bound, 1u);
@@ -367,21 +396,47 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
       mine = x.e;
       mine_l = x.l;
       if constexpr (KEYS) {
-        if (p.bias && lane + 1 < min(count, K + 1)) {
+        if (bias && lane + 1 < min(count, K + 1)) {
           const Cand y = s_sorted[warp][lane + 1];
           const float a = order_key_f32(x.key), b = order_key_f32(y.key);
           const bool same = x.l == y.l && __ldg(p.bias + x.e) == __ldg(p.bias + y.e);
-          if (!same && a - b <= 0x1p-18f * smax + 0x1p-21f * fmaxf(fabsf(a), fabsf(b))) close = true;
+          close = !same && a - b <= tol_s + 0x1p-22f * fmaxf(fabsf(a), fabsf(b));
+        }
+      }
+    }
+    if constexpr (KEYS) {
+      if (__any_sync(0xffffffffu, close) && !p.softmax && count <= 32) {
+        // the candidates' keys in fp64, ranked again, one lane each
+        close = false;
+        double* s64 = reinterpret_cast<double*>(s_key);
+        double k64 = 0.0;
+        Cand x = {};
+        __syncwarp();
+        if (lane < count) {
+          x = s_cand[warp][lane];
+          k64 = sigmoid64((double)x.l) + (double)__ldg(p.bias + x.e);
+          s64[lane] = k64;
+        }
+        __syncwarp();
+        if (lane < count) {
+          int rank = 0;
+          for (int o = 0; o < count; o++) rank += s64[o] > k64 || (s64[o] == k64 && s_cand[warp][o].e < x.e);
+          if (rank < K) s_sorted[warp][rank] = x;
+        }
+        __syncwarp();
+        if (lane < have) {
+          mine = s_sorted[warp][lane].e;
+          mine_l = s_sorted[warp][lane].l;
         }
       }
     }
   } else {
-    if constexpr (KEYS) close = true;  // too many to rank: decide them in fp64
-    else mine = choose_rounds<N>(key, K, lane, at);
+    if (bias) close = true;  // too many to rank: decide them in fp64
+    else mine = choose_rounds<T>(p, src, keep, lane);
     if (mine >= 0) mine_l = clean(to_f32(src[mine]));
   }
   if constexpr (KEYS) {
-    if (__any_sync(0xffffffffu, close)) {
+    if (__any_sync(0xffffffffu, close || close_group)) {
       __syncwarp();
       mine = choose64<T>(p, src, reinterpret_cast<double*>(s_key), lane);
       mine_l = mine >= 0 ? clean(to_f32(src[mine])) : 0.0f;
@@ -459,6 +514,7 @@ cudaError_t launch_route(const moe_route_config& c, const void* logits, int64_t 
   p.kept = c.top_groups;
   p.best = c.group_best;
   p.group_size = c.num_experts / c.num_groups;
+  p.group_magic = p.group_size > 1 ? 0xffffffffu / p.group_size + 1 : 0;
   p.renormalise = c.renormalise != 0;
   p.scale = c.scale;
   const bool keys = bias || c.top_groups < c.num_groups;
