@@ -17,6 +17,7 @@
 // Bound by the logits' bytes for many rows, by launch latency for few.
 #include <cuda_bf16.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "ptx.cuh"
@@ -29,6 +30,7 @@ namespace {
 constexpr int kWarps = 4;     // rows per CTA
 constexpr int kCand = 64;     // candidates listed per row
 constexpr float kMasked = -0x1.2ced34p+126f;  // the first fp32 at or below -1e38
+constexpr float kLeast = -0x1.2ced32p+126f;   // the next one above it
 constexpr float kLargest = 3e38f;
 
 struct RouteParams {
@@ -64,7 +66,7 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+__device__ __forceinline__ float warp_max(float v) {  // not for NaN
   return order_key_f32(warp_max_u32(f32_order_key(v)));
 }
 
@@ -192,7 +194,8 @@ struct Cand {
 template <typename T, int N, bool VEC, bool KEYS>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ __align__(16) uint8_t s_dyn[];  // KEYS: per warp E doubles
-  __shared__ Cand s_cand[kWarps][kCand];
+  __shared__ uint64_t s_order[kWarps][kCand];  // key, then the complement of the expert: larger comes first
+  __shared__ float s_logit[kWarps][kCand];
   __shared__ Cand s_sorted[kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
@@ -208,13 +211,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
       const int e = at(j);
       if (e < E) {  // E % 4 == 0
         if constexpr (sizeof(T) == 4) {
-          const float4 v = __ldcs(reinterpret_cast<const float4*>(src + e));
+          const float4 v = __ldg(reinterpret_cast<const float4*>(src + e));
           l[j] = v.x;
           l[j + 1] = v.y;
           l[j + 2] = v.z;
           l[j + 3] = v.w;
         } else {
-          const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + e));
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + e));
           l[j] = bf16lo(v.x);
           l[j + 1] = bf16hi(v.x);
           l[j + 2] = bf16lo(v.y);
@@ -228,17 +231,21 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 #pragma unroll
     for (int j = 0; j < N; j++) l[j] = at(j) < E ? to_f32(src[at(j)]) : -INFINITY;
   }
+  const bool bias = KEYS && p.bias;
+  const bool whole = p.softmax && (bias || !p.renormalise);
   float lmax = -INFINITY;
+  // Where the logits alone are compared they stay as they are: maxima pass over NaN,
+  // the bounds are cut to the finite range, and so is each candidate.
+  if (KEYS || whole) {
 #pragma unroll
-  for (int j = 0; j < N; j++) {
-    l[j] = clean(l[j]);
-    lmax = fmaxf(lmax, l[j]);
+    for (int j = 0; j < N; j++) {
+      l[j] = clean(l[j]);
+      lmax = fmaxf(lmax, l[j]);
+    }
   }
 
   // sum over the row's softmax (its weights unnormalised over the chosen, or its keys)
   float top = 0.0f, norm = 1.0f;
-  const bool bias = KEYS && p.bias;
-  const bool whole = p.softmax && (bias || !p.renormalise);
   if (whole || (KEYS && p.softmax)) top = warp_max(lmax);
   if (whole) {
     float s = 0.0f;
@@ -247,20 +254,17 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     norm = warp_sum(s);
   }
 
-  // 32-bit keys, order-preserving; 0: not to be chosen
-  uint32_t key[N];
+  float (&f)[N] = l;  // the keys: without a bias the logits, whose order is the scores'
   float tol_s = 0.0f;  // with a bias: how far two keys' scores may be off together
   bool close = false, close_group = false;
   uint32_t keep = 0xffffffffu;
   float* s_key = nullptr;
   if constexpr (KEYS) {
     s_key = reinterpret_cast<float*>(s_dyn + (size_t)warp * E * 8);
-    float f[N];  // key values; without a bias the logits, whose order is the scores'
     float smax = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; j++) {
       const int e = at(j);
-      f[j] = l[j];
       if (bias) {
         const float s = p.softmax ? expf(l[j] - top) / norm : 1.0f / (1.0f + expf(-l[j]));
         const bool ok = l[j] > kMasked;
@@ -329,42 +333,36 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         if (v1 > -INFINITY && !same) close_group = v0 - v1 <= (bias ? 2.0f * tol_s + 0x1p-21f * big : 0x1p-19f * big);
       }
     }
+    if (p.kept < p.groups) {
 #pragma unroll
-    for (int j = 0; j < N; j++) {
-      const int e = at(j);
-      const bool in = p.kept >= p.groups || (e < E && (keep >> group_of(p, e) & 1u));
-      key[j] = in && f[j] > kMasked ? f32_order_key(f[j] + 0.0f) : 0u;
+      for (int j = 0; j < N; j++)
+        if (at(j) < E && !(keep >> group_of(p, at(j)) & 1u)) f[j] = -INFINITY;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; j++) key[j] = l[j] > kMasked ? f32_order_key(l[j] + 0.0f) : 0u;
   }
 
-  // 1. a lower bound on the K-th largest key
-  uint32_t lane_max = 0;
+  // 1. a lower bound on the K-th largest key; keys below least are not to be chosen
+  const float least = bias ? -FLT_MAX : kLeast;
+  float lane_max = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < N; j++) lane_max = max(lane_max, key[j]);
-  uint32_t bound = 0, rest = lane_max;
+  for (int j = 0; j < N; j++) lane_max = fmaxf(lane_max, f[j]);
+  lane_max = fminf(lane_max, kLargest);
+  uint32_t rest = lane_max >= least ? f32_order_key(lane_max) : 0, last = 0;
   for (int r = 0; r < K; r++) {
     const uint32_t m = warp_max_u32(rest);
     if (m == 0) break;
-    bound = m;
-    if (rest == m) rest = 0;
+    last = m;
+    rest = rest == m ? 0 : rest;
   }
-  if (K > 1 && __popc(__ballot_sync(0xffffffffu, lane_max >= bound && lane_max)) < K) bound = 1;  // fewer lanes than K
-  if constexpr (KEYS) {
-    // a key below the bound by less than its rounding error is a candidate too
-    if (bound > 1 && bias) {
-      const float f = order_key_f32(bound);
-      bound = f32_order_key(f - (tol_s + 0x1p-21f * fabsf(f)));
-    }
-  }
-  bound = max(bound, 1u);
+  float bound = last ? order_key_f32(last) : least;
+  if (__popc(__ballot_sync(0xffffffffu, lane_max >= bound)) < K) bound = least;  // fewer lanes than K
+  // a key below the bound by less than its rounding error is a candidate too
+  if (KEYS && bias) bound = fmaxf(bound - (tol_s + 0x1p-21f * fabsf(bound)), least);
 
-  // 2. list and rank the candidates
-  int n = 0;
+  // 2. list and rank the candidates: about one in every lane that has any
+  uint32_t mask = 0;
 #pragma unroll
-  for (int j = 0; j < N; j++) n += key[j] >= bound;
+  for (int j = 0; j < N; j++) mask |= f[j] >= bound ? 1u << j : 0u;
+  const int n = __popc(mask);
   int before = n;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -376,18 +374,18 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   int mine = -1;       // lane j: the j-th chosen expert
   float mine_l = 0.0f;
   if (count <= kCand) {
-#pragma unroll
-    for (int j = 0; j < N; j++)
-      if (key[j] >= bound) s_cand[warp][before++] = Cand{key[j], at(j), l[j]};
+    for (; mask; mask &= mask - 1) {
+      const int e = at(__ffs(mask) - 1);
+      const float x = clean(to_f32(src[e]));
+      s_order[warp][before] = (uint64_t)f32_order_key((bias ? s_key[e] : x) + 0.0f) << 32 | (uint32_t)~e;
+      s_logit[warp][before++] = x;
+    }
     __syncwarp();
     for (int c = lane; c < count; c += 32) {
-      const Cand x = s_cand[warp][c];
+      const uint64_t x = s_order[warp][c];
       int rank = 0;
-      for (int o = 0; o < count; o++) {
-        const uint32_t k = s_cand[warp][o].key;
-        rank += k > x.key || (k == x.key && s_cand[warp][o].e < x.e);
-      }
-      if (rank <= K && rank < 32) s_sorted[warp][rank] = x;
+      for (int o = 0; o < count; o++) rank += s_order[warp][o] > x;
+      if (rank <= K && rank < 32) s_sorted[warp][rank] = Cand{(uint32_t)(x >> 32), (int)~(uint32_t)x, s_logit[warp][c]};
     }
     __syncwarp();
     const int have = min(count, K);
@@ -413,14 +411,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         Cand x = {};
         __syncwarp();
         if (lane < count) {
-          x = s_cand[warp][lane];
+          x = Cand{0, (int)~(uint32_t)s_order[warp][lane], s_logit[warp][lane]};
           k64 = sigmoid64((double)x.l) + (double)__ldg(p.bias + x.e);
           s64[lane] = k64;
         }
         __syncwarp();
         if (lane < count) {
           int rank = 0;
-          for (int o = 0; o < count; o++) rank += s64[o] > k64 || (s64[o] == k64 && s_cand[warp][o].e < x.e);
+          for (int o = 0; o < count; o++) rank += s64[o] > k64 || (s64[o] == k64 && (int)~(uint32_t)s_order[warp][o] < x.e);
           if (rank < K) s_sorted[warp][rank] = x;
         }
         __syncwarp();
