@@ -108,14 +108,11 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// 16 accumulator columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(addr));
+// 8 accumulator columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr));
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
@@ -516,8 +513,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
   } else if (warp >= 4 && warp < 4 + epilogue_warps(FMT)) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;  // this warp's 32 TMEM lanes; two warps (bf16) share them, 16 columns in turn
-    const int c0 = warp >= 8 ? 16 : 0;
+    const int q = warp & 3;  // this warp's 32 TMEM lanes; two warps share them, 8 columns in turn
+    const int c0 = warp >= 8 ? 8 : 0;
     float* s_ad = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + p.ad_off);
     const int r = q * 32 + lane;
     Ring acc;
@@ -548,6 +545,16 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
           }
           s_ad[i] = v;
+        }
+      }
+      if (EPI != EPI_SWIGLU && p.addend) {  // the tile's addends on their way to L2
+        const int first = tl.rb * sub_rows, cols = min(2 * p.rt, p.R - first);
+        const int lines = (cols * 2 + 127) / 128 + 1;
+        for (int i = tid - 128; i < tl.n * lines; i += 32 * epilogue_warps(FMT)) {
+          const int pos = tl.p0 + i / lines;
+          const int row = p.out_row ? __ldg(p.out_row + pos) : pos;
+          const int col = min(first + (i % lines) * 64, first + cols - 1);
+          if (row >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.addend + (size_t)row * p.out_stride + col));
         }
       }
       // one warp polls, the others wait at a barrier that costs no issue slots; all
@@ -584,59 +591,64 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         // neighbouring results of one column: lane 2 i those of the even column.
         const bool odd = lane & 1;
         const int yp0 = y0 & ~1, yp1 = y1 & ~1;
-        const bool extra = p.ad_mode == AD_EPILOGUE || (EPI != EPI_SWIGLU && p.addend);
-        for (int c = c0; c < tl.n; c += 4 * epilogue_warps(FMT)) {
-          // Everything that is loaded is on its way before the first sum is used, and
-          // all 16 columns' results are made before the first is stored, without
-          // branches: with them each column waited for the one before (225 clocks).
-          uint32_t v0[16], v1[16];
-          const int m = min(16, tl.n - c);
+        // Eight columns at a time, the next eight's sums and addends on their way
+        // meanwhile. No branches between columns: with them each column waited for the
+        // one before (225 clocks).
+        constexpr int kStep = 2 * epilogue_warps(FMT);
+        const bool add = EPI != EPI_SWIGLU && p.addend;
+        uint32_t n0[8], n1[8];
+        __nv_bfloat16 q0[8], q1[8];
+        int row_n = -1;
+        auto fetch = [&](int c) {
           __syncwarp();
-          tmem_ld16(d0 + c, v0);
-          tmem_ld16(d1 + c, v1);
-          int row_l = tl.p0 + c + (lane & 15);  // lane j: the row of out of column j
-          if (p.out_row) row_l = __ldg(p.out_row + min(row_l, tl.p0 + tl.n - 1));
-          row_l = (lane & 15) < m ? row_l : -1;
-          float e0[16], e1[16];
-          if (extra) {
+          tmem_ld8(d0 + c, n0);
+          tmem_ld8(d1 + c, n1);
+          row_n = tl.p0 + min(c + (lane & 7), tl.n - 1);  // lane j: the row of out of column j
+          if (p.out_row) row_n = __ldg(p.out_row + row_n);
+          if (add) {
 #pragma unroll
-            for (int j = 0; j < 16; j++) e0[j] = e1[j] = 0.0f;
-            if (EPI != EPI_SWIGLU && p.addend) {
-#pragma unroll
-              for (int j = 0; j < 16; j++) {
-                const __nv_bfloat16* a = p.addend + (size_t)max(__shfl_sync(0xffffffffu, row_l, j), 0) * p.out_stride;
-                e0[j] = __bfloat162float(a[ok0 ? y0 : 0]);
-                e1[j] = __bfloat162float(a[ok1 ? y1 : 0]);
-              }
-            }
-            if (p.ad_mode == AD_EPILOGUE) {
-              const float* ad = s_ad + c * 2 * p.rt + min(r, p.rt - 1);
-#pragma unroll
-              for (int j = 0; j < 16; j++) {
-                const int at = j < m ? j * 2 * p.rt : 0;
-                e0[j] += ad[at];
-                e1[j] += ad[at + p.rt];
-              }
+            for (int j = 0; j < 8; j++) {
+              const __nv_bfloat16* a = p.addend + (size_t)max(__shfl_sync(0xffffffffu, row_n, j), 0) * p.out_stride;
+              q0[j] = a[ok0 ? y0 : 0];
+              q1[j] = a[ok1 ? y1 : 0];
             }
           }
+        };
+        if (c0 < tl.n) fetch(c0);
+        for (int c = c0; c < tl.n; c += kStep) {
+          float a0[8], a1[8];
           tmem_ld_wait();
-          float a0[16], a1[16];
+          const int m = min(8, tl.n - c);
+          const int row_l = row_n;
 #pragma unroll
-          for (int j = 0; j < 16; j++) {
-            a0[j] = __uint_as_float(v0[j]);
-            a1[j] = __uint_as_float(v1[j]);
+          for (int j = 0; j < 8; j++) {
+            a0[j] = __uint_as_float(n0[j]);
+            a1[j] = __uint_as_float(n1[j]);
             if (FMT == FMT_NVFP4 || EPI == EPI_BF16) {
               a0[j] *= g0;
               a1[j] *= g1;
             }
-            if (extra) {
-              a0[j] += e0[j];
-              a1[j] += e1[j];
+            if (add) {
+              a0[j] += __bfloat162float(q0[j]);
+              a1[j] += __bfloat162float(q1[j]);
             }
-            if (EPI == EPI_SWIGLU) a0[j] = silu_mul(a0[j], a1[j]);
+          }
+          if (c + kStep < tl.n) fetch(c + kStep);
+          if (p.ad_mode == AD_EPILOGUE) {
+            const float* ad = s_ad + c * 2 * p.rt + min(r, p.rt - 1);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              const int at = j < m ? j * 2 * p.rt : 0;
+              a0[j] += ad[at];
+              a1[j] += ad[at + p.rt];
+            }
+          }
+          if (EPI == EPI_SWIGLU) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) a0[j] = silu_mul(a0[j], a1[j]);
           }
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
+          for (int j = 0; j < 8; j += 2) {
             const int row = p.out_row ? __shfl_sync(0xffffffffu, row_l, j + odd) : tl.p0 + c + j + odd;
             const bool there = j + odd < m && row >= 0;
             const size_t o = (size_t)row * p.out_stride;
