@@ -117,8 +117,10 @@ bool layout(int rt, int nmax, int fmt, int ksteps, int ad_mode, int smem_max, La
   return l->stages >= 2;
 }
 
+constexpr double kSmallStep = 390.0;  // clocks of a step's eight products with few rows of x
+
 // Rows of a sub-tile. A tile costs, per 64 k, the larger of its weight bytes (an
-// SM's share of the HBM rate is about 23 bytes a clock), its operand bytes (about 45
+// SM's share of the HBM rate is about 23 bytes a clock), its operand bytes (about 55
 // a clock from L2) and its tensor time (a sub-tile takes 2 n16 clocks whatever rt
 // is), and a fixed share for its start and epilogue. The tiles go round the SMs in
 // waves: rt is what makes the sum least. It is a multiple of 16 (or 8, when that
@@ -126,7 +128,7 @@ bool layout(int rt, int nmax, int fmt, int ksteps, int ad_mode, int smem_max, La
 // part of a sector cost more than the product (rt = 104 against 112: 575 against ...).
 // reuse: tiles that read the same weights.
 int choose_rt(int64_t R, bool swiglu, double entries, double reuse, int n, int fmt, int nmax, int ksteps, int ad_mode,
-              const Device& d) {
+              const Device& d, double* cost_out = nullptr) {
   int best = 128;
   double least = 1e300;
   const double bytes = fmt == FMT_BF16 ? 256.0 : fmt == FMT_FP8 ? 128.0 : 72.0;
@@ -135,14 +137,42 @@ int choose_rt(int64_t R, bool swiglu, double entries, double reuse, int n, int f
     if (!layout(rt, nmax, fmt, ksteps, ad_mode, d.smem, &l)) continue;
     const int64_t nrb = cdiv(R, swiglu ? rt : 2 * rt);
     const double waves = std::ceil(entries * (double)nrb / d.sms);
-    const double step = std::max({rt * bytes / (23.0 * reuse), (rt * 256.0 + n * 128.0) / 45.0, 4.0 * n});
+    const double step =
+        std::max({rt * bytes / (23.0 * reuse), (rt * 256.0 + n * 128.0) / 55.0, kSmallStep, 4.0 * n});
     const double cost = waves * (ksteps * step + 2500.0);
     if (cost < least * 0.999) {
       least = cost;
       best = rt;
     }
   }
+  if (cost_out) *cost_out = least;
   return best;
+}
+
+// For few rows: the CTAs that share a tile's K (1: none) and the rows of a sub-tile.
+// All tiles run at once (clusters do not fill every SM: 7 of 8 are counted on); joining
+// the sums costs about 1800 clocks.
+int choose_split(int64_t R, bool swiglu, int entries, int nmax, int ksteps, int ad_mode, const Device& d, int* rt) {
+  double least = 0.0;
+  *rt = choose_rt(R, swiglu, entries, entries, nmax, FMT_BF16, nmax, ksteps, ad_mode, d, &least);
+  int split = 1;
+  for (int s = 2; s <= 8; s *= 2) {
+    if (ksteps < 2 * s) break;
+    for (int t = 128; t >= 16; t -= 16) {
+      const int64_t ctas = entries * cdiv(R, swiglu ? t : 2 * t) * s;
+      Layout l;
+      if (ctas > d.sms * 7 / 8 || !layout(t, nmax, FMT_BF16, (int)cdiv(ksteps, s), ad_mode, d.smem, &l)) continue;
+      if (l.stages * l.stage_bytes < nmax * 2 * t * 4) continue;
+      const double rate = std::min(45.0, 23.0 * d.sms / ctas);
+      const double cost = cdiv(ksteps, s) * std::max({t * 256.0 / rate, kSmallStep, 4.0 * nmax}) + 2500.0 + 1800.0;
+      if (cost < least * 0.98) {
+        least = cost;
+        split = s;
+        *rt = t;
+      }
+    }
+  }
+  return split;
 }
 
 struct Maps {
@@ -164,15 +194,19 @@ cudaError_t launch_gemm(GemmParams& p, int epi, int fmt, Maps& m, int64_t tiles,
   p.ad_off = l.ad_off;
   p.pdl = pdl;
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)std::min<int64_t>(d.sms, std::max<int64_t>(tiles, 1)));
+  p.split = std::max(1, p.split);
+  c.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : std::min<int64_t>(d.sms, std::max<int64_t>(tiles, 1))));
   c.blockDim = dim3(threads_of(fmt));
   c.dynamicSmemBytes = l.smem;
   c.stream = st;
-  cudaLaunchAttribute a[1];
+  cudaLaunchAttribute a[2];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = p.split;
+  a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
   c.attrs = a;
-  c.numAttrs = 1;
+  c.numAttrs = p.split > 1 ? 2 : 1;
   void* args[] = {&p, &m.w, &m.s, &m.x, &m.u};
   return cudaLaunchKernelExC(&c, k, args);
 }
@@ -524,7 +558,10 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
   g.R = c->outer;
   g.K = c->inner;
   const double entries = (double)cdiv(p.positions, p.nmax);
-  g.rt = choose_rt(c->outer, swiglu, entries, entries, p.nmax, fmt, p.nmax, ksteps, p.mode, d);
+  if (fmt == FMT_BF16 && p.mode != AD_STEPS && rows <= 64)
+    g.split = choose_split(c->outer, swiglu, (int)entries, p.nmax, ksteps, p.mode, d, &g.rt);
+  else
+    g.rt = choose_rt(c->outer, swiglu, entries, entries, p.nmax, fmt, p.nmax, ksteps, p.mode, d);
   g.nrb = (int)cdiv(c->outer, swiglu ? g.rt : 2 * g.rt);
   g.groups_main = 1;
   g.wscale = wt->w_scale;
@@ -544,7 +581,7 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
     return MOE_ERR_CUDA;
   m.s = m.u = m.w;
   Layout l, la;
-  if (!layout(g.rt, p.nmax, fmt, ksteps, p.mode, d.smem, &l)) return MOE_ERR_UNSUPPORTED;
+  if (!layout(g.rt, p.nmax, fmt, (int)cdiv(ksteps, std::max(1, g.split)), p.mode, d.smem, &l)) return MOE_ERR_UNSUPPORTED;
 
   cudaError_t e = cudaSuccess;
   g.ad_mode = p.mode;

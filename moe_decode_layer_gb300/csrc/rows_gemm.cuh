@@ -123,6 +123,22 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
          ((uint64_t)2 << 61);
 }
 
+// All threads of the cluster's CTAs; their shared memory is in order afterwards.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// A float at this CTA's shared address in the CTA of rank r of its cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t r) {
+  float v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
+      : "=f"(v)
+      : "r"(addr), "r"(r)
+      : "memory");
+  return v;
+}
+
 // Waits for a phase of an mbarrier, at most kWaitLimit probes of up to a
 // microsecond each; false when the limit or another warp's (*abort) ended the wait.
 // (Probes are counted: reading the global timer in this loop cost more than a stage.)
@@ -330,6 +346,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 
   const int ntiles = num_tiles(p);
   const int main_steps = (p.K + 63) / 64;
+  // Few rows: the CTAs of a cluster take parts of K of one tile, and the sums are
+  // joined through distributed shared memory. (A step costs the tensor core about
+  // 390 clocks however few rows there are: 40 of them one after another were most
+  // of a decoding projection's time.)
+  const int split = FMT == FMT_BF16 ? p.split : 1;
+  const int part_of = split > 1 ? blockIdx.x % split : 0;
+  const int k_first = main_steps * part_of / split, k_last = main_steps * (part_of + 1) / split;
+  const int t_first = split > 1 ? blockIdx.x / split : blockIdx.x;
+  const int t_step = split > 1 ? ntiles : gridDim.x;
   const int a_half = p.rt * 128;  // bytes of a sub-tile of a stage
   const uint32_t stage_bytes = p.stage_bytes;
   const bool ad_steps = p.ad_mode == AD_STEPS;
@@ -346,7 +371,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     if (lane == 0) {
       Ring it, rit;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+      for (int t = t_first; ok && t < ntiles; t += t_step) {
         const Tile tl = tile_at(p, t);
         const bool sh = tl.g >= p.groups_main;
         const CUtensorMap* m = sh ? &map_s : &map_w;
@@ -354,7 +379,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const int y0 = tl.rb * sub_rows;
         const int y1 = EPI == EPI_SWIGLU ? y0 : y0 + p.rt, z1 = EPI == EPI_SWIGLU ? 1 : 0;
         if (FMT == FMT_BF16) {
-          for (int k = 0; k < main_steps; k++, it.next(p.stages)) {
+          for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
             const uint32_t s = it.slot;
             if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
             const uint32_t dst = base + s * stage_bytes;
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     if (lane == 0) {
       Ring it, acc;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, acc.next(nbuf)) {
+      for (int t = t_first; ok && t < ntiles; t += t_step, acc.next(nbuf)) {
         const Tile tl = tile_at(p, t);
         const int b = acc.slot;
         if (!(ok = wait_phase(tempty(b), acc.parity ^ 1, &s_abort))) break;
@@ -436,7 +461,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           it.next(p.stages);
           return true;
         };
-        for (int k = 0; ok && k < main_steps; k++) ok = step(0, tl.n, k == 0, true);
+        for (int k = k_first; ok && k < k_last; k++) ok = step(0, tl.n, k == k_first, true);
         if (ok && ad_steps)
           for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
                a = adapter_next(p, a + 1, tl.p0, tl.n)) {
@@ -457,7 +482,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     // ---------------------------------------------------------------- rows of x
     Ring it;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+    for (int t = t_first; ok && t < ntiles; t += t_step) {
       const Tile tl = tile_at(p, t);
       // a group that every row belongs to has its rows in x's own order (map_u)
       const bool all = p.all_rows && tl.g >= p.groups_main;
@@ -478,7 +503,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
       }
       const uint32_t bytes = copies * (listed ? 512u : p.box_rows * 128u);
-      for (int k = 0; k < main_steps; k++, it.next(p.stages)) {
+      for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
         const uint32_t s = it.slot;
         if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
         if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
@@ -520,7 +545,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     Ring acc;
     uint32_t tcount = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, tcount++, acc.next(nbuf)) {
+    for (int t = t_first; ok && t < ntiles; t += t_step, tcount++, acc.next(nbuf)) {
       const Tile tl = tile_at(p, t);
       const int b = acc.slot;
       if (p.ad_mode == AD_EPILOGUE) {
@@ -529,6 +554,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         bar_sync(1, 32 * epilogue_warps(FMT));  // the last tile's products are read
         for (int i = tid - 128; i < tl.n * 2 * p.rt; i += 32 * epilogue_warps(FMT)) {
           const int c = i / (2 * p.rt), wr = i % (2 * p.rt);
+          if (split > 1 && c % split != part_of) continue;  // another CTA joins that column
           const int sub = wr >= p.rt;
           const int y = tl.rb * sub_rows + (EPI == EPI_SWIGLU ? wr - sub * p.rt : wr);
           const int a = __ldg(p.ids + tl.p0 + c);
@@ -547,7 +573,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           s_ad[i] = v;
         }
       }
-      if (EPI != EPI_SWIGLU && p.addend) {  // the tile's addends on their way to L2
+      if (EPI != EPI_SWIGLU && p.addend && split == 1) {  // the tile's addends on their way to L2
         const int first = tl.rb * sub_rows, cols = min(2 * p.rt, p.R - first);
         const int lines = (cols * 2 + 127) / 128 + 1;
         for (int i = tid - 128; i < tl.n * lines; i += 32 * epilogue_warps(FMT)) {
@@ -583,7 +609,24 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       } else if (EPI == EPI_BF16 && FMT == FMT_BF16 && p.gscale) {
         g0 = g1 = __ldg(p.gscale + tl.g);
       }
-      if (q * 32 < p.rt) {
+      if (split > 1 && q * 32 < p.rt) {
+        // the partial sums, [column][weight row], where the stages were: all are used
+        for (int c = c0; c < tl.n; c += 2 * epilogue_warps(FMT)) {
+          uint32_t v0[8], v1[8];
+          __syncwarp();
+          tmem_ld8(d0 + c, v0);
+          tmem_ld8(d1 + c, v1);
+          tmem_ld_wait();
+          const uint32_t at = base + (uint32_t)(c * 2 * p.rt + r) * 4u;
+          if (r < p.rt)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+              if (c + j < tl.n) {
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + j * 8 * p.rt), "r"(v0[j]) : "memory");
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + j * 8 * p.rt + 4 * p.rt), "r"(v1[j]) : "memory");
+              }
+        }
+      } else if (q * 32 < p.rt) {
         const int y0 = tl.rb * sub_rows + r;
         const int y1 = y0 + p.rt;
         const bool ok0 = r < p.rt && y0 < p.R, ok1 = EPI != EPI_SWIGLU && r < p.rt && y1 < p.R;
@@ -689,7 +732,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     const int row = sub * p.rt + rr;
     Ring it, rit;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
+    for (int t = t_first; ok && t < ntiles; t += t_step) {
       const Tile tl = tile_at(p, t);
       const bool sh = tl.g >= p.groups_main;
       const int g = sh ? tl.g - p.groups_main : tl.g;
@@ -804,6 +847,38 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
   }
 
+  if (split > 1) {
+    // Each CTA joins every split-th column, in the order of the parts. All threads
+    // come here, whatever became of their waits.
+    __syncwarp();
+    cluster_sync();
+    if (p.pdl) pdl_wait();  // (addends may be of the launch before)
+    const Tile tl = tile_at(p, min(t_first, ntiles - 1));
+    const int rows_out = EPI == EPI_SWIGLU ? p.rt : 2 * p.rt;
+    const int cols = (tl.n - part_of + split - 1) / split;
+    const float* s_ad = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + p.ad_off);
+    for (int i = tid; i < cols * rows_out; i += threads_of(FMT)) {
+      const int c = part_of + i / rows_out * split, wr = i % rows_out;
+      const int y = tl.rb * rows_out + wr;
+      if (y >= p.R) continue;
+      const int at = c * 2 * p.rt + wr;
+      float a0 = 0.0f, a1 = 0.0f;
+      for (int k = 0; k < split; k++) {
+        a0 += ld_cluster(base + at * 4u, k);
+        if (EPI == EPI_SWIGLU) a1 += ld_cluster(base + (at + p.rt) * 4u, k);
+      }
+      if (p.ad_mode == AD_EPILOGUE) {
+        a0 += s_ad[at];
+        if (EPI == EPI_SWIGLU) a1 += s_ad[at + p.rt];
+      }
+      const size_t o = (size_t)(tl.p0 + c) * p.out_stride + y;
+      if (EPI != EPI_SWIGLU && p.addend) a0 += __bfloat162float(p.addend[o]);
+      if (EPI == EPI_SWIGLU) a0 = silu_mul(a0, a1);
+      if (EPI == EPI_F32) reinterpret_cast<float*>(p.out)[o] = a0;
+      else reinterpret_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a0);
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();

@@ -93,6 +93,7 @@ struct GemmParams {
   int raw_off;
   int raw_slots;
   int pdl;
+  int split;  // CTAs of a cluster that share a tile's K (bf16 weights, uniform tiles, no AD_STEPS)
 };
 
 const void* gemm_kernel(int epi, int fmt);
