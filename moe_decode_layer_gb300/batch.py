@@ -39,35 +39,37 @@ def _need(cond: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _tensor(t: torch.Tensor, name: str, dtype, shape, device) -> int:
-    """The address of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}: got "
+def _tensor(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of this type, shape and device index (-1: the CPU)."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on device {dev}: got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, cols: int, device) -> tuple[int, int]:
-    """(address, row stride) of a bf16 [T, cols] tensor whose rows are contiguous."""
-    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 2 or t.shape[1] != cols or \
-            (t.shape[0] and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a bf16 [rows, {cols}] tensor on {device} with contiguous rows: got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _rows(t: torch.Tensor, name: str, cols: int, dev: int) -> tuple[int, int, int]:
+    """(address, rows, row stride) of a bf16 [T, cols] tensor whose rows are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or len(shape) != 2 or shape[1] != cols or \
+            (shape[0] and stride[1] != 1):
+        raise ValueError(f"{name} must be a bf16 [rows, {cols}] tensor on device {dev} with contiguous rows: got "
+                         f"{t.dtype} {tuple(shape)} on {t.device}")
     # one row, or none, has no stride of its own
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
+    return t.data_ptr(), shape[0], stride[0] if shape[0] > 1 else cols
 
 
-def _enter(device: torch.device, stream):
-    """(stream handle, what to leave): makes ``device`` the current one while the
+def _enter(dev: int, stream):
+    """(stream handle, what to leave): makes device ``dev`` the current one while the
     library is called, and ``stream`` the one that results and workspaces are allocated
     for. The usual call, on the current device and stream, has nothing to leave."""
-    _need(device.type == "cuda", "tensors must be on a CUDA device")
-    if stream is None and device.index == torch._C._cuda_getDevice():
-        return torch._C._cuda_getCurrentRawStream(device.index), None
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None and dev == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(dev), None
     stack = contextlib.ExitStack()
-    stack.enter_context(torch.cuda.device(device))
+    stack.enter_context(torch.cuda.device(dev))
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        stream = torch.cuda.current_stream(dev)
     else:
         stack.enter_context(torch.cuda.stream(stream))
     return stream.cuda_stream, stack
@@ -89,20 +91,29 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: tor
     """The chosen experts of each row of ``logits`` (bf16 or fp32 [T, E], any row
     stride) and their weights: (int32 [T, k], fp32 [T, k]), as moe_decode_route
     documents. ``score``: "softmax" or "sigmoid"; ``bias`` fp32 [E]."""
-    _need(logits.dim() == 2 and logits.dtype in _DTYPES, "logits must be a bf16 or fp32 [rows, experts] tensor")
+    dtype = logits.dtype
+    if logits.dim() != 2 or dtype not in _DTYPES:
+        raise ValueError("logits must be a bf16 or fp32 [rows, experts] tensor")
     t, e = logits.shape
     row, col = logits.stride()
-    _need(t == 0 or e == 1 or col == 1, "a row of logits must be contiguous")
-    cfg = _route_config(e, top_k, score, num_groups, top_groups, group_best, bool(renormalise), logits.dtype, scale)
-    dev = logits.device
+    if col != 1 and t and e != 1:
+        raise ValueError("a row of logits must be contiguous")
+    cfg = _route_config(e, top_k, score, num_groups, top_groups, group_best, bool(renormalise), dtype, scale)
+    dev = logits.get_device()
     b = None if bias is None else _tensor(bias, "bias", torch.float32, (e,), dev)
     s, leave = _enter(dev, stream)
     try:
-        idx = torch.empty((t, top_k), dtype=torch.int32, device=dev) if idx is None else idx
-        w = torch.empty((t, top_k), dtype=torch.float32, device=dev) if w is None else w
-        st = _lib.load().moe_decode_route(cfg, logits.data_ptr(), row if t > 1 else e, b, t,
-                                          _tensor(idx, "idx", torch.int32, (t, top_k), dev),
-                                          _tensor(w, "w", torch.float32, (t, top_k), dev), s)
+        if idx is None:
+            idx = torch.empty((t, top_k), dtype=torch.int32, device=dev)
+            pi = idx.data_ptr()
+        else:
+            pi = _tensor(idx, "idx", torch.int32, (t, top_k), dev)
+        if w is None:
+            w = torch.empty((t, top_k), dtype=torch.float32, device=dev)
+            pw = w.data_ptr()
+        else:
+            pw = _tensor(w, "w", torch.float32, (t, top_k), dev)
+        st = _lib.load().moe_decode_route(cfg, logits.data_ptr(), row if t > 1 else e, b, t, pi, pw, s)
     finally:
         if leave is not None:
             leave.close()
@@ -125,27 +136,38 @@ _SUFFIX = {"bf16": ("",), "fp8": ("_q", "_s"), "nvfp4": ("_q", "_s", "_gs")}
 _FIELDS = {"": "", "_q": "", "_s": "_scale", "_gs": "_gscale"}
 
 
-def expert_weights(shape: LayerShape, weights: dict, device) -> _lib.Weights:
-    """The C struct of a layer's routed and shared expert weights (dict layout of synth.make_layer)."""
-    _need(weights.get("w2_layout", "h_i") == "h_i", "down matrices must be stored [E, H, I] (w2_layout h_i)")
+@functools.lru_cache(maxsize=64)
+def _expert_tensors(shape: LayerShape) -> tuple:
+    """(key in a layer's dict, field of the C struct, type, size) of each weight tensor."""
     h, i = shape.hidden, shape.inter
+    return tuple((prefix + name + sfx, prefix + name + _FIELDS[sfx], dtype, size)
+                 for prefix, n in (("", shape.num_experts), ("sh_", shape.num_shared)) if n
+                 for name, rows, cols, halves in (("w13", 2 * i, h, 2), ("w2", h, i, 1))
+                 for sfx, (dtype, size) in zip(_SUFFIX[shape.wdtype],
+                                               _quantised(shape.wdtype, (n,), rows, cols, halves)))
+
+
+def expert_weights(shape: LayerShape, weights: dict, device) -> _lib.Weights:
+    """The C struct of a layer's routed and shared expert weights (dict layout of
+    synth.make_layer) on ``device`` (an index or a torch device)."""
+    if weights.get("w2_layout", "h_i") != "h_i":
+        raise ValueError("down matrices must be stored [E, H, I] (w2_layout h_i)")
+    dev = device if isinstance(device, int) else -1 if device.type == "cpu" else device.index
     out = _lib.Weights()
-    for prefix, n in (("", shape.num_experts), ("sh_", shape.num_shared)):
-        if n == 0:
-            continue
-        for name, rows, cols, halves in (("w13", 2 * i, h, 2), ("w2", h, i, 1)):
-            for sfx, (dtype, size) in zip(_SUFFIX[shape.wdtype], _quantised(shape.wdtype, (n,), rows, cols, halves)):
-                key = prefix + name + sfx
-                _need(key in weights, f"weights lack {key}")
-                setattr(out, prefix + name + _FIELDS[sfx], _tensor(weights[key], key, dtype, size, device))
+    for key, field, dtype, size in _expert_tensors(shape):
+        t = weights.get(key)
+        if t is None:
+            raise ValueError(f"weights lack {key}")
+        setattr(out, field, _tensor(t, key, dtype, size, dev))
     return out
 
 
-def _workspace(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor:
+def _workspace(workspace: torch.Tensor | None, need: int, dev: int) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.device == device and
-          workspace.numel() >= need, f"the workspace must be a contiguous uint8 tensor of at least {need} bytes on {device}")
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev and
+          workspace.numel() >= need,
+          f"the workspace must be a contiguous uint8 tensor of at least {need} bytes on device {dev}")
     return workspace
 
 
@@ -176,9 +198,8 @@ def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: t
     [T, H], any row stride of a multiple of 8; ``idx`` int32 and ``w`` fp32 [T, k];
     an index outside the experts (-1) takes no part."""
     cfg = _experts_config(shape)
-    dev = x.device
-    px, sx = _rows(x, "x", shape.hidden, dev)
-    t = x.shape[0]
+    dev = x.get_device()
+    px, t, sx = _rows(x, "x", shape.hidden, dev)
     cw = weights if isinstance(weights, _lib.Weights) else expert_weights(shape, weights, dev)
     pi = _tensor(idx, "idx", torch.int32, (t, shape.top_k), dev)
     pw = _tensor(w, "w", torch.float32, (t, shape.top_k), dev)
@@ -187,10 +208,11 @@ def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: t
     try:
         if out is None:
             out = torch.empty((t, shape.hidden), dtype=torch.bfloat16, device=dev)
+            po = out.data_ptr()
+        else:
+            po = _tensor(out, "out", torch.bfloat16, (t, shape.hidden), dev)
         ws = _workspace(workspace, experts_workspace(shape, t), dev)
-        st = _lib.load().moe_decode_experts(cfg, cw, px, sx, pi, pw, pr,
-                                            _tensor(out, "out", torch.bfloat16, (t, shape.hidden), dev), t,
-                                            ws.data_ptr(), ws.numel(), s)
+        st = _lib.load().moe_decode_experts(cfg, cw, px, sx, pi, pw, pr, po, t, ws.data_ptr(), ws.numel(), s)
     finally:
         if leave is not None:
             leave.close()
@@ -209,13 +231,17 @@ def _project_config(wdtype: str, inner: int, outer: int, swiglu: bool, rank: int
 
 
 @functools.lru_cache(maxsize=1024)
+def _project_bytes(wdtype, inner, outer, swiglu, rank, num_adapters, out_dtype, rows) -> int:
+    n = ctypes.c_size_t()
+    cfg = _project_config(wdtype, inner, outer, swiglu, rank, num_adapters, out_dtype)
+    _lib.check(_lib.load().moe_decode_project_workspace(cfg, rows, n), "moe_decode_project_workspace")
+    return n.value
+
+
 def project_workspace(inner: int, outer: int, rows: int, *, wdtype: str = "bf16", swiglu: bool = False, rank: int = 0,
                       num_adapters: int = 0, out_dtype=torch.bfloat16) -> int:
     """Bytes of workspace that :func:`project` needs for at most ``rows`` rows."""
-    n = ctypes.c_size_t()
-    cfg = _project_config(wdtype, inner, outer, bool(swiglu), rank, num_adapters, out_dtype)
-    _lib.check(_lib.load().moe_decode_project_workspace(cfg, rows, n), "moe_decode_project_workspace")
-    return n.value
+    return _project_bytes(wdtype, inner, outer, bool(swiglu), rank, num_adapters, out_dtype, rows)
 
 
 def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters | None = None,
@@ -228,7 +254,7 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
     ([2 O, K] with swiglu), or for ``wdtype`` "fp8" / "nvfp4" the tuple (codes, block
     scales) / (codes, block scales, tensor scale [] or [2]). ``adapter_ids`` int32 [T]: the
     adapter of each row, outside 0..L-1 (-1) none."""
-    dev = x.device
+    dev = x.get_device()
     parts = weight if isinstance(weight, (tuple, list)) else (weight,)
     _need(x.dim() == 2, "x must be [rows, inner]")
     halves = 2 if swiglu else 1
@@ -244,28 +270,28 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
     if out is not None:
         out_dtype = out.dtype
     cfg = _project_config(wdtype, k, o, bool(swiglu), r, n, out_dtype)
-    px, sx = _rows(x, "x", k, dev)
+    px, _, sx = _rows(x, "x", k, dev)
     want = _quantised(wdtype, (), rows, k, halves)
     _need(len(parts) == len(want), f"a {wdtype} weight comes in {len(want)} tensors")
-    cw = _lib.ProjectWeights()
-    for field, t_, (dtype, size) in zip(("w", "w_scale", "w_gscale"), parts, want):
-        setattr(cw, field, _tensor(t_, field, dtype, size, dev))
-    ids = None
+    pw = [_tensor(t_, "weight", dtype, size, dev) for t_, (dtype, size) in zip(parts, want)] + [None, None]
+    ids = a = b = scale = None
     if adapters is not None:
-        cw.a = _tensor(adapters.a, "adapters.a", torch.bfloat16, (n, r, k), dev)
-        cw.b = _tensor(adapters.b, "adapters.b", torch.bfloat16, (n, rows, r), dev)
+        a = _tensor(adapters.a, "adapters.a", torch.bfloat16, (n, r, k), dev)
+        b = _tensor(adapters.b, "adapters.b", torch.bfloat16, (n, rows, r), dev)
         if adapters.scale is not None:
-            cw.scale = _tensor(adapters.scale, "adapters.scale", torch.float32, (n,), dev)
+            scale = _tensor(adapters.scale, "adapters.scale", torch.float32, (n,), dev)
         ids = _tensor(adapter_ids, "adapter_ids", torch.int32, (t,), dev)
+    cw = _lib.ProjectWeights(pw[0], pw[1], pw[2], a, b, scale)
     pa = None if addend is None else _tensor(addend, "addend", torch.bfloat16, (t, o), dev)
     s, leave = _enter(dev, stream)
     try:
         if out is None:
             out = torch.empty((t, o), dtype=out_dtype, device=dev)
-        ws = _workspace(workspace, project_workspace(k, o, t, wdtype=wdtype, swiglu=swiglu, rank=r, num_adapters=n,
-                                                     out_dtype=out_dtype), dev)
-        st = _lib.load().moe_decode_project(cfg, cw, px, sx, ids, pa, _tensor(out, "out", out_dtype, (t, o), dev), t,
-                                            ws.data_ptr(), ws.numel(), s)
+            po = out.data_ptr()
+        else:
+            po = _tensor(out, "out", out_dtype, (t, o), dev)
+        ws = _workspace(workspace, _project_bytes(wdtype, k, o, bool(swiglu), r, n, out_dtype, t), dev)
+        st = _lib.load().moe_decode_project(cfg, cw, px, sx, ids, pa, po, t, ws.data_ptr(), ws.numel(), s)
     finally:
         if leave is not None:
             leave.close()
@@ -276,7 +302,7 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
 
 def status(workspace: torch.Tensor, stream=None) -> int:
     """Synchronise and return the status code of the last call that used ``workspace``."""
-    s, leave = _enter(workspace.device, stream)
+    s, leave = _enter(workspace.get_device(), stream)
     try:
         return _lib.load().moe_decode_rows_status(workspace.data_ptr(), s)
     finally:

@@ -80,10 +80,19 @@ struct Device {
   int sms = 0, smem = 0, id = 0;
 };
 bool device(Device* d) {
-  return cudaGetDevice(&d->id) == cudaSuccess &&
-         cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) == cudaSuccess &&
-         cudaDeviceGetAttribute(&d->smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, d->id) == cudaSuccess &&
-         d->sms <= kMaxSms;
+  static std::atomic<uint64_t> known[64];  // per device: SMs, then shared memory; they do not change
+  if (cudaGetDevice(&d->id) != cudaSuccess) return false;
+  uint64_t v = d->id < 64 ? known[d->id].load(std::memory_order_relaxed) : 0;
+  if (!v) {
+    if (cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d->smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, d->id) != cudaSuccess)
+      return false;
+    v = (uint64_t)d->sms << 32 | (uint32_t)d->smem;
+    if (d->id < 64) known[d->id].store(v, std::memory_order_relaxed);
+  }
+  d->sms = (int)(v >> 32);
+  d->smem = (int)(uint32_t)v;
+  return d->sms <= kMaxSms;
 }
 
 // Shared memory of a launch: stages (and raw slots) for tiles of 2 rt x nmax.
@@ -122,7 +131,7 @@ constexpr double kSmallStep = 390.0;  // clocks of a step's eight products with 
 // Rows of a sub-tile. A tile costs, per 64 k, the larger of its weight bytes (an
 // SM's share of the HBM rate is about 23 bytes a clock), its operand bytes (about 55
 // a clock from L2) and its tensor time (a sub-tile takes 2 n16 clocks whatever rt
-// is), and a fixed share for its start and epilogue. The tiles go round the SMs in
+// is), and its start and epilogue (45 clocks a column). The tiles go round the SMs in
 // waves: rt is what makes the sum least. It is a multiple of 16 (or 8, when that
 // little is wanted): a warp's results then start on a 32-byte sector, and stores of
 // part of a sector cost more than the product (rt = 104 against 112: 575 against ...).
@@ -139,7 +148,7 @@ int choose_rt(int64_t R, bool swiglu, double entries, double reuse, int n, int f
     const double waves = std::ceil(entries * (double)nrb / d.sms);
     const double step =
         std::max({rt * bytes / (23.0 * reuse), (rt * 256.0 + n * 128.0) / 55.0, kSmallStep, 4.0 * n});
-    const double cost = waves * (ksteps * step + 2500.0);
+    const double cost = waves * (ksteps * step + 1500.0 + 45.0 * n);
     if (cost < least * 0.999) {
       least = cost;
       best = rt;
@@ -548,7 +557,7 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
   if (!device(&d)) return MOE_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const ProjectPlan p = project_plan(*c, rows);
+  ProjectPlan p = project_plan(*c, rows);
   int* status = reinterpret_cast<int*>(ws + p.status);
   const bool swiglu = c->swiglu != 0;
   const int epi = swiglu ? EPI_SWIGLU : c->out_dtype == MOE_F32 ? EPI_F32 : EPI_BF16;
@@ -557,6 +566,21 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
   GemmParams g = {};
   g.R = c->outer;
   g.K = c->inner;
+  if (fmt == FMT_BF16 && p.nmax > 128) {
+    // many rows: the tile width that fills the last round of tiles best
+    double least = 1e300;
+    int best = p.nmax;
+    for (int n = kMaxN; n >= 96; n -= 16) {
+      double cost;
+      const double e = (double)cdiv(rows, n);
+      choose_rt(c->outer, swiglu, e, e, n, fmt, n, ksteps, p.mode, d, &cost);
+      if (cost < least * 0.995) {
+        least = cost;
+        best = n;
+      }
+    }
+    p.nmax = best;
+  }
   const double entries = (double)cdiv(p.positions, p.nmax);
   if (fmt == FMT_BF16 && p.mode != AD_STEPS && rows <= 64)
     g.split = choose_split(c->outer, swiglu, (int)entries, p.nmax, ksteps, p.mode, d, &g.rt);
