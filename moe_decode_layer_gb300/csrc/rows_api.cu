@@ -306,7 +306,8 @@ ProjectPlan project_plan(const moe_project_config& c, int64_t rows) {
   };
   p.status = take((size_t)kStatusKernels * kMaxSms * 4);
   if (p.mode == AD_STEPS) {
-    p.nmax_a = std::max(16, std::min(128, round16(2.0 * rows / used)));
+    // A x is thin: enough tiles for every SM come from the rows
+    p.nmax_a = std::max(32, std::min(128, round16(rows / 140.0)));
     p.off = take((size_t)(c.num_adapters + 2) * 4);
     p.nent = take(4);
     p.ents = take((size_t)(cdiv(rows, 16) + c.num_adapters) * sizeof(int4));

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kCombineThreads)
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s) {
   cudaLaunchConfig_t c = {};
-  const int ctas = p.pairs > 8192 ? kPlanCtas : 1;
+  const int ctas = p.pairs > 2048 ? kPlanCtas : 1;
   c.gridDim = dim3(ctas);
   c.blockDim = dim3(kPlanThreads);
   c.stream = s;
