@@ -104,6 +104,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t v;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(v));
+  return v != 0;
+}
 // Arrives on bar when all earlier tcgen05.mma of this thread have completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -422,13 +428,16 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- tensor core
-    if (lane == 0) {
+    // The whole warp walks the loop and one lane issues: addresses and descriptors
+    // stay uniform values, which the instructions take from uniform registers.
+    {
+      const bool leader = elect_one();
       Ring it, acc;
       bool ok = true;
       for (int t = t_first; ok && t < ntiles; t += t_step, acc.next(nbuf)) {
         const Tile tl = tile_at(p, t);
         const int b = acc.slot;
-        if (!(ok = wait_phase(tempty(b), acc.parity ^ 1, &s_abort))) break;
+        if (!(ok = warp_wait(tempty(b), acc.parity ^ 1, &s_abort))) break;
         tc_fence_after();
         // fp32 accumulators, bf16 x bf16, both K-major, M = 128
         constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
@@ -436,11 +445,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         // one stage into the accumulators of n rows from the tile's row c on
         auto step = [&](int c, int n, bool first, bool main) {
           const uint32_t s = it.slot;
-          if (!wait_phase(full(s), it.parity, &s_abort)) return false;
+          if (!warp_wait(full(s), it.parity, &s_abort)) return false;
           tc_fence_after();
           const uint32_t idesc = kDesc | ((uint32_t)((n + 15) >> 4) << 18);
           const uint32_t a = base + s * stage_bytes, bb = a + b_off + c * 128;
           const uint64_t da = smem_desc(a), db = smem_desc(bb), da1 = smem_desc(a + a_half);
+          if (leader) {
           if (FMT != FMT_BF16 && main) {
             const uint32_t ta = a_tmem + s * 64;
 #pragma unroll
@@ -458,6 +468,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             }
           }
           mma_commit(empty(s));
+          }
+          __syncwarp();
           it.next(p.stages);
           return true;
         };
@@ -469,9 +481,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const int c1 = min(__ldg(p.adapter_off + a + 1) - tl.p0, tl.n);
             for (int k = 0; ok && k < per_adapter; k++) ok = step(c0, c1 - c0, false, false);
           }
-        if (ok) mma_commit(tfull(b));
+        if (ok && leader) mma_commit(tfull(b));
       }
-      if (!ok) {
+      if (!ok && leader) {
         mma_commit(drain);
         const uint64_t t0 = global_ns();
         while (!mbar_try_wait(drain, 0) && global_ns() - t0 < kDrainNs) {
