@@ -149,6 +149,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t r) {
 // microsecond each; false when the limit or another warp's (*abort) ended the wait.
 // (Probes are counted: reading the global timer in this loop cost more than a stage.)
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_test_wait(bar, parity)) return true;
   for (uint32_t i = 0; i < kWaitLimit; i++) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63) == 63 && *abort) return false;
