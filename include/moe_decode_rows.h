@@ -52,6 +52,7 @@ typedef enum moe_route_score {
  * A logit that is NaN or at most -1e38 masks its expert (-inf and the lowest
  * bf16 / fp32 value do): it is never chosen. A row with fewer than top_k experts
  * to choose from fills up with index -1 and weight 0. Logits above 3e38 count as 3e38.
+ * An expert whose bias is -inf or NaN is not chosen either.
  * Supported: 1 <= E <= 1024, top_k <= 16, num_groups <= 32 and dividing E,
  * top_k <= top_groups * E / num_groups.
  */

@@ -126,16 +126,18 @@ bool layout(int rt, int nmax, int fmt, int ksteps, int ad_mode, int smem_max, La
   return l->stages >= 2;
 }
 
-constexpr double kSmallStep = 390.0;  // clocks of a step's eight products with few rows of x
+// Clocks of a step with few rows of x: its waits and eight products. (200 in its place
+// chooses smaller tiles and measured the same within the noise.)
+constexpr double kSmallStep = 390.0;
 
 // Rows of a sub-tile. A tile costs, per 64 k, the larger of its weight bytes (an
 // SM's share of the HBM rate is about 23 bytes a clock), its operand bytes (about 55
 // a clock from L2) and its tensor time (a sub-tile takes 2 n16 clocks whatever rt
 // is), and its start and epilogue (45 clocks a column). The tiles go round the SMs in
 // waves: rt is what makes the sum least. It is a multiple of 16 (or 8, when that
-// little is wanted): a warp's results then start on a 32-byte sector, and stores of
-// part of a sector cost more than the product (rt = 104 against 112: 575 against ...).
-// reuse: tiles that read the same weights.
+// little is wanted): a warp's results then start on a 32-byte sector. Stores of parts of
+// sectors cost more than the product (8192 rows over 64 experts: 2345 us with
+// rt = 104, 1870 us with 128). reuse: tiles that read the same weights.
 int choose_rt(int64_t R, bool swiglu, double entries, double reuse, int n, int fmt, int nmax, int ksteps, int ad_mode,
               const Device& d, double* cost_out = nullptr) {
   int best = 128;
@@ -206,7 +208,10 @@ cudaError_t launch_gemm(GemmParams& p, int epi, int fmt, Maps& m, int64_t tiles,
   p.split = std::max(1, p.split);
   c.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : std::min<int64_t>(d.sms, std::max<int64_t>(tiles, 1))));
   c.blockDim = dim3(threads_of(fmt));
-  c.dynamicSmemBytes = l.smem;
+  // All of the SM's shared memory, used or not: a CTA takes all of its tensor memory,
+  // and where CTAs of a cluster wait for one another none of them may wait for tensor
+  // memory that a CTA of another cluster on its SM holds.
+  c.dynamicSmemBytes = d.smem - 4096;
   c.stream = st;
   cudaLaunchAttribute a[2];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

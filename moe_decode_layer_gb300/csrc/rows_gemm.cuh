@@ -354,9 +354,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   const int ntiles = num_tiles(p);
   const int main_steps = (p.K + 63) / 64;
   // Few rows: the CTAs of a cluster take parts of K of one tile, and the sums are
-  // joined through distributed shared memory. (A step costs the tensor core about
-  // 390 clocks however few rows there are: 40 of them one after another were most
-  // of a decoding projection's time.)
+  // joined through distributed shared memory. (A step costs 200 to 400 clocks however
+  // few rows there are: 40 of them one after another were most of a decoding
+  // projection's time. 32 rows, K = 2560, 2 x 768 columns: 54 -> 46 us for a call alone.)
   const int split = FMT == FMT_BF16 ? p.split : 1;
   const int part_of = split > 1 ? blockIdx.x % split : 0;
   const int k_first = main_steps * part_of / split, k_last = main_steps * (part_of + 1) / split;

@@ -399,6 +399,43 @@ def test_project_strides_streams_and_graphs():
     assert torch.equal(out, batch.project(x, weight, adapters=ad, adapter_ids=ids))
 
 
+def test_project_of_few_rows_on_many_streams():
+    """Calls whose CTAs wait for one another (a tile's K shared in a cluster), several at once on the same SMs."""
+    g = _gen(14)
+    weight = (0.05 * _normal(g, 1536, 4096)).bfloat16()
+    ad = _adapters(g, 8, 16, 4096, 1536)
+    xs = [_normal(g, n, 4096).bfloat16() for n in (1, 7, 16, 40)]
+    ids = [torch.randint(-1, 8, (x.shape[0],), generator=g, device="cuda", dtype=torch.int32) for x in xs]
+    want = [_check_project(x, weight, adapters=ad, adapter_ids=i, swiglu=n % 2 == 1) for n, (x, i) in enumerate(zip(xs, ids))]
+    want32 = [_check_project(x, weight, out_dtype=torch.float32) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got, got32 = [], []
+        for n, st in enumerate(streams):
+            got.append(batch.project(xs[n], weight, adapters=ad, adapter_ids=ids[n], swiglu=n % 2 == 1, stream=st))
+            got32.append(batch.project(xs[n], weight, out_dtype=torch.float32, stream=st))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got + got32, want + want32))
+
+
+@pytest.mark.parametrize("bias", [math.inf, -math.inf, math.nan])
+def test_route_bias_not_finite(bias):
+    """An expert whose bias is +inf is chosen first; one whose bias is -inf or NaN is not to be had."""
+    g = _gen(15)
+    logits = _normal(g, 30, 96)
+    b = 0.1 * _normal(g, 96)
+    b[40] = bias
+    idx, w = batch.route(logits, 6, score="sigmoid", bias=b)
+    if bias == math.inf:
+        assert bool((idx[:, 0] == 40).all())
+    else:
+        masked = logits.clone()
+        masked[:, 40] = -math.inf
+        want = batch.route(masked, 6, score="sigmoid", bias=torch.where(torch.isfinite(b), b, torch.zeros_like(b)))
+        assert torch.equal(idx, want[0]) and torch.equal(w, want[1])
+
+
 # ------------------------------------------------------------------ the layer
 
 
