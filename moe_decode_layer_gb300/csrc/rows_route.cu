@@ -154,6 +154,33 @@ __device__ __noinline__ int choose64(const RouteParams& p, const T* src, double*
   return mine;
 }
 
+// Whether group b's value comes before group a's, in fp64: half a warp each. Sigmoid
+// scores, or softmax scores without a bias (times the row's common factor).
+template <typename T>
+__device__ __noinline__ bool border64(const RouteParams& p, const T* src, int a, int b, double top, int lane) {
+  const int g = lane < 16 ? a : b;
+  double b1 = -INFINITY, b2 = -INFINITY;
+  for (int i = lane & 15; i < p.group_size; i += 16) {
+    const int e = g * p.group_size + i;
+    const float l = clean(to_f32(src[e]));
+    double x = -INFINITY;
+    if (l > kMasked) {
+      x = p.softmax ? exp((double)l - top) : sigmoid64((double)l);
+      if (p.bias) x = fmax(x + (double)__ldg(p.bias + e), -INFINITY);
+    }
+    b2 = fmax(b2, fmin(b1, x));
+    b1 = fmax(b1, x);
+  }
+  for (int d = 8; d; d >>= 1) {
+    const double o1 = __shfl_xor_sync(0xffffffffu, b1, d), o2 = __shfl_xor_sync(0xffffffffu, b2, d);
+    b2 = fmax(fmax(b2, o2), fmin(b1, o1));
+    b1 = fmax(b1, o1);
+  }
+  const double v = p.best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+  const double va = __shfl_sync(0xffffffffu, v, 0), vb = __shfl_sync(0xffffffffu, v, 16);
+  return vb > va || (vb == va && b < a);
+}
+
 // The row's choice by K warp maxima over the logits: when so many tie at the bound
 // that they cannot all be listed. keep: bits of the groups in the choice.
 template <typename T>
@@ -269,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         const float s = p.softmax ? expf(l[j] - top) / norm : 1.0f / (1.0f + expf(-l[j]));
         const bool ok = l[j] > kMasked;
         smax = fmaxf(smax, ok ? s : 0.0f);
-        f[j] = ok ? s + __ldg(p.bias + e) : -INFINITY;
+        f[j] = ok ? fmaxf(s + __ldg(p.bias + e), -INFINITY) : -INFINITY;  // (a NaN bias: -inf)
       }
       if (e < E) s_key[e] = f[j];
     }
@@ -330,7 +357,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         const bool same = !bias && __shfl_sync(0xffffffffu, b1, i0) == __shfl_sync(0xffffffffu, b1, i1) &&
                           __shfl_sync(0xffffffffu, b2, i0) == __shfl_sync(0xffffffffu, b2, i1);
         const float big = fmaxf(fabsf(v0), fabsf(v1));
-        if (v1 > -INFINITY && !same) close_group = v0 - v1 <= (bias ? 2.0f * tol_s + 0x1p-21f * big : 0x1p-19f * big);
+        const float tol = bias ? 2.0f * tol_s + 0x1p-21f * big : 0x1p-19f * big;
+        if (v1 > -INFINITY && !same) close_group = v0 - v1 <= tol;
+        // the next ones on both sides: when they are clear, it is between these two alone
+        const bool near = lead && ((rank < p.kept - 1 && v - v1 <= tol) || (rank > p.kept && v0 - v <= tol));
+        if (close_group && !__any_sync(0xffffffffu, near) && !(p.softmax && bias)) {
+          const int ga = i0 / sub, gb = i1 / sub;
+          keep ^= border64(p, src, ga, gb, (double)top, lane) ? (1u << ga | 1u << gb) : 0u;
+          close_group = false;
+        }
       }
     }
     if (p.kept < p.groups) {

@@ -434,6 +434,10 @@ def test_route_bias_not_finite(bias):
         masked[:, 40] = -math.inf
         want = batch.route(masked, 6, score="sigmoid", bias=torch.where(torch.isfinite(b), b, torch.zeros_like(b)))
         assert torch.equal(idx, want[0]) and torch.equal(w, want[1])
+        kw = dict(score="sigmoid", num_groups=8, top_groups=2, group_best=2)
+        got = batch.route(logits, 6, bias=b, **kw)
+        want = batch.route(masked, 6, bias=torch.where(torch.isfinite(b), b, torch.zeros_like(b)), **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 # ------------------------------------------------------------------ the layer
