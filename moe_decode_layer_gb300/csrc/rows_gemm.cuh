@@ -20,11 +20,18 @@
 // rows four to a copy, neighbouring ones as a box), 4..11 epilogue; the quantised
 // formats add 8 warps that widen the codes to bf16, into tensor memory, from where the
 // tensor core takes them as its A operand. (Through shared memory a step moved
-// 92 to 108 KB there, 720 to 845 clocks at its 128 bytes a clock, and FP8 weights
-// streamed at 59 % of the HBM rate, NVFP4 at 22 %.) All copies are TMA
-// with the 128-byte swizzle of the operands, zero-filled past K. (A first version
-// gathered rows with 16-byte cp.async from four warps: with 256 rows a stage its
-// loop took 5900 clocks where the tensor core needs 1024.)
+// 92 to 108 KB there, 720 to 845 clocks at its 128 bytes a clock.) All copies are TMA
+// with the 128-byte swizzle of the operands, zero-filled past K. (Rows gathered with
+// 16-byte cp.async by four warps took 5900 clocks a step of 256 rows, where the tensor
+// core needs 1024.)
+//
+// What bounds it: with few rows for each weight (bf16) the weights' bytes -- 1001
+// rows over 512 experts of 2560 x 768, 6.07 GB, run at 6.8 to 7.0 TB/s; with many,
+// the tensor core beside an epilogue that it does not overlap (256 columns of two
+// sub-tiles fill tensor memory) -- 619 GFLOP of gate/up products, 8192 rows over 64
+// experts of 2048 x 1024, in 439 us, 1.41 PFLOP/s. FP8 (3.0 GB for 300 rows) runs at
+// 5.7 TB/s, NVFP4 (1.82 GB for 512 rows) at 2.1 TB/s: a widening warp's chain of
+// waits, conversions and stores, about 1000 clocks a step, where its bytes take 400.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -239,8 +246,8 @@ __device__ __forceinline__ int adapter_next(const GemmParams& p, int a, int p0, 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // Widening of quantised codes to the bf16 operand.
-// FP8: w = bf16(e4m3 * block scale): one rounding of the product (2^-9 relative,
-// 1/32 of the codes' own step); the tensor core takes bf16 operands with the bf16
+// FP8: w = bf16(e4m3 * block scale): one rounding of the product (at most 2^-8 of it,
+// 1/16 of the codes' own rounding); the tensor core takes bf16 operands with the bf16
 // rows of x, and a block scale of 128 k cannot be taken out of the sum over all k.
 __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float s) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
@@ -430,65 +437,60 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- tensor core
     // The whole warp walks the loop and one lane issues: addresses and descriptors
-    // stay uniform values, which the instructions take from uniform registers.
-    {
-      const bool leader = elect_one();
-      Ring it, acc;
-      bool ok = true;
-      for (int t = t_first; ok && t < ntiles; t += t_step, acc.next(nbuf)) {
-        const Tile tl = tile_at(p, t);
-        const int b = acc.slot;
-        if (!(ok = warp_wait(tempty(b), acc.parity ^ 1, &s_abort))) break;
+    // stay uniform values, which the instructions take from uniform registers (a step's
+    // eight products issue in 80 clocks; in a one-lane loop they took 390 to 550).
+    const bool leader = elect_one();
+    Ring it, acc;
+    bool ok = true;
+    for (int t = t_first; ok && t < ntiles; t += t_step, acc.next(nbuf)) {
+      const Tile tl = tile_at(p, t);
+      const int b = acc.slot;
+      if (!(ok = warp_wait(tempty(b), acc.parity ^ 1, &s_abort))) break;
+      tc_fence_after();
+      // fp32 accumulators, bf16 x bf16, both K-major, M = 128
+      constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
+      const uint32_t d0 = tmem + b * 2 * p.nmax, d1 = d0 + p.nmax;
+      // one stage into the accumulators of n rows from the tile's row c on
+      auto step = [&](int c, int n, bool first, bool main) {
+        const uint32_t s = it.slot;
+        if (!warp_wait(full(s), it.parity, &s_abort)) return false;
         tc_fence_after();
-        // fp32 accumulators, bf16 x bf16, both K-major, M = 128
-        constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
-        const uint32_t d0 = tmem + b * 2 * p.nmax, d1 = d0 + p.nmax;
-        // one stage into the accumulators of n rows from the tile's row c on
-        auto step = [&](int c, int n, bool first, bool main) {
-          const uint32_t s = it.slot;
-          if (!warp_wait(full(s), it.parity, &s_abort)) return false;
-          tc_fence_after();
-          const uint32_t idesc = kDesc | ((uint32_t)((n + 15) >> 4) << 18);
-          const uint32_t a = base + s * stage_bytes, bb = a + b_off + c * 128;
-          const uint64_t da = smem_desc(a), db = smem_desc(bb), da1 = smem_desc(a + a_half);
-          if (leader) {
-          if (FMT != FMT_BF16 && main) {
-            const uint32_t ta = a_tmem + s * 64;
+        const uint32_t idesc = kDesc | ((uint32_t)((n + 15) >> 4) << 18);
+        const uint32_t a = base + s * stage_bytes, bb = a + b_off + c * 128;
+        const uint64_t da = smem_desc(a), db = smem_desc(bb), da1 = smem_desc(a + a_half);
+        const uint32_t ta = a_tmem + s * 64;
+        if (leader) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-              const uint32_t acc = !first || j != 0;
-              mma_bf16_ta(d0, ta + 8 * j, db + 2 * j, idesc, acc);
-              mma_bf16_ta(d1, ta + 32 + 8 * j, db + 2 * j, idesc, acc);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-              const uint32_t acc = !first || j != 0;
-              mma_bf16(d0 + c, da + 2 * j, db + 2 * j, idesc, acc);
-              mma_bf16(d1 + c, da1 + 2 * j, db + 2 * j, idesc, acc);
+          for (int j = 0; j < 4; j++) {
+            const uint32_t more = !first || j != 0;
+            if (FMT != FMT_BF16 && main) {
+              mma_bf16_ta(d0, ta + 8 * j, db + 2 * j, idesc, more);
+              mma_bf16_ta(d1, ta + 32 + 8 * j, db + 2 * j, idesc, more);
+            } else {
+              mma_bf16(d0 + c, da + 2 * j, db + 2 * j, idesc, more);
+              mma_bf16(d1 + c, da1 + 2 * j, db + 2 * j, idesc, more);
             }
           }
           mma_commit(empty(s));
-          }
-          __syncwarp();
-          it.next(p.stages);
-          return true;
-        };
-        for (int k = k_first; ok && k < k_last; k++) ok = step(0, tl.n, k == k_first, true);
-        if (ok && ad_steps)
-          for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
-               a = adapter_next(p, a + 1, tl.p0, tl.n)) {
-            const int c0 = max(__ldg(p.adapter_off + a) - tl.p0, 0);
-            const int c1 = min(__ldg(p.adapter_off + a + 1) - tl.p0, tl.n);
-            for (int k = 0; ok && k < per_adapter; k++) ok = step(c0, c1 - c0, false, false);
-          }
-        if (ok && leader) mma_commit(tfull(b));
-      }
-      if (!ok && leader) {
-        mma_commit(drain);
-        const uint64_t t0 = global_ns();
-        while (!mbar_try_wait(drain, 0) && global_ns() - t0 < kDrainNs) {
         }
+        __syncwarp();
+        it.next(p.stages);
+        return true;
+      };
+      for (int k = k_first; ok && k < k_last; k++) ok = step(0, tl.n, k == k_first, true);
+      if (ok && ad_steps)
+        for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
+             a = adapter_next(p, a + 1, tl.p0, tl.n)) {
+          const int c0 = max(__ldg(p.adapter_off + a) - tl.p0, 0);
+          const int c1 = min(__ldg(p.adapter_off + a + 1) - tl.p0, tl.n);
+          for (int k = 0; ok && k < per_adapter; k++) ok = step(c0, c1 - c0, false, false);
+        }
+      if (ok && leader) mma_commit(tfull(b));
+    }
+    if (!ok && leader) {
+      mma_commit(drain);
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(drain, 0) && global_ns() - t0 < kDrainNs) {
       }
     }
   } else if (warp == 2) {

@@ -42,7 +42,8 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
 // pairs, read one another's counts through distributed shared memory, and give
 // out positions from their own part of each group. The order inside a group is that
 // of the atomics; no result depends on it (a row's sums are its own, and the
-// combine finds them through pos).
+// combine finds them through pos). 8008 pairs of 512 experts: 7 us; bound by its
+// chain of passes and barriers.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   __shared__ int s_count[kMaxGroups + 1];
   __shared__ int s_next[kMaxGroups + 1];
@@ -128,7 +129,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 
 constexpr int kSpreadWarps = 8;
 
-// One warp per position; the grouped product then copies its rows in boxes.
+// One warp per position; the grouped product then copies its rows in boxes. Bound by
+// the bytes written (and read from L2): 65536 positions of 2048 columns, 0.30 GB, 54 us.
 __global__ void __launch_bounds__(kSpreadWarps * 32)
     spread_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, const int* src_row, const int* count,
                   int inner, __nv_bfloat16* __restrict__ dst) {
@@ -155,7 +157,8 @@ __global__ void __launch_bounds__(kSpreadWarps * 32)
 constexpr int kShrinkWarps = 8;
 
 // One warp per (row, rank column): the adapter's row and the row of x, 16 bytes a
-// lane and load. For few rows: bound by the latency of one pass over K.
+// lane and load. For few rows: bound by the latency of one pass over K (32 rows, rank
+// 16, K = 2560: 7 us from cold caches).
 __global__ void __launch_bounds__(kShrinkWarps * 32)
     shrink_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, const __nv_bfloat16* __restrict__ a,
                   const float* __restrict__ scale, const int* __restrict__ ids, float* __restrict__ u, int inner,
@@ -185,7 +188,9 @@ __global__ void __launch_bounds__(kShrinkWarps * 32)
 
 constexpr int kCombineThreads = 256;
 
-// One thread per 4 columns of a row; y is fp32 and every y row is read once.
+// One thread per 4 columns of a row; y is fp32 and every y row is read once. Bound by
+// those bytes: 8192 rows of 9 x 2048, 0.67 GB in all, 109 us (6.1 TB/s). In bf16 they
+// would halve, and add the rounding of each of a row's terms to the sum's.
 __global__ void __launch_bounds__(kCombineThreads)
     combine_kernel(const float* __restrict__ y, const int* __restrict__ pos, const float* __restrict__ w,
                    const __nv_bfloat16* residual, __nv_bfloat16* out, int rows, int hidden, int top_k, int shared) {
