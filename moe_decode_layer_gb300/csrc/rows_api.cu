@@ -103,7 +103,7 @@ bool layout(int rt, int nmax, int fmt, int ksteps, int ad_mode, int smem_max, La
   const int a = 2 * rt * 128;
   // a quantised format's stages hold the rows of x alone, but for adapters' steps
   const bool a_smem = fmt == FMT_BF16 || ad_mode == AD_STEPS;
-  l->stage_bytes = (a_smem ? a : 0) + nmax * 128;
+  l->stage_bytes = (a_smem ? a : 0) + stage_steps(fmt) * nmax * 128;
   // 1024 for alignment, 4096 for the kernel's own; the tensor core reads whole
   // 128-row sub-tiles, so up to 16 KB past a short one's start
   const int slack = 1024 + 4096 + (a_smem ? std::max(0, 128 * 128 + rt * 128 - l->stage_bytes) : 0);
@@ -111,8 +111,8 @@ bool layout(int rt, int nmax, int fmt, int ksteps, int ad_mode, int smem_max, La
   int room = smem_max - slack - ad;
   l->raw_slots = 0;
   if (fmt != FMT_BF16) {
-    // as many stages as tensor memory holds (4 to 7), the rest for codes
-    const int most = (512 - acc_buffers(fmt, nmax) * 2 * nmax) / 64;
+    // as many stages as tensor memory holds (2 or 3), the rest for codes
+    const int most = (512 - acc_buffers(fmt, nmax) * 2 * nmax) / (64 * stage_steps(fmt));
     l->stages = std::min(most, a_smem ? (room - 2 * a) / l->stage_bytes : most);
     l->raw_slots = std::min(kMaxRaw, (room - l->stages * l->stage_bytes) / a);
     if (l->stages < 2 || l->raw_slots < 2) return false;

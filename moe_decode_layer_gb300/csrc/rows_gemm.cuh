@@ -374,9 +374,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   const bool ad_steps = p.ad_mode == AD_STEPS;
   const int per_adapter = ad_steps ? (p.rank + 63) / 64 : 0;
   // tensor memory: accumulators [buffer][sub-tile][nmax], then the quantised formats'
-  // widened weights [stage][sub-tile][32]
+  // widened weights [stage][step][sub-tile][32]
   const int nbuf = acc_buffers(FMT, p.nmax);
   const uint32_t a_tmem = tmem + nbuf * 2 * p.nmax;
+  // A stage of a quantised format holds two steps, so that its waits and arrivals, some
+  // 400 clocks of a widening warp's time, come half as often.
+  constexpr int kHalves = stage_steps(FMT);
+  const int half_bytes = p.nmax * 128;  // the rows of x of one step
   const int b_off = FMT == FMT_BF16 || ad_steps ? 2 * a_half : 0;  // the rows of x in a stage
   const int sub_rows = EPI == EPI_SWIGLU ? p.rt : 2 * p.rt;  // output rows per tile
 
@@ -458,15 +462,23 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const uint32_t idesc = kDesc | ((uint32_t)((n + 15) >> 4) << 18);
         const uint32_t a = base + s * stage_bytes, bb = a + b_off + c * 128;
         const uint64_t da = smem_desc(a), db = smem_desc(bb), da1 = smem_desc(a + a_half);
-        const uint32_t ta = a_tmem + s * 64;
         if (leader) {
+          if (FMT != FMT_BF16 && main) {
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const uint32_t more = !first || j != 0;
-            if (FMT != FMT_BF16 && main) {
-              mma_bf16_ta(d0, ta + 8 * j, db + 2 * j, idesc, more);
-              mma_bf16_ta(d1, ta + 32 + 8 * j, db + 2 * j, idesc, more);
-            } else {
+            for (int h = 0; h < kHalves; h++) {
+              const uint32_t ta = a_tmem + (s * kHalves + h) * 64;
+              const uint64_t dh = smem_desc(bb + h * half_bytes);
+#pragma unroll
+              for (int j = 0; j < 4; j++) {
+                const uint32_t more = !first || (h | j) != 0;
+                mma_bf16_ta(d0, ta + 8 * j, dh + 2 * j, idesc, more);
+                mma_bf16_ta(d1, ta + 32 + 8 * j, dh + 2 * j, idesc, more);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+              const uint32_t more = !first || j != 0;
               mma_bf16(d0 + c, da + 2 * j, db + 2 * j, idesc, more);
               mma_bf16(d1 + c, da1 + 2 * j, db + 2 * j, idesc, more);
             }
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         it.next(p.stages);
         return true;
       };
-      for (int k = k_first; ok && k < k_last; k++) ok = step(0, tl.n, k == k_first, true);
+      for (int k = k_first; ok && k < k_last; k += kHalves) ok = step(0, tl.n, k == k_first, true);
       if (ok && ad_steps)
         for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
              a = adapter_next(p, a + 1, tl.p0, tl.n)) {
@@ -517,18 +529,22 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           y[h] = make_int4(v[0], v[1], v[2], v[3]);
         }
       }
-      const uint32_t bytes = copies * (listed ? 512u : p.box_rows * 128u);
-      for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
+      const uint32_t bytes = kHalves * copies * (listed ? 512u : p.box_rows * 128u);
+      for (int k = k_first; k < k_last; k += kHalves, it.next(p.stages)) {
         const uint32_t s = it.slot;
         if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
         if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
         __syncwarp();
-        const uint32_t dst = base + s * stage_bytes + b_off;
-        if (listed) {
-          if (lane < copies) tma_gather4(dst + lane * 512, &map_x, k * 64, y[0], full(s));
-          if (lane + 32 < copies) tma_gather4(dst + (lane + 32) * 512, &map_x, k * 64, y[1], full(s));
-        } else if (lane < copies) {
-          tma_load_2d(dst + lane * p.box_rows * 128, mx, k * 64, y_box + lane * p.box_rows, full(s));
+#pragma unroll
+        for (int h = 0; h < kHalves; h++) {
+          const uint32_t dst = base + s * stage_bytes + b_off + h * half_bytes;
+          const int kx = (k + h) * 64;
+          if (listed) {
+            if (lane < copies) tma_gather4(dst + lane * 512, &map_x, kx, y[0], full(s));
+            if (lane + 32 < copies) tma_gather4(dst + (lane + 32) * 512, &map_x, kx, y[1], full(s));
+          } else if (lane < copies) {
+            tma_load_2d(dst + lane * p.box_rows * 128, mx, kx, y_box + lane * p.box_rows, full(s));
+          }
         }
       }
       if (ok && ad_steps) {
@@ -780,10 +796,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         if (!(ok = warp_wait(rfull(rs), rit.parity, &s_abort))) break;
         const uint32_t raw = base + p.raw_off + rs * (2 * a_half) + row * 128;
 #pragma unroll
-        for (int h = 0; h < kParts; h++, it.next(p.stages)) {
+        for (int h = 0; h < kParts; h++) {
           const uint32_t s = it.slot;
-          if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
-          tc_fence_after();
+          if (h % kHalves == 0) {
+            if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
+            tc_fence_after();
+          }
           uint4 codes[kChunks];
 #pragma unroll
           for (int q = 0; q < kChunks; q++)
@@ -828,11 +846,14 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
               }
             }
           }
-          tmem_st32(a_tmem + s * 64 + sub * 32 + lanes, o);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full(s), wt == 0 ? 2 : 1);  // thread 0: also in the weight copies' place
+          tmem_st32(a_tmem + (s * kHalves + h % kHalves) * 64 + sub * 32 + lanes, o);
+          if (h % kHalves == kHalves - 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full(s), wt == 0 ? 2 : 1);  // thread 0: also in the weight copies' place
+            it.next(p.stages);
+          }
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(rempty(rs), 1);

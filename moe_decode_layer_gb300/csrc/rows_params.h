@@ -38,8 +38,10 @@ __host__ __device__ constexpr int epilogue_warps(int fmt) { return 8; }
 // Accumulators at once: two while tensor memory (512 columns) has room for them, beside
 // the widened weights of a quantised format.
 __host__ __device__ constexpr int acc_buffers(int fmt, int nmax) {
-  return 4 * nmax <= (fmt == FMT_BF16 ? 512 : 256) ? 2 : 1;
+  return 4 * nmax <= (fmt == FMT_BF16 ? 512 : 128) ? 2 : 1;
 }
+// Steps of 64 k in a stage.
+__host__ __device__ constexpr int stage_steps(int fmt) { return fmt == FMT_BF16 ? 1 : 2; }
 constexpr int threads_of(int fmt) {
   return 128 + 32 * epilogue_warps(fmt) + (fmt == FMT_BF16 ? 0 : kWidenThreads);
 }
