@@ -30,8 +30,8 @@
 // the tensor core beside an epilogue that it does not overlap (256 columns of two
 // sub-tiles fill tensor memory) -- 619 GFLOP of gate/up products, 8192 rows over 64
 // experts of 2048 x 1024, in 439 us, 1.41 PFLOP/s. FP8 (3.0 GB for 300 rows) runs at
-// 5.7 TB/s, NVFP4 (1.82 GB for 512 rows) at 2.1 TB/s: a widening warp's chain of
-// waits, conversions and stores, about 1000 clocks a step, where its bytes take 400.
+// 6.7 TB/s, NVFP4 (1.82 GB for 512 rows) at 2.6 TB/s: a widening warp's chain of
+// waits, conversions and stores takes about 1000 clocks a step, where its bytes take 400.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -250,8 +250,12 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(
 // 1/16 of the codes' own rounding); the tensor core takes bf16 operands with the bf16
 // rows of x, and a block scale of 128 k cannot be taken out of the sum over all k.
 __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float s) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+  float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
+  // both products in one instruction (FP8 479 -> 451 us, NVFP4 747 -> 703 us)
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(f.x), "+f"(f.y)
+      : "f"(s));
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 __device__ __forceinline__ void fp8x4_bf16x4(uint32_t w, float s, uint32_t& o0, uint32_t& o1) {
@@ -273,26 +277,8 @@ __device__ __forceinline__ void fp4x8_f16x8(uint32_t w, uint32_t (&h)[4]) {
 // NVFP4: e2m1 * e4m3 has at most 6 significant bits: the bf16 operand is exact; the
 // tensor scale multiplies the fp32 sum. (Where adapters share the sum it is
 // multiplied into the weights, which are rounded to bf16 as FP8's are.)
-// Two ways to the same values keep both arithmetic pipes busy: conversions to fp16
-// and on to bf16 (per two codes 4 clocks of the integer pipe, 6 of the
-// floating-point pipe), and byte permutes (7.5 and 2); of four groups of codes one
-// takes the second.
-// Four codes (the low 16 bits of w): the bytes of the bf16 values of 0, 0.5, 1, 1.5,
-// 2, 3, 4, 6 come out of byte permutes with the codes as selectors; a permute's
-// selector with its top bit set replicates the byte's sign, which gives the signs.
-__device__ __forceinline__ void fp4x4_bf16x4(uint32_t w, __nv_bfloat162 s, uint32_t& o0, uint32_t& o1) {
-  const uint32_t m = w & 0x7777u;
-  const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, m);
-  const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, m);
-  uint32_t sg;  // __byte_perm takes three bits of a selector only
-  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sg) : "r"(0x80808080u), "r"(w));  // 0xff: negative, 0x80: not
-  const uint32_t h = hi | ((sg << 7) & 0x80808080u);
-  const uint32_t p0 = __byte_perm(lo, h, 0x5140), p1 = __byte_perm(lo, h, 0x7362);
-  const __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&p0), s);
-  const __nv_bfloat162 b = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&p1), s);
-  o0 = *reinterpret_cast<const uint32_t*>(&a);
-  o1 = *reinterpret_cast<const uint32_t*>(&b);
-}
+// (Byte permutes with the codes as selectors, for all or some of the codes, were
+// slower: 840 to 862 us against 803 for 512 rows at the time.)
 
 template <int EPI, int FMT>
 __global__ void __launch_bounds__(threads_of(FMT), 1)
@@ -819,30 +805,13 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             } else {
               const uint32_t hs = e4m3x2_to_f16x2(q ? f4[h & 3] >> 16 : f4[h & 3] & 0xffffu);
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hs));
-              if (!ad_steps) {
-                const __nv_bfloat162 s1 = __float2bfloat162_rn(f.y);
+              const float f0 = ad_steps ? f.x * ts : f.x, f1 = ad_steps ? f.y * ts : f.y;
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                  const int at = (kOut * q + 4 * j) & 31;
-                  if (j == 3) {
-                    fp4x4_bf16x4(w[j], s1, o[at], o[at + 1]);
-                    fp4x4_bf16x4(w[j] >> 16, s1, o[at + 2], o[at + 3]);
-                  } else {
-                    uint32_t v[4];
-                    fp4x8_f16x8(w[j], v);
+              for (int j = 0; j < 4; j++) {
+                uint32_t v[4];
+                fp4x8_f16x8(w[j], v);
 #pragma unroll
-                    for (int b = 0; b < 4; b++) o[at + b] = scaled_bf16x2(v[b], j < 2 ? f.x : f.y);
-                  }
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                  uint32_t v[4];
-                  fp4x8_f16x8(w[j], v);
-#pragma unroll
-                  for (int b = 0; b < 4; b++)
-                    o[(kOut * q + 4 * j + b) & 31] = scaled_bf16x2(v[b], (j < 2 ? f.x : f.y) * ts);
-                }
+                for (int b = 0; b < 4; b++) o[(kOut * q + 4 * j + b) & 31] = scaled_bf16x2(v[b], j < 2 ? f0 : f1);
               }
             }
           }
