@@ -117,9 +117,9 @@ moe_status moe_decode_experts(const moe_experts_config* cfg, const moe_decode_we
  * A projection that all rows share, with the rows' adapters beside it:
  *   y_t = W x_t + B_a (scale_a A_a x_t) (+ addend_t),  a = adapter_ids[t]
  *   out_t = y_t, or with swiglu silu(y_t[0..O)) * y_t[O..2O)
- * with fp32 sums, rounded once to out_dtype. With many rows scale_a A_a x_t is
- * rounded to bf16 (an operand of the tensor cores), and an NVFP4 weight to bf16 after
- * both its scales. Rows whose id is outside 0..num_adapters-1 have no adapter. Rows
+ * with fp32 sums, rounded once to out_dtype. With many rows scale_a A_a x_t is held
+ * as the sum of two bf16 numbers (operands of the tensor cores), and an NVFP4 weight
+ * is rounded to bf16 after both its scales. Rows whose id is outside 0..num_adapters-1 have no adapter. Rows
  * may come in any order. What an adapter holds reaches its own rows only.
  * Supported: inner % 8 == 0, outer % 8 == 0 (FP8: both % 128, NVFP4: % 256), <= 16384;
  * rank % 8 == 0, <= 256; num_adapters <= 1024 (0: no adapters, their arguments are not read).

@@ -293,13 +293,16 @@ struct ProjectPlan {
   int64_t positions = 0;  // rows, with AD_STEPS those of each adapter padded to 16
   size_t status = 0, off = 0, nent = 0, ents = 0, src_row = 0, u = 0, x = 0, bytes = 0;
 };
-// Adapters' rows go through the tensor core, 16 columns at least for each adapter,
-// when that pads little or there are many rows; else (decoding, where every row may
-// have its own) their products are fp32 sums in the epilogue.
+// Adapters' rows go through the tensor core, 16 columns at least for each adapter, when
+// that pads not too much or there are many rows; else (decoding, where every row may
+// have its own) their products are fp32 sums in the epilogue. 223 rows of 9 of 16 adapters
+// (K = 320, 2 x 1168 columns, rank 64): 46 us in the epilogue, 35 as steps; 900 rows of 30
+// of 64 (2048 to 4096, rank 64): 200 and 61.
+constexpr int64_t kMostEpilogue = 512;
 ProjectPlan project_plan(const moe_project_config& c, int64_t rows) {
   ProjectPlan p;
   const int64_t used = std::min<int64_t>(c.num_adapters, rows);
-  p.mode = !c.num_adapters ? AD_NONE : (rows >= 16 * used && rows > 64) || rows >= 1024 ? AD_STEPS : AD_EPILOGUE;
+  p.mode = !c.num_adapters ? AD_NONE : rows > 64 && (rows >= 4 * used || rows >= kMostEpilogue) ? AD_STEPS : AD_EPILOGUE;
   p.positions = p.mode == AD_STEPS ? rows + 15 * used : rows;
   p.nmax = std::max(16, std::min(p.mode == AD_EPILOGUE ? 64 : kMaxN, round16((double)p.positions)));
   if (fmt_of(c.wdtype) != FMT_BF16) p.nmax = std::min(p.nmax, 128);
@@ -317,7 +320,7 @@ ProjectPlan project_plan(const moe_project_config& c, int64_t rows) {
     p.nent = take(4);
     p.ents = take((size_t)(cdiv(rows, 16) + c.num_adapters) * sizeof(int4));
     p.src_row = take((size_t)p.positions * 4);
-    p.u = take((size_t)p.positions * c.rank * 2);
+    p.u = take((size_t)p.positions * c.rank * 4);
     p.x = take((size_t)p.positions * c.inner * 2);  // x in the adapters' order
   } else if (p.mode == AD_EPILOGUE) {
     p.u = take((size_t)rows * c.rank * 4);
@@ -530,7 +533,7 @@ moe_status moe_decode_project_workspace(const moe_project_config* c, int64_t row
     return MOE_OK;
   }
   // fewer rows may go the other way, whose fp32 products may need more
-  const int64_t few = std::min<int64_t>({rows, 1023, std::max<int64_t>(64, 16 * (int64_t)c->num_adapters - 1)});
+  const int64_t few = std::min<int64_t>({rows, kMostEpilogue - 1, std::max<int64_t>(64, 4 * (int64_t)c->num_adapters - 1)});
   const size_t status_bytes = up((size_t)kStatusKernels * kMaxSms * 4, 256);
   *bytes = std::max(project_plan(*c, rows).bytes,
                     c->num_adapters ? status_bytes + up((size_t)few * c->rank * 4, 256) : 0);
@@ -637,7 +640,7 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
     pl.src_row = reinterpret_cast<int*>(ws + p.src_row);
     pl.ents = reinterpret_cast<int4*>(ws + p.ents);
     pl.nent = reinterpret_cast<int*>(ws + p.nent);
-    // u = bf16(scale_a A_a x)
+    // u = scale_a A_a x, as two bf16 numbers
     GemmParams ga = {};
     ga.R = c->rank;
     ga.K = c->inner;
@@ -652,11 +655,12 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
     ga.ents = pl.ents;
     ga.nent = pl.nent;
     ga.out = ws + p.u;
-    ga.out_stride = c->rank;
+    ga.out_stride = 2 * c->rank;
+    ga.lo_off = c->rank;
     ga.status = status;
     if (!make_map(&ma.w, wt->a, FMT_BF16, c->inner, c->rank, 1, c->num_adapters, ga.rt) ||
         !make_map(&m.s, wt->b, FMT_BF16, c->rank, c->outer, swiglu ? 2 : 1, c->num_adapters, g.rt) ||
-        !make_rows_map(&m.u, ws + p.u, c->rank, p.positions, c->rank, 16))
+        !make_rows_map(&m.u, ws + p.u, 2 * c->rank, p.positions, 2 * c->rank, 16))
       return MOE_ERR_CUDA;
     if (!make_rows_map(&ma.x, ws + p.x, c->inner, p.positions, c->inner, ga.box_rows)) return MOE_ERR_CUDA;
     ma.s = ma.u = ma.w;

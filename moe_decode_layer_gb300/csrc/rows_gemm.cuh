@@ -358,7 +358,10 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   const int a_half = p.rt * 128;  // bytes of a sub-tile of a stage
   const uint32_t stage_bytes = p.stage_bytes;
   const bool ad_steps = p.ad_mode == AD_STEPS;
-  const int per_adapter = ad_steps ? (p.rank + 63) / 64 : 0;
+  // A row's products u = A x are two bf16 numbers each, u = hi + lo, so that they
+  // keep 16 bits: an adapter's steps are its rank's for hi, then again for lo.
+  const int rank_steps = ad_steps ? (p.rank + 63) / 64 : 0;
+  const int per_adapter = 2 * rank_steps;
   // tensor memory: accumulators [buffer][sub-tile][nmax], then the quantised formats'
   // widened weights [stage][step][sub-tile][32]
   const int nbuf = acc_buffers(FMT, p.nmax);
@@ -413,8 +416,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
               if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
               const uint32_t dst = base + s * stage_bytes;
               mbar_arrive_expect_tx(full(s), 2 * a_half);
-              tma_load_4d(dst, &map_s, k * 64, y0, 0, a, full(s));
-              tma_load_4d(dst + a_half, &map_s, k * 64, y1, z1, a, full(s));
+              const int kx = (k < rank_steps ? k : k - rank_steps) * 64;
+              tma_load_4d(dst, &map_s, kx, y0, 0, a, full(s));
+              tma_load_4d(dst + a_half, &map_s, kx, y1, z1, a, full(s));
             }
           }
         }
@@ -544,7 +548,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             if (lane == 0) mbar_arrive_expect_tx(full(s), boxes * 2048u);
             __syncwarp();
             const uint32_t dst = base + s * stage_bytes + b_off + b * 128;
-            if (lane < boxes) tma_load_2d(dst + lane * 2048, &map_u, k * 64, tl.p0 + b + lane * 16, full(s));
+            // (past hi's columns lo's follow; their weights are zeros there)
+            const int kx = k < rank_steps ? k * 64 : p.rank + (k - rank_steps) * 64;
+            if (lane < boxes) tma_load_2d(dst + lane * 2048, &map_u, kx, tl.p0 + b + lane * 16, full(s));
           }
         }
       }
@@ -580,6 +586,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const size_t brow = EPI == EPI_SWIGLU ? ((size_t)a * 2 + sub) * p.R + y : (size_t)a * p.R + y;
             const uint4* bp = reinterpret_cast<const uint4*>(p.b + brow * p.rank);
             const float* up = p.u32 + (size_t)(tl.p0 + c) * p.rank;
+            // four chunks' loads at a time: one by one they were most of the launch
+#pragma unroll 4
             for (int j = 0; j < p.rank / 8; j++) {
               const float4 u0 = *reinterpret_cast<const float4*>(up + 8 * j);
               const float4 u1 = *reinterpret_cast<const float4*>(up + 8 * j + 4);
@@ -725,9 +733,17 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
               if (ok1 && there) *reinterpret_cast<float2*>(out + yp1) = f1;
             } else {
               __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + o;
-              if (ok0 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp0) = __floats2bfloat162_rn(f0.x, f0.y);
-              if (EPI == EPI_BF16 && ok1 && there)
-                *reinterpret_cast<__nv_bfloat162*>(out + yp1) = __floats2bfloat162_rn(f1.x, f1.y);
+              const __nv_bfloat162 h0 = __floats2bfloat162_rn(f0.x, f0.y), h1 = __floats2bfloat162_rn(f1.x, f1.y);
+              if (ok0 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp0) = h0;
+              if (EPI == EPI_BF16 && ok1 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp1) = h1;
+              if (EPI == EPI_BF16 && p.lo_off) {  // what the rounding left
+                const float2 r0 = __bfloat1622float2(h0), r1 = __bfloat1622float2(h1);
+                out += p.lo_off;
+                if (ok0 && there)
+                  *reinterpret_cast<__nv_bfloat162*>(out + yp0) = __floats2bfloat162_rn(f0.x - r0.x, f0.y - r0.y);
+                if (ok1 && there)
+                  *reinterpret_cast<__nv_bfloat162*>(out + yp1) = __floats2bfloat162_rn(f1.x - r1.x, f1.y - r1.y);
+              }
             }
           }
         }
@@ -838,8 +854,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             if (wt == 0) {
               const uint32_t dst = base + s * stage_bytes;
               mbar_arrive_expect_tx(full(s), 2 * a_half);
-              tma_load_4d(dst, &map_s, k * 64, y0, 0, a, full(s));
-              tma_load_4d(dst + a_half, &map_s, k * 64, y1, z1, a, full(s));
+              const int kx = (k < rank_steps ? k : k - rank_steps) * 64;
+              tma_load_4d(dst, &map_s, kx, y0, 0, a, full(s));
+              tma_load_4d(dst + a_half, &map_s, kx, y1, z1, a, full(s));
             }
             if (lane == 0) mbar_arrive(full(s), 1);
           }

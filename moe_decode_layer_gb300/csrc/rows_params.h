@@ -75,7 +75,7 @@ struct GemmParams {
   // AD_STEPS: positions off[a] .. off[a + 1] (multiples of 16) belong to adapter a,
   // off[num_adapters] .. off[num_adapters + 1] to none; B is map_s
   const int* adapter_off;
-  // and the rows' products A x are map_u's, [positions, rank]
+  // and the rows' products A x are map_u's, [positions, 2 rank]: hi, then lo
   // AD_EPILOGUE: rows in their own order
   const int* ids;
   const float* u32;        // [rows, rank]
@@ -86,6 +86,7 @@ struct GemmParams {
   int64_t out_stride;
   const int* out_row;  // row of out at each sorted position (NULL: the position)
   const __nv_bfloat16* addend;  // laid out as out
+  int lo_off;          // EPI_BF16: columns from a result to what its rounding left, or 0 (not wanted)
   int* status;         // [kMaxSms] one word per CTA: 1 = a wait ran into its limit
   int* status_clear;   // [kMaxSms] another launch's words when that launch is left out, or NULL
   int status_keep;     // 1: a later round of the same call; words are only set
