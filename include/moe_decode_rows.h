@@ -121,7 +121,7 @@ moe_status moe_decode_experts(const moe_experts_config* cfg, const moe_decode_we
  * as the sum of two bf16 numbers (operands of the tensor cores), and an NVFP4 weight
  * is rounded to bf16 after both its scales. Rows whose id is outside 0..num_adapters-1 have no adapter. Rows
  * may come in any order. What an adapter holds reaches its own rows only.
- * Supported: inner % 8 == 0, outer % 8 == 0 (FP8: both % 128, NVFP4: % 256), <= 16384;
+ * Supported: inner % 8 == 0, outer even (FP8: both % 128, NVFP4: % 256), <= 16384;
  * rank % 8 == 0, <= 256; num_adapters <= 1024 (0: no adapters, their arguments are not read).
  */
 typedef struct moe_project_config {

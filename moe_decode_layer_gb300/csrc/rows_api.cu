@@ -335,7 +335,9 @@ moe_status check_project(const moe_project_config* c) {
   if (c->wdtype != MOE_W_BF16 && c->wdtype != MOE_W_NVFP4 && c->wdtype != MOE_W_FP8_BLOCK) return MOE_ERR_UNSUPPORTED;
   if (c->out_dtype != MOE_BF16 && c->out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
   if (c->swiglu && c->out_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-  if (!widths_ok(c->wdtype, c->inner, c->outer)) return MOE_ERR_UNSUPPORTED;
+  // (results are stored two at a time: an even number of bf16 rows will do, as a router has)
+  const bool router = c->wdtype == MOE_W_BF16 && c->outer % 2 == 0;
+  if (!widths_ok(c->wdtype, c->inner, router ? c->inner : c->outer) || c->outer > 16384) return MOE_ERR_UNSUPPORTED;
   if (c->num_adapters) {
     if (c->rank <= 0) return MOE_ERR_INVALID_ARG;
     if (c->num_adapters > kMaxAdapters || c->rank % 8 || c->rank > 256) return MOE_ERR_UNSUPPORTED;

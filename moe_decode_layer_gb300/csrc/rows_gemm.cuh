@@ -7,8 +7,8 @@
 // 128 TMEM lanes) and the rows of x the N side: with few rows per group, as in a
 // wide mixture of experts, N shrinks to 16 and the kernel is a pure weight
 // stream; with many it is a dense product. That is why this orientation was
-// taken: padding goes to no weight byte and the accumulator columns of a row
-// never mix with another row's, so a row's result does not depend on the batch.
+// taken: no weight byte is padding, and a row has accumulator columns of its own,
+// which nothing that another row holds can reach.
 //
 // A CTA works on tiles of (2 sub-tiles of rt <= 128 weight rows) x (<= nmax rows
 // of x). The two sub-tiles are the gate and the up rows of the same intermediate

@@ -341,6 +341,22 @@ def test_project_quantised(wdtype, swiglu):
         _check_project(x, weight, wdtype, swiglu=swiglu, adapters=ad, adapter_ids=ids)
 
 
+@pytest.mark.parametrize("outer", [2, 6, 20, 60, 126, 250])
+def test_project_even_widths(outer):
+    """As many columns as a router has experts."""
+    g = _gen(outer)
+    weight = (0.05 * _normal(g, outer, 264)).bfloat16()
+    ad = _adapters(g, 3, 16, 264, outer)
+    for rows in (1, 33, 400):
+        x = _normal(g, rows, 264).bfloat16()
+        ids = torch.randint(-1, 3, (rows,), generator=g, device="cuda", dtype=torch.int32)
+        add = _normal(g, rows, outer).bfloat16()
+        _check_project(x, weight, out_dtype=torch.float32)
+        _check_project(x, weight, adapters=ad, adapter_ids=ids, addend=add)
+        if outer % 4 == 0:
+            _check_project(x, weight, adapters=ad, adapter_ids=ids, swiglu=True)
+
+
 def test_project_ids():
     """All rows one adapter's, none at all, every row its own, ids out of range; adapters of no row may hold anything."""
     g = _gen(12)
@@ -441,6 +457,22 @@ def test_route_bias_not_finite(bias):
 
 
 # ------------------------------------------------------------------ the layer
+
+
+def test_layer_with_an_even_number_of_experts():
+    """A layer whose experts are no multiple of 8, on 50 rows against the C++ oracle."""
+    shape = LayerShape(256, 128, 22, 3, 1)
+    layer = _layer(shape, 16)
+    layer["router_w"] = (4 * layer["router_w"].float()).bfloat16()
+    x = helpers.hidden_with_margin(layer["router_w"], 50, 3, seed=3, margin=0.002)
+    from moe_decode_layer_gb300.layer import MoEDecodeLayer
+    mod = MoEDecodeLayer(shape, layer, max_rows=1)
+    want, ridx, rw = helpers.oracle_layer(shape, layer, x, x)
+    idx = torch.empty(50, 3, dtype=torch.int32, device="cuda")
+    w = torch.empty(50, 3, device="cuda")
+    helpers.assert_close(mod.run_rows(x.cuda(), topk_idx=idx, topk_w=w).cpu(), want)
+    helpers.assert_routing(idx, w, ridx, rw)
+    mod.close()
 
 
 @pytest.mark.parametrize("wdtype,score", [("bf16", 0), ("bf16", 1), ("fp8", 0), ("nvfp4", 1)])

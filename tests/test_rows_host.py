@@ -61,7 +61,7 @@ def test_experts_check(kw, status):
     (dict(wdtype=2), OK), (dict(wdtype=1, outer=256), OK), (dict(num_adapters=1024), OK),
     (dict(inner=0), BAD), (dict(num_adapters=-1), BAD), (dict(rank=0), BAD),
     (dict(rank=12), UNSUPPORTED), (dict(rank=264), UNSUPPORTED), (dict(num_adapters=1025), UNSUPPORTED),
-    (dict(inner=252), UNSUPPORTED), (dict(outer=100), UNSUPPORTED), (dict(swiglu=1, out_dtype=1), UNSUPPORTED),
+    (dict(inner=252), UNSUPPORTED), (dict(outer=100), OK), (dict(outer=101), UNSUPPORTED), (dict(outer=16386), UNSUPPORTED), (dict(wdtype=2, outer=100), UNSUPPORTED), (dict(swiglu=1, out_dtype=1), UNSUPPORTED),
     (dict(out_dtype=2), UNSUPPORTED), (dict(wdtype=2, inner=64), UNSUPPORTED),
 ])
 def test_project_check(kw, status):
