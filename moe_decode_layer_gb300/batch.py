@@ -256,24 +256,32 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
     adapter of each row, outside 0..L-1 (-1) none."""
     dev = x.get_device()
     parts = weight if isinstance(weight, (tuple, list)) else (weight,)
-    _need(x.dim() == 2, "x must be [rows, inner]")
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, inner]")
     halves = 2 if swiglu else 1
     t, k = x.shape
     rows = parts[0].shape[0]
-    _need(rows % halves == 0, "a gate/up weight has an even number of rows")
+    if rows % halves:
+        raise ValueError("a gate/up weight has an even number of rows")
     o = rows // halves
-    _need((adapters is None) == (adapter_ids is None), "adapters and adapter_ids come together")
+    if (adapters is None) != (adapter_ids is None):
+        raise ValueError("adapters and adapter_ids come together")
     n = r = 0
     if adapters is not None:
-        _need(adapters.a.dim() == 3 and adapters.a.shape[0] > 0 and adapters.a.shape[1] > 0, "adapters.a must be [L, r, K]")
-        n, r = adapters.a.shape[:2]
+        size = adapters.a.shape
+        if len(size) != 3 or not size[0] or not size[1]:
+            raise ValueError("adapters.a must be [L, r, K]")
+        n, r, _ = size
     if out is not None:
         out_dtype = out.dtype
     cfg = _project_config(wdtype, k, o, bool(swiglu), r, n, out_dtype)
     px, _, sx = _rows(x, "x", k, dev)
-    want = _quantised(wdtype, (), rows, k, halves)
-    _need(len(parts) == len(want), f"a {wdtype} weight comes in {len(want)} tensors")
-    pw = [_tensor(t_, "weight", dtype, size, dev) for t_, (dtype, size) in zip(parts, want)] + [None, None]
+    if wdtype == "bf16" and len(parts) == 1:
+        pw = (_tensor(parts[0], "weight", torch.bfloat16, (rows, k), dev), None, None)
+    else:
+        want = _quantised(wdtype, (), rows, k, halves)
+        _need(len(parts) == len(want), f"a {wdtype} weight comes in {len(want)} tensors")
+        pw = [_tensor(t_, "weight", dtype, size, dev) for t_, (dtype, size) in zip(parts, want)] + [None]
     ids = a = b = scale = None
     if adapters is not None:
         a = _tensor(adapters.a, "adapters.a", torch.bfloat16, (n, r, k), dev)
