@@ -198,13 +198,13 @@ __device__ __forceinline__ Tile tile_at(const GemmParams& p, int t) {
   if (p.ents) {
     const int e = t / p.nrb;
     const int4 v = __ldg(p.ents + e);
-    const int tb = v.w & 0xffff, ntb = v.w >> 16;
+    const int tb = tile_block(v), ntb = tile_blocks(v);
     const int local = t - (e - tb) * p.nrb;
     r.rb = local / ntb;
     const int4 u = __ldg(p.ents + (e - tb) + local % ntb);
-    r.g = u.x;
-    r.p0 = u.y;
-    r.n = u.z;
+    r.g = tile_group(u);
+    r.p0 = tile_first(u);
+    r.n = tile_rows(u);
   } else {
     const int rows = num_rows(p);
     const int ntb = (rows + p.nmax - 1) / p.nmax;

@@ -112,15 +112,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       const int sb = (p.rows + p.nmax - 1) / p.nmax;
       for (int i = tid; i < p.shared * sb; i += kPlanThreads) {
         const int s = i / sb, t = i % sb;
-        p.ents[i] = make_int4(p.groups + s, p.pairs + s * p.rows + t * p.nmax, min(p.nmax, p.rows - t * p.nmax),
-                              t | (sb << 16));
+        p.ents[i] = pack_tile(p.groups + s, p.pairs + s * p.rows + t * p.nmax, min(p.nmax, p.rows - t * p.nmax), t, sb);
       }
       const int n = tid < p.groups ? total : 0;
       const int nb = (n + p.nmax - 1) / p.nmax;
       const int last = block_scan(nb, s_warp);
       const int first = p.shared * sb + last - nb;
       for (int t = 0; t < nb; t++)
-        p.ents[first + t] = make_int4(tid, start + t * p.nmax, min(p.nmax, n - t * p.nmax), t | (nb << 16));
+        p.ents[first + t] = pack_tile(tid, start + t * p.nmax, min(p.nmax, n - t * p.nmax), t, nb);
       if (tid == kPlanThreads - 1) *p.nent = p.shared * sb + last;
     }
   }

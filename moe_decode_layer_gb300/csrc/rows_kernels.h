@@ -22,7 +22,7 @@ struct PlanParams {
   int* off;          // [groups + 1] first position of each group; keep_none: [groups + 2] and the end
   int* src_row;      // [pairs] row at each position, -1 between groups
   int* pos;          // [pairs] position of each pair or -1 (may be NULL)
-  int4* ents;        // tiles: {group, first position, rows, block | blocks << 16}
+  int4* ents;        // tiles (pack_tile)
   int* nent;
 };
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);

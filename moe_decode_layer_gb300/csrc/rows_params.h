@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <vector_functions.h>
 #include <cstdint>
 
 #include "moe_params.h"
@@ -48,6 +49,20 @@ constexpr int threads_of(int fmt) {
 // k's in 128 bytes of codes
 constexpr int kmath(int fmt) { return fmt == FMT_FP8 ? 128 : 256; }
 
+// A tile of a launch with grouped rows: `n` rows of `group` from position p0 on, the
+// block-th of the group's `blocks` tiles. Block and count have a word each (a group of
+// 2^24 rows has more than 2^16 tiles); group and rows share one.
+constexpr int kTileGroupBits = 16;
+static_assert(kMaxGroups <= 1 << kTileGroupBits && kMaxN < 1 << (31 - kTileGroupBits), "a tile's group and rows share a word");
+__host__ __device__ inline int4 pack_tile(int group, int p0, int n, int block, int blocks) {
+  return make_int4(group | n << kTileGroupBits, p0, block, blocks);
+}
+__host__ __device__ inline int tile_group(const int4& t) { return t.x & ((1 << kTileGroupBits) - 1); }
+__host__ __device__ inline int tile_rows(const int4& t) { return t.x >> kTileGroupBits; }
+__host__ __device__ inline int tile_first(const int4& t) { return t.y; }
+__host__ __device__ inline int tile_block(const int4& t) { return t.z; }
+__host__ __device__ inline int tile_blocks(const int4& t) { return t.w; }
+
 struct GemmParams {
   // weights
   int R;            // output rows per group (EPI_SWIGLU: gate rows)
@@ -66,7 +81,7 @@ struct GemmParams {
   int all_first;       // the first such group's first position
   int rows;            // uniform tiles: rows in all
   int nmax;            // rows per tile at most
-  const int4* ents;    // {group, first position, rows, block | blocks << 16}, or NULL: uniform tiles
+  const int4* ents;    // pack_tile's, or NULL: uniform tiles
   const int* nent;
   // adapters
   int ad_mode;         // AdMode
