@@ -8,9 +8,11 @@
 //      memory; each is ranked against the others, one lane per candidate.
 // Without a bias the order is the logits' own and exact. Where the keys are rounded
 // values (a bias, sums over groups), neighbours in the order that are closer than
-// their rounding errors, and not equal inputs, are decided in fp64: sigmoid keys by
-// the candidates' keys alone, else the row's whole choice by the definition. That is
-// rare, and makes the choice independent of how the scores were computed. (fp64 runs
+// their rounding errors, and not equal inputs, are decided in fp64: sums over groups
+// without a bias by the groups' two logits, one lane each; sigmoid keys by the
+// candidates' keys alone or the two groups at the border; else the row's whole choice by
+// the definition. That is rare, and makes the choice independent of how the scores were
+// computed. (fp64 runs
 // at 1/64 of the fp32 rate: one row decided as a whole takes longer than all the
 // others of a 4096-row launch, so the bounds below count each rounding.)
 //
@@ -74,8 +76,8 @@ __device__ __forceinline__ float warp_max(float v) {  // not for NaN
 
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// The row's choice by the definition, in fp64. src: the row's logits; key: E
-// doubles of shared memory. Lane j < K returns its expert or -1.
+// The row's choice by the definition, in fp64 (there is a bias). src: the row's logits;
+// key: E doubles of shared memory. Lane j < K returns its expert or -1.
 template <typename T>
 __device__ __noinline__ int choose64(const RouteParams& p, const T* src, double* key, int lane) {
   const int E = p.E;
@@ -95,7 +97,7 @@ __device__ __noinline__ int choose64(const RouteParams& p, const T* src, double*
     double v = -INFINITY;
     if (l(e) > kMasked) {
       v = p.softmax ? exp((double)l(e) - top) / norm : sigmoid64((double)l(e));
-      if (p.bias) v += (double)__ldg(p.bias + e);
+      v += (double)__ldg(p.bias + e);
     }
     key[e] = v;
   }
@@ -124,11 +126,6 @@ __device__ __noinline__ int choose64(const RouteParams& p, const T* src, double*
     }
     keep = __ballot_sync(0xffffffffu, lane < p.groups && rank < p.kept);
   }
-  if (!p.bias) {  // inside the kept groups the logits' order is the scores', also where fp64 holds them as equal
-    __syncwarp();
-    for (int e = lane; e < E; e += 32) key[e] = (double)l(e);
-    __syncwarp();
-  }
   int mine = -1;
   for (int j = 0; j < p.K; j++) {
     double b = -INFINITY;
@@ -156,20 +153,30 @@ __device__ __noinline__ int choose64(const RouteParams& p, const T* src, double*
   return mine;
 }
 
+// Where this lane's group (b1, b2: its two largest logits, or -inf; sub lanes a group) comes
+// among the sums of two scores, in fp64. Without a bias; softmax scores times the row's
+// common factor.
+__device__ __noinline__ int group_rank64(const RouteParams& p, float b1, float b2, float top, int g, int sub) {
+  auto score = [&](float l) { return p.softmax ? exp((double)l - (double)top) : sigmoid64((double)l); };  // -inf: 0
+  const double v = b1 > -INFINITY ? score(b1) + score(b2) : -INFINITY;
+  int rank = 0;
+  for (int o = 0; o < p.groups; o++) {
+    const double x = __shfl_sync(0xffffffffu, v, o * sub);
+    rank += x > v || (x == v && o < g);
+  }
+  return rank;
+}
+
 // Whether group b's value comes before group a's, in fp64: half a warp each. Sigmoid
-// scores, or softmax scores without a bias (times the row's common factor).
+// scores with a bias.
 template <typename T>
-__device__ __noinline__ bool border64(const RouteParams& p, const T* src, int a, int b, double top, int lane) {
+__device__ __noinline__ bool border64(const RouteParams& p, const T* src, int a, int b, int lane) {
   const int g = lane < 16 ? a : b;
   double b1 = -INFINITY, b2 = -INFINITY;
   for (int i = lane & 15; i < p.group_size; i += 16) {
     const int e = g * p.group_size + i;
     const float l = clean(to_f32(src[e]));
-    double x = -INFINITY;
-    if (l > kMasked) {
-      x = p.softmax ? exp((double)l - top) : sigmoid64((double)l);
-      if (p.bias) x = fmax(x + (double)__ldg(p.bias + e), -INFINITY);
-    }
+    const double x = l > kMasked ? fmax(sigmoid64((double)l) + (double)__ldg(p.bias + e), -INFINITY) : -INFINITY;
     b2 = fmax(b2, fmin(b1, x));
     b1 = fmax(b1, x);
   }
@@ -348,24 +355,28 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         rank += x > v || (x == v && o < g);
       }
       const bool lead = u == 0 && g < p.groups;
+      // the last kept and the first dropped group: too close to tell in fp32?
+      float v0 = 0.0f, v1 = -INFINITY;
+      int i0 = 0, i1 = 0;
+      if (bias || p.best == 2) {
+        i0 = __ffs(__ballot_sync(0xffffffffu, lead && rank == p.kept - 1)) - 1;
+        i1 = __ffs(__ballot_sync(0xffffffffu, lead && rank == p.kept)) - 1;
+        v0 = __shfl_sync(0xffffffffu, v, i0);
+        v1 = __shfl_sync(0xffffffffu, v, i1);
+      }
+      // Without a bias each lane has its group's two logits: all groups again in fp64.
+      if (!bias && v1 > -INFINITY && v0 - v1 <= 0x1p-19f * v0) rank = group_rank64(p, b1, b2, top, g, sub);
       const uint32_t in = __ballot_sync(0xffffffffu, lead && rank < p.kept);
       keep = 0;  // groups -> bits
       for (int o = 0; o < p.groups; o++) keep |= (in >> (o * sub) & 1u) << o;
-      // the last kept and the first dropped group: too close to tell in fp32?
-      if (bias || p.best == 2) {
-        const int i0 = __ffs(__ballot_sync(0xffffffffu, lead && rank == p.kept - 1)) - 1;
-        const int i1 = __ffs(__ballot_sync(0xffffffffu, lead && rank == p.kept)) - 1;
-        const float v0 = __shfl_sync(0xffffffffu, v, i0), v1 = __shfl_sync(0xffffffffu, v, i1);
-        const bool same = !bias && __shfl_sync(0xffffffffu, b1, i0) == __shfl_sync(0xffffffffu, b1, i1) &&
-                          __shfl_sync(0xffffffffu, b2, i0) == __shfl_sync(0xffffffffu, b2, i1);
-        const float big = fmaxf(fabsf(v0), fabsf(v1));
-        const float tol = bias ? 2.0f * tol_s + 0x1p-21f * big : 0x1p-19f * big;
-        if (v1 > -INFINITY && !same) close_group = v0 - v1 <= tol;
+      if (bias) {
+        const float tol = 2.0f * tol_s + 0x1p-21f * fmaxf(fabsf(v0), fabsf(v1));
+        close_group = v1 > -INFINITY && v0 - v1 <= tol;
         // the next ones on both sides: when they are clear, it is between these two alone
         const bool near = lead && ((rank < p.kept - 1 && v - v1 <= tol) || (rank > p.kept && v0 - v <= tol));
-        if (close_group && !__any_sync(0xffffffffu, near) && !(p.softmax && bias)) {
+        if (close_group && !__any_sync(0xffffffffu, near) && !p.softmax) {
           const int ga = i0 / sub, gb = i1 / sub;
-          keep ^= border64(p, src, ga, gb, (double)top, lane) ? (1u << ga | 1u << gb) : 0u;
+          keep ^= border64(p, src, ga, gb, lane) ? (1u << ga | 1u << gb) : 0u;
           close_group = false;
         }
       }
