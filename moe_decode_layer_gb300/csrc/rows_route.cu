@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kWarps = 4;     // rows per CTA
 constexpr int kCand = 64;     // candidates listed per row
+constexpr int kMostK = 16;
 constexpr float kMasked = -0x1.2ced34p+126f;  // the first fp32 at or below -1e38
 constexpr float kLeast = -0x1.2ced32p+126f;   // the next one above it
 constexpr float kLargest = 3e38f;
@@ -224,6 +225,14 @@ struct Cand {
   float l;
 };
 
+// Whether fp32 keys cannot tell x from y, which comes after it: their rounding errors
+// together reach their difference, and their inputs are not equal.
+__device__ __forceinline__ bool confusable(const RouteParams& p, const Cand& x, const Cand& y, float tol_s) {
+  const float a = order_key_f32(x.key), b = order_key_f32(y.key);
+  const bool same = x.l == y.l && __ldg(p.bias + x.e) == __ldg(p.bias + y.e);
+  return !same && a - b <= tol_s + 0x1p-22f * fmaxf(fabsf(a), fabsf(b));
+}
+
 // N: logits per lane (32 N >= E). VEC: 4 consecutive logits per lane and load.
 // KEYS: there is a bias, or groups (else the choice is by the logits alone, whose
 // order is the scores').
@@ -232,7 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   extern __shared__ __align__(16) uint8_t s_dyn[];  // KEYS: per warp E doubles
   __shared__ uint64_t s_order[kWarps][kCand];  // key, then the complement of the expert: larger comes first
   __shared__ float s_logit[kWarps][kCand];
-  __shared__ Cand s_sorted[kWarps][32];
+  __shared__ Cand s_sorted[kWarps][kMostK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
   if (row >= p.rows) return;
@@ -433,7 +442,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
       const uint64_t x = s_order[warp][c];
       int rank = 0;
       for (int o = 0; o < count; o++) rank += s_order[warp][o] > x;
-      if (rank <= K && rank < 32) s_sorted[warp][rank] = Cand{(uint32_t)(x >> 32), (int)~(uint32_t)x, s_logit[warp][c]};
+      if (rank < K) s_sorted[warp][rank] = Cand{(uint32_t)(x >> 32), (int)~(uint32_t)x, s_logit[warp][c]};
     }
     __syncwarp();
     const int have = min(count, K);
@@ -442,15 +451,23 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
       mine = x.e;
       mine_l = x.l;
       if constexpr (KEYS) {
-        if (bias && lane + 1 < min(count, K + 1)) {
+        if (bias && lane + 1 < have) {
           const Cand y = s_sorted[warp][lane + 1];
-          const float a = order_key_f32(x.key), b = order_key_f32(y.key);
-          const bool same = x.l == y.l && __ldg(p.bias + x.e) == __ldg(p.bias + y.e);
-          close = !same && a - b <= tol_s + 0x1p-22f * fmaxf(fabsf(a), fabsf(b));
+          close = confusable(p, x, y, tol_s);
         }
       }
     }
     if constexpr (KEYS) {
+      // the last chosen one against all that were not: behind some with its own inputs there
+      // may be others
+      if (bias && count > K) {
+        const Cand z = s_sorted[warp][K - 1];
+        const uint64_t chosen = (uint64_t)z.key << 32 | (uint32_t)~z.e;
+        for (int c = lane; c < count; c += 32) {
+          const uint64_t x = s_order[warp][c];
+          if (x < chosen) close |= confusable(p, z, Cand{(uint32_t)(x >> 32), (int)~(uint32_t)x, s_logit[warp][c]}, tol_s);
+        }
+      }
       if (__any_sync(0xffffffffu, close) && !p.softmax && count <= 32) {
         // the candidates' keys in fp64, ranked again, one lane each
         close = false;

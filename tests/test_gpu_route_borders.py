@@ -44,3 +44,23 @@ def test_groups_of_saturated_scores(shift, dtype):
     logits = (_normal(_gen(int(shift) + 200), 500, 128) + shift).to(dtype)
     for kept in (1, 4):
         _check(logits, 8, "sigmoid", None, 8, kept, 2)
+
+
+def test_equal_experts_at_the_border_beside_a_better_one():
+    """Three keys that fp32 holds as 1: two equal ones, and a larger one after them."""
+    logits = torch.tensor([[20.0, 20, 21], [20.0, 21, 20], [21.0, 20, 20], [20.0, 20, 20]], device="cuda")
+    for k in (1, 2, 3):
+        _check(logits, k, "sigmoid", torch.zeros(3, device="cuda"))
+        _check(logits, k, "sigmoid", torch.full((3,), 0.25, device="cuda"))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_equal_keys_with_a_bias(score):
+    """Few distinct logits around a saturated score, few distinct biases: long runs of equal inputs."""
+    g = _gen(3)
+    for experts, k in ((24, 4), (96, 8), (300, 16)):
+        logits = 19 + torch.randint(0, 4, (200, experts), generator=g, device="cuda").float()
+        bias = 0.125 * torch.randint(0, 2, (experts,), generator=g, device="cuda").float()
+        _check(logits, k, score, bias)
+        _check(logits.bfloat16(), k, score, torch.zeros_like(bias))
+        _check(logits, k, score, bias, 4, 2, 2)
