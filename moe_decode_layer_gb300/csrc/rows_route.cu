@@ -319,8 +319,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
       if (e < E) s_key[e] = f[j];
     }
     // exp and the quotients are off by 2^-21.4 of a score at most; a softmax's sum by
-    // one step for each addition, and its exponent's rounding weighs 2^-25 of the top score
-    if (bias) tol_s = warp_max(smax) * (p.softmax ? (N + 16) * 0x1p-23f : 0x1p-20f);
+    // one step for each addition, and its exponent's rounding weighs 2^-25 of the top score.
+    // (2^-126: an exp past fp32's range makes a sigmoid below 2^-128 zero.)
+    if (bias) tol_s = warp_max(smax) * (p.softmax ? (N + 16) * 0x1p-23f : 0x1p-20f) + 0x1p-126f;
     __syncwarp();
     if (p.kept < p.groups) {
       // lanes share a group's keys: sub lanes each (a power of two), merged by shuffles
@@ -373,16 +374,26 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         v0 = __shfl_sync(0xffffffffu, v, i0);
         v1 = __shfl_sync(0xffffffffu, v, i1);
       }
-      // Without a bias each lane has its group's two logits: all groups again in fp64.
-      if (!bias && v1 > -INFINITY && v0 - v1 <= 0x1p-19f * v0) rank = group_rank64(p, b1, b2, top, g, sub);
+      // Without a bias each lane has its group's two logits: all groups again in fp64. (A
+      // score is off by 2^-17.9 of itself at most, the rounding of an exponent near -104,
+      // or where fp32 ends by less than 2^-128.)
+      if (!bias && v1 > -INFINITY && v0 - v1 <= 0x1p-16f * v0 + 0x1p-120f) rank = group_rank64(p, b1, b2, top, g, sub);
       const uint32_t in = __ballot_sync(0xffffffffu, lead && rank < p.kept);
       keep = 0;  // groups -> bits
       for (int o = 0; o < p.groups; o++) keep |= (in >> (o * sub) & 1u) << o;
       if (bias) {
-        const float tol = 2.0f * tol_s + 0x1p-21f * fmaxf(fabsf(v0), fabsf(v1));
-        close_group = v1 > -INFINITY && v0 - v1 <= tol;
+        // A value is off by its scores' errors and by the roundings of its keys and sum,
+        // 2^-23 of the keys' magnitudes (not of the sum, where biases cancel). Four times
+        // that: then a pair beside the border is clear when each is clear of the border's.
+        const float mag = fabsf(b1) + (p.best == 2 && b2 > -INFINITY ? fabsf(b2) : 0.0f);
+        const float m0 = __shfl_sync(0xffffffffu, mag, i0), m1 = __shfl_sync(0xffffffffu, mag, i1);
+        auto within = [&](float hi, float lo, float m) {  // (infinite values are equal or clear)
+          return lo > -INFINITY && hi < INFINITY && hi - lo <= 2.0f * tol_s + 0x1p-21f * m;
+        };
+        close_group = within(v0, v1, m0 + m1);
         // the next ones on both sides: when they are clear, it is between these two alone
-        const bool near = lead && ((rank < p.kept - 1 && v - v1 <= tol) || (rank > p.kept && v0 - v <= tol));
+        const bool near = lead && ((rank < p.kept - 1 && within(v, v1, mag + m1)) ||
+                                   (rank > p.kept && within(v0, v, m0 + mag)));
         if (close_group && !__any_sync(0xffffffffu, near) && !p.softmax) {
           const int ga = i0 / sub, gb = i1 / sub;
           keep ^= border64(p, src, ga, gb, lane) ? (1u << ga | 1u << gb) : 0u;

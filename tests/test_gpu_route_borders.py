@@ -37,7 +37,7 @@ def test_equal_groups_at_the_border_beside_a_better_one():
         _check(logits, 2, "sigmoid", torch.zeros(6, device="cuda"), 3, kept, 2)
 
 
-@pytest.mark.parametrize("shift", [12.0, 18.0, 30.0])
+@pytest.mark.parametrize("shift", [12.0, 18.0, 30.0, -95.0])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_groups_of_saturated_scores(shift, dtype):
     """Sums of two sigmoids that fp32 holds as nearly equal, with many equal logits (bf16)."""
@@ -64,3 +64,53 @@ def test_many_equal_keys_with_a_bias(score):
         _check(logits, k, score, bias)
         _check(logits.bfloat16(), k, score, torch.zeros_like(bias))
         _check(logits, k, score, bias, 4, 2, 2)
+
+
+def test_group_sums_that_underflow():
+    """Scores at and below the smallest that fp32 holds: exp overflows (sigmoid) or vanishes (softmax)."""
+    inf = float("inf")
+    _check(torch.tensor([[-88.6, -89.0, -88.5, -120.0]], device="cuda"), 1, "sigmoid", None, 2, 1, 2)
+    _check(torch.tensor([[0.0, 0.0, -103.9, -500.0, -104.2, -104.2], [0.0, -inf, -103.9, -inf, -104.2, -104.2]],
+                        device="cuda"), 2, "softmax", None, 3, 2, 2)
+    g = _gen(4)
+    for mean in (-86.0, -88.5, -100.0, -104.0):
+        logits = mean + 2 * _normal(g, 300, 64)
+        _check(logits, 4, "sigmoid", None, 8, 3, 2)
+        _check(logits.bfloat16(), 4, "sigmoid", None, 8, 3, 2)
+        logits[:, :8] = _normal(g, 300, 8)  # one group far above the others
+        _check(logits, 4, "softmax", None, 8, 3, 2)
+
+
+def test_keys_that_underflow_with_a_bias():
+    """Without a bias to speak of the keys are the scores themselves."""
+    g = _gen(5)
+    for mean in (-87.0, -88.7, -95.0):
+        logits = mean + _normal(g, 200, 64)
+        _check(logits, 6, "sigmoid", torch.zeros(64, device="cuda"))
+        _check(logits, 6, "sigmoid", torch.zeros(64, device="cuda"), 8, 3, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_that_cancel(score):
+    """Large biases of opposite sign: the keys' roundings are far above the sums' own."""
+    g = _gen(6)
+    for size, big in ((2, 1000.0), (4, 5e5)):
+        bias = torch.zeros(8 * size, device="cuda")
+        bias[0::size], bias[1::size] = big, 1 - big
+        if size > 2:
+            bias[2::size] = bias[3::size] = -2 * big
+        logits = 0.3 + 1e-4 * _normal(g, 400, 8 * size)
+        for best in (1, 2):
+            _check(logits, 4, score, bias, 8, 3, best)
+
+
+def test_infinite_biases_at_the_border():
+    """+inf is a key like any other: equal ones go to the lower index, and nothing is NaN."""
+    g = _gen(7)
+    bias = 0.1 * _normal(g, 64)
+    bias[3] = bias[40] = bias[41] = float("inf")
+    for kept, best in ((1, 1), (2, 2), (3, 2)):
+        idx, w = batch.route(_normal(g, 50, 64), 4, score="sigmoid", bias=bias, num_groups=8, top_groups=kept, group_best=best)
+        assert bool((idx[:, 0] == 3).all()) and bool(torch.isfinite(w).all())
+        if kept > 1:
+            assert bool((idx[:, 1] == 40).all()) and bool((idx[:, 2] == 41).all())
