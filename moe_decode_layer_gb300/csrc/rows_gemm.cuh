@@ -245,6 +245,15 @@ __device__ __forceinline__ int adapter_next(const GemmParams& p, int a, int p0, 
 // exp(-g) past fp32's range makes the quotient 0, as it should be.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// A number as hi + lo, two bf16 numbers: hi = bf16(high(v)), lo = low(v, hi). A finite one
+// above bf16's largest gives that and the rest; an infinity or NaN is hi's alone, so that
+// the products' sum is what the number itself would make it, and not inf - inf.
+__device__ __forceinline__ float high(float v) {
+  constexpr float kMost = 0x1.fep+127f;  // bf16's largest
+  return fabsf(v) < INFINITY ? fminf(fmaxf(v, -kMost), kMost) : v;
+}
+__device__ __forceinline__ float low(float v, float hi) { return fabsf(v) < INFINITY ? v - hi : 0.0f; }
+
 // Widening of quantised codes to the bf16 operand.
 // FP8: w = bf16(e4m3 * block scale): one rounding of the product (at most 2^-8 of it,
 // 1/16 of the codes' own rounding); the tensor core takes bf16 operands with the bf16
@@ -733,16 +742,18 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
               if (ok1 && there) *reinterpret_cast<float2*>(out + yp1) = f1;
             } else {
               __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + o;
-              const __nv_bfloat162 h0 = __floats2bfloat162_rn(f0.x, f0.y), h1 = __floats2bfloat162_rn(f1.x, f1.y);
+              const bool two = EPI == EPI_BF16 && p.lo_off;  // results as the sum of two bf16 numbers
+              const __nv_bfloat162 h0 = two ? __floats2bfloat162_rn(high(f0.x), high(f0.y)) : __floats2bfloat162_rn(f0.x, f0.y);
+              const __nv_bfloat162 h1 = two ? __floats2bfloat162_rn(high(f1.x), high(f1.y)) : __floats2bfloat162_rn(f1.x, f1.y);
               if (ok0 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp0) = h0;
               if (EPI == EPI_BF16 && ok1 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp1) = h1;
-              if (EPI == EPI_BF16 && p.lo_off) {  // what the rounding left
+              if (two) {  // what the rounding left
                 const float2 r0 = __bfloat1622float2(h0), r1 = __bfloat1622float2(h1);
                 out += p.lo_off;
                 if (ok0 && there)
-                  *reinterpret_cast<__nv_bfloat162*>(out + yp0) = __floats2bfloat162_rn(f0.x - r0.x, f0.y - r0.y);
+                  *reinterpret_cast<__nv_bfloat162*>(out + yp0) = __floats2bfloat162_rn(low(f0.x, r0.x), low(f0.y, r0.y));
                 if (ok1 && there)
-                  *reinterpret_cast<__nv_bfloat162*>(out + yp1) = __floats2bfloat162_rn(f1.x - r1.x, f1.y - r1.y);
+                  *reinterpret_cast<__nv_bfloat162*>(out + yp1) = __floats2bfloat162_rn(low(f1.x, r1.x), low(f1.y, r1.y));
               }
             }
           }
