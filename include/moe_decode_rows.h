@@ -16,8 +16,10 @@
  * or threads when their workspaces and outputs are different memory. Each enqueues its work on
  * `stream` and returns without waiting, allocates nothing, and can be captured in a
  * CUDA graph (the graph then owns the workspace: two graphs that may run at the
- * same time need one each). Arguments are checked on the host; a call that
- * returns an error has enqueued nothing. Rows beyond `rows` are not touched.
+ * same time need one each). Arguments are checked on the host: a call that
+ * returns MOE_ERR_INVALID_ARG or MOE_ERR_UNSUPPORTED has enqueued nothing. After
+ * MOE_ERR_CUDA (a launch failed) a part of its work may be on the stream, and its
+ * outputs are undefined. Rows beyond `rows` are not touched.
  * The calls use the current CUDA device, which must be the buffers'.
  */
 #ifndef MOE_DECODE_ROWS_H

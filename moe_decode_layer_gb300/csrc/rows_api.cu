@@ -286,6 +286,138 @@ moe_status check_experts(const moe_experts_config* c) {
   return MOE_OK;
 }
 
+// ------------------------------------------------------------------ a round of experts
+struct ExpertsArgs {
+  const moe_experts_config& c;
+  const moe_decode_weights& wt;
+  const __nv_bfloat16* x;
+  int64_t x_stride;
+  const int32_t* idx;
+  const float* w;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* out;
+  uint8_t* ws;
+};
+struct ExpertsRound {
+  ExpertsPlan p;
+  int64_t rows = 0, ents_max = 0;
+  const __nv_bfloat16* x = nullptr;
+  float* y = nullptr;
+  PlanParams plan = {};
+  GemmParams up = {}, down = {};
+  Maps up_maps, down_maps;
+  Layout up_layout, down_layout;
+};
+
+// What rows r0 .. r0 + n of a call need; nothing is launched.
+moe_status prepare_round(const ExpertsArgs& a, int64_t r0, int64_t n, const Device& d, ExpertsRound* r) {
+  const moe_experts_config& c = a.c;
+  const moe_decode_weights& wt = a.wt;
+  const int fmt = fmt_of(c.wdtype);
+  const bool sh = c.num_shared > 0;
+  r->rows = n;
+  const ExpertsPlan& p = r->p = experts_plan(c, n);
+  const int64_t pairs = n * c.top_k;
+  const double blocks = std::max(1.0, std::ceil(pairs / std::max(1.0, p.touched) / p.nmax));
+  const double entries = p.touched * blocks + c.num_shared * (double)cdiv(n, p.nmax);
+  r->ents_max = cdiv(pairs, p.nmax) + std::min<int64_t>(c.num_experts, pairs) + c.num_shared * cdiv(n, p.nmax);
+  const int n_avg = std::min<int>(p.nmax, std::max(16, round16((double)p.positions / entries)));
+
+  PlanParams& pl = r->plan;
+  pl = {};
+  pl.idx = a.idx + r0 * c.top_k;
+  pl.pairs = (int)pairs;
+  pl.per_row = c.top_k;
+  pl.groups = c.num_experts;
+  pl.shared = c.num_shared;
+  pl.rows = (int)n;
+  pl.nmax = p.nmax;
+  pl.align = 1;
+  pl.off = reinterpret_cast<int*>(a.ws + p.off);
+  pl.src_row = reinterpret_cast<int*>(a.ws + p.src_row);
+  pl.pos = reinterpret_cast<int*>(a.ws + p.pos);
+  pl.ents = reinterpret_cast<int4*>(a.ws + p.ents);
+  pl.nent = reinterpret_cast<int*>(a.ws + p.nent);
+
+  __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(a.ws + p.h);
+  float* y = r->y = reinterpret_cast<float*>(a.ws + p.y);
+  int* status = reinterpret_cast<int*>(a.ws + p.status);
+  GemmParams g = {};
+  g.groups_main = c.num_experts;
+  g.nmax = p.nmax;
+  g.ents = pl.ents;
+  g.nent = pl.nent;
+
+  // gate/up
+  GemmParams& g1 = r->up = g;
+  g1.R = c.inter;
+  g1.K = c.hidden;
+  g1.rt = choose_rt(c.inter, true, entries, blocks, n_avg, fmt, p.nmax, (c.hidden + 63) / 64, AD_NONE, d);
+  g1.nrb = (int)cdiv(c.inter, g1.rt);
+  g1.wscale = wt.w13_scale;
+  g1.wscale_s = wt.sh_w13_scale;
+  g1.gscale = wt.w13_gscale;
+  g1.gscale_s = wt.sh_w13_gscale;
+  g1.src_row = p.spread ? nullptr : pl.src_row;
+  g1.box_rows = p.nmax % 32 ? 16 : 32;
+  g1.all_rows = sh ? (int)n : 0;
+  g1.all_first = (int)pairs;
+  g1.out = h;
+  g1.out_stride = c.inter;
+  g1.status = status;
+  g1.status_keep = r0 > 0;
+  // down
+  GemmParams& g2 = r->down = g;
+  g2.R = c.hidden;
+  g2.K = c.inter;
+  g2.rt = choose_rt(c.hidden, false, entries, blocks, n_avg, fmt, p.nmax, (c.inter + 63) / 64, AD_NONE, d);
+  g2.nrb = (int)cdiv(c.hidden, 2 * g2.rt);
+  g2.wscale = wt.w2_scale;
+  g2.wscale_s = wt.sh_w2_scale;
+  g2.gscale = wt.w2_gscale;
+  g2.gscale_s = wt.sh_w2_gscale;
+  g2.box_rows = p.nmax % 32 ? 16 : 32;
+  g2.out = y;
+  g2.out_stride = c.hidden;
+  g2.status = status + kMaxSms;
+  g2.status_keep = r0 > 0;
+
+  Maps &m1 = r->up_maps, &m2 = r->down_maps;
+  const __nv_bfloat16* xr = r->x = a.x + r0 * a.x_stride;
+  if (!make_map(&m1.w, wt.w13, fmt, c.hidden, c.inter, 2, c.num_experts, g1.rt) ||
+      !make_map(&m2.w, wt.w2, fmt, c.inter, c.hidden, 1, c.num_experts, g2.rt) ||
+      !(p.spread ? make_rows_map(&m1.x, y, c.hidden, pairs, c.hidden, g1.box_rows)
+                 : make_rows_map(&m1.x, xr, c.hidden, n, a.x_stride, 1)) ||
+      !make_rows_map(&m1.u, xr, c.hidden, n, a.x_stride, g1.box_rows) ||
+      !make_rows_map(&m2.x, h, c.inter, p.positions, c.inter, g2.box_rows))
+    return MOE_ERR_CUDA;
+  m1.s = m1.w;
+  m2.s = m2.u = m2.w;
+  if (sh && (!make_map(&m1.s, wt.sh_w13, fmt, c.hidden, c.inter, 2, c.num_shared, g1.rt) ||
+             !make_map(&m2.s, wt.sh_w2, fmt, c.inter, c.hidden, 1, c.num_shared, g2.rt)))
+    return MOE_ERR_CUDA;
+  if (!layout(g1.rt, p.nmax, fmt, (c.hidden + 63) / 64, AD_NONE, d.smem, &r->up_layout) ||
+      !layout(g2.rt, p.nmax, fmt, (c.inter + 63) / 64, AD_NONE, d.smem, &r->down_layout))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+cudaError_t launch_round(const ExpertsArgs& a, int64_t r0, ExpertsRound& r, const Device& d, cudaStream_t s) {
+  const moe_experts_config& c = a.c;
+  const int fmt = fmt_of(c.wdtype);
+  const int64_t pairs = r.plan.pairs;
+  cudaError_t e = launch_plan(r.plan, s);
+  if (e == cudaSuccess && r.p.spread)
+    e = launch_spread(r.x, a.x_stride, r.plan.src_row, r.plan.off + c.num_experts, pairs, c.hidden,
+                      reinterpret_cast<__nv_bfloat16*>(r.y), s);
+  if (e == cudaSuccess) e = launch_gemm(r.up, EPI_SWIGLU, fmt, r.up_maps, r.ents_max * r.up.nrb, r.up_layout, d, true, s);
+  if (e == cudaSuccess) e = launch_gemm(r.down, EPI_F32, fmt, r.down_maps, r.ents_max * r.down.nrb, r.down_layout, d, true, s);
+  if (e == cudaSuccess)
+    e = launch_combine(r.y, r.plan.pos, a.w + r0 * c.top_k, a.residual ? a.residual + r0 * c.hidden : nullptr,
+                       a.out + r0 * c.hidden, (int)r.rows, c.hidden, c.top_k, c.num_shared, s);
+  return e;
+}
+
 // ------------------------------------------------------------------ project
 struct ProjectPlan {
   int mode = AD_NONE;
@@ -420,105 +552,26 @@ moe_status moe_decode_experts(const moe_experts_config* c, const moe_decode_weig
   Device d;
   if (!device(&d)) return MOE_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-
-  for (int64_t r0 = 0; r0 < rows; r0 += kRoundRows) {
-    const int64_t n = std::min(kRoundRows, rows - r0);
-    const ExpertsPlan p = experts_plan(*c, n);
-    const int64_t pairs = n * c->top_k;
-    const double blocks = std::max(1.0, std::ceil(pairs / std::max(1.0, p.touched) / p.nmax));
-    const double entries = p.touched * blocks + c->num_shared * (double)cdiv(n, p.nmax);
-    const int64_t ents_max = cdiv(pairs, p.nmax) + std::min<int64_t>(c->num_experts, pairs) +
-                             c->num_shared * cdiv(n, p.nmax);
-    const int n_avg = std::min<int>(p.nmax, std::max(16, round16((double)p.positions / entries)));
-
-    PlanParams pl = {};
-    pl.idx = idx + r0 * c->top_k;
-    pl.pairs = (int)pairs;
-    pl.per_row = c->top_k;
-    pl.groups = c->num_experts;
-    pl.shared = c->num_shared;
-    pl.rows = (int)n;
-    pl.nmax = p.nmax;
-    pl.align = 1;
-    pl.off = reinterpret_cast<int*>(ws + p.off);
-    pl.src_row = reinterpret_cast<int*>(ws + p.src_row);
-    pl.pos = reinterpret_cast<int*>(ws + p.pos);
-    pl.ents = reinterpret_cast<int4*>(ws + p.ents);
-    pl.nent = reinterpret_cast<int*>(ws + p.nent);
-
-    __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(ws + p.h);
-    float* y = reinterpret_cast<float*>(ws + p.y);
-    int* status = reinterpret_cast<int*>(ws + p.status);
-    GemmParams g = {};
-    g.groups_main = c->num_experts;
-    g.nmax = p.nmax;
-    g.ents = pl.ents;
-    g.nent = pl.nent;
-
-    // gate/up
-    GemmParams g1 = g;
-    g1.R = c->inter;
-    g1.K = c->hidden;
-    g1.rt = choose_rt(c->inter, true, entries, blocks, n_avg, fmt, p.nmax, (c->hidden + 63) / 64, AD_NONE, d);
-    g1.nrb = (int)cdiv(c->inter, g1.rt);
-    g1.wscale = wt->w13_scale;
-    g1.wscale_s = wt->sh_w13_scale;
-    g1.gscale = wt->w13_gscale;
-    g1.gscale_s = wt->sh_w13_gscale;
-    g1.src_row = p.spread ? nullptr : pl.src_row;
-    g1.box_rows = p.nmax % 32 ? 16 : 32;
-    g1.all_rows = sh ? (int)n : 0;
-    g1.all_first = (int)pairs;
-    g1.out = h;
-    g1.out_stride = c->inter;
-    g1.status = status;
-    g1.status_keep = r0 > 0;
-    // down
-    GemmParams g2 = g;
-    g2.R = c->hidden;
-    g2.K = c->inter;
-    g2.rt = choose_rt(c->hidden, false, entries, blocks, n_avg, fmt, p.nmax, (c->inter + 63) / 64, AD_NONE, d);
-    g2.nrb = (int)cdiv(c->hidden, 2 * g2.rt);
-    g2.wscale = wt->w2_scale;
-    g2.wscale_s = wt->sh_w2_scale;
-    g2.gscale = wt->w2_gscale;
-    g2.gscale_s = wt->sh_w2_gscale;
-    g2.box_rows = p.nmax % 32 ? 16 : 32;
-    g2.out = y;
-    g2.out_stride = c->hidden;
-    g2.status = status + kMaxSms;
-    g2.status_keep = r0 > 0;
-
-    Maps m1, m2;
-    const __nv_bfloat16* xr = static_cast<const __nv_bfloat16*>(x) + r0 * x_stride;
-    if (!make_map(&m1.w, wt->w13, fmt, c->hidden, c->inter, 2, c->num_experts, g1.rt) ||
-        !make_map(&m2.w, wt->w2, fmt, c->inter, c->hidden, 1, c->num_experts, g2.rt) ||
-        !(p.spread ? make_rows_map(&m1.x, y, c->hidden, pairs, c->hidden, g1.box_rows)
-                   : make_rows_map(&m1.x, xr, c->hidden, n, x_stride, 1)) ||
-        !make_rows_map(&m1.u, xr, c->hidden, n, x_stride, g1.box_rows) ||
-        !make_rows_map(&m2.x, h, c->inter, p.positions, c->inter, g2.box_rows))
-      return MOE_ERR_CUDA;
-    m1.s = m1.w;
-    m2.s = m2.u = m2.w;
-    if (sh && (!make_map(&m1.s, wt->sh_w13, fmt, c->hidden, c->inter, 2, c->num_shared, g1.rt) ||
-               !make_map(&m2.s, wt->sh_w2, fmt, c->inter, c->hidden, 1, c->num_shared, g2.rt)))
-      return MOE_ERR_CUDA;
-    Layout l1, l2;
-    if (!layout(g1.rt, p.nmax, fmt, (c->hidden + 63) / 64, AD_NONE, d.smem, &l1) ||
-        !layout(g2.rt, p.nmax, fmt, (c->inter + 63) / 64, AD_NONE, d.smem, &l2))
-      return MOE_ERR_UNSUPPORTED;
-    cudaError_t e = launch_plan(pl, s);
-    if (e == cudaSuccess && p.spread)
-      e = launch_spread(xr, x_stride, pl.src_row, pl.off + c->num_experts, pairs, c->hidden,
-                        reinterpret_cast<__nv_bfloat16*>(y), s);
-    if (e == cudaSuccess) e = launch_gemm(g1, EPI_SWIGLU, fmt, m1, ents_max * g1.nrb, l1, d, true, s);
-    if (e == cudaSuccess) e = launch_gemm(g2, EPI_F32, fmt, m2, ents_max * g2.nrb, l2, d, true, s);
-    if (e == cudaSuccess)
-      e = launch_combine(y, pl.pos, w + r0 * c->top_k,
-                         residual ? static_cast<const __nv_bfloat16*>(residual) + r0 * c->hidden : nullptr,
-                         static_cast<__nv_bfloat16*>(out) + r0 * c->hidden, (int)n, c->hidden, c->top_k,
-                         c->num_shared, s);
+  const ExpertsArgs a = {*c,
+                         *wt,
+                         static_cast<const __nv_bfloat16*>(x),
+                         x_stride,
+                         idx,
+                         w,
+                         static_cast<const __nv_bfloat16*>(residual),
+                         static_cast<__nv_bfloat16*>(out),
+                         static_cast<uint8_t*>(workspace)};
+  // The first round's and the last one's descriptors and layouts before any launch (those
+  // between are the first's on other rows): what cannot be done is refused as a whole.
+  const int64_t last = (rows - 1) / kRoundRows * kRoundRows;
+  ExpertsRound first, end, mid;
+  st = prepare_round(a, 0, std::min(rows, kRoundRows), d, &first);
+  if (st == MOE_OK && last) st = prepare_round(a, last, rows - last, d, &end);
+  if (st != MOE_OK) return st;
+  for (int64_t r0 = 0; r0 <= last; r0 += kRoundRows) {
+    ExpertsRound& r = r0 == 0 ? first : r0 == last ? end : mid;
+    if (&r == &mid && (st = prepare_round(a, r0, kRoundRows, d, &mid)) != MOE_OK) return st;
+    const cudaError_t e = launch_round(a, r0, r, d, s);
     if (e != cudaSuccess) return cuda_status(e);
   }
   return MOE_OK;

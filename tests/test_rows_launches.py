@@ -1,0 +1,81 @@
+"""What the many-row entry points put on a stream, over a stand-in for the CUDA runtime (no GPU)."""
+
+import ctypes
+
+import pytest
+
+from moe_decode_layer_gb300 import _lib
+from tests import fake_cuda
+
+OK, CUDA = _lib.MOE_OK, _lib.MOE_ERR_CUDA
+P = ctypes.c_void_p(1 << 20)
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    return fake_cuda.make(str(tmp_path_factory.mktemp("fake")))
+
+
+def _weights(cls):
+    w = cls()
+    for name, _ in cls._fields_:
+        setattr(w, name, P)
+    return w
+
+
+def _experts(lib, rows, fail_encode=-1, fail_launch=-1, pending=0, stride=256, **kw):
+    cfg = _lib.ExpertsConfig(**{**dict(hidden=256, inter=128, num_experts=16, top_k=2, num_shared=1, wdtype=0), **kw})
+    need = ctypes.c_size_t()
+    assert lib.moe_decode_experts_workspace(cfg, rows, need) == OK
+    lib.fake_reset(fail_encode, fail_launch, pending)
+    return lib.moe_decode_experts(cfg, _weights(_lib.Weights), P, stride, P, P, P, P, rows, P, need, None)
+
+
+def _project(lib, rows, fail_encode=-1, fail_launch=-1, pending=0, **kw):
+    cfg = _lib.ProjectConfig(**{**dict(inner=256, outer=128, swiglu=0, wdtype=0, rank=16, num_adapters=4, out_dtype=0), **kw})
+    need = ctypes.c_size_t()
+    assert lib.moe_decode_project_workspace(cfg, rows, need) == OK
+    lib.fake_reset(fail_encode, fail_launch, pending)
+    return lib.moe_decode_project(cfg, _weights(_lib.ProjectWeights), P, 256, P, None, P, rows, P, need, None)
+
+
+def _names(lib):
+    return [next(n for n in ("plan", "spread", "gemm", "combine", "shrink", "route") if n + "_kernel" in lib.fake_name(i).decode())
+            for i in range(lib.fake_launches())]
+
+
+@pytest.mark.parametrize("rows", [1, 16384 + 5, 2 * 16384])
+@pytest.mark.parametrize("wdtype", [0, 2])
+def test_experts_without_descriptors_enqueue_nothing(lib, rows, wdtype):
+    """Whichever descriptor cannot be made, of the first round's or a later one's, nothing was launched."""
+    assert _experts(lib, rows, wdtype=wdtype) == OK
+    encodes, launches = lib.fake_encodes(), lib.fake_launches()
+    assert launches >= 4
+    for n in range(encodes):
+        assert _experts(lib, rows, fail_encode=n, wdtype=wdtype) == CUDA
+        assert lib.fake_launches() == 0, n
+
+
+@pytest.mark.parametrize("rows", [8, 100, 5003])
+def test_project_without_descriptors_enqueues_nothing(lib, rows):
+    assert _project(lib, rows) == OK
+    for n in range(lib.fake_encodes()):
+        assert _project(lib, rows, fail_encode=n) == CUDA
+        assert lib.fake_launches() == 0, n
+
+
+def test_failed_launches_are_reported(lib):
+    """A launch that fails ends the call with its error; the ones after it are left out."""
+    for call, rows in ((_experts, 16384 + 5), (_project, 8), (_project, 5003)):
+        assert call(lib, rows) == OK
+        names = _names(lib)
+        for n in range(len(names)):
+            assert call(lib, rows, fail_launch=n) == CUDA
+            assert _names(lib) == names[:n] and lib.fake_pending() == 0
+
+
+def test_rounds(lib):
+    """A call of many rows goes through its rounds in order."""
+    assert _experts(lib, 3 * 16384 + 1) == OK
+    full, short = ["plan", "spread", "gemm", "gemm", "combine"], ["plan", "gemm", "gemm", "combine"]
+    assert _names(lib) == 3 * full + short
