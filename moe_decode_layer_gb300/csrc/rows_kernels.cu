@@ -262,9 +262,11 @@ cudaError_t launch_spread(const __nv_bfloat16* x, int64_t x_stride, const int* s
 
 cudaError_t launch_shrink(const __nv_bfloat16* x, int64_t x_stride, const __nv_bfloat16* a, const float* scale,
                           const int* ids, float* u, int rows, int inner, int rank, int adapters, cudaStream_t s) {
-  const dim3 grid((unsigned)rows, (unsigned)((rank + kShrinkWarps - 1) / kShrinkWarps));
-  shrink_kernel<<<grid, kShrinkWarps * 32, 0, s>>>(x, x_stride, a, scale, ids, u, inner, rank, adapters);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)rows, (unsigned)((rank + kShrinkWarps - 1) / kShrinkWarps));
+  c.blockDim = dim3(kShrinkWarps * 32);
+  c.stream = s;
+  return cudaLaunchKernelEx(&c, shrink_kernel, x, x_stride, a, scale, ids, u, inner, rank, adapters);
 }
 
 cudaError_t launch_combine(const float* y, const int* pos, const float* w, const __nv_bfloat16* residual,

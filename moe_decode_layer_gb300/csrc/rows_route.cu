@@ -542,14 +542,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 
 template <typename T, int N, bool VEC>
 cudaError_t launch_n(const RouteParams& p, bool keys, cudaStream_t s) {
-  const unsigned grid = (unsigned)((p.rows + kWarps - 1) / kWarps);
-  if (keys) {
-    const size_t smem = (size_t)kWarps * p.E * 8;  // at most 32 KB (E = 1024)
-    route_kernel<T, N, VEC, true><<<grid, kWarps * 32, smem, s>>>(p);
-  } else {
-    route_kernel<T, N, VEC, false><<<grid, kWarps * 32, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)((p.rows + kWarps - 1) / kWarps));
+  c.blockDim = dim3(kWarps * 32);
+  c.dynamicSmemBytes = keys ? (size_t)kWarps * p.E * 8 : 0;  // at most 32 KB (E = 1024)
+  c.stream = s;
+  return keys ? cudaLaunchKernelEx(&c, route_kernel<T, N, VEC, true>, p)
+              : cudaLaunchKernelEx(&c, route_kernel<T, N, VEC, false>, p);
 }
 
 template <typename T>

@@ -79,3 +79,15 @@ def test_rounds(lib):
     assert _experts(lib, 3 * 16384 + 1) == OK
     full, short = ["plan", "spread", "gemm", "gemm", "combine"], ["plan", "gemm", "gemm", "combine"]
     assert _names(lib) == 3 * full + short
+
+
+def test_an_earlier_error_is_not_this_call_s(lib):
+    """An error that some call before left behind does not make a call fail whose launches went well."""
+    cfg = _lib.RouteConfig(64, 4, 0, 1, 1, 1, 1, 1, 1.0)
+    for bias in (None, P):
+        lib.fake_reset(-1, -1, 1)
+        assert lib.moe_decode_route(cfg, P, 64, bias, 100, P, P, None) == OK and _names(lib) == ["route"]
+        lib.fake_reset(-1, 0, 0)
+        assert lib.moe_decode_route(cfg, P, 64, bias, 100, P, P, None) == CUDA and lib.fake_launches() == 0
+    for call, rows in ((_experts, 100), (_project, 8), (_project, 5003)):
+        assert call(lib, rows, pending=1) == OK
