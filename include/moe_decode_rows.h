@@ -159,7 +159,8 @@ moe_status moe_decode_project(const moe_project_config* cfg, const moe_project_w
                               int64_t rows, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /*
- * Synchronises `stream` and reports on the last call that used `workspace`:
+ * Synchronises `stream` and reports on the last call of one row or more that used
+ * `workspace`, whose first 4096 bytes it reads:
  * MOE_ERR_DEVICE_TIMEOUT when one of its device-side waits ran into its limit
  * (its outputs are undefined then), MOE_OK otherwise.
  */

@@ -66,6 +66,7 @@ STATIC_SCRATCH_BYTES = 4 << 20
 
 MOE_BF16 = 0
 MOE_F32 = 1
+ROWS_STATUS_BYTES = 4096  # the status words, a workspace's first bytes
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 EXPORTS = ("moe_decode_config_check", "moe_decode_plan", "moe_decode_create", "moe_decode_run", "moe_decode_run_host",

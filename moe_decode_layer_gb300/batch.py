@@ -309,7 +309,9 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
 
 
 def status(workspace: torch.Tensor, stream=None) -> int:
-    """Synchronise and return the status code of the last call that used ``workspace``."""
+    """Synchronise and return the status code of the last call of one row or more that
+    used ``workspace`` (from its first byte on)."""
+    _workspace(workspace, _lib.ROWS_STATUS_BYTES, workspace.get_device())
     s, leave = _enter(workspace.get_device(), stream)
     try:
         return _lib.load().moe_decode_rows_status(workspace.data_ptr(), s)

@@ -17,7 +17,7 @@ constexpr int kMaxRaw = 8;        // slots of quantised codes
 constexpr int kWidenThreads = 256;
 constexpr int kMaxGroups = 1024 + 8;  // experts and shared experts, or adapters
 constexpr int kMaxAdapters = 1024;
-constexpr int kMaxSms = 512;      // status words of a launch
+constexpr int kMaxSms = 512;      // status words of a launch (two launches': the 4096 bytes of the header)
 constexpr uint32_t kWaitLimit = 1u << 21;
 constexpr unsigned long long kDrainNs = 1000000ull;
 

@@ -101,6 +101,7 @@ const char* fake_name(int i) { return g_launches[i].name.c_str(); }
 unsigned fake_grid(int i) { return g_launches[i].grid; }
 int fake_pdl(int i) { return g_launches[i].pdl; }
 int fake_encodes() { return g_encodes; }
+int fake_bytes_read() { return (int)g_read; }
 int fake_pending() { return (int)g_last; }
 }
 """

@@ -3,8 +3,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from moe_decode_layer_gb300 import _lib
+from moe_decode_layer_gb300 import _lib, batch
 from tests import fake_cuda
 
 OK, CUDA = _lib.MOE_OK, _lib.MOE_ERR_CUDA
@@ -91,3 +92,19 @@ def test_an_earlier_error_is_not_this_call_s(lib):
         assert lib.moe_decode_route(cfg, P, 64, bias, 100, P, P, None) == CUDA and lib.fake_launches() == 0
     for call, rows in ((_experts, 100), (_project, 8), (_project, 5003)):
         assert call(lib, rows, pending=1) == OK
+
+
+def test_status_reads_what_the_binding_checks(lib):
+    """The bytes that the status call copies are those that the binding asks a workspace for."""
+    assert lib.moe_decode_rows_status(P, None) == OK
+    assert lib.fake_bytes_read() == _lib.ROWS_STATUS_BYTES
+    for rows in (1, 100):
+        need = ctypes.c_size_t()
+        assert lib.moe_decode_project_workspace(_lib.ProjectConfig(8, 8, 0, 0, 0, 0, 0), rows, need) == OK
+        assert need.value >= _lib.ROWS_STATUS_BYTES
+
+
+def test_status_of_a_short_workspace_is_refused():
+    for bad in (torch.empty(_lib.ROWS_STATUS_BYTES - 1, dtype=torch.uint8), torch.empty(4096), torch.empty(0, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace must be"):
+            batch.status(bad)
