@@ -8,6 +8,8 @@ stream (or ``stream``) without waiting. No arithmetic happens here.
 
 A workspace that is handed in must not be in use by another call at the same time,
 and must stay alive while a CUDA graph that captured a call with it is replayed.
+``status`` reads from it whether the call's device-side waits ended in time; a call
+without one leaves nothing behind that could be asked.
 """
 
 from __future__ import annotations

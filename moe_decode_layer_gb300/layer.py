@@ -117,7 +117,7 @@ class MoEDecodeLayer:
                  topk_idx: torch.Tensor | None = None, topk_w: torch.Tensor | None = None, *,
                  num_groups: int = 1, top_groups: int = 1, group_best: int = 1,
                  adapters: tuple[batch.Adapters, batch.Adapters] | None = None,
-                 adapter_ids: torch.Tensor | None = None, stream=None):
+                 adapter_ids: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
         """The same layer for any number of rows (a chunk of a prompt, many requests):
         router logits, batch.route and batch.experts one after another, with this
         layer's weights, scoring rule and routed scale. Nothing of the handle is
@@ -126,12 +126,22 @@ class MoEDecodeLayer:
         experts. ``adapters``: the low-rank adapters of the one shared expert's
         gate/up and down projections, and ``adapter_ids`` int32 [T] each row's; the
         shared expert's output is then added to the residual in a rounding to
-        bf16 of its own. Not for layers with pre_rmsnorm or transposed down matrices."""
+        bf16 of its own. Not for layers with pre_rmsnorm or transposed down matrices.
+
+        ``workspace``: uint8, of rows_workspace bytes; after a run with one rows_status
+        tells whether its device-side waits ended in time (without one, each operator
+        takes a workspace from torch's allocator, and nobody can be asked)."""
         if self._cfg.pre_rmsnorm:
             raise ValueError("run_rows takes the layer's normalised input: pre_rmsnorm is not computed")
         residual = x if residual is None else residual
+        ws = dict.fromkeys(("router", "up", "down", "experts"))
+        if workspace is not None:
+            parts, need = self._rows_parts(x.shape[0], adapters)
+            batch._workspace(workspace, need, x.get_device())
+            ws.update({name: workspace[at:at + n] for name, (at, n) in parts.items()})
         sig = self._cfg.score == _lib.MOE_SCORE_SIGMOID_BIAS
-        logits = batch.project(x, self._weights["router_w"], out_dtype=torch.float32, stream=stream)
+        logits = batch.project(x, self._weights["router_w"], out_dtype=torch.float32, workspace=ws["router"],
+                               stream=stream)
         idx, w = batch.route(logits, self.shape.top_k, score="sigmoid" if sig else "softmax",
                              bias=self._weights["router_bias"] if sig else None, num_groups=num_groups,
                              top_groups=top_groups, group_best=group_best, scale=self._cfg.routed_scale,
@@ -143,13 +153,45 @@ class MoEDecodeLayer:
             sfx = batch._SUFFIX[shape.wdtype]
             w13, w2 = (tuple(self._weights["sh_" + n + f][0] for f in sfx) for n in ("w13", "w2"))
             h = batch.project(x, w13, wdtype=shape.wdtype, swiglu=True, adapters=adapters[0], adapter_ids=adapter_ids,
-                              stream=stream)
+                              workspace=ws["up"], stream=stream)
             residual = batch.project(h, w2, wdtype=shape.wdtype, adapters=adapters[1], adapter_ids=adapter_ids,
-                                     addend=residual, stream=stream)
+                                     addend=residual, workspace=ws["down"], stream=stream)
             shape = dataclasses.replace(shape, num_shared=0)
         elif adapter_ids is not None:
             raise ValueError("adapters and adapter_ids come together")
-        return batch.experts(shape, self._weights, x, idx, w, residual=residual, out=out, stream=stream)
+        return batch.experts(shape, self._weights, x, idx, w, residual=residual, out=out,
+                             workspace=ws["experts"], stream=stream)
+
+    def _rows_parts(self, rows: int, adapters):
+        """({operator: (offset, bytes)}, bytes in all) of a workspace of run_rows."""
+        s = self.shape
+        need = {"router": batch.project_workspace(s.hidden, s.num_experts, rows, out_dtype=torch.float32)}
+        if adapters is not None:
+            for name, ad, inner, outer, swiglu in (("up", adapters[0], s.hidden, s.inter, True),
+                                                   ("down", adapters[1], s.inter, s.hidden, False)):
+                need[name] = batch.project_workspace(inner, outer, rows, wdtype=s.wdtype, swiglu=swiglu,
+                                                     rank=ad.a.shape[1], num_adapters=ad.a.shape[0])
+            s = dataclasses.replace(s, num_shared=0)
+        need["experts"] = batch.experts_workspace(s, rows)
+        parts, at = {}, 0
+        for name, n in need.items():
+            parts[name] = at, n
+            at += (n + 255) // 256 * 256
+        return parts, at
+
+    def rows_workspace(self, rows: int, adapters: tuple[batch.Adapters, batch.Adapters] | None = None) -> int:
+        """Bytes of a workspace for run_rows with this many rows and these adapters."""
+        return self._rows_parts(rows, adapters)[1]
+
+    def rows_status(self, workspace: torch.Tensor, rows: int,
+                    adapters: tuple[batch.Adapters, batch.Adapters] | None = None, stream=None) -> int:
+        """Synchronise and return the status code of the last run_rows of this many rows
+        with these adapters and this workspace: MOE_ERR_DEVICE_TIMEOUT when a device-side
+        wait of any of its operators ran into its limit (the outputs are undefined then)."""
+        parts, need = self._rows_parts(rows, adapters)
+        batch._workspace(workspace, need, workspace.get_device())
+        codes = [batch.status(workspace[at:at + n], stream) for at, n in parts.values() if n]
+        return next((c for c in codes if c != _lib.MOE_OK), _lib.MOE_OK)
 
     def host_copy_bytes(self, m: int) -> tuple[int, int]:
         """Bytes run_host copies per call with m rows and x as the residual: (in, out).
@@ -162,7 +204,8 @@ class MoEDecodeLayer:
         return m * self.shape.hidden * 2, out
 
     def status(self, stream=None) -> int:
-        """Synchronise and return (and clear) the device status code."""
+        """Synchronise and return (and clear) the device status code of run's steps
+        (run_rows keeps nothing in the handle: rows_status)."""
         return self.lib.moe_decode_get_status(self.handle, _stream_ptr(stream))
 
     def set_option(self, option: int, value: int) -> None:

@@ -1,0 +1,52 @@
+"""The layer on any number of rows: its workspace and status, rows with a stride, adapters for each weight type."""
+
+import pytest
+import torch
+
+from moe_decode_layer_gb300 import LayerShape, _lib, batch, synth
+from moe_decode_layer_gb300.layer import MoEDecodeLayer
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _adapters(g, n, r, k, o):
+    return batch.Adapters((torch.randn(n, r, k, generator=g, device="cuda") / k ** 0.5).bfloat16(),
+                          (0.1 * torch.randn(n, o, r, generator=g, device="cuda")).bfloat16(),
+                          0.5 + torch.rand(n, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("rows", [3, 150])
+@pytest.mark.parametrize("with_adapters", [False, True])
+def test_workspace_and_status(rows, with_adapters):
+    """A run in a workspace of the caller's gives the same bits, and a time-out of any of its operators is seen."""
+    shape = LayerShape(256, 128, 16, 2, 1)
+    mod = MoEDecodeLayer(shape, synth.make_layer(shape, seed=1, device="cuda"), max_rows=1)
+    g = _gen(rows)
+    x = torch.randn(rows, 256, generator=g, device="cuda").bfloat16()
+    kw = {}
+    if with_adapters:
+        kw = dict(adapters=(_adapters(g, 4, 16, 256, 256), _adapters(g, 4, 8, 128, 256)),
+                  adapter_ids=torch.randint(-1, 4, (rows,), generator=g, device="cuda", dtype=torch.int32))
+    ad = kw.get("adapters")
+    ws = torch.full((mod.rows_workspace(rows, ad),), 255, dtype=torch.uint8, device="cuda")
+    want = mod.run_rows(x, **kw)
+    assert torch.equal(mod.run_rows(x, workspace=ws, **kw), want)
+    assert mod.rows_status(ws, rows, ad) == _lib.MOE_OK
+    parts, _ = mod._rows_parts(rows, ad)
+    assert len(parts) == (4 if with_adapters else 2)
+    for at, _ in parts.values():  # a word that a wait past its limit would set
+        ws[at:at + 4].view(torch.int32).fill_(1)
+        assert mod.rows_status(ws, rows, ad) == _lib.MOE_ERR_DEVICE_TIMEOUT
+        ws[at:at + 4].zero_()
+    assert mod.rows_status(ws, rows, ad) == _lib.MOE_OK
+    assert mod.rows_workspace(0, ad) == 0 and mod.run_rows(x[:0], workspace=ws, adapters=ad, adapter_ids=kw["adapter_ids"][:0] if ad else None).shape == (0, 256)
+    for bad in (ws[:-256], ws.cpu(), ws.view(torch.int8)):
+        with pytest.raises(ValueError):
+            mod.run_rows(x, workspace=bad, **kw)
+        with pytest.raises(ValueError):
+            mod.rows_status(bad, rows, ad)
+    mod.close()
