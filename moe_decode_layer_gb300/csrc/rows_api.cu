@@ -192,7 +192,7 @@ struct Maps {
 
 cudaError_t launch_gemm(GemmParams& p, int epi, int fmt, Maps& m, int64_t tiles, const Layout& l, const Device& d, bool pdl, cudaStream_t st) {
   const void* k = gemm_kernel(epi, fmt);
-  static std::atomic<uint64_t> ready[3][3];  // per kernel: devices whose limit is set
+  static std::atomic<uint64_t> ready[4][3];  // per kernel: devices whose limit is set
   if (d.id >= 64 || !(ready[epi][fmt].load() >> d.id & 1)) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem - 4096);
     if (e != cudaSuccess) return e;
@@ -725,7 +725,7 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
     if (e == cudaSuccess)
       e = launch_spread(static_cast<const __nv_bfloat16*>(x), x_stride, pl.src_row, pl.off + c->num_adapters + 1,
                         p.positions, c->inner, reinterpret_cast<__nv_bfloat16*>(ws + p.x), s);
-    if (e == cudaSuccess) e = launch_gemm(ga, EPI_BF16, FMT_BF16, ma, tiles, la, d, true, s);
+    if (e == cudaSuccess) e = launch_gemm(ga, EPI_TWO, FMT_BF16, ma, tiles, la, d, true, s);
     g.adapter_off = pl.off;
     g.out_row = pl.src_row;
   }

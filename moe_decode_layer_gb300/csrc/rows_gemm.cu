@@ -13,6 +13,7 @@ const void* gemm_kernel(int epi, int fmt) {
   switch (epi) {
     case EPI_SWIGLU: return reinterpret_cast<const void*>(&rows_gemm_kernel<EPI_SWIGLU, FMT_BF16>);
     case EPI_F32: return reinterpret_cast<const void*>(&rows_gemm_kernel<EPI_F32, FMT_BF16>);
+    case EPI_TWO: return reinterpret_cast<const void*>(&rows_gemm_kernel<EPI_TWO, FMT_BF16>);
     default: return reinterpret_cast<const void*>(&rows_gemm_kernel<EPI_BF16, FMT_BF16>);
   }
 }

@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         } else {
           g0 = g1 = __ldg(gs + g);
         }
-      } else if (EPI == EPI_BF16 && FMT == FMT_BF16 && p.gscale) {
+      } else if (EPI == EPI_TWO && p.gscale) {
         g0 = g1 = __ldg(p.gscale + tl.g);
       }
       if (split > 1 && q * 32 < p.rt) {
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           for (int j = 0; j < 8; j++) {
             a0[j] = __uint_as_float(n0[j]);
             a1[j] = __uint_as_float(n1[j]);
-            if (FMT == FMT_NVFP4 || EPI == EPI_BF16) {
+            if (FMT == FMT_NVFP4 || EPI == EPI_TWO) {
               a0[j] *= g0;
               a1[j] *= g1;
             }
@@ -742,12 +742,12 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
               if (ok1 && there) *reinterpret_cast<float2*>(out + yp1) = f1;
             } else {
               __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + o;
-              const bool two = EPI == EPI_BF16 && p.lo_off;  // results as the sum of two bf16 numbers
-              const __nv_bfloat162 h0 = two ? __floats2bfloat162_rn(high(f0.x), high(f0.y)) : __floats2bfloat162_rn(f0.x, f0.y);
-              const __nv_bfloat162 h1 = two ? __floats2bfloat162_rn(high(f1.x), high(f1.y)) : __floats2bfloat162_rn(f1.x, f1.y);
+              constexpr bool kTwo = EPI == EPI_TWO;
+              const __nv_bfloat162 h0 = kTwo ? __floats2bfloat162_rn(high(f0.x), high(f0.y)) : __floats2bfloat162_rn(f0.x, f0.y);
+              const __nv_bfloat162 h1 = kTwo ? __floats2bfloat162_rn(high(f1.x), high(f1.y)) : __floats2bfloat162_rn(f1.x, f1.y);
               if (ok0 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp0) = h0;
-              if (EPI == EPI_BF16 && ok1 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp1) = h1;
-              if (two) {  // what the rounding left
+              if (EPI != EPI_SWIGLU && ok1 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp1) = h1;
+              if (kTwo) {  // what the rounding left
                 const float2 r0 = __bfloat1622float2(h0), r1 = __bfloat1622float2(h1);
                 out += p.lo_off;
                 if (ok0 && there)

@@ -25,7 +25,8 @@ constexpr unsigned long long kDrainNs = 1000000ull;
 enum Epi {
   EPI_SWIGLU = 0,  // bf16 silu(gate) * up
   EPI_F32 = 1,     // fp32
-  EPI_BF16 = 2     // bf16, with a scale per group
+  EPI_BF16 = 2,    // bf16
+  EPI_TWO = 3      // the sum of two bf16 numbers, with a scale per group (bf16 weights)
 };
 
 // How the rows' adapters join the sum.
@@ -72,7 +73,7 @@ struct GemmParams {
   int groups_main;  // groups of map_w; later ones are map_s's
   const void* wscale;    // FP8 / NVFP4 block scales
   const void* wscale_s;
-  const float* gscale;   // NVFP4 tensor scales; EPI_BF16: a scale per group
+  const float* gscale;   // NVFP4 tensor scales; EPI_TWO: a scale per group
   const float* gscale_s;
   // rows of x (map_x)
   const int* src_row;  // row at each sorted position (NULL: the position)
@@ -101,7 +102,7 @@ struct GemmParams {
   int64_t out_stride;
   const int* out_row;  // row of out at each sorted position (NULL: the position)
   const __nv_bfloat16* addend;  // laid out as out
-  int lo_off;          // EPI_BF16: columns from a result to what its rounding left, or 0 (not wanted)
+  int lo_off;          // EPI_TWO: columns from a result to what its rounding left
   int* status;         // [kMaxSms] one word per CTA: 1 = a wait ran into its limit
   int* status_clear;   // [kMaxSms] another launch's words when that launch is left out, or NULL
   int status_keep;     // 1: a later round of the same call; words are only set
