@@ -186,9 +186,13 @@ struct Tile {
   int g, p0, n, rb;
 };
 
+// (What the launches before this one wrote, the lists of tiles and rows among it, is read
+// with plain loads behind pdl_wait(): the read-only path is for what stays as it is while
+// the grid is resident, and with an early launch these do not.)
+
 // Rows of a launch with uniform tiles; adapters' rows are padded to 16 each.
 __device__ __forceinline__ int num_rows(const GemmParams& p) {
-  return p.ad_mode == AD_STEPS ? __ldg(p.adapter_off + p.num_adapters + 1) : p.rows;
+  return p.ad_mode == AD_STEPS ? p.adapter_off[p.num_adapters + 1] : p.rows;
 }
 
 // Tiles of one group follow one another with the row blocks of x innermost, so
@@ -197,11 +201,11 @@ __device__ __forceinline__ Tile tile_at(const GemmParams& p, int t) {
   Tile r;
   if (p.ents) {
     const int e = t / p.nrb;
-    const int4 v = __ldg(p.ents + e);
+    const int4 v = p.ents[e];
     const int tb = tile_block(v), ntb = tile_blocks(v);
     const int local = t - (e - tb) * p.nrb;
     r.rb = local / ntb;
-    const int4 u = __ldg(p.ents + (e - tb) + local % ntb);
+    const int4 u = p.ents[(e - tb) + local % ntb];
     r.g = tile_group(u);
     r.p0 = tile_first(u);
     r.n = tile_rows(u);
@@ -216,7 +220,7 @@ __device__ __forceinline__ Tile tile_at(const GemmParams& p, int t) {
   return r;
 }
 __device__ __forceinline__ int num_tiles(const GemmParams& p) {
-  return (p.ents ? __ldg(p.nent) : (num_rows(p) + p.nmax - 1) / p.nmax) * p.nrb;
+  return (p.ents ? *p.nent : (num_rows(p) + p.nmax - 1) / p.nmax) * p.nrb;
 }
 
 // The K steps of a tile: first K / 64 steps of the weights, then, for each adapter
@@ -227,14 +231,14 @@ __device__ __forceinline__ int adapter_of(const GemmParams& p, int pos) {
   int lo = 0, hi = p.num_adapters;  // largest a with off[a] <= pos (off[num_adapters] = first row without one)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.adapter_off + mid) <= pos) lo = mid; else hi = mid - 1;
+    if (p.adapter_off[mid] <= pos) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 // The next adapter >= a with rows in [p0, p0 + n), or num_adapters.
 __device__ __forceinline__ int adapter_next(const GemmParams& p, int a, int p0, int n) {
   while (a < p.num_adapters) {
-    const int b = __ldg(p.adapter_off + a), e = __ldg(p.adapter_off + a + 1);
+    const int b = p.adapter_off[a], e = p.adapter_off[a + 1];
     if (b >= p0 + n) return p.num_adapters;
     if (e > b && e > p0) return a;
     a++;
@@ -492,8 +496,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       if (ok && ad_steps)
         for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
              a = adapter_next(p, a + 1, tl.p0, tl.n)) {
-          const int c0 = max(__ldg(p.adapter_off + a) - tl.p0, 0);
-          const int c1 = min(__ldg(p.adapter_off + a + 1) - tl.p0, tl.n);
+          const int c0 = max(p.adapter_off[a] - tl.p0, 0);
+          const int c1 = min(p.adapter_off[a + 1] - tl.p0, tl.n);
           for (int k = 0; ok && k < per_adapter; k++) ok = step(c0, c1 - c0, false, false);
         }
       if (ok && leader) mma_commit(tfull(b));
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         for (int h = 0; h < 2; h++) {
           int v[4];
 #pragma unroll
-          for (int j = 0; j < 4; j++) v[j] = max(__ldg(p.src_row + tl.p0 + min(4 * (lane + 32 * h) + j, tl.n - 1)), 0);
+          for (int j = 0; j < 4; j++) v[j] = max(p.src_row[tl.p0 + min(4 * (lane + 32 * h) + j, tl.n - 1)], 0);
           y[h] = make_int4(v[0], v[1], v[2], v[3]);
         }
       }
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       if (ok && ad_steps) {
         for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
              a = adapter_next(p, a + 1, tl.p0, tl.n)) {
-          const int b = max(__ldg(p.adapter_off + a) - tl.p0, 0), e = min(__ldg(p.adapter_off + a + 1) - tl.p0, tl.n);
+          const int b = max(p.adapter_off[a] - tl.p0, 0), e = min(p.adapter_off[a + 1] - tl.p0, tl.n);
           const int boxes = (e - b + 15) / 16;  // 16 rows each, as the adapter's are padded
           for (int k = 0; k < per_adapter; k++, it.next(p.stages)) {
             const uint32_t s = it.slot;
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const int lines = (cols * 2 + 127) / 128 + 1;
         for (int i = tid - 128; i < tl.n * lines; i += 32 * epilogue_warps(FMT)) {
           const int pos = tl.p0 + i / lines;
-          const int row = p.out_row ? __ldg(p.out_row + pos) : pos;
+          const int row = p.out_row ? p.out_row[pos] : pos;
           const int col = min(first + (i % lines) * 64, first + cols - 1);
           if (row >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.addend + (size_t)row * p.out_stride + col));
         }
@@ -681,7 +685,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           tmem_ld8(d0 + c, n0);
           tmem_ld8(d1 + c, n1);
           row_n = tl.p0 + min(c + (lane & 7), tl.n - 1);  // lane j: the row of out of column j
-          if (p.out_row) row_n = __ldg(p.out_row + row_n);
+          if (p.out_row) row_n = p.out_row[row_n];
           if (add) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {

@@ -191,7 +191,7 @@ constexpr int kCombineThreads = 256;
 // those bytes: 8192 rows of 9 x 2048, 0.67 GB in all, 109 us (6.1 TB/s). In bf16 they
 // would halve, and add the rounding of each of a row's terms to the sum's.
 __global__ void __launch_bounds__(kCombineThreads)
-    combine_kernel(const float* __restrict__ y, const int* __restrict__ pos, const float* __restrict__ w,
+    combine_kernel(const float* y, const int* pos, const float* __restrict__ w,
                    const __nv_bfloat16* residual, __nv_bfloat16* out, int rows, int hidden, int top_k, int shared) {
   pdl_wait();
   const int cols = hidden / 4;
@@ -205,10 +205,10 @@ __global__ void __launch_bounds__(kCombineThreads)
   }
 #pragma unroll 4
   for (int j = 0; j < top_k; j++) {
-    const int at = __ldg(pos + (size_t)t * top_k + j);
+    const int at = pos[(size_t)t * top_k + j];  // (pos and y are of the launches before: plain loads)
     const float f = __ldg(w + (size_t)t * top_k + j);
     if (at >= 0) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(y + (size_t)at * hidden + c));
+      const float4 v = *reinterpret_cast<const float4*>(y + (size_t)at * hidden + c);
       a.x = fmaf(f, v.x, a.x);
       a.y = fmaf(f, v.y, a.y);
       a.z = fmaf(f, v.z, a.z);
@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
   }
   for (int s = 0; s < shared; s++) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(
-        y + ((size_t)rows * top_k + (size_t)s * rows + t) * hidden + c));
+    const float4 v =
+        *reinterpret_cast<const float4*>(y + ((size_t)rows * top_k + (size_t)s * rows + t) * hidden + c);
     a.x += v.x;
     a.y += v.y;
     a.z += v.z;

@@ -1,11 +1,13 @@
 """What the many-row entry points put on a stream, over a stand-in for the CUDA runtime (no GPU)."""
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
 
-from moe_decode_layer_gb300 import _lib, batch
+from moe_decode_layer_gb300 import _lib, batch, build
 from tests import fake_cuda
 
 OK, CUDA = _lib.MOE_OK, _lib.MOE_ERR_CUDA
@@ -73,6 +75,17 @@ def test_failed_launches_are_reported(lib):
         for n in range(len(names)):
             assert call(lib, rows, fail_launch=n) == CUDA
             assert _names(lib) == names[:n] and lib.fake_pending() == 0
+
+
+def test_lists_of_the_launch_before_are_read_plainly():
+    """With early launches the read-only path would be used on memory that changes while the grid is resident."""
+    gemm, small = (open(os.path.join(build.CSRC, f)).read() for f in ("rows_gemm.cuh", "rows_kernels.cu"))
+    for name in ("ents", "nent", "adapter_off", "src_row", "out_row", "u32"):
+        assert f"p.{name}" in gemm and not re.search(rf"__ldg\(\s*p\.{name}\b", gemm), name
+    combine = small[small.index("combine_kernel(const float*"):small.index("cudaError_t launch_plan")]
+    assert not re.search(r"__ldg\([^;]*\b(y|pos)\b", combine) and not re.search(r"__restrict__ (y|pos)\b", combine)
+    spread = small[small.index("spread_kernel(const"):small.index("constexpr int kShrinkWarps")]
+    assert not re.search(r"__restrict__ (src_row|count)\b", spread) and not re.search(r"__ldg\((src_row|count)", spread)
 
 
 def test_rounds(lib):
