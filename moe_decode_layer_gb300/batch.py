@@ -77,6 +77,16 @@ def _enter(dev: int, stream):
     return stream.cuda_stream, stack
 
 
+def contiguous(t: torch.Tensor, stream=None) -> torch.Tensor:
+    """A contiguous copy of ``t``, made and allocated on the stream that the operators run on."""
+    _, leave = _enter(t.get_device(), stream)
+    try:
+        return t.contiguous()
+    finally:
+        if leave is not None:
+            leave.close()
+
+
 @functools.lru_cache(maxsize=256)
 def _route_config(e: int, top_k: int, score: str, num_groups: int, top_groups: int, group_best: int,
                   renormalise: bool, dtype, scale: float) -> _lib.RouteConfig:

@@ -121,7 +121,8 @@ class MoEDecodeLayer:
         """The same layer for any number of rows (a chunk of a prompt, many requests):
         router logits, batch.route and batch.experts one after another, with this
         layer's weights, scoring rule and routed scale. Nothing of the handle is
-        used, so runs on different streams may overlap. ``num_groups``,
+        used, so runs on different streams may overlap. ``x`` may have any row stride of
+        a multiple of 8; ``residual`` (x, when not given) is contiguous. ``num_groups``,
         ``top_groups`` and ``group_best`` limit the choice to the best groups of
         experts. ``adapters``: the low-rank adapters of the one shared expert's
         gate/up and down projections, and ``adapter_ids`` int32 [T] each row's; the
@@ -133,7 +134,8 @@ class MoEDecodeLayer:
         takes a workspace from torch's allocator, and nobody can be asked)."""
         if self._cfg.pre_rmsnorm:
             raise ValueError("run_rows takes the layer's normalised input: pre_rmsnorm is not computed")
-        residual = x if residual is None else residual
+        if residual is None:
+            residual = x if x.is_contiguous() else batch.contiguous(x, stream)
         ws = dict.fromkeys(("router", "up", "down", "experts"))
         if workspace is not None:
             parts, need = self._rows_parts(x.shape[0], adapters)

@@ -50,3 +50,27 @@ def test_workspace_and_status(rows, with_adapters):
         with pytest.raises(ValueError):
             mod.rows_status(bad, rows, ad)
     mod.close()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_rows_with_a_stride(rows):
+    """x as a part of wider rows, with no residual of its own, also on another stream and captured."""
+    shape = LayerShape(256, 128, 16, 2, 1)
+    mod = MoEDecodeLayer(shape, synth.make_layer(shape, seed=2, device="cuda"), max_rows=1)
+    wide = torch.randn(rows, 512, generator=_gen(rows), device="cuda").bfloat16()
+    x = wide[:, 128:384]
+    want = mod.run_rows(x.contiguous())
+    assert torch.equal(mod.run_rows(x), want)
+    assert torch.equal(mod.run_rows(x, x.contiguous()), want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = mod.run_rows(x, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = mod.run_rows(x)
+    wide.copy_(torch.randn(rows, 512, generator=_gen(9), device="cuda").bfloat16())
+    graph.replay()
+    assert torch.equal(got, mod.run_rows(x.contiguous()))
+    mod.close()
