@@ -98,7 +98,8 @@ typedef struct moe_experts_config {
   int32_t num_experts;
   int32_t top_k;
   int32_t num_shared;
-  int32_t wdtype; /* moe_wdtype */
+  int32_t wdtype;         /* moe_wdtype            */
+  int32_t residual_dtype; /* moe_dtype of residual */
 } moe_experts_config;
 
 moe_status moe_decode_experts_check(const moe_experts_config* cfg);
@@ -107,7 +108,7 @@ moe_status moe_decode_experts_workspace(const moe_experts_config* cfg, int64_t r
 /*
  *   x        bf16 [rows, H], row r at x + r * x_stride elements (x_stride % 8 == 0, >= H)
  *   idx, w   int32 / fp32 [rows, top_k]
- *   residual bf16 [rows, H] or NULL (zero); out bf16 [rows, H], may be residual
+ *   residual [rows, H] of residual_dtype or NULL (zero); out bf16 [rows, H], may be a bf16 residual
  * x, residual, out and workspace 16-byte aligned; out must not overlap x.
  */
 moe_status moe_decode_experts(const moe_experts_config* cfg, const moe_decode_weights* weights, const void* x,

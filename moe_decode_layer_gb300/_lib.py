@@ -108,7 +108,8 @@ class RouteConfig(ctypes.Structure):
 
 
 class ExpertsConfig(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "num_experts", "top_k", "num_shared", "wdtype")]
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "num_experts", "top_k", "num_shared", "wdtype",
+                                              "residual_dtype")]
 
 
 class ProjectConfig(ctypes.Structure):

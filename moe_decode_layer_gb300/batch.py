@@ -193,10 +193,10 @@ def experts_workspace(shape: LayerShape, rows: int) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _experts_config(shape: LayerShape) -> _lib.ExpertsConfig:
+def _experts_config(shape: LayerShape, residual_dtype=torch.bfloat16) -> _lib.ExpertsConfig:
     _need(shape.wdtype in _lib.WDTYPE, f"unknown weight type {shape.wdtype!r}")
     cfg = _lib.ExpertsConfig(shape.hidden, shape.inter, shape.num_experts, shape.top_k, shape.num_shared,
-                             _lib.WDTYPE[shape.wdtype])
+                             _lib.WDTYPE[shape.wdtype], _DTYPES[residual_dtype])
     _lib.check(_lib.load().moe_decode_experts_check(cfg), "moe_decode_experts_check")
     return cfg
 
@@ -208,14 +208,17 @@ def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: t
     the shared experts'), as moe_decode_experts documents. ``weights``: the dict
     layout of synth.make_layer, or what :func:`expert_weights` made of it; ``x`` bf16
     [T, H], any row stride of a multiple of 8; ``idx`` int32 and ``w`` fp32 [T, k];
-    an index outside the experts (-1) takes no part."""
-    cfg = _experts_config(shape)
+    an index outside the experts (-1) takes no part. ``residual`` bf16 or fp32 [T, H];
+    ``out`` may be a bf16 one."""
+    rdtype = torch.bfloat16 if residual is None else residual.dtype
+    _need(rdtype in _DTYPES, "the residual is bf16 or fp32")
+    cfg = _experts_config(shape, rdtype)
     dev = x.get_device()
     px, t, sx = _rows(x, "x", shape.hidden, dev)
     cw = weights if isinstance(weights, _lib.Weights) else expert_weights(shape, weights, dev)
     pi = _tensor(idx, "idx", torch.int32, (t, shape.top_k), dev)
     pw = _tensor(w, "w", torch.float32, (t, shape.top_k), dev)
-    pr = None if residual is None else _tensor(residual, "residual", torch.bfloat16, (t, shape.hidden), dev)
+    pr = None if residual is None else _tensor(residual, "residual", rdtype, (t, shape.hidden), dev)
     s, leave = _enter(dev, stream)
     try:
         if out is None:

@@ -281,6 +281,7 @@ moe_status check_experts(const moe_experts_config* c) {
   if (c->hidden <= 0 || c->inter <= 0 || c->num_experts <= 0 || c->top_k <= 0 || c->num_shared < 0)
     return MOE_ERR_INVALID_ARG;
   if (c->wdtype != MOE_W_BF16 && c->wdtype != MOE_W_NVFP4 && c->wdtype != MOE_W_FP8_BLOCK) return MOE_ERR_UNSUPPORTED;
+  if (c->residual_dtype != MOE_BF16 && c->residual_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
   if (c->num_experts > 1024 || c->top_k > 16 || c->num_shared > 4 || !widths_ok(c->wdtype, c->hidden, c->inter))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -294,7 +295,7 @@ struct ExpertsArgs {
   int64_t x_stride;
   const int32_t* idx;
   const float* w;
-  const __nv_bfloat16* residual;
+  const void* residual;
   __nv_bfloat16* out;
   uint8_t* ws;
 };
@@ -412,9 +413,11 @@ cudaError_t launch_round(const ExpertsArgs& a, int64_t r0, ExpertsRound& r, cons
                       reinterpret_cast<__nv_bfloat16*>(r.y), s);
   if (e == cudaSuccess) e = launch_gemm(r.up, EPI_SWIGLU, fmt, r.up_maps, r.ents_max * r.up.nrb, r.up_layout, d, true, s);
   if (e == cudaSuccess) e = launch_gemm(r.down, EPI_F32, fmt, r.down_maps, r.ents_max * r.down.nrb, r.down_layout, d, true, s);
+  const bool f32 = c.residual_dtype == MOE_F32;
+  const void* residual = a.residual ? static_cast<const uint8_t*>(a.residual) + r0 * c.hidden * (f32 ? 4 : 2) : nullptr;
   if (e == cudaSuccess)
-    e = launch_combine(r.y, r.plan.pos, a.w + r0 * c.top_k, a.residual ? a.residual + r0 * c.hidden : nullptr,
-                       a.out + r0 * c.hidden, (int)r.rows, c.hidden, c.top_k, c.num_shared, s);
+    e = launch_combine(r.y, r.plan.pos, a.w + r0 * c.top_k, residual, f32, a.out + r0 * c.hidden, (int)r.rows, c.hidden,
+                       c.top_k, c.num_shared, s);
   return e;
 }
 
@@ -535,6 +538,7 @@ moe_status moe_decode_experts(const moe_experts_config* c, const moe_decode_weig
   if (!aligned16(x) || !aligned16(residual) || !aligned16(out) || !aligned16(workspace)) return MOE_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(idx) % 4 || reinterpret_cast<uintptr_t>(w) % 4) return MOE_ERR_INVALID_ARG;
   if (x_stride < c->hidden || x_stride % 8) return MOE_ERR_INVALID_ARG;
+  if (residual == out && c->residual_dtype == MOE_F32) return MOE_ERR_INVALID_ARG;
   const int fmt = fmt_of(c->wdtype);
   const bool sh = c->num_shared > 0;
   if (!wt->w13 || !wt->w2 || !aligned16(wt->w13) || !aligned16(wt->w2)) return MOE_ERR_INVALID_ARG;
@@ -558,7 +562,7 @@ moe_status moe_decode_experts(const moe_experts_config* c, const moe_decode_weig
                          x_stride,
                          idx,
                          w,
-                         static_cast<const __nv_bfloat16*>(residual),
+                         residual,
                          static_cast<__nv_bfloat16*>(out),
                          static_cast<uint8_t*>(workspace)};
   // The first round's and the last one's descriptors and layouts before any launch (those

@@ -192,15 +192,17 @@ constexpr int kCombineThreads = 256;
 // would halve, and add the rounding of each of a row's terms to the sum's.
 __global__ void __launch_bounds__(kCombineThreads)
     combine_kernel(const float* y, const int* pos, const float* __restrict__ w,
-                   const __nv_bfloat16* residual, __nv_bfloat16* out, int rows, int hidden, int top_k, int shared) {
+                   const void* residual, bool residual_f32, __nv_bfloat16* out, int rows, int hidden, int top_k, int shared) {
   pdl_wait();
   const int cols = hidden / 4;
   const int64_t i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
   if (i >= (int64_t)rows * cols) return;
   const int t = (int)(i / cols), c = (int)(i % cols) * 4;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (residual) {
-    const uint2 r = *reinterpret_cast<const uint2*>(residual + (size_t)t * hidden + c);
+  if (residual && residual_f32) {
+    a = *reinterpret_cast<const float4*>(static_cast<const float*>(residual) + (size_t)t * hidden + c);
+  } else if (residual) {
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(residual) + (size_t)t * hidden + c);
     a = make_float4(bf16lo(r.x), bf16hi(r.x), bf16lo(r.y), bf16hi(r.y));
   }
 #pragma unroll 4
@@ -269,7 +271,7 @@ cudaError_t launch_shrink(const __nv_bfloat16* x, int64_t x_stride, const __nv_b
   return cudaLaunchKernelEx(&c, shrink_kernel, x, x_stride, a, scale, ids, u, inner, rank, adapters);
 }
 
-cudaError_t launch_combine(const float* y, const int* pos, const float* w, const __nv_bfloat16* residual,
+cudaError_t launch_combine(const float* y, const int* pos, const float* w, const void* residual, bool residual_f32,
                            __nv_bfloat16* out, int rows, int hidden, int top_k, int shared, cudaStream_t s) {
   cudaLaunchConfig_t c = {};
   const int64_t n = (int64_t)rows * (hidden / 4);
@@ -281,7 +283,7 @@ cudaError_t launch_combine(const float* y, const int* pos, const float* w, const
   a[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, combine_kernel, y, pos, w, residual, out, rows, hidden, top_k, shared);
+  return cudaLaunchKernelEx(&c, combine_kernel, y, pos, w, residual, residual_f32, out, rows, hidden, top_k, shared);
 }
 
 }  // namespace rows

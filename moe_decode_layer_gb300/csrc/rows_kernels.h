@@ -32,7 +32,8 @@ cudaError_t launch_spread(const __nv_bfloat16* x, int64_t x_stride, const int* s
                           int64_t positions, int inner, __nv_bfloat16* dst, cudaStream_t s);
 
 // out = bf16(residual + sum_j w_j y[pos_j] + sum_s y[pairs + s * rows + row])
-cudaError_t launch_combine(const float* y, const int* pos, const float* w, const __nv_bfloat16* residual,
+// residual: bf16 or (residual_f32) fp32
+cudaError_t launch_combine(const float* y, const int* pos, const float* w, const void* residual, bool residual_f32,
                            __nv_bfloat16* out, int rows, int hidden, int top_k, int shared, cudaStream_t s);
 
 // u[t, j] = scale_a sum_k A_a[j, k] x[t, k] in fp32, a = ids[t]; nothing for rows without an adapter

@@ -125,9 +125,8 @@ class MoEDecodeLayer:
         a multiple of 8; ``residual`` (x, when not given) is contiguous. ``num_groups``,
         ``top_groups`` and ``group_best`` limit the choice to the best groups of
         experts. ``adapters``: the low-rank adapters of the one shared expert's
-        gate/up and down projections, and ``adapter_ids`` int32 [T] each row's; the
-        shared expert's output is then added to the residual in a rounding to
-        bf16 of its own. Not for layers with pre_rmsnorm or transposed down matrices.
+        gate/up and down projections, and ``adapter_ids`` int32 [T] each row's. All terms
+        and the residual are summed in fp32 and rounded once. Not for layers with pre_rmsnorm or transposed down matrices.
 
         ``workspace``: uint8, of rows_workspace bytes; after a run with one rows_status
         tells whether its device-side waits ended in time (without one, each operator
@@ -157,7 +156,7 @@ class MoEDecodeLayer:
             h = batch.project(x, w13, wdtype=shape.wdtype, swiglu=True, adapters=adapters[0], adapter_ids=adapter_ids,
                               workspace=ws["up"], stream=stream)
             residual = batch.project(h, w2, wdtype=shape.wdtype, adapters=adapters[1], adapter_ids=adapter_ids,
-                                     addend=residual, workspace=ws["down"], stream=stream)
+                                     addend=residual, out_dtype=torch.float32, workspace=ws["down"], stream=stream)
             shape = dataclasses.replace(shape, num_shared=0)
         elif adapter_ids is not None:
             raise ValueError("adapters and adapter_ids come together")
@@ -172,7 +171,8 @@ class MoEDecodeLayer:
             for name, ad, inner, outer, swiglu in (("up", adapters[0], s.hidden, s.inter, True),
                                                    ("down", adapters[1], s.inter, s.hidden, False)):
                 need[name] = batch.project_workspace(inner, outer, rows, wdtype=s.wdtype, swiglu=swiglu,
-                                                     rank=ad.a.shape[1], num_adapters=ad.a.shape[0])
+                                                     rank=ad.a.shape[1], num_adapters=ad.a.shape[0],
+                                                     out_dtype=torch.bfloat16 if swiglu else torch.float32)
             s = dataclasses.replace(s, num_shared=0)
         need["experts"] = batch.experts_workspace(s, rows)
         parts, at = {}, 0

@@ -5,6 +5,7 @@ import torch
 
 from moe_decode_layer_gb300 import LayerShape, _lib, batch, synth
 from moe_decode_layer_gb300.layer import MoEDecodeLayer
+from tests import rows_reference as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,40 @@ def test_rows_with_a_stride(rows):
     graph.replay()
     assert torch.equal(got, mod.run_rows(x.contiguous()))
     mod.close()
+
+
+@pytest.mark.parametrize("rows", [2, 100])
+def test_one_rounding_with_adapters(rows):
+    """256 + 1 (shared expert) + 1 (routed) is 258: a rounding to bf16 after the first sum would lose both."""
+    shape = LayerShape(256, 128, 16, 1, 1)
+    layer = {k: torch.zeros_like(v) if torch.is_tensor(v) else v for k, v in synth.make_layer(shape, seed=3, device="cuda").items()}
+    for p in ("", "sh_"):  # h_0 = silu(64) / 64 = 1, y = h_0
+        layer[p + "w13"][:, 0, 0], layer[p + "w13"][:, 128, 0] = 64, 1 / 64
+        layer[p + "w2"][:, :, 0] = 1
+    mod = MoEDecodeLayer(shape, layer, max_rows=1)
+    x = torch.zeros(rows, 256, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    r = torch.full_like(x, 256)
+    g = _gen(1)
+    up, down = _adapters(g, 2, 8, 256, 256), _adapters(g, 2, 8, 128, 256)
+    up.b.zero_(), down.b.zero_()
+    ids = torch.randint(-1, 2, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    assert bool((mod.run_rows(x, r) == 258).all())
+    assert bool((mod.run_rows(x, r, adapters=(up, down), adapter_ids=ids) == 258).all())
+    mod.close()
+
+
+@pytest.mark.parametrize("rows", [1, 50, 16384 + 3])
+def test_fp32_residual(rows):
+    shape = LayerShape(72, 24, 5, 2, 1)
+    layer = synth.make_layer(shape, seed=4, device="cuda")
+    g = _gen(rows)
+    x = torch.randn(rows, 72, generator=g, device="cuda").bfloat16()
+    idx = torch.randint(0, 5, (rows, 2), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand(rows, 2, generator=g, device="cuda")
+    r = torch.randn(rows, 72, generator=g, device="cuda")
+    out = batch.experts(shape, layer, x, idx, w, residual=r)
+    want, bound = ref.experts(shape, layer, x, idx, w, r)
+    assert bool(((out.double() - want).abs() <= bound).all())
+    with pytest.raises(ValueError):
+        batch.experts(shape, layer, x, idx, w, residual=r.half())

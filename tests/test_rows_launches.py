@@ -121,3 +121,12 @@ def test_status_of_a_short_workspace_is_refused():
     for bad in (torch.empty(_lib.ROWS_STATUS_BYTES - 1, dtype=torch.uint8), torch.empty(4096), torch.empty(0, dtype=torch.uint8)):
         with pytest.raises(ValueError, match="workspace must be"):
             batch.status(bad)
+
+
+def test_residual_types(lib):
+    """fp32 and bf16 residuals; the result may be in a bf16 one's place only."""
+    check = lib.moe_decode_experts_check
+    base = dict(hidden=256, inter=128, num_experts=16, top_k=2, num_shared=1, wdtype=0)
+    assert [check(_lib.ExpertsConfig(**base, residual_dtype=d)) for d in (0, 1, 2)] == [OK, OK, _lib.MOE_ERR_UNSUPPORTED]
+    assert _experts(lib, 8) == OK  # residual and out are one address
+    assert _experts(lib, 8, residual_dtype=1) == _lib.MOE_ERR_INVALID_ARG
