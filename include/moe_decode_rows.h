@@ -11,6 +11,7 @@
  *   moe_decode_project  one projection that all rows share, beside it a low-rank
  *                       adapter per row (requests with adapters of their own)
  *
+ * Addresses are multiples of 16 where it says so below, and of their type elsewhere.
  * They keep no state: every call gets its buffers, and the workspace that two of
  * them need, from the caller. Calls may run at the same time on different streams
  * or threads when their workspaces and outputs are different memory. Each enqueues its work on

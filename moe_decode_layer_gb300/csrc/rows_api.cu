@@ -25,6 +25,7 @@ constexpr int kStatusKernels = 2;
 constexpr int kMinN = 32;  // rows of a tile of experts' rows at least
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -511,8 +512,7 @@ moe_status moe_decode_route(const moe_route_config* c, const void* logits, int64
   if (rows == 0) return MOE_OK;
   const int align = c->logits_dtype == MOE_F32 ? 4 : 2;
   if (!logits || !idx || !w || stride < c->num_experts) return MOE_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(logits) % align || reinterpret_cast<uintptr_t>(bias) % 4 ||
-      reinterpret_cast<uintptr_t>(idx) % 4 || reinterpret_cast<uintptr_t>(w) % 4)
+  if (reinterpret_cast<uintptr_t>(logits) % align || !aligned4(bias) || !aligned4(idx) || !aligned4(w))
     return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_route(*c, logits, stride, bias, rows, idx, w, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -536,7 +536,7 @@ moe_status moe_decode_experts(const moe_experts_config* c, const moe_decode_weig
   if (rows == 0) return MOE_OK;
   if (!wt || !x || !idx || !w || !out || !workspace) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(out) || !aligned16(workspace)) return MOE_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(idx) % 4 || reinterpret_cast<uintptr_t>(w) % 4) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(idx) || !aligned4(w)) return MOE_ERR_INVALID_ARG;
   if (x_stride < c->hidden || x_stride % 8) return MOE_ERR_INVALID_ARG;
   if (residual == out && c->residual_dtype == MOE_F32) return MOE_ERR_INVALID_ARG;
   const int fmt = fmt_of(c->wdtype);
@@ -549,6 +549,9 @@ moe_status moe_decode_experts(const moe_experts_config* c, const moe_decode_weig
       return MOE_ERR_INVALID_ARG;
   }
   if (fmt == FMT_NVFP4 && (!wt->w13_gscale || !wt->w2_gscale || (sh && (!wt->sh_w13_gscale || !wt->sh_w2_gscale))))
+    return MOE_ERR_INVALID_ARG;
+  if (fmt == FMT_NVFP4 && (!aligned4(wt->w13_gscale) || !aligned4(wt->w2_gscale) ||
+                           (sh && (!aligned4(wt->sh_w13_gscale) || !aligned4(wt->sh_w2_gscale)))))
     return MOE_ERR_INVALID_ARG;
   size_t need = 0;
   moe_decode_experts_workspace(c, rows, &need);
@@ -613,10 +616,10 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
   if (x_stride < c->inner || x_stride % 8) return MOE_ERR_INVALID_ARG;
   const int fmt = fmt_of(c->wdtype);
   if (fmt != FMT_BF16 && (!wt->w_scale || !aligned16(wt->w_scale))) return MOE_ERR_INVALID_ARG;
-  if (fmt == FMT_NVFP4 && !wt->w_gscale) return MOE_ERR_INVALID_ARG;
+  if (fmt == FMT_NVFP4 && (!wt->w_gscale || !aligned4(wt->w_gscale))) return MOE_ERR_INVALID_ARG;
   if (c->num_adapters) {
     if (!wt->a || !wt->b || !ids || !aligned16(wt->a) || !aligned16(wt->b)) return MOE_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(ids) % 4) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(ids) || !aligned4(wt->scale)) return MOE_ERR_INVALID_ARG;
   }
   size_t need = 0;
   moe_decode_project_workspace(c, rows, &need);

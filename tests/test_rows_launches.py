@@ -10,7 +10,7 @@ import torch
 from moe_decode_layer_gb300 import _lib, batch, build
 from tests import fake_cuda
 
-OK, CUDA = _lib.MOE_OK, _lib.MOE_ERR_CUDA
+OK, CUDA, BAD = _lib.MOE_OK, _lib.MOE_ERR_CUDA, _lib.MOE_ERR_INVALID_ARG
 P = ctypes.c_void_p(1 << 20)
 
 
@@ -26,20 +26,32 @@ def _weights(cls):
     return w
 
 
-def _experts(lib, rows, fail_encode=-1, fail_launch=-1, pending=0, stride=256, **kw):
+# places far enough apart for the largest call here
+X, OUT, RES, WS = (ctypes.c_void_p(i << 36) for i in (1, 2, 3, 4))
+
+
+def _experts(lib, rows, fail_encode=-1, fail_launch=-1, pending=0, stride=256, x=X, out=OUT, residual=RES, idx=P, w=P,
+             weights=(), **kw):
     cfg = _lib.ExpertsConfig(**{**dict(hidden=256, inter=128, num_experts=16, top_k=2, num_shared=1, wdtype=0), **kw})
     need = ctypes.c_size_t()
     assert lib.moe_decode_experts_workspace(cfg, rows, need) == OK
     lib.fake_reset(fail_encode, fail_launch, pending)
-    return lib.moe_decode_experts(cfg, _weights(_lib.Weights), P, stride, P, P, P, P, rows, P, need, None)
+    wt = _weights(_lib.Weights)
+    for name, v in dict(weights).items():
+        setattr(wt, name, v)
+    return lib.moe_decode_experts(cfg, wt, x, stride, idx, w, residual, out, rows, WS, need, None)
 
 
-def _project(lib, rows, fail_encode=-1, fail_launch=-1, pending=0, **kw):
-    cfg = _lib.ProjectConfig(**{**dict(inner=256, outer=128, swiglu=0, wdtype=0, rank=16, num_adapters=4, out_dtype=0), **kw})
+def _project(lib, rows, fail_encode=-1, fail_launch=-1, pending=0, stride=256, x=X, out=OUT, addend=None, ids=P,
+             weights=(), **kw):
+    cfg = _lib.ProjectConfig(**{**dict(inner=256, outer=256, swiglu=0, wdtype=0, rank=16, num_adapters=4, out_dtype=0), **kw})
     need = ctypes.c_size_t()
     assert lib.moe_decode_project_workspace(cfg, rows, need) == OK
     lib.fake_reset(fail_encode, fail_launch, pending)
-    return lib.moe_decode_project(cfg, _weights(_lib.ProjectWeights), P, 256, P, None, P, rows, P, need, None)
+    wt = _weights(_lib.ProjectWeights)
+    for name, v in dict(weights).items():
+        setattr(wt, name, v)
+    return lib.moe_decode_project(cfg, wt, x, stride, ids, addend, out, rows, WS, need, None)
 
 
 def _names(lib):
@@ -128,5 +140,34 @@ def test_residual_types(lib):
     check = lib.moe_decode_experts_check
     base = dict(hidden=256, inter=128, num_experts=16, top_k=2, num_shared=1, wdtype=0)
     assert [check(_lib.ExpertsConfig(**base, residual_dtype=d)) for d in (0, 1, 2)] == [OK, OK, _lib.MOE_ERR_UNSUPPORTED]
-    assert _experts(lib, 8) == OK  # residual and out are one address
-    assert _experts(lib, 8, residual_dtype=1) == _lib.MOE_ERR_INVALID_ARG
+    assert _experts(lib, 8, residual=OUT) == OK
+    assert _experts(lib, 8, residual=RES, residual_dtype=1) == OK
+    assert _experts(lib, 8, residual=OUT, residual_dtype=1) == BAD
+
+
+def _at(v):
+    return ctypes.c_void_p(v)
+
+
+@pytest.mark.parametrize("kw", [dict(x=None), dict(x=_at(4104)), dict(stride=248), dict(stride=260), dict(idx=None), dict(idx=_at(4098)),
+                                dict(w=None), dict(w=_at(4098)), dict(out=None), dict(out=_at(4104)), dict(residual=_at(4104))] +
+                         [dict(weights={n: v}) for n in ("w13", "w2", "sh_w13", "sh_w2", "w13_scale", "w2_scale", "sh_w13_scale",
+                                                         "sh_w2_scale") for v in (None, _at(4104))] +
+                         [dict(weights={n: v}) for n in ("w13_gscale", "w2_gscale", "sh_w13_gscale", "sh_w2_gscale")
+                          for v in (None, _at(4098))], ids=str)
+def test_experts_refuse_one_bad_address(lib, kw):
+    """Each argument alone, beside others that are taken."""
+    shape = dict(hidden=256, inter=256, wdtype=1)
+    assert _experts(lib, 4, **shape) == OK
+    assert _experts(lib, 4, **{**shape, **kw}) == BAD and lib.fake_launches() == 0
+
+
+@pytest.mark.parametrize("kw", [dict(x=None), dict(x=_at(4104)), dict(stride=248), dict(stride=260), dict(ids=None), dict(ids=_at(4098)),
+                                dict(out=None), dict(out=_at(4104)), dict(addend=_at(4104)), dict(swiglu=1, addend=RES)] +
+                         [dict(weights={n: v}) for n in ("w", "w_scale", "a", "b") for v in (None, _at(4104))] +
+                         [dict(weights={"w_gscale": None}), dict(weights={"w_gscale": _at(4098)}), dict(weights={"scale": _at(4098)})],
+                         ids=str)
+@pytest.mark.parametrize("rows", [4, 200])
+def test_project_refuses_one_bad_address(lib, rows, kw):
+    assert _project(lib, rows, wdtype=1) == OK and _project(lib, rows, wdtype=1, addend=RES, weights={"scale": None}) == OK
+    assert _project(lib, rows, wdtype=1, **kw) == BAD and lib.fake_launches() == 0
