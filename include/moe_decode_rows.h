@@ -110,7 +110,8 @@ moe_status moe_decode_experts_workspace(const moe_experts_config* cfg, int64_t r
  *   x        bf16 [rows, H], row r at x + r * x_stride elements (x_stride % 8 == 0, >= H)
  *   idx, w   int32 / fp32 [rows, top_k]
  *   residual [rows, H] of residual_dtype or NULL (zero); out bf16 [rows, H], may be a bf16 residual
- * x, residual, out and workspace 16-byte aligned; out must not overlap x.
+ * x, residual, out and workspace 16-byte aligned. out may be x as well (rows without gaps,
+ * x_stride H); any other overlap of out with x or the residual is refused.
  */
 moe_status moe_decode_experts(const moe_experts_config* cfg, const moe_decode_weights* weights, const void* x,
                               int64_t x_stride, const int32_t* idx, const float* w, const void* residual,
@@ -154,7 +155,8 @@ moe_status moe_decode_project_workspace(const moe_project_config* cfg, int64_t r
  *   adapter_ids int32 [rows]
  *   addend      bf16 [rows, O] or NULL; not with swiglu. May be out (out_dtype MOE_BF16)
  *   out         [rows, O] of out_dtype
- * x, addend, out, workspace and the weights 16-byte aligned; out must not overlap x.
+ * x, addend, out, workspace and the weights 16-byte aligned; an overlap of out with x, or
+ * another one with addend, is refused.
  */
 moe_status moe_decode_project(const moe_project_config* cfg, const moe_project_weights* weights, const void* x,
                               int64_t x_stride, const int32_t* adapter_ids, const void* addend, void* out,

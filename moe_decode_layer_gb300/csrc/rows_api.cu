@@ -26,6 +26,18 @@ constexpr int kMinN = 32;  // rows of a tile of experts' rows at least
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Whether the bytes at a share any with those at b.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const intptr_t d = static_cast<const char*>(b) - static_cast<const char*>(a);
+  return a && b && d < a_bytes && -d < b_bytes;
+}
+// Whether rows of `width` bytes every `stride` bytes share any with those at out.
+bool rows_overlap(const void* x, int64_t stride, int64_t width, int64_t rows, const void* out, int64_t bytes) {
+  const intptr_t d = static_cast<const char*>(out) - static_cast<const char*>(x);
+  if (d + bytes <= 0) return false;
+  const int64_t last = std::min(rows - 1, (d + bytes - 1) / stride);  // the last row that starts before out's end
+  return last * stride + width > d;
+}
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -538,7 +550,14 @@ moe_status moe_decode_experts(const moe_experts_config* c, const moe_decode_weig
   if (!aligned16(x) || !aligned16(residual) || !aligned16(out) || !aligned16(workspace)) return MOE_ERR_INVALID_ARG;
   if (!aligned4(idx) || !aligned4(w)) return MOE_ERR_INVALID_ARG;
   if (x_stride < c->hidden || x_stride % 8) return MOE_ERR_INVALID_ARG;
-  if (residual == out && c->residual_dtype == MOE_F32) return MOE_ERR_INVALID_ARG;
+  // The combine writes a round's rows after the products have read them: out may be x
+  // itself, row for row, and so it may be the residual; nothing in between.
+  const bool f32 = c->residual_dtype == MOE_F32;
+  const int64_t out_bytes = rows * c->hidden * 2;
+  if ((residual != out || f32) && overlap(residual, f32 ? 2 * out_bytes : out_bytes, out, out_bytes)) return MOE_ERR_INVALID_ARG;
+  if ((x != out || (x_stride != c->hidden && rows > 1)) &&
+      rows_overlap(x, x_stride * 2, c->hidden * 2, rows, out, out_bytes))
+    return MOE_ERR_INVALID_ARG;
   const int fmt = fmt_of(c->wdtype);
   const bool sh = c->num_shared > 0;
   if (!wt->w13 || !wt->w2 || !aligned16(wt->w13) || !aligned16(wt->w2)) return MOE_ERR_INVALID_ARG;
@@ -614,6 +633,11 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
   if (!aligned16(x) || !aligned16(addend) || !aligned16(out) || !aligned16(workspace) || !aligned16(wt->w))
     return MOE_ERR_INVALID_ARG;
   if (x_stride < c->inner || x_stride % 8) return MOE_ERR_INVALID_ARG;
+  // a tile of out is written while others still read x; its addends are read just before
+  const bool f32 = c->out_dtype == MOE_F32;
+  const int64_t add_bytes = rows * c->outer * 2, out_bytes = f32 ? 2 * add_bytes : add_bytes;
+  if (rows_overlap(x, x_stride * 2, c->inner * 2, rows, out, out_bytes)) return MOE_ERR_INVALID_ARG;
+  if ((addend != out || f32) && overlap(addend, add_bytes, out, out_bytes)) return MOE_ERR_INVALID_ARG;
   const int fmt = fmt_of(c->wdtype);
   if (fmt != FMT_BF16 && (!wt->w_scale || !aligned16(wt->w_scale))) return MOE_ERR_INVALID_ARG;
   if (fmt == FMT_NVFP4 && (!wt->w_gscale || !aligned4(wt->w_gscale))) return MOE_ERR_INVALID_ARG;

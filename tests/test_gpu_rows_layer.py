@@ -112,3 +112,15 @@ def test_fp32_residual(rows):
     assert bool(((out.double() - want).abs() <= bound).all())
     with pytest.raises(ValueError):
         batch.experts(shape, layer, x, idx, w, residual=r.half())
+
+
+@pytest.mark.parametrize("wdtype", ["bf16", "fp8", "nvfp4"])
+def test_result_in_the_place_of_x(wdtype):
+    """A step in place, as run() does it: one round of rows, and three."""
+    shape = LayerShape(256, 256, 16, 2, 1, wdtype)
+    mod = MoEDecodeLayer(shape, synth.make_layer(shape, seed=5, device="cuda"), max_rows=8)
+    for rows in (1, 8, 700, 2 * 16384 + 77):
+        x = torch.randn(rows, 256, generator=_gen(rows), device="cuda").bfloat16()
+        want = mod.run_rows(x)
+        assert mod.run_rows(x, out=x) is x and torch.equal(x, want)
+    mod.close()

@@ -171,3 +171,33 @@ def test_experts_refuse_one_bad_address(lib, kw):
 def test_project_refuses_one_bad_address(lib, rows, kw):
     assert _project(lib, rows, wdtype=1) == OK and _project(lib, rows, wdtype=1, addend=RES, weights={"scale": None}) == OK
     assert _project(lib, rows, wdtype=1, **kw) == BAD and lib.fake_launches() == 0
+
+
+def test_experts_overlaps(lib):
+    """out in x's or the residual's place, row for row, is taken; anything between is refused."""
+    rows, row = 40, 512  # bytes of a row
+    size = rows * row
+    for x, residual, out, stride, status in (
+            (X, X, X, 256, OK), (X, None, X, 256, OK), (X, RES, RES, 256, OK), (X, X, X, 264, BAD), (X, RES, X, 264, BAD),
+            (X, RES, _at(X.value + row), 256, BAD), (X, RES, _at(X.value - row), 256, BAD), (X, RES, _at(X.value + 16), 256, BAD),
+            (X, RES, _at(X.value + size), 256, OK), (X, RES, _at(X.value - size), 256, OK), (X, RES, _at(X.value + size - 16), 256, BAD),
+            (X, RES, _at(RES.value + row), 256, BAD), (X, RES, _at(RES.value - size + 16), 256, BAD), (X, RES, _at(RES.value + size), 256, OK),
+            # out in a gap between two rows of x
+            (X, RES, _at(X.value + 512), 16384, OK), (X, RES, _at(X.value + 32768 - size), 16384, OK),
+            (X, RES, _at(X.value + 32784 - size), 16384, BAD), (X, RES, _at(X.value + 32768 + 512), 16384, OK)):
+        assert _experts(lib, rows, x=x, residual=residual, out=out, stride=stride) == status, (x, residual, out, stride)
+    # one row has no stride; fp32 residuals are twice as wide
+    assert _experts(lib, 1, x=X, residual=X, out=X, stride=512) == OK
+    assert _experts(lib, rows, residual=_at(OUT.value - 2 * size), residual_dtype=1) == OK
+    assert _experts(lib, rows, residual=_at(OUT.value - 2 * size + 16), residual_dtype=1) == BAD
+
+
+@pytest.mark.parametrize("rows", [4, 200])
+def test_project_overlaps(lib, rows):
+    size = rows * 512
+    for kw, status in ((dict(out=X), BAD), (dict(out=_at(X.value + size)), OK), (dict(out=_at(X.value + size - 16)), BAD),
+                       (dict(out=_at(X.value - size)), OK), (dict(out=_at(X.value - size + 16)), BAD),
+                       (dict(addend=OUT), OK), (dict(addend=OUT, out_dtype=1), BAD), (dict(addend=_at(OUT.value + 16)), BAD),
+                       (dict(addend=_at(OUT.value + size)), OK), (dict(addend=_at(OUT.value + size), out_dtype=1), BAD),
+                       (dict(addend=_at(OUT.value - size), out_dtype=1), OK), (dict(out=_at(X.value - size), out_dtype=1), BAD)):
+        assert _project(lib, rows, **kw) == status, kw
