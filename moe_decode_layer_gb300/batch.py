@@ -161,17 +161,36 @@ def _expert_tensors(shape: LayerShape) -> tuple:
 
 def expert_weights(shape: LayerShape, weights: dict, device) -> _lib.Weights:
     """The C struct of a layer's routed and shared expert weights (dict layout of
-    synth.make_layer) on ``device`` (an index or a torch device)."""
+    synth.make_layer) on ``device`` (an index or a torch device). It keeps the tensors
+    alive, and experts() takes it for these weights' sizes and device only."""
     if weights.get("w2_layout", "h_i") != "h_i":
         raise ValueError("down matrices must be stored [E, H, I] (w2_layout h_i)")
-    dev = device if isinstance(device, int) else -1 if device.type == "cpu" else device.index
+    if isinstance(device, int):
+        dev = device
+    elif device.type == "cpu":
+        dev = -1
+    else:
+        dev = torch.cuda.current_device() if device.index is None else device.index
     out = _lib.Weights()
+    out.made_for, out.tensors = (shape, dev), []
     for key, field, dtype, size in _expert_tensors(shape):
         t = weights.get(key)
         if t is None:
             raise ValueError(f"weights lack {key}")
         setattr(out, field, _tensor(t, key, dtype, size, dev))
+        out.tensors.append(t)
     return out
+
+
+def _made_for(weights: _lib.Weights, shape: LayerShape, dev: int) -> _lib.Weights:
+    """``weights``, when expert_weights made it for this shape's weights on this device."""
+    if not hasattr(weights, "made_for"):
+        raise ValueError("weights must be a layer's dict or what expert_weights made of it")
+    have, at = weights.made_for
+    if at != dev or shape.num_shared > have.num_shared or \
+            any(getattr(have, f) != getattr(shape, f) for f in ("hidden", "inter", "num_experts", "wdtype")):
+        raise ValueError(f"these weights are of {have} on device {at}, and not of {shape} on device {dev}")
+    return weights
 
 
 def _workspace(workspace: torch.Tensor | None, need: int, dev: int) -> torch.Tensor:
@@ -215,7 +234,7 @@ def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: t
     cfg = _experts_config(shape, rdtype)
     dev = x.get_device()
     px, t, sx = _rows(x, "x", shape.hidden, dev)
-    cw = weights if isinstance(weights, _lib.Weights) else expert_weights(shape, weights, dev)
+    cw = _made_for(weights, shape, dev) if isinstance(weights, _lib.Weights) else expert_weights(shape, weights, dev)
     pi = _tensor(idx, "idx", torch.int32, (t, shape.top_k), dev)
     pw = _tensor(w, "w", torch.float32, (t, shape.top_k), dev)
     pr = None if residual is None else _tensor(residual, "residual", rdtype, (t, shape.hidden), dev)

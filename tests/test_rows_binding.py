@@ -1,0 +1,56 @@
+"""The binding of the many-row operators without a GPU: weights kept as a C struct, devices and streams."""
+
+import contextlib
+import dataclasses
+import gc
+import types
+import weakref
+
+import pytest
+import torch
+
+from moe_decode_layer_gb300 import LayerShape, _lib, batch
+
+SHAPE = LayerShape(256, 128, 16, 2, 1)
+
+
+def _layer():
+    return {n: torch.zeros(s, dtype=torch.bfloat16) for n, s in (("w13", (16, 256, 256)), ("w2", (16, 256, 128)),
+                                                                 ("sh_w13", (1, 256, 256)), ("sh_w2", (1, 256, 128)))}
+
+
+def test_weights_struct_keeps_its_tensors():
+    """The addresses that a call will read stay valid when the dict goes."""
+    layer = _layer()
+    refs = [weakref.ref(t) for t in layer.values()]
+    w = batch.expert_weights(SHAPE, layer, torch.device("cpu"))
+    addresses = [t.data_ptr() for t in layer.values()]
+    del layer
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    assert [w.w13, w.w2, w.sh_w13, w.sh_w2] == addresses
+    del w
+    gc.collect()
+    assert all(r() is None for r in refs)
+
+
+def test_weights_struct_of_another_layer_is_refused():
+    """Sizes that the kernels would read past, and another device."""
+    w = batch.expert_weights(SHAPE, _layer(), -1)
+    x, idx, f = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for kw in (dict(inter=256), dict(num_experts=17), dict(num_shared=2), dict(wdtype="fp8")):
+        with pytest.raises(ValueError, match="these weights are of"):
+            batch.experts(dataclasses.replace(SHAPE, **kw), w, x, idx, f)
+    with pytest.raises(ValueError, match="these weights are of"):
+        batch._made_for(w, SHAPE, 0)
+    with pytest.raises(ValueError, match="what expert_weights made"):
+        batch.experts(SHAPE, _lib.Weights(), x, idx, f)
+    # other choices, or without the shared expert: the same weights
+    for kw in (dict(), dict(top_k=3), dict(num_shared=0)):
+        assert batch._made_for(w, dataclasses.replace(SHAPE, **kw), -1) is w
+
+
+def test_weights_on_the_current_device(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    with pytest.raises(ValueError, match="on device 3: got"):
+        batch.expert_weights(SHAPE, _layer(), torch.device("cuda"))
