@@ -66,6 +66,8 @@ def _enter(dev: int, stream):
     for. The usual call, on the current device and stream, has nothing to leave."""
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"a stream of device {stream.device.index} for tensors on device {dev}")
     if stream is None and dev == torch._C._cuda_getDevice():
         return torch._C._cuda_getCurrentRawStream(dev), None
     stack = contextlib.ExitStack()

@@ -54,3 +54,55 @@ def test_weights_on_the_current_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
     with pytest.raises(ValueError, match="on device 3: got"):
         batch.expert_weights(SHAPE, _layer(), torch.device("cuda"))
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """torch's device and stream contexts as a log; device 0 is current."""
+    log = []
+
+    def context(name):
+        @contextlib.contextmanager
+        def enter(what):
+            log.append((name, what))
+            yield
+            log.append((name, "left"))
+        return enter
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 100 + dev, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", context("device"))
+    monkeypatch.setattr(torch.cuda, "stream", context("stream"))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: _stream(dev, 200 + dev))
+    return log
+
+
+def _stream(dev, handle):
+    return types.SimpleNamespace(device=torch.device("cuda", dev), cuda_stream=handle)
+
+
+def test_devices_and_streams_of_a_call(two_devices):
+    """Tensors on the current device, on another one, and a stream that is given: the handle the library gets,
+    what is current while it is called, and that both are left again in order."""
+    assert batch._enter(0, None) == (100, None) and two_devices == []
+    handle, leave = batch._enter(1, None)
+    assert handle == 201 and two_devices == [("device", 1)]
+    leave.close()
+    assert two_devices == [("device", 1), ("device", "left")]
+    for dev in (0, 1):
+        two_devices.clear()
+        stream = _stream(dev, 7)
+        handle, leave = batch._enter(dev, stream)
+        assert handle == 7 and two_devices == [("device", dev), ("stream", stream)]
+        leave.close()
+        assert two_devices[2:] == [("stream", "left"), ("device", "left")]
+
+
+def test_streams_of_another_device_are_refused(two_devices):
+    """The stream's context would make its own device current, which is not the buffers'."""
+    for dev in (0, 1):
+        with pytest.raises(ValueError, match="a stream of device"):
+            batch._enter(dev, _stream(1 - dev, 7))
+    with pytest.raises(ValueError, match="CUDA device"):
+        batch._enter(-1, None)
+    assert two_devices == []
