@@ -70,13 +70,13 @@ def measured_peak():
 
 
 def sources_digest() -> str:
-    """Digest of the CUDA sources: a traffic record holds only for the sources it
-    was captured with."""
+    """Digest of the decode step's CUDA sources, the headers they include among them:
+    a traffic record holds only for the sources it was captured with."""
     import hashlib
-    csrc = os.path.join(ROOT, "moe_decode_layer_gb300", "csrc")
+    from moe_decode_layer_gb300 import build
     h = hashlib.sha256()
-    for name in sorted(os.listdir(csrc)):
-        with open(os.path.join(csrc, name), "rb") as f:
+    for name in build.sources_of(build.DECODE_SOURCES):
+        with open(os.path.join(build.CSRC, name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
 

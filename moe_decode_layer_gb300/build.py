@@ -13,6 +13,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -25,8 +26,11 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_decode.so")
 
-SOURCES = ["api.cu", "kernels_bf16.cu", "kernels_nvfp4.cu", "kernels_fp8.cu", "kernels_flat.cu", "kernels_sk.cu", "static_run.cu",
-           "rows_api.cu", "rows_kernels.cu", "rows_route.cu", "rows_gemm.cu", "rows_gemm_fp8.cu", "rows_gemm_nvfp4.cu"]
+DECODE_SOURCES = ["api.cu", "kernels_bf16.cu", "kernels_nvfp4.cu", "kernels_fp8.cu", "kernels_flat.cu", "kernels_sk.cu",
+                  "static_run.cu"]
+ROWS_SOURCES = ["rows_api.cu", "rows_kernels.cu", "rows_route.cu", "rows_gemm.cu", "rows_gemm_fp8.cu",
+                "rows_gemm_nvfp4.cu"]
+SOURCES = DECODE_SOURCES + ROWS_SOURCES
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
          "--expt-relaxed-constexpr"]
@@ -44,6 +48,19 @@ def _deps() -> list[str]:
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
+
+
+def sources_of(units: list[str]) -> list[str]:
+    """Names of these translation units and of every header of csrc/ that they include, sorted."""
+    todo, found = list(units), set()
+    while todo:
+        name = todo.pop()
+        if name in found or not os.path.exists(os.path.join(CSRC, name)):
+            continue
+        found.add(name)
+        with open(os.path.join(CSRC, name)) as f:
+            todo += re.findall(r'^\s*#include "([^"]+)"', f.read(), re.M)
+    return sorted(n for n in found if os.sep not in n)
 
 
 def up_to_date() -> bool:
