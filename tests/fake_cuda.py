@@ -102,6 +102,7 @@ unsigned fake_grid(int i) { return g_launches[i].grid; }
 int fake_pdl(int i) { return g_launches[i].pdl; }
 int fake_encodes() { return g_encodes; }
 int fake_bytes_read() { return (int)g_read; }
+int fake_bad_maps() { return g_bad_maps; }
 int fake_pending() { return (int)g_last; }
 }
 """

@@ -1,5 +1,7 @@
 """The layer on any number of rows: its workspace and status, rows with a stride, adapters for each weight type."""
 
+import dataclasses
+
 import pytest
 import torch
 
@@ -123,4 +125,38 @@ def test_result_in_the_place_of_x(wdtype):
         x = torch.randn(rows, 256, generator=_gen(rows), device="cuda").bfloat16()
         want = mod.run_rows(x)
         assert mod.run_rows(x, out=x) is x and torch.equal(x, want)
+    mod.close()
+
+
+@pytest.mark.parametrize("wdtype", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("rows", [7, 150, 1200])
+def test_adapters_of_every_weight_type(wdtype, rows):
+    """The layer with requests' adapters on its shared expert, against its parts in 64 bits."""
+    shape = LayerShape(512, 256, 24, 3, 1, wdtype)
+    layer = synth.make_layer(shape, seed=6, device="cuda")
+    mod = MoEDecodeLayer(shape, layer, max_rows=1)
+    g = _gen(rows)
+    x, r = (torch.randn(rows, 512, generator=g, device="cuda").bfloat16() for _ in range(2))
+    up, down = _adapters(g, 5, 16, 512, 512), _adapters(g, 5, 8, 256, 512)
+    ids = torch.randint(-1, 5, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    idx = torch.empty(rows, 3, dtype=torch.int32, device="cuda")
+    w = torch.empty(rows, 3, device="cuda")
+    out = mod.run_rows(x, r, topk_idx=idx, topk_w=w, adapters=(up, down), adapter_ids=ids)
+    logits = batch.project(x, layer["router_w"], out_dtype=torch.float32)
+    assert torch.equal(idx.cpu(), ref.route(logits, 3, "softmax")[0])
+    w13, w2 = (ref.matrix(layer, n, wdtype, 0) for n in ("sh_w13", "sh_w2"))
+    widened = wdtype != "bf16"
+    h, dh = ref.project(x, w13, up, ids, swiglu=True, widened=widened)
+    shared, ds = ref.project(h, w2, down, ids, addend=r, widened=widened, bf16=False)
+    # h's own rounding and bound, through the down matrix and its adapters; then the bound again of what that adds
+    extra = dh @ w2.abs().t()
+    for a in range(5):
+        of = ids == a
+        extra[of] += float(down.scale[a]) * ((dh[of] @ down.a[a].double().abs().t()) @ down.b[a].double().abs().t())
+    ds = ds + (1 + 2 * ref.BF16) * extra
+    routed, dr = ref.experts(dataclasses.replace(shape, num_shared=0), layer, x, idx, w)
+    total = shared + routed
+    bound = ds + dr + ref.FP32 * (shared.abs() + routed.abs()) + ref.BF16 * (total.abs() + ds + dr)
+    off = (out.double() - total).abs()
+    assert bool((off <= bound).all()), f"{float((off - bound).max()):.3e} over the bound {float(bound.max()):.3e}"
     mod.close()

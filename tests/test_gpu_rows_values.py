@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from moe_decode_layer_gb300 import batch
+from moe_decode_layer_gb300 import LayerShape, batch
 from tests import rows_reference as ref
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +48,23 @@ def test_infinite_adapter_products(rows, rank):
     assert bool((out[0] == math.inf).all()) and bool((out[1] == -math.inf).all())
     want, bound = ref.project(x[2:], weight.double(), ad, ids[2:])
     assert bool(((out[2:].double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_silu_far_below_zero(rows):
+    """exp(-g) above 2^126: the quotient is small and not zero, which a large up value shows."""
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    weight = torch.zeros(64, 8, dtype=torch.bfloat16, device="cuda")
+    gates = torch.linspace(-88.25, -80.0, 32)
+    weight[:32, 0], weight[32:, 0] = gates.bfloat16(), 2.0 ** 120
+    out = batch.project(x, weight, swiglu=True)
+    want, bound = ref.project(x, weight.double(), swiglu=True)
+    assert bool((want.abs() > 0).all()) and bool(((out.double() - want).abs() <= bound).all())
+    # the same in the experts' intermediate row, through a down matrix of ones
+    layer = {"w13": weight[None].contiguous(), "w2": torch.ones(1, 8, 32, dtype=torch.bfloat16, device="cuda")}
+    shape = LayerShape(8, 32, 1, 1, 0)
+    idx, w = torch.zeros(rows, 1, dtype=torch.int32, device="cuda"), torch.ones(rows, 1, device="cuda")
+    got = batch.experts(shape, layer, x, idx, w)
+    want, bound = ref.experts(shape, layer, x, idx, w)
+    assert bool(((got.double() - want).abs() <= bound).all())

@@ -2,6 +2,7 @@
 
 import ctypes
 import os
+import random
 import re
 
 import pytest
@@ -27,7 +28,7 @@ def _weights(cls):
 
 
 # places far enough apart for the largest call here
-X, OUT, RES, WS = (ctypes.c_void_p(i << 36) for i in (1, 2, 3, 4))
+X, OUT, RES, WS = (ctypes.c_void_p(i << 40) for i in (1, 2, 3, 4))
 
 
 def _experts(lib, rows, fail_encode=-1, fail_launch=-1, pending=0, stride=256, x=X, out=OUT, residual=RES, idx=P, w=P,
@@ -201,3 +202,25 @@ def test_project_overlaps(lib, rows):
                        (dict(addend=_at(OUT.value + size)), OK), (dict(addend=_at(OUT.value + size), out_dtype=1), BAD),
                        (dict(addend=_at(OUT.value - size), out_dtype=1), OK), (dict(out=_at(X.value - size), out_dtype=1), BAD)):
         assert _project(lib, rows, **kw) == status, kw
+
+
+def _size(rng, low, high, step=1):
+    return max(step, min(high, round(low * (high / low) ** rng.random()) // step * step))
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_every_supported_size_has_a_launch(lib, seed):
+    """Sizes over the whole supported range: a tile shape whose stages fit, descriptors by the rules, whole clusters."""
+    rng = random.Random(seed)
+    for _ in range(200):
+        wdtype = rng.randrange(3)
+        step = (8, 256, 128)[wdtype]
+        hidden, inter = _size(rng, step, 16384, step), _size(rng, step, 16384, step)
+        rows = _size(rng, 1, rng.choice((16, 300, 5000, 1 << 24)))
+        kw = dict(hidden=hidden, inter=inter, num_experts=_size(rng, 1, 1024), top_k=rng.randint(1, 16), num_shared=rng.randint(0, 4),
+                  wdtype=wdtype, residual_dtype=rng.randrange(2), stride=hidden)
+        assert _experts(lib, min(rows, 40000), **kw) == OK and lib.fake_bad_maps() == 0, (rows, kw)
+        swiglu = rng.randrange(2)
+        kw = dict(inner=hidden, outer=inter if wdtype else _size(rng, 2, 16384, 2), swiglu=swiglu, wdtype=wdtype, rank=8 * _size(rng, 1, 32),
+                  num_adapters=rng.choice((0, 1, 3, 24, 200, 1024)), out_dtype=0 if swiglu else rng.randrange(2), stride=hidden)
+        assert _project(lib, rows, addend=None if swiglu else RES, **kw) == OK and lib.fake_bad_maps() == 0, (rows, kw)
