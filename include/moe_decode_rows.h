@@ -164,7 +164,8 @@ moe_status moe_decode_project(const moe_project_config* cfg, const moe_project_w
 
 /*
  * Synchronises `stream` and reports on the last call of one row or more that used
- * `workspace`, whose first 4096 bytes it reads:
+ * `workspace`, whose first 4096 bytes it reads (MOE_ERR_INVALID_ARG for a stream under
+ * capture):
  * MOE_ERR_DEVICE_TIMEOUT when one of its device-side waits ran into its limit
  * (its outputs are undefined then), MOE_OK otherwise.
  */

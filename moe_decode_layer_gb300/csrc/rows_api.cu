@@ -769,9 +769,14 @@ moe_status moe_decode_rows_status(const void* workspace, moe_stream_t stream) {
   if (!workspace || !aligned16(workspace)) return MOE_ERR_INVALID_ARG;
   int words[kStatusKernels * kMaxSms];
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // the read-back cannot be waited for in a stream under capture, and its target is this frame
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(s, &cap);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (cap != cudaStreamCaptureStatusNone) return MOE_ERR_INVALID_ARG;
   Device d;
   if (!device(&d)) return MOE_ERR_CUDA;
-  cudaError_t e = cudaMemcpyAsync(words, workspace, sizeof(words), cudaMemcpyDeviceToHost, s);
+  e = cudaMemcpyAsync(words, workspace, sizeof(words), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_status(e);
   for (int k = 0; k < kStatusKernels; k++)

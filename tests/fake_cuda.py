@@ -27,6 +27,7 @@ std::unordered_map<const void*, std::string> g_names;
 std::unordered_map<const void*, int> g_smem;
 cudaError_t g_last = cudaSuccess;
 int g_fail_encode = -1, g_fail_launch = -1, g_encodes = 0, g_tries = 0, g_bad_maps = 0;
+int g_capturing = 0;
 size_t g_read = 0;
 struct Config { dim3 grid, block; size_t smem; cudaStream_t stream; } g_config;
 
@@ -84,6 +85,7 @@ cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr a, int) {
 }
 cudaError_t cudaFuncSetAttribute(const void* f, cudaFuncAttribute, int v) { g_smem[f] = v; return cudaSuccess; }
 cudaError_t cudaMemcpyAsync(void* d, const void*, size_t n, cudaMemcpyKind, cudaStream_t) { g_read = n; memset(d, 0, n); return cudaSuccess; }
+cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus* s) { *s = (cudaStreamCaptureStatus)g_capturing; return cudaSuccess; }
 cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
 cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** f, unsigned, unsigned long long, cudaDriverEntryPointQueryResult* r) {
   *f = (void*)encode;
@@ -96,6 +98,7 @@ void fake_reset(int fail_encode, int fail_launch, int pending) {
   g_fail_encode = fail_encode, g_fail_launch = fail_launch, g_last = (cudaError_t)pending;
   g_encodes = g_tries = g_bad_maps = 0;
 }
+void fake_capture(int on) { g_capturing = on, g_read = 0; }
 int fake_launches() { return (int)g_launches.size(); }
 const char* fake_name(int i) { return g_launches[i].name.c_str(); }
 unsigned fake_grid(int i) { return g_launches[i].grid; }

@@ -160,3 +160,21 @@ def test_adapters_of_every_weight_type(wdtype, rows):
     off = (out.double() - total).abs()
     assert bool((off <= bound).all()), f"{float((off - bound).max()):.3e} over the bound {float(bound.max()):.3e}"
     mod.close()
+
+
+def test_status_leaves_a_capture_intact():
+    """Asked for in the middle of a capture, the status is refused and the graph is whole."""
+    shape = LayerShape(256, 128, 16, 2, 1)
+    layer = synth.make_layer(shape, seed=7, device="cuda")
+    x = torch.randn(9, 256, generator=_gen(7), device="cuda").bfloat16()
+    idx = torch.randint(0, 16, (9, 2), generator=_gen(8), device="cuda", dtype=torch.int32)
+    w = torch.rand(9, 2, generator=_gen(9), device="cuda")
+    ws = torch.empty(batch.experts_workspace(shape, 9), dtype=torch.uint8, device="cuda")
+    want = batch.experts(shape, layer, x, idx, w, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = batch.experts(shape, layer, x, idx, w, workspace=ws)
+        code = batch.status(ws)
+    assert code == _lib.MOE_ERR_INVALID_ARG
+    graph.replay()
+    assert torch.equal(out, want) and batch.status(ws) == _lib.MOE_OK

@@ -130,6 +130,14 @@ def test_status_reads_what_the_binding_checks(lib):
         assert need.value >= _lib.ROWS_STATUS_BYTES
 
 
+def test_status_of_a_stream_under_capture_is_refused(lib):
+    """Nothing of it gets into the graph."""
+    lib.fake_capture(1)
+    assert lib.moe_decode_rows_status(P, None) == BAD and lib.fake_bytes_read() == 0
+    lib.fake_capture(0)
+    assert lib.moe_decode_rows_status(P, None) == OK
+
+
 def test_status_of_a_short_workspace_is_refused():
     for bad in (torch.empty(_lib.ROWS_STATUS_BYTES - 1, dtype=torch.uint8), torch.empty(4096), torch.empty(0, dtype=torch.uint8)):
         with pytest.raises(ValueError, match="workspace must be"):
