@@ -87,8 +87,10 @@ moe_status moe_decode_route(const moe_route_config* cfg, const void* logits, int
  *   y(x) = W2 bf16_rne(silu(Wg x) * (Wu x))
  * with fp32 sums. An index outside 0..E-1 (-1 from moe_decode_route, padding) takes no part; an
  * expert that a row names twice counts twice. The intermediate row is rounded to
- * bf16 (it is an operand of the tensor cores); FP8 weights are rounded to bf16
- * after their block scale. The weights are those of moe_decode_create with
+ * bf16 (it is an operand of the tensor cores), silu is off by at most 2^-16 of itself
+ * before that; FP8 weights are rounded to bf16 after their block scale. (moe_decode_run keeps
+ * all three in fp32: a row's output is 1.66e-3 off the exact one there, its own rounding, and
+ * 1.75e-3 here, with FP8 weights 2.0e-3.) The weights are those of moe_decode_create with
  * w2_layout MOE_W2_H_I; the router's are not used.
  * Supported: 1 <= E <= 1024, 0 <= S <= 4, 1 <= top_k <= 16; bf16: hidden, inter % 8 == 0;
  * FP8: % 128; NVFP4: % 256; hidden, inter <= 16384.
@@ -104,7 +106,12 @@ typedef struct moe_experts_config {
 } moe_experts_config;
 
 moe_status moe_decode_experts_check(const moe_experts_config* cfg);
-/* Bytes of workspace that a call with at most `rows` rows needs. */
+/*
+ * Bytes of workspace that a call with at most `rows` rows needs: for each of the pairs of a
+ * row and a chosen or shared expert 4 H + 2 I bytes and a few more, for 16384 rows at most (a
+ * longer call goes through its rows in rounds). 1.7 GB for 16384 rows with H = 2560, I = 768,
+ * 8 + 1 experts; 32 GB at the limits above.
+ */
 moe_status moe_decode_experts_workspace(const moe_experts_config* cfg, int64_t rows, size_t* bytes);
 /*
  *   x        bf16 [rows, H], row r at x + r * x_stride elements (x_stride % 8 == 0, >= H)
@@ -122,7 +129,7 @@ moe_status moe_decode_experts(const moe_experts_config* cfg, const moe_decode_we
  * A projection that all rows share, with the rows' adapters beside it:
  *   y_t = W x_t + B_a (scale_a A_a x_t) (+ addend_t),  a = adapter_ids[t]
  *   out_t = y_t, or with swiglu silu(y_t[0..O)) * y_t[O..2O)
- * with fp32 sums, rounded once to out_dtype. With many rows scale_a A_a x_t is held
+ * with fp32 sums, rounded once to out_dtype (silu as above). With many rows scale_a A_a x_t is held
  * as the sum of two bf16 numbers (operands of the tensor cores), and an NVFP4 weight
  * is rounded to bf16 after both its scales. Rows whose id is outside 0..num_adapters-1 have no adapter. Rows
  * may come in any order. What an adapter holds reaches its own rows only.

@@ -149,8 +149,8 @@ constexpr double kSmallStep = 390.0;
 // is), and its start and epilogue (45 clocks a column). The tiles go round the SMs in
 // waves: rt is what makes the sum least. It is a multiple of 16 (or 8, when that
 // little is wanted): a warp's results then start on a 32-byte sector. Stores of parts of
-// sectors cost more than the product (8192 rows over 64 experts: 2345 us with
-// rt = 104, 1870 us with 128). reuse: tiles that read the same weights.
+// sectors cost more than the product (8192 rows over 64 experts: 1106 us with
+// rt = 104, 936 us with 128). reuse: tiles that read the same weights.
 int choose_rt(int64_t R, bool swiglu, double entries, double reuse, int n, int fmt, int nmax, int ksteps, int ad_mode,
               const Device& d, double* cost_out = nullptr) {
   int best = 128;

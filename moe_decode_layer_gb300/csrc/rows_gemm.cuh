@@ -30,7 +30,7 @@
 // the tensor core beside an epilogue that it does not overlap (256 columns of two
 // sub-tiles fill tensor memory) -- 619 GFLOP of gate/up products, 8192 rows over 64
 // experts of 2048 x 1024, in 439 us, 1.41 PFLOP/s. FP8 (3.0 GB for 300 rows) runs at
-// 6.7 TB/s, NVFP4 (1.82 GB for 512 rows) at 2.6 TB/s: a widening warp's chain of
+// 6.6 TB/s, NVFP4 (1.82 GB for 512 rows) at 2.5 TB/s: a widening warp's chain of
 // waits, conversions and stores takes about 1000 clocks a step, where its bytes take 400.
 #pragma once
 #include <cuda.h>
@@ -246,7 +246,9 @@ __device__ __forceinline__ int adapter_next(const GemmParams& p, int a, int p0, 
   return p.num_adapters;
 }
 
-// exp(-g) past fp32's range makes the quotient 0, as it should be.
+// CUDA's fast exp and division: at most 105 + 2 steps of fp32 (2^-16 of the value) at g = -88,
+// a few near 0; the result is rounded to bf16 (2^-8) next. exp(-g) past fp32's range makes
+// the quotient 0, as it should be.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // A number as hi + lo, two bf16 numbers: hi = bf16(high(v)), lo = low(v, hi). A finite one

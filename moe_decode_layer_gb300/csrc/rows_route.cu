@@ -18,7 +18,9 @@
 //
 // One row takes 4 us, a launch's latency. 65536 rows of 512 logits (138 MB) take
 // 39 us: 570 instructions a row, most on the integer pipe, where the bytes need 20.
-// 4096 rows of 256 with a bias and groups take 11 us.
+// 4096 rows of 256 with a bias and groups take 12 us: 1460 instructions a row (a quotient
+// and an exp for every expert, a shared-memory round for the groups' best keys, loops over
+// the groups) on 27 rows an SM, which fill 55 to 60 % of the issue slots.
 #include <cuda_bf16.h>
 
 #include <cfloat>
