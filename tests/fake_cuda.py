@@ -114,10 +114,12 @@ int fake_pending() { return (int)g_last; }
 def make(folder) -> ctypes.CDLL:
     """The library's many-row entry points over the stand-in, built in ``folder``."""
     build.build()
+    objs = [os.path.join(build.BUILD, s.replace(".cu", ".o")) for s in build.ROWS_SOURCES]
+    if not all(os.path.exists(o) for o in objs):  # a library that was brought along without its objects
+        build.build(force=True)
     src, out = os.path.join(folder, "stub.cpp"), os.path.join(folder, "librows_fake.so")
     with open(src, "w") as f:
         f.write(STUB)
-    objs = [os.path.join(build.BUILD, s.replace(".cu", ".o")) for s in build.SOURCES if s.startswith("rows_")]
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
     subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-O1", "-w", "-Wl,-Bsymbolic", "-I", cuda, src, *objs, "-o", out],
                    check=True)
