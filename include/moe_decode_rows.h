@@ -51,7 +51,7 @@ typedef enum moe_route_score {
  *   w_j = scale * s_j / sum_chosen s_i (renormalise), or scale * s_j
  * Ties, among experts and among groups, go to the lower index. Where keys in fp32 cannot tell
  * two candidates apart, the row is decided in fp64. Without a bias experts are ordered by
- * their logits.
+ * their logits, and so are groups of one best key (also where 64 bits hold the scores as equal).
  * A logit that is NaN or at most -1e38 masks its expert (-inf and the lowest
  * bf16 / fp32 value do): it is never chosen. A row with fewer than top_k experts
  * to choose from fills up with index -1 and weight 0. Logits above 3e38 count as 3e38.

@@ -392,14 +392,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         auto within = [&](float hi, float lo, float m) {  // (infinite values are equal or clear)
           return lo > -INFINITY && hi < INFINITY && hi - lo <= 2.0f * tol_s + 0x1p-21f * m;
         };
-        close_group = within(v0, v1, m0 + m1);
-        // the next ones on both sides: when they are clear, it is between these two alone
+        const bool pair = within(v0, v1, m0 + m1);
+        // the others on both sides, which may have larger keys: when they are clear, it is
+        // between these two alone
         const bool near = lead && ((rank < p.kept - 1 && within(v, v1, mag + m1)) ||
                                    (rank > p.kept && within(v0, v, m0 + mag)));
-        if (close_group && !__any_sync(0xffffffffu, near) && !p.softmax) {
+        close_group = __any_sync(0xffffffffu, near) || (pair && p.softmax);
+        if (pair && !close_group) {
           const int ga = i0 / sub, gb = i1 / sub;
           keep ^= border64(p, src, ga, gb, lane) ? (1u << ga | 1u << gb) : 0u;
-          close_group = false;
         }
       }
     }

@@ -114,3 +114,17 @@ def test_infinite_biases_at_the_border():
         assert bool((idx[:, 0] == 3).all()) and bool(torch.isfinite(w).all())
         if kept > 1:
             assert bool((idx[:, 1] == 40).all()) and bool((idx[:, 2] == 41).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [1000.0, 3e4])
+def test_groups_with_and_without_cancelling_biases(score, big):
+    """A border between two groups of small keys, which is clear, beside groups whose keys are rounded far more."""
+    g = _gen(8)
+    bias = torch.zeros(64, device="cuda")
+    for n in range(0, 32, 2):
+        bias[2 * n], bias[2 * n + 1] = big, -big
+    for spread in (1e-4, 1e-5):
+        logits = -1.5 + spread * _normal(g, 500, 64)
+        for kept in (5, 16, 28):
+            _check(logits, 8, score, bias, 32, kept, 2)
