@@ -523,15 +523,17 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   // weights
   const bool there = lane < K && mine >= 0;
   float s;
+  // (a renormalised row's common factor, exp of its largest chosen logit, is taken out before
+  // fp32 loses it: a bias may choose experts whose scores are far below the row's largest)
+  const float most = warp_max(there ? mine_l : -INFINITY);
   if (p.softmax) {
-    const float m = whole ? top : warp_max(there ? mine_l : -INFINITY);
-    s = there ? expf(mine_l - m) : 0.0f;
+    s = there ? expf(mine_l - (p.renormalise ? most : top)) : 0.0f;
     if (!p.renormalise) s /= norm;
+  } else if (p.renormalise && most < 0.0f) {
+    s = there ? expf(mine_l - most) / (1.0f + expf(mine_l)) : 0.0f;
   } else {
-    // far below 0 a sigmoid is exp(l): common factors are taken out before fp32 loses them
-    const float m = warp_max(there ? mine_l : -INFINITY);
-    if (p.renormalise && m < -30.0f) s = there ? expf(mine_l - m) : 0.0f;
-    else s = there ? 1.0f / (1.0f + expf(-mine_l)) : 0.0f;
+    // (below -80 a sigmoid is exp(l), whose inverse would overflow)
+    s = !there ? 0.0f : mine_l < -80.0f ? expf(mine_l) : 1.0f / (1.0f + expf(-mine_l));
   }
   if (p.renormalise) {
     const float sum = warp_sum(s);

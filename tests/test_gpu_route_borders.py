@@ -128,3 +128,39 @@ def test_groups_with_and_without_cancelling_biases(score, big):
         logits = -1.5 + spread * _normal(g, 500, 64)
         for kept in (5, 16, 28):
             _check(logits, 8, score, bias, 32, kept, 2)
+
+
+def _check_weights(logits, k, score, bias, renormalise, scale=1.0):
+    idx, w = batch.route(logits, k, score=score, bias=bias, renormalise=renormalise, scale=scale)
+    want_idx, want = ref.route(logits, k, score, bias, renormalise=renormalise, scale=scale)
+    assert torch.equal(idx.cpu(), want_idx)
+    off = (w.cpu().double() - want).abs()
+    assert bool((off <= ref.route_tolerance(logits, score, renormalise) * want.abs() + 1e-37).all()), float((off / want.clamp(min=1e-37)).max())
+    return want
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+def test_weights_of_experts_far_below_the_rows_largest(scale):
+    """A bias chooses experts whose softmax scores fp32 does not hold; their weights are between themselves."""
+    g = _gen(9)
+    logits = _normal(g, 100, 40)
+    logits[:, 20:] -= 95 + 10 * torch.rand(100, 1, generator=g, device="cuda")
+    bias = torch.zeros(40, device="cuda")
+    bias[20:] = torch.arange(20, device="cuda") + 2.0
+    for k in (1, 4, 16):
+        want = _check_weights(logits, k, "softmax", bias, True, scale)
+        assert bool((want.sum(1) > 0.99 * scale).all())
+        _check_weights(logits - 30, k, "softmax", bias, True, scale)
+        _check_weights(logits, k, "softmax", bias, False, scale)
+
+
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_weights_of_sigmoids_far_below_zero(renormalise):
+    """Chosen logits from a little below 0 to -110: the small ones of a renormalised row are held too."""
+    g = _gen(10)
+    for top in (2.0, -1.0, -10.0, -29.0, -31.0, -80.0):
+        logits = top - 80 * torch.rand(100, 24, generator=g, device="cuda")
+        bias = torch.arange(24, device="cuda").float()
+        for k in (1, 5, 16):
+            _check_weights(logits, k, "sigmoid", None, renormalise)
+            _check_weights(logits, k, "sigmoid", bias, renormalise)
