@@ -525,15 +525,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   float s;
   // (a renormalised row's common factor, exp of its largest chosen logit, is taken out before
   // fp32 loses it: a bias may choose experts whose scores are far below the row's largest)
-  const float most = warp_max(there ? mine_l : -INFINITY);
   if (p.softmax) {
-    s = there ? expf(mine_l - (p.renormalise ? most : top)) : 0.0f;
+    // (without keys `whole` says the same; asking for it again: 65536 rows 41 us, not 39)
+    const float m = (KEYS ? !p.renormalise : whole) ? top : warp_max(there ? mine_l : -INFINITY);
+    s = there ? expf(mine_l - m) : 0.0f;
     if (!p.renormalise) s /= norm;
-  } else if (p.renormalise && most < 0.0f) {
-    s = there ? expf(mine_l - most) / (1.0f + expf(mine_l)) : 0.0f;
   } else {
-    // (below -80 a sigmoid is exp(l), whose inverse would overflow)
-    s = !there ? 0.0f : mine_l < -80.0f ? expf(mine_l) : 1.0f / (1.0f + expf(-mine_l));
+    // exp(l) / (1 + exp(l)) below 0: the other form's exp would overflow
+    const float m = p.renormalise ? fminf(warp_max(there ? mine_l : -INFINITY), 0.0f) : 0.0f;
+    s = there ? (mine_l < 0.0f ? expf(mine_l - m) : 1.0f) / (1.0f + expf(-fabsf(mine_l))) : 0.0f;
   }
   if (p.renormalise) {
     const float sum = warp_sum(s);
