@@ -89,8 +89,8 @@ moe_status moe_decode_route(const moe_route_config* cfg, const void* logits, int
  * expert that a row names twice counts twice. The intermediate row is rounded to
  * bf16 (it is an operand of the tensor cores), silu is off by at most 2^-16 of itself
  * before that; FP8 weights are rounded to bf16 after their block scale. (moe_decode_run keeps
- * all three in fp32: a row's output is 1.66e-3 off the exact one there, its own rounding, and
- * 1.75e-3 here, with FP8 weights 2.0e-3.) The weights are those of moe_decode_create with
+ * all three in fp32: its outputs are 1.66e-3 off the exact ones relative to their norm, the
+ * output's own rounding, and these 1.75e-3, with FP8 weights 2.0e-3.) The weights are those of moe_decode_create with
  * w2_layout MOE_W2_H_I; the router's are not used.
  * Supported: 1 <= E <= 1024, 0 <= S <= 4, 1 <= top_k <= 16; bf16: hidden, inter % 8 == 0;
  * FP8: % 128; NVFP4: % 256; hidden, inter <= 16384.

@@ -126,13 +126,20 @@ class MoEDecodeLayer:
         ``top_groups`` and ``group_best`` limit the choice to the best groups of
         experts. ``adapters``: the low-rank adapters of the one shared expert's
         gate/up and down projections, and ``adapter_ids`` int32 [T] each row's. All terms
-        and the residual are summed in fp32 and rounded once. Not for layers with pre_rmsnorm or transposed down matrices.
+        and the residual are summed in fp32 and rounded once. ``out`` may be x. Not for
+        layers with pre_rmsnorm or transposed down matrices.
 
         ``workspace``: uint8, of rows_workspace bytes; after a run with one rows_status
         tells whether its device-side waits ended in time (without one, each operator
         takes a workspace from torch's allocator, and nobody can be asked)."""
         if self._cfg.pre_rmsnorm:
             raise ValueError("run_rows takes the layer's normalised input: pre_rmsnorm is not computed")
+        if adapters is not None and self.shape.num_shared != 1:
+            raise ValueError("adapters belong to the one shared expert of a layer")
+        if (adapters is None) != (adapter_ids is None):
+            raise ValueError("adapters and adapter_ids come together")
+        if self._cfg.w2_layout != _lib.W2_LAYOUT["h_i"]:
+            raise ValueError("run_rows takes down matrices stored [E, H, I] (w2_layout h_i)")
         if residual is None:
             residual = x if x.is_contiguous() else batch.contiguous(x, stream)
         ws = dict.fromkeys(("router", "up", "down", "experts"))
@@ -149,8 +156,6 @@ class MoEDecodeLayer:
                              idx=topk_idx, w=topk_w, stream=stream)
         shape = self.shape
         if adapters is not None:
-            if shape.num_shared != 1:
-                raise ValueError("adapters belong to the one shared expert of a layer")
             sfx = batch._SUFFIX[shape.wdtype]
             w13, w2 = (tuple(self._weights["sh_" + n + f][0] for f in sfx) for n in ("w13", "w2"))
             h = batch.project(x, w13, wdtype=shape.wdtype, swiglu=True, adapters=adapters[0], adapter_ids=adapter_ids,
@@ -158,8 +163,6 @@ class MoEDecodeLayer:
             residual = batch.project(h, w2, wdtype=shape.wdtype, adapters=adapters[1], adapter_ids=adapter_ids,
                                      addend=residual, out_dtype=torch.float32, workspace=ws["down"], stream=stream)
             shape = dataclasses.replace(shape, num_shared=0)
-        elif adapter_ids is not None:
-            raise ValueError("adapters and adapter_ids come together")
         return batch.experts(shape, self._weights, x, idx, w, residual=residual, out=out,
                              workspace=ws["experts"], stream=stream)
 

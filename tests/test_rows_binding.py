@@ -10,6 +10,7 @@ import pytest
 import torch
 
 from moe_decode_layer_gb300 import LayerShape, _lib, batch
+from moe_decode_layer_gb300.layer import MoEDecodeLayer
 
 SHAPE = LayerShape(256, 128, 16, 2, 1)
 
@@ -54,6 +55,20 @@ def test_weights_on_the_current_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
     with pytest.raises(ValueError, match="on device 3: got"):
         batch.expert_weights(SHAPE, _layer(), torch.device("cuda"))
+
+
+@pytest.mark.parametrize("cfg,shape,kw", [
+    (dict(pre_rmsnorm=1), SHAPE, {}), (dict(w2_layout=1), SHAPE, {}), ({}, SHAPE, dict(adapter_ids=0)), ({}, SHAPE, dict(adapters=(0, 0))),
+    ({}, dataclasses.replace(SHAPE, num_shared=2), dict(adapters=(0, 0), adapter_ids=0)),
+    ({}, dataclasses.replace(SHAPE, num_shared=0), dict(adapters=(0, 0), adapter_ids=0))], ids=str)
+def test_layer_refuses_before_any_operator_runs(monkeypatch, cfg, shape, kw):
+    """What run_rows does not take is refused as a whole: no operator of it has been called."""
+    for name in ("project", "route", "experts", "contiguous"):
+        monkeypatch.setattr(batch, name, lambda *a, **k: pytest.fail("an operator was called"))
+    mod = MoEDecodeLayer.__new__(MoEDecodeLayer)
+    mod.shape, mod._weights, mod._cfg = shape, {}, _lib.Config(**cfg)
+    with pytest.raises(ValueError):
+        mod.run_rows(torch.zeros(4, 256, dtype=torch.bfloat16), **kw)
 
 
 @pytest.fixture
