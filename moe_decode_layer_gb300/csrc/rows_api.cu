@@ -9,6 +9,7 @@
 #include <cstring>
 
 #include "../../include/moe_decode_rows.h"
+#include "rows_host.h"
 #include "rows_kernels.h"
 #include "rows_params.h"
 
@@ -17,46 +18,10 @@ using namespace moe::rows;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 24;  // rows of one call
 // Experts: rows handled by one round of launches; the fp32 outputs of a round's
 // (row, expert) pairs are the workspace's largest part.
 constexpr int64_t kRoundRows = 16384;
-constexpr int kStatusKernels = 2;
 constexpr int kMinN = 32;  // rows of a tile of experts' rows at least
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-// Whether the bytes at a share any with those at b.
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  const intptr_t d = static_cast<const char*>(b) - static_cast<const char*>(a);
-  return a && b && d < a_bytes && -d < b_bytes;
-}
-// Whether rows of `width` bytes every `stride` bytes share any with those at out.
-bool rows_overlap(const void* x, int64_t stride, int64_t width, int64_t rows, const void* out, int64_t bytes) {
-  const intptr_t d = static_cast<const char*>(out) - static_cast<const char*>(x);
-  if (d + bytes <= 0) return false;
-  const int64_t last = std::min(rows - 1, (d + bytes - 1) / stride);  // the last row that starts before out's end
-  return last * stride + width > d;
-}
-size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static std::atomic<void*> fn{nullptr};
-  void* f = fn.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<EncodeTiled>(f);
-}
 
 // [groups][halves][rows][cols] row-major, copied in boxes of 128 bytes x rt rows;
 // what lies past a matrix's rows or columns reads as zero.
@@ -87,25 +52,6 @@ bool make_rows_map(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, 
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, b, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Device {
-  int sms = 0, smem = 0, id = 0;
-};
-bool device(Device* d) {
-  static std::atomic<uint64_t> known[64];  // per device: SMs, then shared memory; they do not change
-  if (cudaGetDevice(&d->id) != cudaSuccess) return false;
-  uint64_t v = d->id < 64 ? known[d->id].load(std::memory_order_relaxed) : 0;
-  if (!v) {
-    if (cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d->smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, d->id) != cudaSuccess)
-      return false;
-    v = (uint64_t)d->sms << 32 | (uint32_t)d->smem;
-    if (d->id < 64) known[d->id].store(v, std::memory_order_relaxed);
-  }
-  d->sms = (int)(v >> 32);
-  d->smem = (int)(uint32_t)v;
-  return d->sms <= kMaxSms;
 }
 
 // Shared memory of a launch: stages (and raw slots) for tiles of 2 rt x nmax.
@@ -491,12 +437,6 @@ moe_status check_project(const moe_project_config* c) {
     if (c->num_adapters > kMaxAdapters || c->rank % 8 || c->rank > 256) return MOE_ERR_UNSUPPORTED;
   }
   return MOE_OK;
-}
-
-moe_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return MOE_OK;
-  cudaGetLastError();  // the error is reported here, not by a later call
-  return MOE_ERR_CUDA;
 }
 
 }  // namespace
