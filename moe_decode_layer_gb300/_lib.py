@@ -66,6 +66,8 @@ STATIC_SCRATCH_BYTES = 4 << 20
 
 MOE_BF16 = 0
 MOE_F32 = 1
+MOE_I8 = 2
+MOE_W_INT8 = 3
 ROWS_STATUS_BYTES = 4096  # the status words, a workspace's first bytes
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -75,7 +77,10 @@ EXPORTS = ("moe_decode_config_check", "moe_decode_plan", "moe_decode_create", "m
            "moe_decode_destroy", "moe_decode_status_string", "moe_decode_abi_version",
            "moe_decode_route_check", "moe_decode_route", "moe_decode_experts_check",
            "moe_decode_experts_workspace", "moe_decode_experts", "moe_decode_project_check",
-           "moe_decode_project_workspace", "moe_decode_project", "moe_decode_rows_status")
+           "moe_decode_project_workspace", "moe_decode_project", "moe_decode_rows_status",
+           "moe_decode_quantise", "moe_decode_project_int8_check", "moe_decode_project_int8_workspace",
+           "moe_decode_project_int8", "moe_decode_ff_check", "moe_decode_ff_workspace", "moe_decode_ff",
+           "moe_decode_ff_backward_workspace", "moe_decode_ff_backward")
 
 
 class Config(ctypes.Structure):
@@ -119,6 +124,18 @@ class ProjectConfig(ctypes.Structure):
 
 class ProjectWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w", "w_scale", "w_gscale", "a", "b", "scale")]
+
+
+class Int8Config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("inner", "outer", "swiglu", "x_dtype", "out_dtype")]
+
+
+class FfConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "wdtype")]
+
+
+class FfWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w13", "w2", "s13", "s2")]
 
 
 class MoEDecodeError(RuntimeError):
@@ -173,6 +190,16 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
         lib.moe_decode_project.argtypes = [project, ctypes.POINTER(ProjectWeights), vp, i64, vp, vp, vp, i64, vp, sz,
                                            vp]
         lib.moe_decode_rows_status.argtypes = [vp, vp]
+        int8, ff, ffw = (ctypes.POINTER(c) for c in (Int8Config, FfConfig, FfWeights))
+        lib.moe_decode_quantise.argtypes = [i32, i32, vp, i64, i64, vp, vp, vp]
+        lib.moe_decode_project_int8_check.argtypes = [int8]
+        lib.moe_decode_project_int8_workspace.argtypes = [int8, i64, ctypes.POINTER(sz)]
+        lib.moe_decode_project_int8.argtypes = [int8, vp, vp, vp, vp, i64, vp, vp, i64, vp, sz, vp]
+        lib.moe_decode_ff_check.argtypes = [ff]
+        lib.moe_decode_ff_workspace.argtypes = [ff, i64, ctypes.POINTER(sz)]
+        lib.moe_decode_ff.argtypes = [ff, ffw, vp, i64, vp, vp, vp, i64, vp, sz, vp]
+        lib.moe_decode_ff_backward_workspace.argtypes = [ff, i64, ctypes.POINTER(sz)]
+        lib.moe_decode_ff_backward.argtypes = [ff, ffw, vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i64, vp, sz, vp]
         for name in EXPORTS:
             if name != "moe_decode_status_string":
                 getattr(lib, name).restype = i32

@@ -1,7 +1,9 @@
-"""The MoE layer's operators for any number of rows, over torch tensors.
+"""The operators for any number of rows, over torch tensors: the MoE layer's, and a dense layer's.
 
 ``route``, ``experts`` and ``project`` marshal tensors into the C entry points of
-include/moe_decode_rows.h, which document what is computed. They check shapes,
+include/moe_decode_rows.h, and ``quantise``, ``project_int8``, ``feed_forward`` and
+``feed_forward_backward`` into those of include/moe_decode_dense.h, which document what is
+computed. They check shapes,
 types and devices, allocate results (and a workspace, unless one is given) with
 torch's allocator on the stream they run on, and enqueue their work on the current
 stream (or ``stream``) without waiting. No arithmetic happens here.
@@ -342,6 +344,242 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
     if st:
         _lib.check(st, "moe_decode_project")
     return out
+
+
+def _row_major(t: torch.Tensor, name: str, dtypes, cols: int | None, dev: int) -> tuple[int, int, int]:
+    """(address, rows, row stride) of a [rows, cols] tensor of one of these types whose rows are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype not in dtypes or t.get_device() != dev or len(shape) != 2 or (cols is not None and shape[1] != cols) or \
+            (shape[0] and shape[1] > 1 and stride[1] != 1):
+        raise ValueError(f"{name} must be a [rows, {'columns' if cols is None else cols}] tensor of {dtypes} on device "
+                         f"{dev} with contiguous rows: got {t.dtype} {tuple(shape)} on {t.device}")
+    return t.data_ptr(), shape[0], stride[0] if shape[0] > 1 else shape[1]
+
+
+_ROWS_DTYPES = (torch.bfloat16, torch.float32)
+
+
+def quantise(x: torch.Tensor, *, codes: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """(int8 [T, K], fp32 [T]): the rows of ``x`` (bf16 or fp32 [T, K], any row stride of a multiple of 16
+    bytes) as 8-bit integers with a scale each, as moe_decode_quantise documents. K % 8 == 0."""
+    dev = x.get_device()
+    px, t, sx = _row_major(x, "x", _ROWS_DTYPES, None, dev)
+    k = x.shape[1]
+    s, leave = _enter(dev, stream)
+    try:
+        if codes is None:
+            codes = torch.empty((t, k), dtype=torch.int8, device=dev)
+            pc = codes.data_ptr()
+        else:
+            pc = _tensor(codes, "codes", torch.int8, (t, k), dev)
+        if scale is None:
+            scale = torch.empty((t,), dtype=torch.float32, device=dev)
+            ps = scale.data_ptr()
+        else:
+            ps = _tensor(scale, "scale", torch.float32, (t,), dev)
+        st = _lib.load().moe_decode_quantise(_DTYPES[x.dtype], k, px, sx, t, pc, ps, s)
+    finally:
+        if leave is not None:
+            leave.close()
+    if st:
+        _lib.check(st, "moe_decode_quantise")
+    return codes, scale
+
+
+@functools.lru_cache(maxsize=1024)
+def _int8_config(inner: int, outer: int, swiglu: bool, x_dtype, out_dtype) -> _lib.Int8Config:
+    _need(out_dtype in _DTYPES, "the result is bf16 or fp32")
+    cfg = _lib.Int8Config(inner, outer, swiglu, _lib.MOE_I8 if x_dtype is torch.int8 else _DTYPES[x_dtype],
+                          _DTYPES[out_dtype])
+    _lib.check(_lib.load().moe_decode_project_int8_check(cfg), "moe_decode_project_int8_check")
+    return cfg
+
+
+@functools.lru_cache(maxsize=1024)
+def _int8_bytes(inner, outer, swiglu, x_dtype, out_dtype, rows) -> int:
+    n = ctypes.c_size_t()
+    cfg = _int8_config(inner, outer, swiglu, x_dtype, out_dtype)
+    _lib.check(_lib.load().moe_decode_project_int8_workspace(cfg, rows, n), "moe_decode_project_int8_workspace")
+    return n.value
+
+
+def project_int8_workspace(inner: int, outer: int, rows: int, *, swiglu: bool = False, x_dtype=torch.int8,
+                           out_dtype=torch.bfloat16) -> int:
+    """Bytes of workspace that :func:`project_int8` needs for at most ``rows`` rows; ``x_dtype``
+    torch.int8: x comes as codes."""
+    return _int8_bytes(inner, outer, bool(swiglu), x_dtype, out_dtype, rows)
+
+
+def _codes(weight, name: str, rows: int, cols: int, dev: int) -> tuple[int, int]:
+    """The addresses of an int8 matrix and of its rows' scales."""
+    _need(isinstance(weight, (tuple, list)) and len(weight) == 2, f"{name} comes as (codes, scale)")
+    return (_tensor(weight[0], name, torch.int8, (rows, cols), dev),
+            _tensor(weight[1], f"{name}'s scale", torch.float32, (rows,), dev))
+
+
+def project_int8(x, weight, *, addend: torch.Tensor | None = None, swiglu: bool = False,
+                 out: torch.Tensor | None = None, out_dtype=torch.bfloat16, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """[T, O]: the product of 8-bit integers s_t c_o sum_k q_tk W_ok (+ addend), or with ``swiglu``
+    silu(gate) * up of its two halves, as moe_decode_project_int8 documents. ``x``: (codes, scale) of
+    :func:`quantise`, or bf16 or fp32 [T, K], which the call quantises; ``weight``: (int8 [O, K], fp32
+    [O]), [2 O] rows with swiglu. K % 16 == 0, O % 8 == 0."""
+    given = isinstance(x, (tuple, list))
+    if given:
+        _need(len(x) == 2, "quantised rows come as (codes, scale)")
+    rows_t, scale = x if given else (x, None)
+    _need(isinstance(weight, (tuple, list)) and len(weight) == 2, "an int8 weight comes as (codes, scale)")
+    halves = 2 if swiglu else 1
+    if rows_t.dim() != 2 or weight[0].dim() != 2 or weight[0].shape[0] % halves:
+        raise ValueError("x must be [rows, inner] and the weight [outer, inner], with an even number of rows for gate/up")
+    dev = rows_t.get_device()
+    t, k = rows_t.shape
+    rows = weight[0].shape[0]
+    o = rows // halves
+    px, _, sx = _row_major(rows_t, "x", (torch.int8,) if given else _ROWS_DTYPES, k, dev)
+    if out is not None:
+        out_dtype = out.dtype
+    cfg = _int8_config(k, o, bool(swiglu), rows_t.dtype, out_dtype)
+    ps = _tensor(scale, "x's scale", torch.float32, (t,), dev) if given else None
+    pw, pc = _codes(weight, "weight", rows, k, dev)
+    pa = None if addend is None else _tensor(addend, "addend", torch.bfloat16, (t, o), dev)
+    s, leave = _enter(dev, stream)
+    try:
+        if out is None:
+            out = torch.empty((t, o), dtype=out_dtype, device=dev)
+            po = out.data_ptr()
+        else:
+            po = _tensor(out, "out", out_dtype, (t, o), dev)
+        ws = _workspace(workspace, _int8_bytes(k, o, bool(swiglu), rows_t.dtype, out_dtype, t), dev)
+        st = _lib.load().moe_decode_project_int8(cfg, pw, pc, px, ps, sx, pa, po, t, ws.data_ptr(), ws.numel(), s)
+    finally:
+        if leave is not None:
+            leave.close()
+    if st:
+        _lib.check(st, "moe_decode_project_int8")
+    return out
+
+
+_FF_WDTYPE = {"bf16": _lib.MOE_W_BF16, "int8": _lib.MOE_W_INT8}
+
+
+@functools.lru_cache(maxsize=256)
+def _ff_config(hidden: int, inter: int, wdtype: str) -> _lib.FfConfig:
+    _need(wdtype in _FF_WDTYPE, f"a feed-forward block's weights are bf16 or int8, not {wdtype!r}")
+    cfg = _lib.FfConfig(hidden, inter, _FF_WDTYPE[wdtype])
+    _lib.check(_lib.load().moe_decode_ff_check(cfg), "moe_decode_ff_check")
+    return cfg
+
+
+@functools.lru_cache(maxsize=1024)
+def feed_forward_workspace(hidden: int, inter: int, rows: int, *, wdtype: str = "bf16") -> int:
+    """Bytes of workspace that :func:`feed_forward` needs for at most ``rows`` rows."""
+    n = ctypes.c_size_t()
+    _lib.check(_lib.load().moe_decode_ff_workspace(_ff_config(hidden, inter, wdtype), rows, n), "moe_decode_ff_workspace")
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def feed_forward_backward_workspace(hidden: int, inter: int, rows: int) -> int:
+    """Bytes of workspace that :func:`feed_forward_backward` needs for at most ``rows`` rows."""
+    n = ctypes.c_size_t()
+    _lib.check(_lib.load().moe_decode_ff_backward_workspace(_ff_config(hidden, inter, "bf16"), rows, n),
+               "moe_decode_ff_backward_workspace")
+    return n.value
+
+
+def _ff_sizes(w13, w2) -> tuple[int, int]:
+    """(hidden, inter) of the block with these weights."""
+    if w13.dim() != 2 or w2.dim() != 2 or w13.shape[0] != 2 * w2.shape[1] or w13.shape[1] != w2.shape[0]:
+        raise ValueError(f"weights must be [2 inter, hidden] and [hidden, inter]: got {tuple(w13.shape)}, {tuple(w2.shape)}")
+    return w2.shape[0], w2.shape[1]
+
+
+def feed_forward(x: torch.Tensor, w13, w2, *, wdtype: str = "bf16", residual: torch.Tensor | None = None,
+                 gate_up: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """bf16 [T, H]: the gated feed-forward block W2 (silu(Wg x) * (Wu x)) (+ residual), as moe_decode_ff
+    documents. ``x`` bf16 [T, H], any row stride of a multiple of 8; ``w13`` = [Wg; Wu] bf16 [2 I, H] and ``w2``
+    bf16 [H, I], or for ``wdtype`` "int8" (codes, scale) of each, a scale a row. ``gate_up``: a bf16
+    [T, 2 I] tensor that receives the sums which :func:`feed_forward_backward` needs (bf16 weights).
+    ``out`` may be the residual, and x."""
+    int8 = wdtype == "int8"
+    if int8:
+        _need(all(isinstance(w, (tuple, list)) and len(w) == 2 for w in (w13, w2)), "int8 weights come as (codes, scale)")
+    hidden, inter = _ff_sizes(w13[0], w2[0]) if int8 else _ff_sizes(w13, w2)
+    cfg = _ff_config(hidden, inter, wdtype)
+    dev = x.get_device()
+    px, t, sx = _rows(x, "x", hidden, dev)
+    if int8:
+        (p13, s13), (p2, s2) = _codes(w13, "w13", 2 * inter, hidden, dev), _codes(w2, "w2", hidden, inter, dev)
+    else:
+        p13 = _tensor(w13, "w13", torch.bfloat16, (2 * inter, hidden), dev)
+        p2, s13, s2 = _tensor(w2, "w2", torch.bfloat16, (hidden, inter), dev), None, None
+    cw = _lib.FfWeights(p13, p2, s13, s2)
+    pr = None if residual is None else _tensor(residual, "residual", torch.bfloat16, (t, hidden), dev)
+    pk = None if gate_up is None else _tensor(gate_up, "gate_up", torch.bfloat16, (t, 2 * inter), dev)
+    s, leave = _enter(dev, stream)
+    try:
+        if out is None:
+            out = torch.empty((t, hidden), dtype=torch.bfloat16, device=dev)
+            po = out.data_ptr()
+        else:
+            po = _tensor(out, "out", torch.bfloat16, (t, hidden), dev)
+        ws = _workspace(workspace, feed_forward_workspace(hidden, inter, t, wdtype=wdtype), dev)
+        st = _lib.load().moe_decode_ff(cfg, cw, px, sx, pr, pk, po, t, ws.data_ptr(), ws.numel(), s)
+    finally:
+        if leave is not None:
+            leave.close()
+    if st:
+        _lib.check(st, "moe_decode_ff")
+    return out
+
+
+def feed_forward_backward(grad: torch.Tensor, x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
+                          gate_up: torch.Tensor, *, dx: torch.Tensor | None = None, dw13: torch.Tensor | None = None,
+                          dw2: torch.Tensor | None = None, accumulate: bool = False, input_grad: bool = True,
+                          weight_grad: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """(dx, dw13, dw2): the gradients of :func:`feed_forward` (bf16 weights) from ``grad``, that of its result,
+    and ``gate_up``, which it kept; as moe_decode_ff_backward documents. ``grad`` and ``x`` bf16 [T, H], any row
+    stride of a multiple of 8. The residual's gradient is ``grad``. The gradients are bf16; ``dw13`` and
+    ``dw2`` may be given as fp32, and with ``accumulate`` are then added to. Without ``input_grad``
+    or ``weight_grad`` what is not wanted is None."""
+    hidden, inter = _ff_sizes(w13, w2)
+    cfg = _ff_config(hidden, inter, "bf16")
+    dev = x.get_device()
+    px, t, sx = _rows(x, "x", hidden, dev)
+    pg, tg, sg = _rows(grad, "grad", hidden, dev)
+    _need(t == tg, "grad and x have the same rows")
+    _need(input_grad or weight_grad, "no gradient is wanted")
+    cw = _lib.FfWeights(_tensor(w13, "w13", torch.bfloat16, (2 * inter, hidden), dev),
+                        _tensor(w2, "w2", torch.bfloat16, (hidden, inter), dev), None, None)
+    pk = _tensor(gate_up, "gate_up", torch.bfloat16, (t, 2 * inter), dev)
+    _need((input_grad or dx is None) and (weight_grad or (dw13 is None and dw2 is None)),
+          "a gradient that is not wanted has no place")
+    given = [d for d in (dw13, dw2) if d is not None]
+    dtype = given[0].dtype if given else torch.bfloat16
+    _need(dtype in _DTYPES, "weight gradients are bf16 or fp32")
+    _need(not accumulate or (len(given) == 2 and dtype is torch.float32), "accumulate adds to fp32 dw13 and dw2 that are given")
+    px_, p13, p2 = None, None, None
+    s, leave = _enter(dev, stream)
+    try:
+        if input_grad:
+            dx = torch.empty((t, hidden), dtype=torch.bfloat16, device=dev) if dx is None else dx
+            px_ = _tensor(dx, "dx", torch.bfloat16, (t, hidden), dev)
+        if weight_grad:
+            dw13 = torch.empty((2 * inter, hidden), dtype=dtype, device=dev) if dw13 is None else dw13
+            dw2 = torch.empty((hidden, inter), dtype=dtype, device=dev) if dw2 is None else dw2
+            p13 = _tensor(dw13, "dw13", dtype, (2 * inter, hidden), dev)
+            p2 = _tensor(dw2, "dw2", dtype, (hidden, inter), dev)
+        ws = _workspace(workspace, feed_forward_backward_workspace(hidden, inter, t), dev)
+        st = _lib.load().moe_decode_ff_backward(cfg, cw, pg, sg, px, sx, pk, px_, p13, p2, _DTYPES[dtype], accumulate, t,
+                                                ws.data_ptr(), ws.numel(), s)
+    finally:
+        if leave is not None:
+            leave.close()
+    if st:
+        _lib.check(st, "moe_decode_ff_backward")
+    return dx, dw13, dw2
 
 
 def status(workspace: torch.Tensor, stream=None) -> int:

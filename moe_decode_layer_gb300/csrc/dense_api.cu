@@ -1,0 +1,549 @@
+// Host side of the dense operators: checks, workspace layout, launch shapes.
+// See include/moe_decode_dense.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "../../include/moe_decode_dense.h"
+#include "dense_params.h"
+#include "rows_host.h"
+
+using namespace moe;
+using namespace moe::rows;
+using namespace moe::dense;
+
+namespace {
+
+constexpr int kMostWidth = 65536;
+constexpr size_t kStatusBytes = kStatusKernels * kMaxSms * 4;
+
+// [halves][rows][cols] of 2-byte numbers (or fp32), copied in boxes of 128 bytes x box_rows rows;
+// what lies past the matrix reads as zero and is not written.
+bool make_map(CUtensorMap* m, const void* ptr, int64_t pitch, int64_t cols, int64_t rows, int box_rows, int halves = 1,
+              int64_t half_bytes = 0, bool f32 = false) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)halves};
+  const cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)(halves > 1 ? half_bytes : pitch)};
+  const cuuint32_t box[3] = {f32 ? 32u : 64u, (cuuint32_t)box_rows, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims,
+             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A matrix operand: a stored matrix [rows][cols], and whether its rows or its columns are k's.
+struct Matrix {
+  const void* ptr;
+  int64_t pitch;  // bytes
+  int64_t rows, cols;
+};
+
+struct PairLaunch {
+  PairParams p = {};
+  CUtensorMap a, b, d, e, g;
+  int form = 0, epi = 0;
+};
+
+// Width of the tiles and pairs that share a tile's K. A step of 64 k costs its tensor time (2 bn
+// clocks), its operand bytes (about 55 a clock and SM from L2) and, where few row tiles share
+// the columns' operand, that operand's bytes at an SM's share of the HBM rate (23 a clock; at
+// most 45 for an SM while others rest); a tile about 2500 clocks of start and epilogue, 1800
+// more where sums are joined. Clusters of four and eight CTAs do not fill every SM (7 of 8 are counted on).
+void shape_of(PairParams& p, bool swiglu, const Device& d) {
+  const int pairs = d.sms / 2, ksteps = (p.K + 63) / 64;
+  double least = 1e300;
+  p.tiles_m = (int)cdiv(p.M, kTileM);
+  for (int bn : {256, 128})
+    for (int split : {1, 2, 4}) {
+      const int tiles_n = (int)cdiv(p.N, swiglu ? bn / 2 : bn);
+      const int64_t tiles = (int64_t)p.tiles_m * tiles_n;
+      if (split > 1 && (tiles * split * 2 > d.sms * 7 / 8 || ksteps < 4 * split)) continue;
+      const double waves = split > 1 ? 1 : (double)cdiv(tiles, pairs);
+      const double ctas = 2.0 * std::min<double>((double)tiles * split, pairs);
+      const double rows = std::min(128.0, std::max(16.0, p.M / 2.0));
+      const double hbm = bn * 64.0 / (std::min(45.0, 23.0 * d.sms / ctas) * std::min(p.tiles_m, kGroupM));
+      const double step = std::max({2.0 * bn, (rows * 128.0 + bn * 64.0) / 55.0, hbm});
+      const double cost = waves * (cdiv(ksteps, split) * step + 600.0) + 2500.0 + (split > 1 ? 1800.0 : 0.0);
+      if (cost < least * 0.98) {
+        least = cost;
+        p.bn = bn;
+        p.split = split;
+        p.tiles_n = tiles_n;
+      }
+    }
+}
+
+// Operands a and b, and results: map d at `out` (and e, g as the epilogue has them). Descriptors only.
+bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b, bool fp16, const Device& d) {
+  PairParams& p = l.p;
+  const bool swiglu = epi == PAIR_SWIGLU || epi == PAIR_SWIGLU_F32;
+  l.form = form;
+  l.epi = epi;
+  shape_of(p, swiglu, d);
+  p.bufs = epi == PAIR_SWIGLU || epi == PAIR_DSWIGLU ? 3 : 2;
+  p.stage_bytes = 128 * 128 + p.bn * 64;
+  p.stages = std::min(kPairStages, (d.smem - 2048 - 8 * p.bufs * kStageBox) / p.stage_bytes);
+  // fp32 accumulators; bf16 or fp16 operands; k or the operand's own index innermost; M = 256 of a pair
+  p.idesc = 1u << 4 | (fp16 ? 0u : 1u << 7 | 1u << 10) | (form == FORM_MM ? 1u << 15 : 0u) |
+            (form != FORM_KK ? 1u << 16 : 0u) | (uint32_t)(p.bn >> 3) << 17 | 16u << 24;
+  const bool ok_a = make_map(&l.a, a.ptr, a.pitch, a.cols, a.rows, form == FORM_MM ? 64 : 128);
+  const bool ok_b = swiglu ? make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows / 2, p.bn / 2, 2, b.pitch * (b.rows / 2))
+                           : make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows, form == FORM_KK ? p.bn / 2 : 64);
+  l.e = l.g = l.a;
+  return ok_a && ok_b && p.stages >= 2 && p.stages * p.stage_bytes >= (p.split > 1 ? p.bn * 512 : 0);
+}
+
+// Results [M, N] of 2 bytes, or fp32 (as pairs of 2 bytes where nothing is added).
+bool prepare_out(PairLaunch& l, const void* out, bool f32) {
+  const PairParams& p = l.p;
+  if (f32 && p.reduce) return make_map(&l.d, out, (int64_t)p.N * 4, p.N, p.M, 32, 1, 0, true);
+  // an fp32 column counts as two
+  return make_map(&l.d, out, (int64_t)p.N * (f32 ? 4 : 2), p.N * (f32 ? 2 : 1), p.M, 32);
+}
+
+cudaError_t launch(PairLaunch& l, const Device& d, bool pdl, cudaStream_t s) {
+  const void* k = pair_kernel(l.form, l.epi);
+  static std::atomic<uint64_t> ready[3][5];  // per kernel: devices whose limit is set
+  if (d.id >= 64 || !(ready[l.form][l.epi].load() >> d.id & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem - 1024);
+    if (e != cudaSuccess) return e;
+    if (d.id < 64) ready[l.form][l.epi].fetch_or(1ull << d.id);
+  }
+  l.p.pdl = pdl;
+  const int64_t tiles = (int64_t)l.p.tiles_m * l.p.tiles_n;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(2 * l.p.split * (l.p.split > 1 ? tiles : std::min<int64_t>(tiles, d.sms / 2))));
+  c.blockDim = dim3(kPairThreads);
+  // All of the SM's shared memory: a CTA takes all tensor memory, and a pair's CTAs wait for one
+  // another, so none may wait for tensor memory that a CTA of another launch on its SM holds.
+  c.dynamicSmemBytes = d.smem - 1024;
+  c.stream = s;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = 2 * l.p.split;
+  a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+  c.attrs = a;
+  c.numAttrs = 2;
+  void* args[] = {&l.p, &l.a, &l.b, &l.d, &l.e, &l.g};
+  return cudaLaunchKernelExC(&c, k, args);
+}
+
+// Places in a workspace, 256 bytes apart at least.
+struct Places {
+  size_t at = 0;
+  size_t take(size_t bytes) {
+    const size_t o = at;
+    at = up(at + bytes, 256);
+    return o;
+  }
+};
+
+bool few(int64_t rows) { return rows <= kStreamRows; }
+
+// ------------------------------------------------------------------ int8
+moe_status check_int8(const moe_int8_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->inner <= 0 || c->outer <= 0) return MOE_ERR_INVALID_ARG;
+  if (c->x_dtype != MOE_I8 && c->x_dtype != MOE_BF16 && c->x_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (c->out_dtype != MOE_BF16 && c->out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (c->inner % 16 || c->outer % 8 || c->inner > kMostWidth || c->outer > kMostWidth) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct Int8Plan {
+  size_t status, codes, scale, w, bytes;
+};
+// Few rows go with the codes as they are, many as fp16 copies of them and of the weights: exact,
+// and the tensor core's full rate for a pass over the weights (3 bytes each).
+Int8Plan int8_plan(const moe_int8_config& c, int64_t rows) {
+  Places pl;
+  Int8Plan p = {};
+  p.status = pl.take(kStatusBytes);
+  const bool made = c.x_dtype != MOE_I8;
+  if (made || !few(rows)) p.codes = pl.take((size_t)rows * c.inner * (few(rows) ? 1 : 2));
+  if (made) p.scale = pl.take((size_t)rows * 4);
+  if (!few(rows)) p.w = pl.take((size_t)c.outer * (c.swiglu ? 2 : 1) * c.inner * 2);
+  p.bytes = pl.at;
+  return p;
+}
+
+// A product of codes (or of what is quantised first) with one matrix; descriptors in l before any launch.
+struct Int8Product {
+  moe_int8_config c;
+  const int8_t* w;
+  const float* w_scale;
+  const void* x;
+  const float* x_scale;  // MOE_I8
+  int64_t x_stride;
+  const void* addend;
+  void* out;
+  int64_t rows;
+  // in the workspace
+  int* status;
+  bool status_keep;
+  uint8_t* codes;
+  float* scale;
+  __half* w16;
+  PairLaunch l;
+};
+
+moe_status prepare_int8(Int8Product& a, const Device& d) {
+  if (few(a.rows)) return MOE_OK;
+  const bool f32 = a.c.out_dtype == MOE_F32;
+  const int epi = a.c.swiglu ? (f32 ? PAIR_SWIGLU_F32 : PAIR_SWIGLU) : f32 ? PAIR_F32 : PAIR_BF16;
+  PairParams& p = a.l.p;
+  p.M = (int)a.rows;
+  p.N = a.c.outer;
+  p.K = a.c.inner;
+  p.row_scale = a.c.x_dtype == MOE_I8 ? a.x_scale : a.scale;
+  p.col_scale = a.w_scale;
+  p.addend = static_cast<const __nv_bfloat16*>(a.addend);
+  p.status = a.status;
+  p.status_keep = a.status_keep;
+  const int64_t k = a.c.inner;
+  return prepare(a.l, FORM_KK, epi, {a.codes, k * 2, a.rows, k}, {a.w16, k * 2, (int64_t)a.c.outer * (a.c.swiglu ? 2 : 1), k},
+                 true, d) &&
+                 prepare_out(a.l, a.out, f32)
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+cudaError_t launch_int8(Int8Product& a, const Device& d, bool pdl, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  const bool made = a.c.x_dtype != MOE_I8, small = few(a.rows);
+  if (made) {
+    e = launch_quantise(a.c.x_dtype, a.x, a.x_stride, a.rows, a.c.inner, a.codes, !small, a.scale, pdl, s);
+    pdl = true;
+  } else if (!small) {
+    e = launch_widen(static_cast<const int8_t*>(a.x), a.x_stride, a.rows, a.c.inner, reinterpret_cast<__half*>(a.codes), pdl, s);
+    pdl = true;
+  }
+  if (e != cudaSuccess) return e;
+  if (!small) {
+    e = launch_widen(a.w, a.c.inner, (int64_t)a.c.outer * (a.c.swiglu ? 2 : 1), a.c.inner, a.w16, pdl, s);
+    return e == cudaSuccess ? launch(a.l, d, true, s) : e;
+  }
+  StreamParams p = {};
+  p.w = a.w;
+  p.x = made ? static_cast<const void*>(a.codes) : a.x;
+  p.x_stride = made ? a.c.inner : a.x_stride;
+  p.T = (int)a.rows;
+  p.K = a.c.inner;
+  p.R = a.c.outer;
+  p.swiglu = a.c.swiglu != 0;
+  p.x_scale = made ? a.scale : a.x_scale;
+  p.w_scale = a.w_scale;
+  p.addend = static_cast<const __nv_bfloat16*>(a.addend);
+  p.out = a.out;
+  p.out_f32 = a.c.out_dtype == MOE_F32;
+  p.status = a.status_keep ? nullptr : a.status;
+  return launch_stream(p, true, pdl, d.sms, s);
+}
+
+// ------------------------------------------------------------------ feed-forward
+moe_status check_ff(const moe_ff_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->hidden <= 0 || c->inter <= 0) return MOE_ERR_INVALID_ARG;
+  if (c->wdtype != MOE_W_BF16 && c->wdtype != MOE_W_INT8) return MOE_ERR_UNSUPPORTED;
+  const int step = c->wdtype == MOE_W_INT8 ? 16 : 8;
+  if (c->hidden % step || c->inter % step || c->hidden > kMostWidth || c->inter > kMostWidth) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct FfPlan {
+  size_t status, h, codes, scale, w, bytes;
+};
+FfPlan ff_plan(const moe_ff_config& c, int64_t rows) {
+  Places pl;
+  FfPlan p = {};
+  p.status = pl.take(kStatusBytes);
+  const bool int8 = c.wdtype == MOE_W_INT8;
+  p.h = pl.take((size_t)rows * c.inter * (int8 ? 4 : 2));
+  if (int8) {
+    p.codes = pl.take((size_t)rows * std::max(c.hidden, c.inter) * (few(rows) ? 1 : 2));
+    p.scale = pl.take((size_t)rows * 4);
+    if (!few(rows)) p.w = pl.take((size_t)c.hidden * c.inter * 4);  // W13 in fp16, then W2
+  }
+  p.bytes = pl.at;
+  return p;
+}
+
+struct BackwardPlan {
+  size_t status, both, h, bytes;
+};
+BackwardPlan backward_plan(const moe_ff_config& c, int64_t rows) {
+  Places pl;
+  BackwardPlan p = {};
+  p.status = pl.take(kStatusBytes);
+  p.both = pl.take((size_t)rows * c.inter * 4);
+  p.h = pl.take((size_t)rows * c.inter * 2);
+  p.bytes = pl.at;
+  return p;
+}
+
+// Byte ranges of a call.
+struct Range {
+  const void* ptr;
+  int64_t bytes;
+};
+bool any_overlap(const Range& a, std::initializer_list<Range> others) {
+  for (const Range& o : others)
+    if (overlap(a.ptr, a.bytes, o.ptr, o.bytes)) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_decode_quantise(int32_t dtype, int32_t inner, const void* x, int64_t x_stride, int64_t rows, int8_t* codes,
+                               float* scale, moe_stream_t stream) {
+  if (inner <= 0 || rows < 0 || rows > kMaxRows) return MOE_ERR_INVALID_ARG;
+  if ((dtype != MOE_BF16 && dtype != MOE_F32) || inner % 8 || inner > kMostWidth) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const int64_t size = dtype == MOE_F32 ? 4 : 2;
+  if (!x || !codes || !scale || !aligned16(x) || !aligned16(codes) || !aligned4(scale)) return MOE_ERR_INVALID_ARG;
+  if (x_stride < inner || x_stride * size % 16) return MOE_ERR_INVALID_ARG;
+  if (rows_overlap(x, x_stride * size, inner * size, rows, codes, rows * inner) ||
+      rows_overlap(x, x_stride * size, inner * size, rows, scale, rows * 4) || overlap(codes, rows * inner, scale, rows * 4))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_quantise(dtype, x, x_stride, rows, inner, codes, false, scale, false,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_decode_project_int8_check(const moe_int8_config* c) { return check_int8(c); }
+
+moe_status moe_decode_project_int8_workspace(const moe_int8_config* c, int64_t rows, size_t* bytes) {
+  const moe_status st = check_int8(c);
+  if (st != MOE_OK) return st;
+  if (!bytes || rows < 0 || rows > kMaxRows) return MOE_ERR_INVALID_ARG;
+  *bytes = rows ? int8_plan(*c, rows).bytes : 0;
+  return MOE_OK;
+}
+
+moe_status moe_decode_project_int8(const moe_int8_config* c, const int8_t* w, const float* w_scale, const void* x,
+                                   const float* x_scale, int64_t x_stride, const void* addend, void* out, int64_t rows,
+                                   void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  moe_status st = check_int8(c);
+  if (st != MOE_OK) return st;
+  if (rows < 0 || rows > kMaxRows) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  const bool codes = c->x_dtype == MOE_I8, f32 = c->out_dtype == MOE_F32;
+  const int64_t size = codes ? 1 : c->x_dtype == MOE_F32 ? 4 : 2;
+  if (!w || !w_scale || !x || !out || !workspace || (codes && !x_scale)) return MOE_ERR_INVALID_ARG;
+  if (c->swiglu && addend) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned16(w_scale) || !aligned16(x) || !aligned16(addend) || !aligned16(out) || !aligned16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  if (codes && !aligned4(x_scale)) return MOE_ERR_INVALID_ARG;
+  if (x_stride < c->inner || x_stride * size % 16) return MOE_ERR_INVALID_ARG;
+  const int64_t add_bytes = rows * c->outer * 2, out_bytes = f32 ? 2 * add_bytes : add_bytes;
+  if (rows_overlap(x, x_stride * size, c->inner * size, rows, out, out_bytes)) return MOE_ERR_INVALID_ARG;
+  if (codes && overlap(x_scale, rows * 4, out, out_bytes)) return MOE_ERR_INVALID_ARG;
+  if ((addend != out || f32) && overlap(addend, add_bytes, out, out_bytes)) return MOE_ERR_INVALID_ARG;
+  const Int8Plan p = int8_plan(*c, rows);
+  if (workspace_bytes < p.bytes) return MOE_ERR_INVALID_ARG;
+  Device d;
+  if (!device(&d)) return MOE_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Int8Product a = {*c,  w,    w_scale, x, x_scale, x_stride, addend, out, rows, reinterpret_cast<int*>(ws + p.status), false,
+                   ws + p.codes, reinterpret_cast<float*>(ws + p.scale), reinterpret_cast<__half*>(ws + p.w), {}};
+  st = prepare_int8(a, d);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_int8(a, d, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_decode_ff_check(const moe_ff_config* c) { return check_ff(c); }
+
+moe_status moe_decode_ff_workspace(const moe_ff_config* c, int64_t rows, size_t* bytes) {
+  const moe_status st = check_ff(c);
+  if (st != MOE_OK) return st;
+  if (!bytes || rows < 0 || rows > kMaxRows) return MOE_ERR_INVALID_ARG;
+  *bytes = rows ? ff_plan(*c, rows).bytes : 0;
+  return MOE_OK;
+}
+
+moe_status moe_decode_ff(const moe_ff_config* c, const moe_ff_weights* wt, const void* x, int64_t x_stride,
+                         const void* residual, void* gate_up, void* out, int64_t rows, void* workspace,
+                         size_t workspace_bytes, moe_stream_t stream) {
+  moe_status st = check_ff(c);
+  if (st != MOE_OK) return st;
+  if (rows < 0 || rows > kMaxRows) return MOE_ERR_INVALID_ARG;
+  const bool int8 = c->wdtype == MOE_W_INT8;
+  if (int8 && gate_up) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!wt || !wt->w13 || !wt->w2 || !x || !out || !workspace || (int8 && (!wt->s13 || !wt->s2))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(wt->w13) || !aligned16(wt->w2) || !aligned16(x) || !aligned16(residual) || !aligned16(gate_up) ||
+      !aligned16(out) || !aligned16(workspace) || (int8 && (!aligned16(wt->s13) || !aligned16(wt->s2))))
+    return MOE_ERR_INVALID_ARG;
+  if (x_stride < c->hidden || x_stride % 8) return MOE_ERR_INVALID_ARG;
+  // The second product, which writes out, starts when the first has read x; each of its
+  // results takes its own residual first.
+  const int64_t out_bytes = rows * c->hidden * 2, kept_bytes = rows * c->inter * 4;
+  if (residual != out && overlap(residual, out_bytes, out, out_bytes)) return MOE_ERR_INVALID_ARG;
+  if ((x != out || (x_stride != c->hidden && rows > 1)) && rows_overlap(x, x_stride * 2, c->hidden * 2, rows, out, out_bytes))
+    return MOE_ERR_INVALID_ARG;
+  if (gate_up && (rows_overlap(x, x_stride * 2, c->hidden * 2, rows, gate_up, kept_bytes) ||
+                  any_overlap({gate_up, kept_bytes}, {{residual, out_bytes}, {out, out_bytes}})))
+    return MOE_ERR_INVALID_ARG;
+  const FfPlan p = ff_plan(*c, rows);
+  if (workspace_bytes < p.bytes) return MOE_ERR_INVALID_ARG;
+  Device d;
+  if (!device(&d)) return MOE_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int* status = reinterpret_cast<int*>(ws + p.status);
+  void* h = ws + p.h;
+  const int64_t hid = c->hidden, in = c->inter;
+
+  if (int8) {
+    uint8_t* codes = ws + p.codes;
+    float* scale = reinterpret_cast<float*>(ws + p.scale);
+    __half* w16 = reinterpret_cast<__half*>(ws + p.w);
+    Int8Product one = {{c->hidden, c->inter, 1, MOE_BF16, MOE_F32}, static_cast<const int8_t*>(wt->w13), wt->s13, x, nullptr,
+                       x_stride, nullptr, h, rows, status, false, codes, scale, w16, {}};
+    Int8Product two = {{c->inter, c->hidden, 0, MOE_F32, MOE_BF16}, static_cast<const int8_t*>(wt->w2), wt->s2, h, nullptr,
+                       in, residual, out, rows, status, true, codes, scale, w16, {}};
+    if ((st = prepare_int8(one, d)) != MOE_OK || (st = prepare_int8(two, d)) != MOE_OK) return st;
+    const cudaError_t e = launch_int8(one, d, false, s);
+    return cuda_status(e == cudaSuccess ? launch_int8(two, d, true, s) : e);
+  }
+
+  if (few(rows)) {
+    StreamParams one = {}, two = {};
+    one.w = wt->w13;
+    one.x = x;
+    one.x_stride = x_stride;
+    one.T = two.T = (int)rows;
+    one.K = two.R = c->hidden;
+    one.R = two.K = c->inter;
+    one.swiglu = 1;
+    one.keep = static_cast<__nv_bfloat16*>(gate_up);
+    one.out = h;
+    one.status = status;
+    two.w = wt->w2;
+    two.x = h;
+    two.x_stride = in;
+    two.addend = static_cast<const __nv_bfloat16*>(residual);
+    two.out = out;
+    const cudaError_t e = launch_stream(one, false, false, d.sms, s);
+    return cuda_status(e == cudaSuccess ? launch_stream(two, false, true, d.sms, s) : e);
+  }
+
+  PairLaunch one, two;
+  one.p.M = two.p.M = (int)rows;
+  one.p.N = two.p.K = c->inter;
+  one.p.K = two.p.N = c->hidden;
+  one.p.keep = gate_up != nullptr;
+  two.p.addend = static_cast<const __nv_bfloat16*>(residual);
+  one.p.status = two.p.status = status;
+  two.p.status_keep = 1;
+  if (!prepare(one, FORM_KK, PAIR_SWIGLU, {x, x_stride * 2, rows, hid}, {wt->w13, hid * 2, 2 * in, hid}, false, d) ||
+      !prepare_out(one, h, false) ||
+      (gate_up && !make_map(&one.e, gate_up, in * 4, in, rows, 32, 2, in * 2)) ||
+      !prepare(two, FORM_KK, PAIR_BF16, {h, in * 2, rows, in}, {wt->w2, in * 2, hid, in}, false, d) ||
+      !prepare_out(two, out, false))
+    return MOE_ERR_CUDA;
+  const cudaError_t e = launch(one, d, false, s);
+  return cuda_status(e == cudaSuccess ? launch(two, d, true, s) : e);
+}
+
+moe_status moe_decode_ff_backward_workspace(const moe_ff_config* c, int64_t rows, size_t* bytes) {
+  const moe_status st = check_ff(c);
+  if (st != MOE_OK) return st;
+  if (c->wdtype != MOE_W_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!bytes || rows < 0 || rows > kMaxRows) return MOE_ERR_INVALID_ARG;
+  *bytes = rows ? backward_plan(*c, rows).bytes : 0;
+  return MOE_OK;
+}
+
+moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* wt, const void* grad, int64_t grad_stride,
+                                  const void* x, int64_t x_stride, const void* gate_up, void* dx, void* dw13, void* dw2,
+                                  int32_t dw_dtype, int32_t accumulate, int64_t rows, void* workspace,
+                                  size_t workspace_bytes, moe_stream_t stream) {
+  moe_status st = check_ff(c);
+  if (st != MOE_OK) return st;
+  if (c->wdtype != MOE_W_BF16) return MOE_ERR_UNSUPPORTED;
+  if (rows < 0 || rows > kMaxRows || (!dx && !dw13 && !dw2)) return MOE_ERR_INVALID_ARG;
+  if (dw_dtype != MOE_BF16 && dw_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  const bool f32 = dw_dtype == MOE_F32;
+  if (accumulate && !f32) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(dx) || !aligned16(dw13) || !aligned16(dw2)) return MOE_ERR_INVALID_ARG;
+  const int64_t hid = c->hidden, in = c->inter, size = f32 ? 4 : 2;
+  const Range r_dx = {dx, rows * hid * 2}, r_13 = {dw13, 2 * in * hid * size}, r_2 = {dw2, hid * in * size};
+  if (any_overlap(r_13, {r_dx, r_2}) || any_overlap(r_dx, {r_2})) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    cudaError_t e = cudaSuccess;
+    if (!accumulate && dw13) e = launch_zero(dw13, r_13.bytes, s);
+    if (!accumulate && dw2 && e == cudaSuccess) e = launch_zero(dw2, r_2.bytes, s);
+    return cuda_status(e);
+  }
+  if (!wt || !wt->w2 || (dx && !wt->w13) || !grad || !gate_up || (dw13 && !x) || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(wt->w13) || !aligned16(wt->w2) || !aligned16(grad) || !aligned16(x) || !aligned16(gate_up) || !aligned16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  if (grad_stride < hid || grad_stride % 8 || (dw13 && (x_stride < hid || x_stride % 8))) return MOE_ERR_INVALID_ARG;
+  for (const Range& o : {r_dx, r_13, r_2}) {
+    if (!o.ptr) continue;
+    if (rows_overlap(grad, grad_stride * 2, hid * 2, rows, o.ptr, o.bytes) ||
+        (dw13 && rows_overlap(x, x_stride * 2, hid * 2, rows, o.ptr, o.bytes)) ||
+        any_overlap(o, {{gate_up, rows * in * 4}, {wt->w2, hid * in * 2}, {dx ? wt->w13 : nullptr, 2 * in * hid * 2}}))
+      return MOE_ERR_INVALID_ARG;
+  }
+  const BackwardPlan p = backward_plan(*c, rows);
+  if (workspace_bytes < p.bytes) return MOE_ERR_INVALID_ARG;
+  Device d;
+  if (!device(&d)) return MOE_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  void *both = ws + p.both, *h = ws + p.h;
+  int* status = reinterpret_cast<int*>(ws + p.status);
+
+  // dh, and from it dg, du and h
+  PairLaunch one, up, down, inputs;
+  for (PairLaunch* l : {&one, &up, &down, &inputs}) {
+    l->p.status = status;
+    l->p.status_keep = l != &one;
+    l->p.reduce = accumulate != 0;
+  }
+  one.p.M = (int)rows;
+  one.p.N = c->inter;
+  one.p.K = c->hidden;
+  one.p.keep = dw2 != nullptr;
+  bool ok = prepare(one, FORM_KM, PAIR_DSWIGLU, {grad, grad_stride * 2, rows, hid}, {wt->w2, in * 2, hid, in}, false, d) &&
+            prepare_out(one, h, false) && make_map(&one.e, both, in * 4, in, rows, 32, 2, in * 2) &&
+            make_map(&one.g, gate_up, in * 4, in, rows, 32, 2, in * 2);
+  if (ok && dw13) {
+    up.p.M = 2 * c->inter;
+    up.p.N = c->hidden;
+    up.p.K = (int)rows;
+    ok = prepare(up, FORM_MM, f32 ? PAIR_F32 : PAIR_BF16, {both, in * 4, rows, 2 * in}, {x, x_stride * 2, rows, hid}, false, d) &&
+         prepare_out(up, dw13, f32);
+  }
+  if (ok && dw2) {
+    down.p.M = c->hidden;
+    down.p.N = c->inter;
+    down.p.K = (int)rows;
+    ok = prepare(down, FORM_MM, f32 ? PAIR_F32 : PAIR_BF16, {grad, grad_stride * 2, rows, hid}, {h, in * 2, rows, in}, false, d) &&
+         prepare_out(down, dw2, f32);
+  }
+  if (ok && dx) {
+    inputs.p.M = (int)rows;
+    inputs.p.N = c->hidden;
+    inputs.p.K = 2 * c->inter;
+    ok = prepare(inputs, FORM_KM, PAIR_BF16, {both, in * 4, rows, 2 * in}, {wt->w13, hid * 2, 2 * in, hid}, false, d) &&
+         prepare_out(inputs, dx, false);
+  }
+  if (!ok) return MOE_ERR_CUDA;
+  cudaError_t e = launch(one, d, false, s);
+  if (e == cudaSuccess && dw2) e = launch(down, d, true, s);
+  if (e == cudaSuccess && dw13) e = launch(up, d, true, s);
+  if (e == cudaSuccess && dx) e = launch(inputs, d, true, s);
+  return cuda_status(e);
+}
+
+}  // extern "C"

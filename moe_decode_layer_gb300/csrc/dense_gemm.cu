@@ -1,0 +1,20 @@
+// Instantiations of the dense pair product for k-innermost operands, and the table of all.
+#include "dense_gemm.cuh"
+
+namespace moe {
+namespace dense {
+
+const void* pair_kernel_backward(int form, int epi);
+
+const void* pair_kernel(int form, int epi) {
+  if (form != FORM_KK) return pair_kernel_backward(form, epi);
+  switch (epi) {
+    case PAIR_SWIGLU: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_SWIGLU>);
+    case PAIR_SWIGLU_F32: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_SWIGLU_F32>);
+    case PAIR_F32: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_F32>);
+    default: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_BF16>);
+  }
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,535 @@
+// Dense matrix products of the feed-forward block and its backward pass (tcgen05, sm_103a):
+// D [M, N] = A B^T over K, fp32 accumulators, bf16 or fp16 operands.
+//
+// Two CTAs of a cluster (a pair of SMs) work on one tile of 256 rows x bn columns with
+// cta_group::2 instructions: each holds 128 rows of A and half of B's columns in shared
+// memory, so that a step of 64 k moves 32 KB into each SM for 2.1 M multiplications -- half
+// of what two separate CTAs would move. Both accumulators (2 x 256 columns) fill tensor memory:
+// the epilogue of one tile runs beside the product of the next.
+//
+// The gradients contract over rows of matrices that are stored by rows, so operands come in two
+// orders: k innermost (rows of x, weights of the forward pass) or the operand's own index
+// innermost (W2 and W13 as the backward pass reads them, and both operands of a weight
+// gradient). The tensor core takes either from a descriptor: nothing is transposed.
+//
+// Few tiles: the pairs of a cluster (2 or 4) take parts of K of one tile, and their sums are
+// joined through distributed shared memory, in the order of the parts.
+//
+// Warps: 0 copies (both CTAs), 1 tensor core (the pair's first CTA), 4..11 epilogue. All
+// copies are TMA with the operands' 128-byte swizzle; results leave through shared memory by
+// TMA stores, which clip what lies past the matrix.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "dense_params.h"
+#include "tc.cuh"
+
+namespace moe {
+namespace dense {
+
+using namespace rows;
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// This CTA's shared address as CTA r of the cluster has it.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t r) {
+  uint32_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(v) : "r"(addr), "r"(r));
+  return v;
+}
+// A copy into this CTA whose bytes count on a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most N of this thread's stores still read shared memory / are not done.
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+// D[tmem of both] (+)= A B^T: 256 rows, each CTA's 128 from its own shared memory.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on bar in the CTAs of the mask when all earlier mma_pair of this thread have completed.
+__device__ __forceinline__ void mma_pair_commit(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t mapped_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
+}
+// 32 accumulator columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&f)[32]) {
+  uint32_t v[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; i++) f[i] = __uint_as_float(v[i]);
+}
+
+// Descriptor of an operand whose own index is innermost: blocks of 64 of it (128 bytes, 128-byte
+// swizzle) x 64 k, 8 KB each, one after another; 8-k groups 1024 bytes apart. A step of 16 k is
+// 2048 bytes further on.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)64 << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// The place of 16-byte chunk c of row r in a box of 128-byte rows, as the TMA's swizzle has it.
+__device__ __forceinline__ uint32_t box_at(uint32_t box, int r, int c) { return box + r * 128 + ((c ^ (r & 7)) << 4); }
+
+// 32 values of a row as bf16, into chunks first .. first + 3 of its box.
+__device__ __forceinline__ void box_bf16(uint32_t box, int r, int first, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 4; c++)
+    st_shared4(box_at(box, r, first + c), pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+               pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+}
+__device__ __forceinline__ void box_f32(uint32_t box, int r, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; c++)
+    st_shared4(box_at(box, r, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+               __float_as_uint(v[4 * c + 3]));
+}
+
+// silu(g) * u in full fp32 (results that are quantised next: codes would flip at 2^-16).
+__device__ __forceinline__ float silu_mul_f32(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// ------------------------------------------------------------------ the kernel
+struct PairTile {
+  int m0, n0;
+};
+// Row tiles go round in groups of kGroupM, the columns outside: the pairs that run at one time
+// read about as much of A as of B, and most of it from L2.
+__device__ __forceinline__ PairTile pair_tile(const PairParams& p, int t, int cols) {
+  const int per = kGroupM * p.tiles_n, group = t / per;
+  const int gm = min(kGroupM, p.tiles_m - group * kGroupM), r = t - group * per;
+  return {(group * kGroupM + r % gm) * kTileM, r / gm * cols};
+}
+
+template <int FORM, int EPI>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    pair_gemm_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap map_a,
+                     const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d,
+                     const __grid_constant__ CUtensorMap map_e, const __grid_constant__ CUtensorMap map_g) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  // full, empty [kPairStages], tmem full / empty [2], an epilogue warp's loads [8], drain
+  __shared__ __align__(8) uint64_t s_bar[2 * kPairStages + 4 + 8 + 1];
+  constexpr bool kSwiglu = EPI == PAIR_SWIGLU || EPI == PAIR_SWIGLU_F32;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bar0 = smem_u32(s_bar);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kPairStages + s); };
+  auto tfull = [&](int b) { return bar0 + 8u * (2 * kPairStages + b); };
+  auto tempty = [&](int b) { return bar0 + 8u * (2 * kPairStages + 2 + b); };
+  auto loads = [&](int w) { return bar0 + 8u * (2 * kPairStages + 4 + w); };
+  const uint32_t drain = bar0 + 8u * (2 * kPairStages + 12);
+  const uint32_t crank = cluster_rank();
+  const int rank = crank & 1, part = crank >> 1;
+  const uint32_t first_cta = crank & ~1u;  // of the pair
+
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < p.stages; s++) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; b++) {
+      mbar_init(tfull(b), 1);
+      mbar_init(tempty(b), 16);  // the epilogue warps of both CTAs
+    }
+    for (int w = 0; w < 8; w++) mbar_init(loads(w), 1);
+    mbar_init(drain, 1);
+    mbar_init_fence();
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+    tma_prefetch_map(&map_d);
+    tma_prefetch_map(&map_e);
+  }
+  if (warp == 1) {
+    tmem_alloc2(smem_u32(&s_tmem), 512);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTA's barriers are there
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  if (p.pdl) {
+    pdl_wait();
+    fence_proxy_async_global();  // what the launch before wrote is read by TMA
+  }
+  pdl_launch_dependents();
+
+  const int cols = kSwiglu ? p.bn / 2 : p.bn;  // result columns of a tile
+  const int ntiles = p.tiles_m * p.tiles_n;
+  const int step = gridDim.x / (2 * p.split);
+  const int t_first = blockIdx.x / (2 * p.split);
+  const int ksteps = (p.K + 63) / 64;
+  const int k_first = ksteps * part / p.split, k_last = ksteps * (part + 1) / p.split;
+  const int b_rows = p.bn / 2;  // of B in this CTA
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- copies
+    if (lane == 0) {
+      Ring it;
+      bool ok = true;
+      for (int t = t_first; ok && t < ntiles; t += step) {
+        const PairTile tl = pair_tile(p, t, cols);
+        const int m = tl.m0 + rank * 128;
+        const int n = kSwiglu ? tl.n0 : tl.n0 + rank * b_rows, half = kSwiglu ? rank : 0;
+        for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
+          const uint32_t s = it.slot;
+          if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
+          const uint32_t bar = map_rank(full(s), first_cta);
+          const uint32_t a = base + s * p.stage_bytes, b = a + 128 * 128;
+          // (the other CTA's bytes may be counted before this; the phase ends with the arrival)
+          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * p.stage_bytes);
+          if (FORM == FORM_MM) {
+            tma_pair_3d(a, &map_a, m, k * 64, 0, bar);
+            tma_pair_3d(a + 8192, &map_a, m + 64, k * 64, 0, bar);
+          } else {
+            tma_pair_3d(a, &map_a, k * 64, m, 0, bar);
+          }
+          if (FORM == FORM_KK) {
+            tma_pair_3d(b, &map_b, k * 64, n, half, bar);
+          } else {
+            tma_pair_3d(b, &map_b, n, k * 64, 0, bar);
+            if (b_rows > 64) tma_pair_3d(b + 8192, &map_b, n + 64, k * 64, 0, bar);
+          }
+        }
+      }
+      // every arrival that the tensor core owes this CTA's barriers
+      for (int s = 0; ok && s < p.stages; s++, it.next(p.stages)) ok = wait_phase(empty(it.slot), it.parity ^ 1, &s_abort);
+      if (!ok) {  // let the copies in flight land before the shared memory goes
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------------- tensor core
+    const bool leader = elect_one();
+    const uint16_t both = (uint16_t)(3u << first_cta);
+    Ring it, acc;
+    bool ok = true;
+    for (int t = t_first; ok && t < ntiles; t += step, acc.next(2)) {
+      const int b = acc.slot;
+      if (!(ok = warp_wait(tempty(b), acc.parity ^ 1, &s_abort))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + b * 256;
+      for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
+        const uint32_t s = it.slot;
+        if (!(ok = warp_wait(full(s), it.parity, &s_abort))) break;
+        tc_fence_after();
+        const uint32_t at = base + s * p.stage_bytes;
+        const uint64_t da = FORM == FORM_MM ? smem_desc_mn(at) : smem_desc(at);
+        const uint64_t db = FORM == FORM_KK ? smem_desc(at + 128 * 128) : smem_desc_mn(at + 128 * 128);
+        constexpr int kA = FORM == FORM_MM ? 2048 >> 4 : 2, kB = FORM == FORM_KK ? 2 : 2048 >> 4;
+        if (leader) {
+#pragma unroll
+          for (int j = 0; j < 4; j++) mma_pair(d, da + kA * j, db + kB * j, p.idesc, k != k_first || j != 0);
+          mma_pair_commit(empty(s), both);
+        }
+        __syncwarp();
+      }
+      if (ok && leader) mma_pair_commit(tfull(b), both);
+    }
+    if (!ok && leader) {
+      mma_pair_commit(drain, (uint16_t)(1u << crank));
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(drain, 0) && global_ns() - t0 < kDrainNs) {
+      }
+    }
+  }
+
+  // ------------------------------------------------------------------ epilogue
+  const int ew = warp - 4;
+  const uint32_t boxes = base + p.stages * p.stage_bytes + max(ew, 0) * p.bufs * kStageBox;
+  uint32_t nload = 0, nstore = 0;
+  bool ok = true;
+  // Columns of a box: a row of it is 128 bytes.
+  constexpr int kBox = EPI == PAIR_F32 || EPI == PAIR_SWIGLU_F32 ? 32 : 64;
+  const int nbox = cols / kBox;
+  auto asks = [&](const PairTile& tl, int box, int q) {  // DSWIGLU: gate and up of a box
+    if (lane == 0) {
+      store_wait_read<0>();
+      mbar_arrive_expect_tx(loads(ew), 2 * kStageBox);
+      tma_load_3d(boxes, &map_g, tl.n0 + box * 64, tl.m0 + rank * 128 + q * 32, 0, loads(ew));
+      tma_load_3d(boxes + kStageBox, &map_g, tl.n0 + box * 64, tl.m0 + rank * 128 + q * 32, 1, loads(ew));
+    }
+    __syncwarp();
+  };
+  auto there = [&](const PairTile& tl, int box, int q) {
+    return tl.m0 + rank * 128 + q * 32 < p.M && tl.n0 + box * kBox < p.N;
+  };
+  // One box: 32 rows of the quadrant q. get(c, v): accumulator columns c .. c + 31 of this lane's row.
+  auto unit = [&](const PairTile& tl, int box, int q, auto get) {
+    const int row0 = tl.m0 + rank * 128 + q * 32, col0 = tl.n0 + box * kBox;
+    const int row = min(row0 + lane, p.M - 1);
+    const float rs = p.row_scale ? p.row_scale[row] : 1.0f;
+    // (columns past N are not stored; their scales are those of the last ones)
+    auto scaled = [&](float (&v)[32], int c, int half) {
+      if (!p.row_scale) return;
+#pragma unroll
+      for (int j = 0; j < 32; j++) v[j] *= rs * __ldg(p.col_scale + half * p.N + min(c + j, p.N - 1));
+    };
+    if (EPI == PAIR_SWIGLU) {
+      if (lane == 0) store_wait_read<0>();
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float g[32], u[32];
+        get(box * 64 + h * 32, g);
+        get(p.bn / 2 + box * 64 + h * 32, u);
+        scaled(g, col0 + h * 32, 0);
+        scaled(u, col0 + h * 32, 1);
+        if (p.keep) {
+          box_bf16(boxes + kStageBox, lane, 4 * h, g);
+          box_bf16(boxes + 2 * kStageBox, lane, 4 * h, u);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j++) g[j] = silu_mul(g[j], u[j]);
+        box_bf16(boxes, lane, 4 * h, g);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&map_d, col0, row0, 0, boxes);
+        if (p.keep) {
+          tma_store_3d(&map_e, col0, row0, 0, boxes + kStageBox);
+          tma_store_3d(&map_e, col0, row0, 1, boxes + 2 * kStageBox);
+        }
+        store_commit();
+      }
+    } else if (EPI == PAIR_DSWIGLU) {
+      ok = ok && warp_wait(loads(ew), nload & 1, &s_abort);
+      nload++;
+      if (!ok) return;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float v[32];
+        get(box * 64 + h * 32, v);
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          const uint32_t ag = box_at(boxes, lane, 4 * h + c), au = ag + kStageBox;
+          const uint4 g4 = ld_shared4(ag), u4 = ld_shared4(au);
+          const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+          uint32_t dg[4], du[4], hh[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            float a[2], b[2], w[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              const float g = e ? bf16hi(gw[j]) : bf16lo(gw[j]), u = e ? bf16hi(uw[j]) : bf16lo(uw[j]);
+              const float dh = v[8 * c + 2 * j + e];
+              const float sig = __fdividef(1.0f, 1.0f + __expf(-g)), s = g * sig;
+              w[e] = s * u;
+              b[e] = dh * s;
+              a[e] = dh * u * (sig + s * (1.0f - sig));
+            }
+            dg[j] = pack_bf16(a[0], a[1]);
+            du[j] = pack_bf16(b[0], b[1]);
+            hh[j] = pack_bf16(w[0], w[1]);
+          }
+          st_shared4(ag, dg[0], dg[1], dg[2], dg[3]);
+          st_shared4(au, du[0], du[1], du[2], du[3]);
+          st_shared4(ag + 2 * kStageBox, hh[0], hh[1], hh[2], hh[3]);
+        }
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&map_e, col0, row0, 0, boxes);
+        tma_store_3d(&map_e, col0, row0, 1, boxes + kStageBox);
+        if (p.keep) tma_store_3d(&map_d, col0, row0, 0, boxes + 2 * kStageBox);
+        store_commit();
+      }
+    } else {
+      // two boxes in turn: one is filled while the other leaves
+      const uint32_t at = boxes + (nstore++ & 1) * kStageBox;
+      if (lane == 0) store_wait_read<1>();
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < kBox / 32; h++) {
+        float v[32];
+        const int c = col0 + h * 32;
+        uint4 ad[4];
+        if (p.addend) {
+          const __nv_bfloat16* a = p.addend + (size_t)row * p.N + c;
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            if (c + 8 * j < p.N) ad[j] = *reinterpret_cast<const uint4*>(a + 8 * j);
+            else ad[j] = make_uint4(0, 0, 0, 0);
+        }
+        if (EPI == PAIR_SWIGLU_F32) {
+          float u[32];
+          get(box * 32, v);
+          get(p.bn / 2 + box * 32, u);
+          scaled(v, c, 0);
+          scaled(u, c, 1);
+#pragma unroll
+          for (int j = 0; j < 32; j++) v[j] = silu_mul_f32(v[j], u[j]);
+        } else {
+          get(box * kBox + h * 32, v);
+          scaled(v, c, 0);
+        }
+        if (p.addend) {
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const uint32_t w[4] = {ad[j].x, ad[j].y, ad[j].z, ad[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              v[8 * j + 2 * i] += bf16lo(w[i]);
+              v[8 * j + 2 * i + 1] += bf16hi(w[i]);
+            }
+          }
+        }
+        if (kBox == 32) box_f32(at, lane, v); else box_bf16(at, lane, 4 * h, v);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (EPI == PAIR_F32 && p.reduce) tma_add_3d(&map_d, col0, row0, 0, at);
+        else tma_store_3d(&map_d, kBox == 32 ? 2 * col0 : col0, row0, 0, at);  // (an fp32 column is two of 2 bytes)
+        store_commit();
+      }
+    }
+  };
+
+  if (warp >= 4) {
+    const int q = warp & 3, which = ew >> 2;  // this warp's TMEM lanes; two warps share them, box by box
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    Ring acc;
+    for (int t = t_first; ok && t < ntiles; t += step, acc.next(2)) {
+      const PairTile tl = pair_tile(p, t, cols);
+      const int b = acc.slot;
+      if (EPI == PAIR_DSWIGLU && p.split == 1 && which < nbox && there(tl, which, q)) asks(tl, which, q);
+      if (!(ok = warp_wait(tfull(b), acc.parity, &s_abort))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + b * 256 + lanes;
+      if (p.split == 1) {
+        for (int box = which; box < nbox && there(tl, box, q); box += 2) {
+          if (EPI == PAIR_DSWIGLU && box != which) asks(tl, box, q);
+          unit(tl, box, q, [&](int c, float (&v)[32]) { tmem_ld32(d + c, v); });
+        }
+      } else {
+        // the partial sums, [column][row], where the stages were: all are used
+        for (int c = which * (p.bn / 2); c < (which + 1) * (p.bn / 2); c += 32) {
+          float v[32];
+          tmem_ld32(d + c, v);
+          const uint32_t at = base + (uint32_t)(c * 128 + q * 32 + lane) * 4u;
+#pragma unroll
+          for (int j = 0; j < 32; j++)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + j * 512), "f"(v[j]) : "memory");
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_rank(tempty(b), first_cta));
+    }
+  }
+  if (p.split > 1) {
+    // Each CTA joins some of the boxes, in the order of the parts. All threads come here,
+    // whatever became of their waits; a cluster has one tile.
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 4) {
+      const PairTile tl = pair_tile(p, min(t_first, ntiles - 1), cols);
+      for (int i = part + p.split * ew; i < 4 * nbox; i += 8 * p.split) {
+        const int q = i & 3, box = i >> 2;
+        if (!there(tl, box, q)) continue;
+        if (EPI == PAIR_DSWIGLU) asks(tl, box, q);
+        unit(tl, box, q, [&](int c, float (&v)[32]) {
+          const uint32_t at = base + (uint32_t)(c * 128 + q * 32 + lane) * 4u;
+#pragma unroll
+          for (int j = 0; j < 32; j++) v[j] = 0.0f;
+          for (int s = 0; s < p.split; s++)
+#pragma unroll
+            for (int j = 0; j < 32; j++) v[j] += ld_cluster(at + j * 512, 2 * s + rank);
+        });
+      }
+    }
+  }
+  if (warp >= 4 && lane == 0) store_wait_all();  // shared memory is read and the results are written
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while the other's instructions or loads reach into it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc2(tmem, 512);
+  // the status words: this CTA's, and from CTA 0 those that no CTA has, and the second launch's
+  if (tid == 0 && (s_abort || !p.status_keep)) p.status[blockIdx.x] = s_abort;
+  if (blockIdx.x == 0 && !p.status_keep)
+    for (int i = gridDim.x + tid; i < 2 * kMaxSms; i += kPairThreads) p.status[i] = 0;
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,81 @@
+// Launch parameters of the dense operators' kernels, shared by the host code
+// (dense_api.cu) and the kernels.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "rows_params.h"
+
+namespace moe {
+namespace dense {
+
+constexpr int kPairStages = 8;       // operand stages at most
+constexpr int kPairThreads = 384;    // copies, tensor core, two idle warps, eight epilogue warps
+constexpr int kTileM = 256;          // rows of a pair's tile
+constexpr int kStageBox = 4096;      // an epilogue warp's box in shared memory: 32 rows of 128 bytes
+constexpr int kSplitMost = 4;        // pairs of a cluster of 8
+constexpr int kGroupM = 8;           // row tiles that go round the columns together
+
+// Which of the operands lies with its own index innermost (MN-major), not with k's.
+enum Form {
+  FORM_KK = 0,  // A [M, K], B [N, K]
+  FORM_KM = 1,  // A [M, K], B [K, N]
+  FORM_MM = 2   // A [K, M], B [K, N]
+};
+enum PairEpi {
+  PAIR_BF16 = 0,
+  PAIR_F32 = 1,
+  PAIR_SWIGLU = 2,      // bf16 silu(gate) * up, and (map_e) gate and up themselves
+  PAIR_SWIGLU_F32 = 3,  // the same in fp32, without them
+  PAIR_DSWIGLU = 4      // from dh, gate and up: bf16 dg, du (map_e) and h
+};
+
+struct PairParams {
+  int M, N, K;   // SWIGLU: N columns of h, 2 N rows of B
+  int bn;        // accumulator columns of a tile, 256 or 128 (SWIGLU: half gate, half up)
+  int tiles_m, tiles_n;
+  int split;     // pairs of a cluster that share a tile's K
+  int stages, stage_bytes;
+  int bufs;      // boxes of an epilogue warp
+  uint32_t idesc;
+  const float* row_scale;  // int8: a scale for each row and each column (gate columns first), or NULL
+  const float* col_scale;
+  const __nv_bfloat16* addend;  // [M, N], or NULL
+  int keep;      // SWIGLU: store gate and up; DSWIGLU: store h
+  int reduce;    // F32: add to what is there
+  int pdl;
+  int* status;   // one word a CTA; 1 = a wait ran into its limit
+  int status_keep;  // 1: not the call's first launch with waits; words are only set
+};
+
+const void* pair_kernel(int form, int epi);
+
+// Few rows: x on the tensor cores' N side, the weights straight from global memory.
+struct StreamParams {
+  const void* w;   // bf16 or int8 [R, K], SWIGLU: [2 R, K]
+  const void* x;   // bf16 or int8 codes, row t at x + t * x_stride elements
+  int64_t x_stride;
+  int T, K, R;
+  int swiglu;
+  const float* x_scale;  // int8
+  const float* w_scale;
+  const __nv_bfloat16* addend;
+  void* out;
+  int out_f32;
+  __nv_bfloat16* keep;   // SWIGLU: [T, 2 R], or NULL
+  int* status;           // the workspace's status words, to be cleared, or NULL
+};
+constexpr int kStreamRows = 32;  // rows at most
+cudaError_t launch_stream(const StreamParams& p, bool int8, bool pdl, int sms, cudaStream_t s);
+
+// codes of rows, as int8 or (half) as fp16 numbers
+cudaError_t launch_quantise(int dtype, const void* x, int64_t x_stride, int64_t rows, int inner, void* codes, bool half,
+                            float* scale, bool pdl, cudaStream_t s);
+// int8 -> fp16, 16 at a time; row r of src at src + r * stride
+cudaError_t launch_widen(const int8_t* src, int64_t stride, int64_t rows, int cols, __half* dst, bool pdl, cudaStream_t s);
+cudaError_t launch_zero(void* p, int64_t bytes, cudaStream_t s);
+
+}  // namespace dense
+}  // namespace moe
