@@ -52,16 +52,19 @@ struct PairLaunch {
 // clocks), its operand bytes (about 55 a clock and SM from L2) and, where few row tiles share
 // the columns' operand, that operand's bytes at an SM's share of the HBM rate (23 a clock; at
 // most 45 for an SM while others rest); a tile about 2500 clocks of start and epilogue, 1800
-// more where sums are joined. Clusters of four and eight CTAs do not fill every SM (7 of 8 are counted on).
+// more where sums are joined. Clusters of four and eight CTAs do not fill every SM: of 152, 36 and 15
+// are resident at once (a 16th of eight waited for another's end: 34 us for a product of 256 rows
+// that takes 12).
 void shape_of(PairParams& p, bool swiglu, const Device& d) {
   const int pairs = d.sms / 2, ksteps = (p.K + 63) / 64;
   double least = 1e300;
   p.tiles_m = (int)cdiv(p.M, kTileM);
-  for (int bn : {256, 128})
+  for (int bn : {256, 192, 128})
     for (int split : {1, 2, 4}) {
+      if (swiglu && bn == 192) continue;
       const int tiles_n = (int)cdiv(p.N, swiglu ? bn / 2 : bn);
       const int64_t tiles = (int64_t)p.tiles_m * tiles_n;
-      if (split > 1 && (tiles * split * 2 > d.sms * 7 / 8 || ksteps < 4 * split)) continue;
+      if (split > 1 && (tiles > (split == 2 ? d.sms * 9 / 38 : d.sms / 10) || ksteps < 4 * split)) continue;
       const double waves = split > 1 ? 1 : (double)cdiv(tiles, pairs);
       const double ctas = 2.0 * std::min<double>((double)tiles * split, pairs);
       const double rows = std::min(128.0, std::max(16.0, p.M / 2.0));
@@ -77,6 +80,8 @@ void shape_of(PairParams& p, bool swiglu, const Device& d) {
     }
 }
 
+constexpr int kFewWarpsK = 2048;
+
 // Operands a and b, and results: map d at `out` (and e, g as the epilogue has them). Descriptors only.
 bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b, bool fp16, const Device& d) {
   PairParams& p = l.p;
@@ -84,9 +89,13 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   l.form = form;
   l.epi = epi;
   shape_of(p, swiglu, d);
-  p.bufs = epi == PAIR_SWIGLU || epi == PAIR_DSWIGLU ? 3 : 2;
-  p.stage_bytes = 128 * 128 + p.bn * 64;
-  p.stages = std::min(kPairStages, (d.smem - 2048 - 8 * p.bufs * kStageBox) / p.stage_bytes);
+  p.bufs = epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU ? 1 : 2;
+  p.stage_bytes = 128 * 128 + (form == FORM_KK ? p.bn * 64 : (int)cdiv(p.bn, 128) * 8192);
+  // Three boxes a warp leave four stages of 256 columns; with four warps there are five. Where a tile's
+  // product is long enough for its epilogue, that is faster.
+  p.ewarps = p.bufs == 3 && p.split == 1 && p.K >= kFewWarpsK ? 4 : 8;
+  p.stages = std::min(kPairStages, (d.smem - 2048 - p.ewarps * p.bufs * kStageBox) / p.stage_bytes);
+  p.ahead = p.tiles_m <= 2 && form != FORM_MM ? 8 : 0;
   // fp32 accumulators; bf16 or fp16 operands; k or the operand's own index innermost; M = 256 of a pair
   p.idesc = 1u << 4 | (fp16 ? 0u : 1u << 7 | 1u << 10) | (form == FORM_MM ? 1u << 15 : 0u) |
             (form != FORM_KK ? 1u << 16 : 0u) | (uint32_t)(p.bn >> 3) << 17 | 16u << 24;
@@ -97,9 +106,10 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   return ok_a && ok_b && p.stages >= 2 && p.stages * p.stage_bytes >= (p.split > 1 ? p.bn * 512 : 0);
 }
 
-// Results [M, N] of 2 bytes, or fp32 (as pairs of 2 bytes where nothing is added).
+// Results [M, N] of 2 bytes, or fp32 (as pairs of 2 bytes where nothing is added), and their addends.
 bool prepare_out(PairLaunch& l, const void* out, bool f32) {
   const PairParams& p = l.p;
+  if (p.addend && l.epi == PAIR_BF16 && !make_map(&l.g, p.addend, (int64_t)p.N * 2, p.N, p.M, 32)) return false;
   if (f32 && p.reduce) return make_map(&l.d, out, (int64_t)p.N * 4, p.N, p.M, 32, 1, 0, true);
   // an fp32 column counts as two
   return make_map(&l.d, out, (int64_t)p.N * (f32 ? 4 : 2), p.N * (f32 ? 2 : 1), p.M, 32);

@@ -99,24 +99,46 @@ __device__ __forceinline__ void mma_pair_commit(uint32_t bar, uint16_t mask) {
       "h"(mask)
       : "memory");
 }
+// (Nothing in memory is handed over with it: the tensor-memory loads before it are done. A release
+// over the cluster waits for the thread's stores as well, 2200 clocks a tile.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mapped_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
-// 32 accumulator columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&f)[32]) {
-  uint32_t v[32];
+// 16 accumulator columns of this thread's TMEM lane; they are there after tmem_wait16.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Waits for loads of this thread; v is one of them (as an operand, so that no use of it comes earlier).
+__device__ __forceinline__ void tmem_wait16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15])
+               :
+               : "memory");
+}
+// The same from partial sums in shared memory, columns 512 bytes apart.
+__device__ __forceinline__ void smem_ld16(uint32_t addr, uint32_t (&v)[16]) {
 #pragma unroll
-  for (int i = 0; i < 32; i++) f[i] = __uint_as_float(v[i]);
+  for (int j = 0; j < 16; j++) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[j]) : "r"(addr + j * 512) : "memory");
+}
+// 16 bytes at this CTA's shared address in CTA r of the cluster.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t r) {
+  float4 v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(r)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
 // Descriptor of an operand whose own index is innermost: blocks of 64 of it (128 bytes, 128-byte
@@ -142,18 +164,19 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
 // The place of 16-byte chunk c of row r in a box of 128-byte rows, as the TMA's swizzle has it.
 __device__ __forceinline__ uint32_t box_at(uint32_t box, int r, int c) { return box + r * 128 + ((c ^ (r & 7)) << 4); }
 
-// 32 values of a row as bf16, into chunks first .. first + 3 of its box.
-__device__ __forceinline__ void box_bf16(uint32_t box, int r, int first, const float (&v)[32]) {
+// 16 values of a row as bf16, into chunks first and first + 1 of its box.
+__device__ __forceinline__ void box_bf16(uint32_t box, int r, int first, const uint32_t (&v)[16]) {
 #pragma unroll
-  for (int c = 0; c < 4; c++)
-    st_shared4(box_at(box, r, first + c), pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-               pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+  for (int c = 0; c < 2; c++) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) o[j] = pack_bf16(__uint_as_float(v[8 * c + 2 * j]), __uint_as_float(v[8 * c + 2 * j + 1]));
+    st_shared4(box_at(box, r, first + c), o[0], o[1], o[2], o[3]);
+  }
 }
-__device__ __forceinline__ void box_f32(uint32_t box, int r, const float (&v)[32]) {
+__device__ __forceinline__ void box_f32(uint32_t box, int r, int first, const uint32_t (&v)[16]) {
 #pragma unroll
-  for (int c = 0; c < 8; c++)
-    st_shared4(box_at(box, r, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
-               __float_as_uint(v[4 * c + 3]));
+  for (int c = 0; c < 4; c++) st_shared4(box_at(box, r, first + c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
 
 // silu(g) * u in full fp32 (results that are quantised next: codes would flip at 2^-16).
@@ -179,8 +202,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  // full, empty [kPairStages], tmem full / empty [2], an epilogue warp's loads [8], drain
-  __shared__ __align__(8) uint64_t s_bar[2 * kPairStages + 4 + 8 + 1];
+  // full, empty [kPairStages], tmem full / empty [2], an epilogue warp's loads [8][2], drain
+  __shared__ __align__(8) uint64_t s_bar[2 * kPairStages + 4 + 16 + 1];
   constexpr bool kSwiglu = EPI == PAIR_SWIGLU || EPI == PAIR_SWIGLU_F32;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -190,8 +213,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   auto empty = [&](int s) { return bar0 + 8u * (kPairStages + s); };
   auto tfull = [&](int b) { return bar0 + 8u * (2 * kPairStages + b); };
   auto tempty = [&](int b) { return bar0 + 8u * (2 * kPairStages + 2 + b); };
-  auto loads = [&](int w) { return bar0 + 8u * (2 * kPairStages + 4 + w); };
-  const uint32_t drain = bar0 + 8u * (2 * kPairStages + 12);
+  auto loads = [&](int w, int i) { return bar0 + 8u * (2 * kPairStages + 4 + 2 * w + i); };
+  const uint32_t drain = bar0 + 8u * (2 * kPairStages + 20);
   const uint32_t crank = cluster_rank();
   const int rank = crank & 1, part = crank >> 1;
   const uint32_t first_cta = crank & ~1u;  // of the pair
@@ -204,9 +227,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), 16);  // the epilogue warps of both CTAs
+      mbar_init(tempty(b), 2 * p.ewarps);  // the epilogue warps of both CTAs
     }
-    for (int w = 0; w < 8; w++) mbar_init(loads(w), 1);
+    for (int w = 0; w < 16; w++) mbar_init(loads(0, w), 1);
     mbar_init(drain, 1);
     mbar_init_fence();
     tma_prefetch_map(&map_a);
@@ -242,15 +265,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (lane == 0) {
       Ring it;
       bool ok = true;
+      // Few rows: the ring holds less of B than HBM's latency asks for; L2 takes the rest.
+      auto fetch_b = [&](int n, int half, int k) {
+        if (FORM == FORM_KK) {
+          tma_prefetch_3d(&map_b, k * 64, n, half);
+        } else {
+          tma_prefetch_3d(&map_b, n, k * 64, 0);
+          if (b_rows > 64) tma_prefetch_3d(&map_b, n + 64, k * 64, 0);
+        }
+      };
       for (int t = t_first; ok && t < ntiles; t += step) {
         const PairTile tl = pair_tile(p, t, cols);
         const int m = tl.m0 + rank * 128;
         const int n = kSwiglu ? tl.n0 : tl.n0 + rank * b_rows, half = kSwiglu ? rank : 0;
+        for (int k = k_first; k < min(k_first + p.ahead, k_last); k++) fetch_b(n, half, k);
         for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
           const uint32_t s = it.slot;
           if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
           const uint32_t bar = map_rank(full(s), first_cta);
           const uint32_t a = base + s * p.stage_bytes, b = a + 128 * 128;
+          if (p.ahead && k + p.ahead < k_last) fetch_b(n, half, k + p.ahead);
           // (the other CTA's bytes may be counted before this; the phase ends with the arrival)
           if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * p.stage_bytes);
           if (FORM == FORM_MM) {
@@ -313,73 +347,87 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   // ------------------------------------------------------------------ epilogue
   const int ew = warp - 4;
   const uint32_t boxes = base + p.stages * p.stage_bytes + max(ew, 0) * p.bufs * kStageBox;
-  uint32_t nload = 0, nstore = 0;
   bool ok = true;
   // Columns of a box: a row of it is 128 bytes.
   constexpr int kBox = EPI == PAIR_F32 || EPI == PAIR_SWIGLU_F32 ? 32 : 64;
+  constexpr bool kThree = EPI == PAIR_SWIGLU || EPI == PAIR_DSWIGLU;  // three boxes at once, else two in turn
   const int nbox = cols / kBox;
-  auto asks = [&](const PairTile& tl, int box, int q) {  // DSWIGLU: gate and up of a box
-    if (lane == 0) {
-      store_wait_read<0>();
-      mbar_arrive_expect_tx(loads(ew), 2 * kStageBox);
-      tma_load_3d(boxes, &map_g, tl.n0 + box * 64, tl.m0 + rank * 128 + q * 32, 0, loads(ew));
-      tma_load_3d(boxes + kStageBox, &map_g, tl.n0 + box * 64, tl.m0 + rank * 128 + q * 32, 1, loads(ew));
-    }
-    __syncwarp();
-  };
+  const bool asks = EPI == PAIR_DSWIGLU || (EPI == PAIR_BF16 && p.addend);  // a unit's inputs come by TMA
+  uint32_t asked = 0, units = 0;
   auto there = [&](const PairTile& tl, int box, int q) {
     return tl.m0 + rank * 128 + q * 32 < p.M && tl.n0 + box * kBox < p.N;
   };
-  // One box: 32 rows of the quadrant q. get(c, v): accumulator columns c .. c + 31 of this lane's row.
-  auto unit = [&](const PairTile& tl, int box, int q, auto get) {
+  // Asks for the next unit's inputs into its boxes, which the store before the last one has left.
+  auto ask = [&](const PairTile& tl, int box, int q) {
+    const uint32_t i = asked++, bar = loads(ew, i & 1);
+    if (lane == 0) {
+      const int row = tl.m0 + rank * 128 + q * 32, col = tl.n0 + box * 64;
+      store_wait_read<0>();
+      if (EPI == PAIR_DSWIGLU) {
+        mbar_arrive_expect_tx(bar, 2 * kStageBox);
+        tma_load_3d(boxes, &map_g, col, row, 0, bar);
+        tma_load_3d(boxes + kStageBox, &map_g, col, row, 1, bar);
+      } else {
+        mbar_arrive_expect_tx(bar, kStageBox);
+        tma_load_3d(boxes + (i & 1) * kStageBox, &map_g, col, row, 0, bar);
+      }
+    }
+    __syncwarp();
+  };
+  // One box: 32 rows of the quadrant q. get(c, v): accumulator columns c .. c + 15 of this lane's row, there
+  // after wait(v).
+  auto unit = [&](const PairTile& tl, int box, int q, auto get, auto wait) {
     const int row0 = tl.m0 + rank * 128 + q * 32, col0 = tl.n0 + box * kBox;
     const int row = min(row0 + lane, p.M - 1);
     const float rs = p.row_scale ? p.row_scale[row] : 1.0f;
+    const uint32_t n = units++, at = kThree ? boxes : boxes + (n & 1) * kStageBox;
     // (columns past N are not stored; their scales are those of the last ones)
-    auto scaled = [&](float (&v)[32], int c, int half) {
+    auto scaled = [&](uint32_t (&v)[16], int c, int half) {
       if (!p.row_scale) return;
 #pragma unroll
-      for (int j = 0; j < 32; j++) v[j] *= rs * __ldg(p.col_scale + half * p.N + min(c + j, p.N - 1));
+      for (int j = 0; j < 16; j++)
+        v[j] = __float_as_uint(__uint_as_float(v[j]) * (rs * __ldg(p.col_scale + half * p.N + min(c + j, p.N - 1))));
     };
-    if (EPI == PAIR_SWIGLU) {
-      if (lane == 0) store_wait_read<0>();
-      __syncwarp();
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        float g[32], u[32];
-        get(box * 64 + h * 32, g);
-        get(p.bn / 2 + box * 64 + h * 32, u);
-        scaled(g, col0 + h * 32, 0);
-        scaled(u, col0 + h * 32, 1);
-        if (p.keep) {
-          box_bf16(boxes + kStageBox, lane, 4 * h, g);
-          box_bf16(boxes + 2 * kStageBox, lane, 4 * h, u);
-        }
-#pragma unroll
-        for (int j = 0; j < 32; j++) g[j] = silu_mul(g[j], u[j]);
-        box_bf16(boxes, lane, 4 * h, g);
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(&map_d, col0, row0, 0, boxes);
-        if (p.keep) {
-          tma_store_3d(&map_e, col0, row0, 0, boxes + kStageBox);
-          tma_store_3d(&map_e, col0, row0, 1, boxes + 2 * kStageBox);
-        }
-        store_commit();
-      }
-    } else if (EPI == PAIR_DSWIGLU) {
-      ok = ok && warp_wait(loads(ew), nload & 1, &s_abort);
-      nload++;
+    if (asks) {
+      ok = ok && warp_wait(loads(ew, n & 1), (n >> 1) & 1, &s_abort);
       if (!ok) return;
+    } else {
+      if (lane == 0) {
+        if (kThree) store_wait_read<0>();
+        else store_wait_read<1>();
+      }
+      __syncwarp();
+    }
+    // (16 columns at a time, not unrolled: a launch's first tile waits for its code, and unrolled over
+    // 32 columns, several thousand instructions, that took 3 us)
+#pragma unroll 1
+    for (int h = 0; h < kBox / 16; h++) {
+      const int c0 = col0 + h * 16;
+      uint32_t v[16];
+      get(box * kBox + h * 16, v);
+      if (EPI == PAIR_SWIGLU || EPI == PAIR_SWIGLU_F32) {
+        uint32_t u[16];
+        get(p.bn / 2 + box * kBox + h * 16, u);
+        wait(v);
+        wait(u);
+        scaled(v, c0, 0);
+        scaled(u, c0, 1);
+        if (EPI == PAIR_SWIGLU && p.keep) {
+          box_bf16(at + kStageBox, lane, 2 * h, v);
+          box_bf16(at + 2 * kStageBox, lane, 2 * h, u);
+        }
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        float v[32];
-        get(box * 64 + h * 32, v);
+        for (int j = 0; j < 16; j++) {
+          const float a = __uint_as_float(v[j]), b = __uint_as_float(u[j]);
+          v[j] = __float_as_uint(EPI == PAIR_SWIGLU ? silu_mul(a, b) : silu_mul_f32(a, b));
+        }
+      } else {
+        wait(v);
+      }
+      if (EPI == PAIR_DSWIGLU) {
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          const uint32_t ag = box_at(boxes, lane, 4 * h + c), au = ag + kStageBox;
+        for (int c = 0; c < 2; c++) {
+          const uint32_t ag = box_at(at, lane, 2 * h + c), au = ag + kStageBox;
           const uint4 g4 = ld_shared4(ag), u4 = ld_shared4(au);
           const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
           uint32_t dg[4], du[4], hh[4];
@@ -389,7 +437,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
               const float g = e ? bf16hi(gw[j]) : bf16lo(gw[j]), u = e ? bf16hi(uw[j]) : bf16lo(uw[j]);
-              const float dh = v[8 * c + 2 * j + e];
+              const float dh = __uint_as_float(v[8 * c + 2 * j + e]);
               const float sig = __fdividef(1.0f, 1.0f + __expf(-g)), s = g * sig;
               w[e] = s * u;
               b[e] = dh * s;
@@ -403,92 +451,85 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           st_shared4(au, du[0], du[1], du[2], du[3]);
           st_shared4(ag + 2 * kStageBox, hh[0], hh[1], hh[2], hh[3]);
         }
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(&map_e, col0, row0, 0, boxes);
-        tma_store_3d(&map_e, col0, row0, 1, boxes + kStageBox);
-        if (p.keep) tma_store_3d(&map_d, col0, row0, 0, boxes + 2 * kStageBox);
-        store_commit();
-      }
-    } else {
-      // two boxes in turn: one is filled while the other leaves
-      const uint32_t at = boxes + (nstore++ & 1) * kStageBox;
-      if (lane == 0) store_wait_read<1>();
-      __syncwarp();
-#pragma unroll
-      for (int h = 0; h < kBox / 32; h++) {
-        float v[32];
-        const int c = col0 + h * 32;
-        uint4 ad[4];
-        if (p.addend) {
-          const __nv_bfloat16* a = p.addend + (size_t)row * p.N + c;
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-            if (c + 8 * j < p.N) ad[j] = *reinterpret_cast<const uint4*>(a + 8 * j);
-            else ad[j] = make_uint4(0, 0, 0, 0);
-        }
-        if (EPI == PAIR_SWIGLU_F32) {
-          float u[32];
-          get(box * 32, v);
-          get(p.bn / 2 + box * 32, u);
-          scaled(v, c, 0);
-          scaled(u, c, 1);
-#pragma unroll
-          for (int j = 0; j < 32; j++) v[j] = silu_mul_f32(v[j], u[j]);
-        } else {
-          get(box * kBox + h * 32, v);
-          scaled(v, c, 0);
-        }
+      } else if (EPI == PAIR_SWIGLU) {
+        box_bf16(at, lane, 2 * h, v);
+      } else {
+        if (EPI != PAIR_SWIGLU_F32) scaled(v, c0, 0);
         if (p.addend) {
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const uint32_t w[4] = {ad[j].x, ad[j].y, ad[j].z, ad[j].w};
+          for (int j = 0; j < 2; j++) {
+            uint4 a = make_uint4(0, 0, 0, 0);
+            if (EPI == PAIR_BF16) a = ld_shared4(box_at(at, lane, 2 * h + j));
+            else if (c0 + 8 * j < p.N) a = *reinterpret_cast<const uint4*>(p.addend + (size_t)row * p.N + c0 + 8 * j);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-              v[8 * j + 2 * i] += bf16lo(w[i]);
-              v[8 * j + 2 * i + 1] += bf16hi(w[i]);
+              v[8 * j + 2 * i] = __float_as_uint(__uint_as_float(v[8 * j + 2 * i]) + bf16lo(w[i]));
+              v[8 * j + 2 * i + 1] = __float_as_uint(__uint_as_float(v[8 * j + 2 * i + 1]) + bf16hi(w[i]));
             }
           }
         }
-        if (kBox == 32) box_f32(at, lane, v); else box_bf16(at, lane, 4 * h, v);
+        if (kBox == 32) box_f32(at, lane, 4 * h, v);
+        else box_bf16(at, lane, 2 * h, v);
       }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        if (EPI == PAIR_F32 && p.reduce) tma_add_3d(&map_d, col0, row0, 0, at);
-        else tma_store_3d(&map_d, kBox == 32 ? 2 * col0 : col0, row0, 0, at);  // (an fp32 column is two of 2 bytes)
-        store_commit();
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (EPI == PAIR_SWIGLU) {
+        tma_store_3d(&map_d, col0, row0, 0, at);
+        if (p.keep) {
+          tma_store_3d(&map_e, col0, row0, 0, at + kStageBox);
+          tma_store_3d(&map_e, col0, row0, 1, at + 2 * kStageBox);
+        }
+      } else if (EPI == PAIR_DSWIGLU) {
+        tma_store_3d(&map_e, col0, row0, 0, at);
+        tma_store_3d(&map_e, col0, row0, 1, at + kStageBox);
+        if (p.keep) tma_store_3d(&map_d, col0, row0, 0, at + 2 * kStageBox);
+      } else if (EPI == PAIR_F32 && p.reduce) {
+        tma_add_3d(&map_d, col0, row0, 0, at);
+      } else {
+        tma_store_3d(&map_d, kBox == 32 ? 2 * col0 : col0, row0, 0, at);  // (an fp32 column is two of 2 bytes)
       }
+      store_commit();
     }
   };
 
-  if (warp >= 4) {
-    const int q = warp & 3, which = ew >> 2;  // this warp's TMEM lanes; two warps share them, box by box
+  const int per_q = p.ewarps >> 2;  // epilogue warps that share a quadrant of TMEM lanes, box by box
+  if (warp >= 4 && ew < p.ewarps) {
+    const int q = warp & 3, which = ew >> 2;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     Ring acc;
     for (int t = t_first; ok && t < ntiles; t += step, acc.next(2)) {
       const PairTile tl = pair_tile(p, t, cols);
       const int b = acc.slot;
-      if (EPI == PAIR_DSWIGLU && p.split == 1 && which < nbox && there(tl, which, q)) asks(tl, which, q);
+      const bool first = p.split == 1 && which < nbox && there(tl, which, q);
+      if (asks && first) {
+        ask(tl, which, q);
+        if (EPI == PAIR_DSWIGLU && lane == 0)  // the others' on their way to L2
+          for (int box = which + per_q; box < nbox && there(tl, box, q); box += per_q)
+            for (int z = 0; z < 2; z++) tma_prefetch_3d(&map_g, tl.n0 + box * 64, tl.m0 + rank * 128 + q * 32, z);
+      }
       if (!(ok = warp_wait(tfull(b), acc.parity, &s_abort))) break;
       tc_fence_after();
       const uint32_t d = tmem + b * 256 + lanes;
       if (p.split == 1) {
-        for (int box = which; box < nbox && there(tl, box, q); box += 2) {
-          if (EPI == PAIR_DSWIGLU && box != which) asks(tl, box, q);
-          unit(tl, box, q, [&](int c, float (&v)[32]) { tmem_ld32(d + c, v); });
+        for (int box = which; box < nbox && there(tl, box, q); box += per_q) {
+          const bool more = asks && box + per_q < nbox && there(tl, box + per_q, q);
+          if (EPI == PAIR_BF16 && more) ask(tl, box + per_q, q);
+          unit(tl, box, q, [&](int c, uint32_t (&v)[16]) { tmem_ld16(d + c, v); }, [](uint32_t (&v)[16]) { tmem_wait16(v); });
+          if (EPI == PAIR_DSWIGLU && more) ask(tl, box + per_q, q);
         }
       } else {
         // the partial sums, [column][row], where the stages were: all are used
-        for (int c = which * (p.bn / 2); c < (which + 1) * (p.bn / 2); c += 32) {
-          float v[32];
-          tmem_ld32(d + c, v);
+        for (int c = which * 16; c < p.bn; c += 16 * per_q) {
+          uint32_t v[16];
+          tmem_ld16(d + c, v);
+          tmem_wait16(v);
           const uint32_t at = base + (uint32_t)(c * 128 + q * 32 + lane) * 4u;
 #pragma unroll
-          for (int j = 0; j < 32; j++)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + j * 512), "f"(v[j]) : "memory");
+          for (int j = 0; j < 16; j++)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + j * 512), "r"(v[j]) : "memory");
         }
       }
       tc_fence_before();
@@ -497,24 +538,46 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   }
   if (p.split > 1) {
-    // Each CTA joins some of the boxes, in the order of the parts. All threads come here,
-    // whatever became of their waits; a cluster has one tile.
+    // Part i joins the rows of the quadrants i, i + split, in the order of the parts, in its own
+    // shared memory: no other reads them there. All threads come here, whatever became of
+    // their waits; a cluster has one tile. (One 4-byte value at a time by the epilogue warps alone
+    // took 10 us.)
     __syncwarp();
     cluster_sync();
-    if (warp >= 4) {
+    const int mine = 4 / p.split, all = p.bn * 8 * mine;  // 16 bytes each: 4 rows of a column
+    auto place = [&](int i) {
+      const int c = i / (8 * mine), r = i % (8 * mine), q = part + p.split * (r >> 3);
+      return base + (uint32_t)(c * 128 + q * 32 + (r & 7) * 4) * 4u;
+    };
+    constexpr int kAtOnce = 3;  // (a load takes most of a microsecond)
+    for (int i0 = tid; i0 < all; i0 += kAtOnce * kPairThreads) {
+      float4 v[kAtOnce][kSplitMost];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; k++) {
+        const uint32_t at = place(min(i0 + k * kPairThreads, all - 1));
+#pragma unroll
+        for (int s = 0; s < kSplitMost; s++)
+          if (s < p.split) v[k][s] = ld_cluster4(at, 2 * s + rank);
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; k++) {
+        float4 sum = v[k][0];
+#pragma unroll
+        for (int s = 1; s < kSplitMost; s++)
+          if (s < p.split) sum.x += v[k][s].x, sum.y += v[k][s].y, sum.z += v[k][s].z, sum.w += v[k][s].w;
+        const int i = i0 + k * kPairThreads;
+        if (i < all)
+          st_shared4(place(i), __float_as_uint(sum.x), __float_as_uint(sum.y), __float_as_uint(sum.z), __float_as_uint(sum.w));
+      }
+    }
+    __syncthreads();
+    if (warp >= 4 && ew < p.ewarps) {
       const PairTile tl = pair_tile(p, min(t_first, ntiles - 1), cols);
-      for (int i = part + p.split * ew; i < 4 * nbox; i += 8 * p.split) {
-        const int q = i & 3, box = i >> 2;
+      for (int i = ew; i < mine * nbox; i += p.ewarps) {
+        const int q = part + p.split * (i % mine), box = i / mine;
         if (!there(tl, box, q)) continue;
-        if (EPI == PAIR_DSWIGLU) asks(tl, box, q);
-        unit(tl, box, q, [&](int c, float (&v)[32]) {
-          const uint32_t at = base + (uint32_t)(c * 128 + q * 32 + lane) * 4u;
-#pragma unroll
-          for (int j = 0; j < 32; j++) v[j] = 0.0f;
-          for (int s = 0; s < p.split; s++)
-#pragma unroll
-            for (int j = 0; j < 32; j++) v[j] += ld_cluster(at + j * 512, 2 * s + rank);
-        });
+        if (asks) ask(tl, box, q);
+        unit(tl, box, q, [&](int c, uint32_t (&v)[16]) { smem_ld16(base + (uint32_t)(c * 128 + q * 32 + lane) * 4u, v); }, [](uint32_t (&)[16]) {});
       }
     }
   }

@@ -34,11 +34,13 @@ enum PairEpi {
 
 struct PairParams {
   int M, N, K;   // SWIGLU: N columns of h, 2 N rows of B
-  int bn;        // accumulator columns of a tile, 256 or 128 (SWIGLU: half gate, half up)
+  int bn;        // accumulator columns of a tile, 256, 192 or 128 (SWIGLU: half gate, half up; not 192)
   int tiles_m, tiles_n;
   int split;     // pairs of a cluster that share a tile's K
   int stages, stage_bytes;
+  int ewarps;    // epilogue warps at work, 8 or 4
   int bufs;      // boxes of an epilogue warp
+  int ahead;     // steps of B that are fetched to L2 before their copies, or 0
   uint32_t idesc;
   const float* row_scale;  // int8: a scale for each row and each column (gate columns first), or NULL
   const float* col_scale;
