@@ -90,16 +90,21 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   l.epi = epi;
   shape_of(p, swiglu, d);
   p.bufs = epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU ? 1 : 2;
-  p.stage_bytes = 128 * 128 + (form == FORM_KK ? p.bn * 64 : (int)cdiv(p.bn, 128) * 8192);
+  // (A copy takes the TMA unit about two clocks a row of 128 bytes, also of rows that it fills with zeros.)
+  const int a_rows = form != FORM_MM && p.M <= 128 ? (int)up(p.M, 8) : 128;
+  const int b_bytes = form == FORM_KK ? p.bn * 64 : (int)cdiv(p.bn, 128) * 8192;
+  p.a_bytes = a_rows * 128;
+  p.stage_bytes = p.a_bytes + b_bytes;
+  p.step_bytes = (a_rows < 128 ? 1 : 2) * p.a_bytes + 2 * b_bytes;
   // Three boxes a warp leave four stages of 256 columns; with four warps there are five. Where a tile's
   // product is long enough for its epilogue, that is faster.
   p.ewarps = p.bufs == 3 && p.split == 1 && p.K >= kFewWarpsK ? 4 : 8;
   p.stages = std::min(kPairStages, (d.smem - 2048 - p.ewarps * p.bufs * kStageBox) / p.stage_bytes);
-  p.ahead = p.tiles_m <= 2 && form != FORM_MM ? 8 : 0;
+  p.ahead = p.tiles_m <= 2 && a_rows == 128 && form != FORM_MM ? 8 : 0;
   // fp32 accumulators; bf16 or fp16 operands; k or the operand's own index innermost; M = 256 of a pair
   p.idesc = 1u << 4 | (fp16 ? 0u : 1u << 7 | 1u << 10) | (form == FORM_MM ? 1u << 15 : 0u) |
             (form != FORM_KK ? 1u << 16 : 0u) | (uint32_t)(p.bn >> 3) << 17 | 16u << 24;
-  const bool ok_a = make_map(&l.a, a.ptr, a.pitch, a.cols, a.rows, form == FORM_MM ? 64 : 128);
+  const bool ok_a = make_map(&l.a, a.ptr, a.pitch, a.cols, a.rows, form == FORM_MM ? 64 : a_rows);
   const bool ok_b = swiglu ? make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows / 2, p.bn / 2, 2, b.pitch * (b.rows / 2))
                            : make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows, form == FORM_KK ? p.bn / 2 : 64);
   l.e = l.g = l.a;

@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
+      const uint32_t bars = map_rank(bar0, first_cta);  // the pair's full barriers
       Ring it;
       bool ok = true;
       // Few rows: the ring holds less of B than HBM's latency asks for; L2 takes the rest.
@@ -282,15 +283,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
           const uint32_t s = it.slot;
           if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
-          const uint32_t bar = map_rank(full(s), first_cta);
-          const uint32_t a = base + s * p.stage_bytes, b = a + 128 * 128;
+          const uint32_t bar = bars + 8u * s;
+          const uint32_t a = base + s * p.stage_bytes, b = a + p.a_bytes;
           if (p.ahead && k + p.ahead < k_last) fetch_b(n, half, k + p.ahead);
           // (the other CTA's bytes may be counted before this; the phase ends with the arrival)
-          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * p.stage_bytes);
+          if (rank == 0) mbar_arrive_expect_tx(full(s), p.step_bytes);
           if (FORM == FORM_MM) {
             tma_pair_3d(a, &map_a, m, k * 64, 0, bar);
             tma_pair_3d(a + 8192, &map_a, m + 64, k * 64, 0, bar);
-          } else {
+          } else if (rank == 0 || p.a_bytes == 128 * 128) {  // (few rows are all the first CTA's)
             tma_pair_3d(a, &map_a, k * 64, m, 0, bar);
           }
           if (FORM == FORM_KK) {
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t at = base + s * p.stage_bytes;
         const uint64_t da = FORM == FORM_MM ? smem_desc_mn(at) : smem_desc(at);
-        const uint64_t db = FORM == FORM_KK ? smem_desc(at + 128 * 128) : smem_desc_mn(at + 128 * 128);
+        const uint64_t db = FORM == FORM_KK ? smem_desc(at + p.a_bytes) : smem_desc_mn(at + p.a_bytes);
         constexpr int kA = FORM == FORM_MM ? 2048 >> 4 : 2, kB = FORM == FORM_KK ? 2 : 2048 >> 4;
         if (leader) {
 #pragma unroll

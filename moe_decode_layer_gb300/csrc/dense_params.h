@@ -11,7 +11,7 @@
 namespace moe {
 namespace dense {
 
-constexpr int kPairStages = 8;       // operand stages at most
+constexpr int kPairStages = 16;      // operand stages at most
 constexpr int kPairThreads = 384;    // copies, tensor core, two idle warps, eight epilogue warps
 constexpr int kTileM = 256;          // rows of a pair's tile
 constexpr int kStageBox = 4096;      // an epilogue warp's box in shared memory: 32 rows of 128 bytes
@@ -38,6 +38,10 @@ struct PairParams {
   int tiles_m, tiles_n;
   int split;     // pairs of a cluster that share a tile's K
   int stages, stage_bytes;
+  // A's part of a stage: 128 rows, or of few rows (M <= 128, no FORM_MM) those in the first CTA alone.
+  // The tensor core reads 128 all the same; what lies behind them becomes rows that nothing reads.
+  int a_bytes;
+  int step_bytes;  // both CTAs' copies of a step
   int ewarps;    // epilogue warps at work, 8 or 4
   int bufs;      // boxes of an epilogue warp
   int ahead;     // steps of B that are fetched to L2 before their copies, or 0
