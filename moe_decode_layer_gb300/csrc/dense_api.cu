@@ -10,6 +10,7 @@
 #include "../../include/moe_decode_dense.h"
 #include "dense_params.h"
 #include "rows_host.h"
+#include "rows_kernels.h"
 
 using namespace moe;
 using namespace moe::rows;
@@ -108,7 +109,8 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   const bool ok_b = swiglu ? make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows / 2, p.bn / 2, 2, b.pitch * (b.rows / 2))
                            : make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows, form == FORM_KK ? p.bn / 2 : 64);
   l.e = l.g = l.a;
-  return ok_a && ok_b && p.stages >= 2 && p.stages * p.stage_bytes >= (p.split > 1 ? p.bn * 512 : 0);
+  p.box_off = std::max(p.stages * p.stage_bytes, p.split > 1 ? p.bn * 512 : 0);
+  return ok_a && ok_b && p.stages >= 2 && p.box_off + p.ewarps * p.bufs * kStageBox <= d.smem - 2048;
 }
 
 // Results [M, N] of 2 bytes, or fp32 (as pairs of 2 bytes where nothing is added), and their addends.
@@ -159,7 +161,16 @@ struct Places {
   }
 };
 
-bool few(int64_t rows) { return rows <= kStreamRows; }
+// Which kernel a product of `rows` rows with `bytes` of weights goes to. Few rows: a stream of the weights.
+constexpr int64_t kStreamBytes = 16 << 20;
+bool few(int64_t rows, int64_t bytes) { return rows <= 8 || (rows <= kStreamRows && bytes <= kStreamBytes); }
+// int8, more rows: weights widened as they come (the grouped product), or fp16 copies of them for the
+// pair product.
+constexpr int64_t kWidenRows = 512;
+enum Int8Way { INT8_STREAM, INT8_ROWS, INT8_PAIR };
+Int8Way int8_way(int64_t rows, int64_t weights) {
+  return few(rows, weights) ? INT8_STREAM : rows <= kWidenRows ? INT8_ROWS : INT8_PAIR;
+}
 
 // ------------------------------------------------------------------ int8
 moe_status check_int8(const moe_int8_config* c) {
@@ -171,19 +182,21 @@ moe_status check_int8(const moe_int8_config* c) {
   return MOE_OK;
 }
 
+int64_t int8_weights(const moe_int8_config& c) { return (int64_t)c.outer * (c.swiglu ? 2 : 1) * c.inner; }
+
 struct Int8Plan {
   size_t status, codes, scale, w, bytes;
 };
-// Few rows go with the codes as they are, many as fp16 copies of them and of the weights: exact,
-// and the tensor core's full rate for a pass over the weights (3 bytes each).
+// A stream takes the codes as they are, the others fp16 copies.
 Int8Plan int8_plan(const moe_int8_config& c, int64_t rows) {
   Places pl;
   Int8Plan p = {};
+  const Int8Way way = int8_way(rows, int8_weights(c));
   p.status = pl.take(kStatusBytes);
   const bool made = c.x_dtype != MOE_I8;
-  if (made || !few(rows)) p.codes = pl.take((size_t)rows * c.inner * (few(rows) ? 1 : 2));
+  if (made || way != INT8_STREAM) p.codes = pl.take((size_t)rows * c.inner * (way == INT8_STREAM ? 1 : 2));
   if (made) p.scale = pl.take((size_t)rows * 4);
-  if (!few(rows)) p.w = pl.take((size_t)c.outer * (c.swiglu ? 2 : 1) * c.inner * 2);
+  if (way == INT8_PAIR) p.w = pl.take((size_t)int8_weights(c) * 2);
   p.bytes = pl.at;
   return p;
 }
@@ -205,33 +218,54 @@ struct Int8Product {
   uint8_t* codes;
   float* scale;
   __half* w16;
+  Int8Way way;
   PairLaunch l;
+  RowsInt8 r;
 };
 
 moe_status prepare_int8(Int8Product& a, const Device& d) {
-  if (few(a.rows)) return MOE_OK;
+  a.way = int8_way(a.rows, int8_weights(a.c));
   const bool f32 = a.c.out_dtype == MOE_F32;
-  const int epi = a.c.swiglu ? (f32 ? PAIR_SWIGLU_F32 : PAIR_SWIGLU) : f32 ? PAIR_F32 : PAIR_BF16;
-  PairParams& p = a.l.p;
-  p.M = (int)a.rows;
-  p.N = a.c.outer;
-  p.K = a.c.inner;
-  p.row_scale = a.c.x_dtype == MOE_I8 ? a.x_scale : a.scale;
-  p.col_scale = a.w_scale;
-  p.addend = static_cast<const __nv_bfloat16*>(a.addend);
-  p.status = a.status;
-  p.status_keep = a.status_keep;
+  const float* scale = a.c.x_dtype == MOE_I8 ? a.x_scale : a.scale;
   const int64_t k = a.c.inner;
-  return prepare(a.l, FORM_KK, epi, {a.codes, k * 2, a.rows, k}, {a.w16, k * 2, (int64_t)a.c.outer * (a.c.swiglu ? 2 : 1), k},
-                 true, d) &&
-                 prepare_out(a.l, a.out, f32)
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  if (a.way == INT8_ROWS) {
+    GemmParams& p = a.r.p;
+    p.R = a.c.outer;
+    p.K = a.c.inner;
+    p.rows = (int)a.rows;
+    p.row_scale = scale;
+    p.wscale = a.w_scale;
+    p.addend = static_cast<const __nv_bfloat16*>(a.addend);
+    p.out = a.out;
+    p.status = a.status;
+    p.status_clear = a.status_keep ? nullptr : a.status + kMaxSms;
+    p.status_keep = a.status_keep;
+    a.r.epi = a.c.swiglu ? (f32 ? EPI_SWIGLU_F32 : EPI_SWIGLU) : f32 ? EPI_F32 : EPI_BF16;
+    a.r.weight = a.w;
+    a.r.x16 = a.codes;
+    return prepare_rows_int8(&a.r, d) ? MOE_OK : MOE_ERR_CUDA;
+  }
+  if (a.way == INT8_PAIR) {
+    const int epi = a.c.swiglu ? (f32 ? PAIR_SWIGLU_F32 : PAIR_SWIGLU) : f32 ? PAIR_F32 : PAIR_BF16;
+    PairParams& p = a.l.p;
+    p.M = (int)a.rows;
+    p.N = a.c.outer;
+    p.K = a.c.inner;
+    p.row_scale = scale;
+    p.col_scale = a.w_scale;
+    p.addend = static_cast<const __nv_bfloat16*>(a.addend);
+    p.status = a.status;
+    p.status_keep = a.status_keep;
+    if (!prepare(a.l, FORM_KK, epi, {a.codes, k * 2, a.rows, k}, {a.w16, k * 2, int8_weights(a.c) / k, k}, true, d) ||
+        !prepare_out(a.l, a.out, f32))
+      return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
 }
 
 cudaError_t launch_int8(Int8Product& a, const Device& d, bool pdl, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  const bool made = a.c.x_dtype != MOE_I8, small = few(a.rows);
+  const bool made = a.c.x_dtype != MOE_I8, small = a.way == INT8_STREAM;
   if (made) {
     e = launch_quantise(a.c.x_dtype, a.x, a.x_stride, a.rows, a.c.inner, a.codes, !small, a.scale, pdl, s);
     pdl = true;
@@ -240,8 +274,9 @@ cudaError_t launch_int8(Int8Product& a, const Device& d, bool pdl, cudaStream_t 
     pdl = true;
   }
   if (e != cudaSuccess) return e;
-  if (!small) {
-    e = launch_widen(a.w, a.c.inner, (int64_t)a.c.outer * (a.c.swiglu ? 2 : 1), a.c.inner, a.w16, pdl, s);
+  if (a.way == INT8_ROWS) return launch_rows_int8(a.r, d, pdl, s);
+  if (a.way == INT8_PAIR) {
+    e = launch_widen(a.w, a.c.inner, int8_weights(a.c) / a.c.inner, a.c.inner, a.w16, pdl, s);
     return e == cudaSuccess ? launch(a.l, d, true, s) : e;
   }
   StreamParams p = {};
@@ -281,9 +316,10 @@ FfPlan ff_plan(const moe_ff_config& c, int64_t rows) {
   const bool int8 = c.wdtype == MOE_W_INT8;
   p.h = pl.take((size_t)rows * c.inter * (int8 ? 4 : 2));
   if (int8) {
-    p.codes = pl.take((size_t)rows * std::max(c.hidden, c.inter) * (few(rows) ? 1 : 2));
+    // (both products' rows in turn; a stream takes a byte each)
+    p.codes = pl.take((size_t)rows * std::max(c.hidden, c.inter) * 2);
     p.scale = pl.take((size_t)rows * 4);
-    if (!few(rows)) p.w = pl.take((size_t)c.hidden * c.inter * 4);  // W13 in fp16, then W2
+    if (rows > kWidenRows) p.w = pl.take((size_t)c.hidden * c.inter * 4);  // W13 in fp16, then W2
   }
   p.bytes = pl.at;
   return p;
@@ -367,7 +403,7 @@ moe_status moe_decode_project_int8(const moe_int8_config* c, const int8_t* w, co
   if (!device(&d)) return MOE_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Int8Product a = {*c,  w,    w_scale, x, x_scale, x_stride, addend, out, rows, reinterpret_cast<int*>(ws + p.status), false,
-                   ws + p.codes, reinterpret_cast<float*>(ws + p.scale), reinterpret_cast<__half*>(ws + p.w), {}};
+                   ws + p.codes, reinterpret_cast<float*>(ws + p.scale), reinterpret_cast<__half*>(ws + p.w), INT8_STREAM, {}, {}};
   st = prepare_int8(a, d);
   if (st != MOE_OK) return st;
   return cuda_status(launch_int8(a, d, false, reinterpret_cast<cudaStream_t>(stream)));
@@ -421,15 +457,15 @@ moe_status moe_decode_ff(const moe_ff_config* c, const moe_ff_weights* wt, const
     float* scale = reinterpret_cast<float*>(ws + p.scale);
     __half* w16 = reinterpret_cast<__half*>(ws + p.w);
     Int8Product one = {{c->hidden, c->inter, 1, MOE_BF16, MOE_F32}, static_cast<const int8_t*>(wt->w13), wt->s13, x, nullptr,
-                       x_stride, nullptr, h, rows, status, false, codes, scale, w16, {}};
+                       x_stride, nullptr, h, rows, status, false, codes, scale, w16, INT8_STREAM, {}, {}};
     Int8Product two = {{c->inter, c->hidden, 0, MOE_F32, MOE_BF16}, static_cast<const int8_t*>(wt->w2), wt->s2, h, nullptr,
-                       in, residual, out, rows, status, true, codes, scale, w16, {}};
+                       in, residual, out, rows, status, true, codes, scale, w16, INT8_STREAM, {}, {}};
     if ((st = prepare_int8(one, d)) != MOE_OK || (st = prepare_int8(two, d)) != MOE_OK) return st;
     const cudaError_t e = launch_int8(one, d, false, s);
     return cuda_status(e == cudaSuccess ? launch_int8(two, d, true, s) : e);
   }
 
-  if (few(rows)) {
+  if (few(rows, hid * in * 4)) {
     StreamParams one = {}, two = {};
     one.w = wt->w13;
     one.x = x;

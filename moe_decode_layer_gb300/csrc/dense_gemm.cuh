@@ -179,9 +179,6 @@ __device__ __forceinline__ void box_f32(uint32_t box, int r, int first, const ui
   for (int c = 0; c < 4; c++) st_shared4(box_at(box, r, first + c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
 
-// silu(g) * u in full fp32 (results that are quantised next: codes would flip at 2^-16).
-__device__ __forceinline__ float silu_mul_f32(float g, float u) { return g / (1.0f + expf(-g)) * u; }
-
 // ------------------------------------------------------------------ the kernel
 struct PairTile {
   int m0, n0;
@@ -347,7 +344,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   // ------------------------------------------------------------------ epilogue
   const int ew = warp - 4;
-  const uint32_t boxes = base + p.stages * p.stage_bytes + max(ew, 0) * p.bufs * kStageBox;
+  const uint32_t boxes = base + p.box_off + max(ew, 0) * p.bufs * kStageBox;
   bool ok = true;
   // Columns of a box: a row of it is 128 bytes.
   constexpr int kBox = EPI == PAIR_F32 || EPI == PAIR_SWIGLU_F32 ? 32 : 64;

@@ -44,6 +44,7 @@ struct PairParams {
   int step_bytes;  // both CTAs' copies of a step
   int ewarps;    // epilogue warps at work, 8 or 4
   int bufs;      // boxes of an epilogue warp
+  int box_off;   // where they are: behind the stages, and behind a split tile's sums
   int ahead;     // steps of B that are fetched to L2 before their copies, or 0
   uint32_t idesc;
   const float* row_scale;  // int8: a scale for each row and each column (gate columns first), or NULL
@@ -73,7 +74,7 @@ struct StreamParams {
   __nv_bfloat16* keep;   // SWIGLU: [T, 2 R], or NULL
   int* status;           // the workspace's status words, to be cleared, or NULL
 };
-constexpr int kStreamRows = 32;  // rows at most
+constexpr int kStreamRows = 16;  // rows at most
 cudaError_t launch_stream(const StreamParams& p, bool int8, bool pdl, int sms, cudaStream_t s);
 
 // codes of rows, as int8 or (half) as fp16 numbers

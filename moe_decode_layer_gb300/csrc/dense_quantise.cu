@@ -5,7 +5,7 @@
 
 #include "../../include/moe_decode_dense.h"
 #include "dense_params.h"
-#include "ptx.cuh"
+#include "tc.cuh"
 
 namespace moe {
 namespace dense {
@@ -142,28 +142,18 @@ __global__ void __launch_bounds__(256) quantise_kernel(const uint8_t* x, int64_t
 }
 
 // 16 codes a thread.
-__global__ void __launch_bounds__(256) widen_kernel(const int8_t* src, int64_t stride, int64_t rows, int cols, __half* dst) {
+__global__ void __launch_bounds__(256) widen_kernel(const int8_t* src, int64_t stride, int64_t count, int cols, __half* dst) {
   pdl_wait();
   pdl_launch_dependents();
   const int per = cols / 16;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count * per; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per);
     const uint4 v = *reinterpret_cast<const uint4*>(src + r * stride + c * 16);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[8];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      // the byte v + 128 under the exponent of 1024 is 1152 + v
-      const uint32_t u = w[j] ^ 0x80808080u;
-      const uint32_t h[2] = {__byte_perm(u, 0x64646464u, 0x4140), __byte_perm(u, 0x64646464u, 0x4342)};
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const __half2 k = __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h[e]), k);
-        o[2 * j + e] = *reinterpret_cast<const uint32_t*>(&d);
-      }
-    }
+    for (int j = 0; j < 4; j++) rows::int8x4_f16x4(w[j], o[2 * j], o[2 * j + 1]);
     uint4* to = reinterpret_cast<uint4*>(dst + r * cols + c * 16);
     to[0] = make_uint4(o[0], o[1], o[2], o[3]);
     to[1] = make_uint4(o[4], o[5], o[6], o[7]);

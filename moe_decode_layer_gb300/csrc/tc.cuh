@@ -2,6 +2,7 @@
 // (sm_103a), bounded waits, and places in rings of barriers.
 #pragma once
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
@@ -151,6 +152,21 @@ struct Ring {
 // a few near 0; the result is rounded to bf16 (2^-8) next. exp(-g) past fp32's range makes
 // the quotient 0, as it should be.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// The same in full fp32 (results that are quantised next: at 2^-16 codes would flip).
+__device__ __forceinline__ float silu_mul_f32(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// Four int8 -> four fp16, exact: the byte v + 128 under the exponent of 1024 is 1152 + v.
+__device__ __forceinline__ uint32_t sub_1152(uint32_t v) {
+  const __half2 k = __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), k);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void int8x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = sub_1152(__byte_perm(u, 0x64646464u, 0x4140));
+  hi = sub_1152(__byte_perm(u, 0x64646464u, 0x4342));
+}
 
 }  // namespace rows
 }  // namespace moe
