@@ -66,6 +66,7 @@ typedef struct moe_int8_config {
 } moe_int8_config;
 
 moe_status moe_decode_project_int8_check(const moe_int8_config* cfg);
+/* 0 for few rows of codes: such a call takes NULL, and has no device-side waits. */
 moe_status moe_decode_project_int8_workspace(const moe_int8_config* cfg, int64_t rows, size_t* bytes);
 /*
  *   w       int8 [O, K] ([2 O, K] with swiglu); w_scale fp32, one a row of w

@@ -38,6 +38,10 @@ class Adapters(NamedTuple):
     scale: torch.Tensor | None = None
 
 
+# (torch.empty with a device's index takes 2 us more than with this, among launches)
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
+
+
 def _need(cond: bool, what: str) -> None:
     if not cond:
         raise ValueError(what)
@@ -120,12 +124,12 @@ def route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: tor
     s, leave = _enter(dev, stream)
     try:
         if idx is None:
-            idx = torch.empty((t, top_k), dtype=torch.int32, device=dev)
+            idx = torch.empty((t, top_k), dtype=torch.int32, device=_DEVICES[dev])
             pi = idx.data_ptr()
         else:
             pi = _tensor(idx, "idx", torch.int32, (t, top_k), dev)
         if w is None:
-            w = torch.empty((t, top_k), dtype=torch.float32, device=dev)
+            w = torch.empty((t, top_k), dtype=torch.float32, device=_DEVICES[dev])
             pw = w.data_ptr()
         else:
             pw = _tensor(w, "w", torch.float32, (t, top_k), dev)
@@ -199,7 +203,7 @@ def _made_for(weights: _lib.Weights, shape: LayerShape, dev: int) -> _lib.Weight
 
 def _workspace(workspace: torch.Tensor | None, need: int, dev: int) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
+        return torch.empty(need, dtype=torch.uint8, device=_DEVICES[dev])
     _need(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev and
           workspace.numel() >= need,
           f"the workspace must be a contiguous uint8 tensor of at least {need} bytes on device {dev}")
@@ -245,7 +249,7 @@ def experts(shape: LayerShape, weights, x: torch.Tensor, idx: torch.Tensor, w: t
     s, leave = _enter(dev, stream)
     try:
         if out is None:
-            out = torch.empty((t, shape.hidden), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((t, shape.hidden), dtype=torch.bfloat16, device=_DEVICES[dev])
             po = out.data_ptr()
         else:
             po = _tensor(out, "out", torch.bfloat16, (t, shape.hidden), dev)
@@ -332,7 +336,7 @@ def project(x: torch.Tensor, weight, *, wdtype: str = "bf16", adapters: Adapters
     s, leave = _enter(dev, stream)
     try:
         if out is None:
-            out = torch.empty((t, o), dtype=out_dtype, device=dev)
+            out = torch.empty((t, o), dtype=out_dtype, device=_DEVICES[dev])
             po = out.data_ptr()
         else:
             po = _tensor(out, "out", out_dtype, (t, o), dev)
@@ -368,12 +372,12 @@ def quantise(x: torch.Tensor, *, codes: torch.Tensor | None = None, scale: torch
     s, leave = _enter(dev, stream)
     try:
         if codes is None:
-            codes = torch.empty((t, k), dtype=torch.int8, device=dev)
+            codes = torch.empty((t, k), dtype=torch.int8, device=_DEVICES[dev])
             pc = codes.data_ptr()
         else:
             pc = _tensor(codes, "codes", torch.int8, (t, k), dev)
         if scale is None:
-            scale = torch.empty((t,), dtype=torch.float32, device=dev)
+            scale = torch.empty((t,), dtype=torch.float32, device=_DEVICES[dev])
             ps = scale.data_ptr()
         else:
             ps = _tensor(scale, "scale", torch.float32, (t,), dev)
@@ -446,12 +450,16 @@ def project_int8(x, weight, *, addend: torch.Tensor | None = None, swiglu: bool 
     s, leave = _enter(dev, stream)
     try:
         if out is None:
-            out = torch.empty((t, o), dtype=out_dtype, device=dev)
+            out = torch.empty((t, o), dtype=out_dtype, device=_DEVICES[dev])
             po = out.data_ptr()
         else:
             po = _tensor(out, "out", out_dtype, (t, o), dev)
-        ws = _workspace(workspace, _int8_bytes(k, o, bool(swiglu), rows_t.dtype, out_dtype, t), dev)
-        st = _lib.load().moe_decode_project_int8(cfg, pw, pc, px, ps, sx, pa, po, t, ws.data_ptr(), ws.numel(), s)
+        pws = nws = None
+        need = _int8_bytes(k, o, bool(swiglu), rows_t.dtype, out_dtype, t)
+        if need or workspace is not None:
+            ws = _workspace(workspace, need, dev)
+            pws, nws = ws.data_ptr(), ws.numel()
+        st = _lib.load().moe_decode_project_int8(cfg, pw, pc, px, ps, sx, pa, po, t, pws, nws or 0, s)
     finally:
         if leave is not None:
             leave.close()
@@ -521,7 +529,7 @@ def feed_forward(x: torch.Tensor, w13, w2, *, wdtype: str = "bf16", residual: to
     s, leave = _enter(dev, stream)
     try:
         if out is None:
-            out = torch.empty((t, hidden), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((t, hidden), dtype=torch.bfloat16, device=_DEVICES[dev])
             po = out.data_ptr()
         else:
             po = _tensor(out, "out", torch.bfloat16, (t, hidden), dev)
@@ -564,11 +572,11 @@ def feed_forward_backward(grad: torch.Tensor, x: torch.Tensor, w13: torch.Tensor
     s, leave = _enter(dev, stream)
     try:
         if input_grad:
-            dx = torch.empty((t, hidden), dtype=torch.bfloat16, device=dev) if dx is None else dx
+            dx = torch.empty((t, hidden), dtype=torch.bfloat16, device=_DEVICES[dev]) if dx is None else dx
             px_ = _tensor(dx, "dx", torch.bfloat16, (t, hidden), dev)
         if weight_grad:
-            dw13 = torch.empty((2 * inter, hidden), dtype=dtype, device=dev) if dw13 is None else dw13
-            dw2 = torch.empty((hidden, inter), dtype=dtype, device=dev) if dw2 is None else dw2
+            dw13 = torch.empty((2 * inter, hidden), dtype=dtype, device=_DEVICES[dev]) if dw13 is None else dw13
+            dw2 = torch.empty((hidden, inter), dtype=dtype, device=_DEVICES[dev]) if dw2 is None else dw2
             p13 = _tensor(dw13, "dw13", dtype, (2 * inter, hidden), dev)
             p2 = _tensor(dw2, "dw2", dtype, (hidden, inter), dev)
         ws = _workspace(workspace, feed_forward_backward_workspace(hidden, inter, t), dev)

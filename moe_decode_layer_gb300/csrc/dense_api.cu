@@ -192,8 +192,9 @@ Int8Plan int8_plan(const moe_int8_config& c, int64_t rows) {
   Places pl;
   Int8Plan p = {};
   const Int8Way way = int8_way(rows, int8_weights(c));
-  p.status = pl.take(kStatusBytes);
   const bool made = c.x_dtype != MOE_I8;
+  if (way == INT8_STREAM && !made) return p;  // nothing is kept, and nothing waits
+  p.status = pl.take(kStatusBytes);
   if (made || way != INT8_STREAM) p.codes = pl.take((size_t)rows * c.inner * (way == INT8_STREAM ? 1 : 2));
   if (made) p.scale = pl.take((size_t)rows * 4);
   if (way == INT8_PAIR) p.w = pl.take((size_t)int8_weights(c) * 2);
@@ -387,7 +388,7 @@ moe_status moe_decode_project_int8(const moe_int8_config* c, const int8_t* w, co
   if (rows == 0) return MOE_OK;
   const bool codes = c->x_dtype == MOE_I8, f32 = c->out_dtype == MOE_F32;
   const int64_t size = codes ? 1 : c->x_dtype == MOE_F32 ? 4 : 2;
-  if (!w || !w_scale || !x || !out || !workspace || (codes && !x_scale)) return MOE_ERR_INVALID_ARG;
+  if (!w || !w_scale || !x || !out || (codes && !x_scale)) return MOE_ERR_INVALID_ARG;
   if (c->swiglu && addend) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w) || !aligned16(w_scale) || !aligned16(x) || !aligned16(addend) || !aligned16(out) || !aligned16(workspace))
     return MOE_ERR_INVALID_ARG;
@@ -398,11 +399,12 @@ moe_status moe_decode_project_int8(const moe_int8_config* c, const int8_t* w, co
   if (codes && overlap(x_scale, rows * 4, out, out_bytes)) return MOE_ERR_INVALID_ARG;
   if ((addend != out || f32) && overlap(addend, add_bytes, out, out_bytes)) return MOE_ERR_INVALID_ARG;
   const Int8Plan p = int8_plan(*c, rows);
-  if (workspace_bytes < p.bytes) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < p.bytes || (p.bytes && !workspace)) return MOE_ERR_INVALID_ARG;
   Device d;
   if (!device(&d)) return MOE_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  Int8Product a = {*c,  w,    w_scale, x, x_scale, x_stride, addend, out, rows, reinterpret_cast<int*>(ws + p.status), false,
+  Int8Product a = {*c,  w,    w_scale, x, x_scale, x_stride, addend, out, rows,
+                   workspace && workspace_bytes >= kStatusBytes ? reinterpret_cast<int*>(ws + p.status) : nullptr, false,
                    ws + p.codes, reinterpret_cast<float*>(ws + p.scale), reinterpret_cast<__half*>(ws + p.w), INT8_STREAM, {}, {}};
   st = prepare_int8(a, d);
   if (st != MOE_OK) return st;
