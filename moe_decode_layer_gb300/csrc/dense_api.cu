@@ -10,7 +10,6 @@
 #include "../../include/moe_decode_dense.h"
 #include "dense_params.h"
 #include "rows_host.h"
-#include "rows_kernels.h"
 
 using namespace moe;
 using namespace moe::rows;
@@ -21,18 +20,18 @@ namespace {
 constexpr int kMostWidth = 65536;
 constexpr size_t kStatusBytes = kStatusKernels * kMaxSms * 4;
 
-// [halves][rows][cols] of 2-byte numbers (or fp32), copied in boxes of 128 bytes x box_rows rows;
+// [halves][rows][cols] of 2-byte numbers (or fp32, or codes), copied in boxes of 128 bytes x box_rows rows;
 // what lies past the matrix reads as zero and is not written.
 bool make_map(CUtensorMap* m, const void* ptr, int64_t pitch, int64_t cols, int64_t rows, int box_rows, int halves = 1,
-              int64_t half_bytes = 0, bool f32 = false) {
+              int64_t half_bytes = 0, bool f32 = false, bool codes = false) {
   EncodeTiled enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)halves};
   const cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)(halves > 1 ? half_bytes : pitch)};
-  const cuuint32_t box[3] = {f32 ? 32u : 64u, (cuuint32_t)box_rows, 1};
+  const cuuint32_t box[3] = {f32 ? 32u : codes ? 128u : 64u, (cuuint32_t)box_rows, 1};
   const cuuint32_t one[3] = {1, 1, 1};
-  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims,
-             strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             3, const_cast<void*>(ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -86,31 +85,40 @@ constexpr int kFewWarpsK = 2048;
 // Operands a and b, and results: map d at `out` (and e, g as the epilogue has them). Descriptors only.
 bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b, bool fp16, const Device& d) {
   PairParams& p = l.p;
-  const bool swiglu = epi == PAIR_SWIGLU || epi == PAIR_SWIGLU_F32;
+  const bool swiglu = epi == PAIR_SWIGLU || epi == PAIR_SWIGLU_F32, codes = form == FORM_KK8;
   l.form = form;
   l.epi = epi;
   shape_of(p, swiglu, d);
   p.bufs = epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU ? 1 : 2;
   // (A copy takes the TMA unit about two clocks a row of 128 bytes, also of rows that it fills with zeros.)
   const int a_rows = form != FORM_MM && p.M <= 128 ? (int)up(p.M, 8) : 128;
-  const int b_bytes = form == FORM_KK ? p.bn * 64 : (int)cdiv(p.bn, 128) * 8192;
+  const int b_bytes = form == FORM_KK || codes ? p.bn * 64 : (int)cdiv(p.bn, 128) * 8192;
   p.a_bytes = a_rows * 128;
   p.stage_bytes = p.a_bytes + b_bytes;
-  p.step_bytes = (a_rows < 128 ? 1 : 2) * p.a_bytes + 2 * b_bytes;
+  p.step_bytes = (a_rows < 128 ? 1 : 2) * p.a_bytes + (codes ? 0 : 2 * b_bytes);
   // Three boxes a warp leave four stages of 256 columns; with four warps there are five. Where a tile's
   // product is long enough for its epilogue, that is faster.
-  p.ewarps = p.bufs == 3 && p.split == 1 && p.K >= kFewWarpsK ? 4 : 8;
-  p.stages = std::min(kPairStages, (d.smem - 2048 - p.ewarps * p.bufs * kStageBox) / p.stage_bytes);
-  p.ahead = p.tiles_m <= 2 && a_rows == 128 && form != FORM_MM ? 8 : 0;
+  p.ewarps = codes || (p.bufs == 3 && p.split == 1 && p.K >= kFewWarpsK) ? 4 : 8;
+  int room = d.smem - 2048 - p.ewarps * p.bufs * kStageBox;
+  p.raw_slots = 0;
+  if (codes) {
+    // the copies in flight are the slots of codes: four at least, and up to six stages
+    p.stages = std::min(6, (room - 4 * p.bn * 64) / p.stage_bytes);
+    p.raw_slots = std::min(kRawSlots, (room - p.stages * p.stage_bytes) / (p.bn * 64));
+    p.raw_off = p.stages * p.stage_bytes;
+  } else {
+    p.stages = std::min(kPairStages, room / p.stage_bytes);
+  }
+  p.ahead = p.tiles_m <= 2 && form != FORM_MM && (codes || a_rows == 128) ? 8 : 0;
   // fp32 accumulators; bf16 or fp16 operands; k or the operand's own index innermost; M = 256 of a pair
   p.idesc = 1u << 4 | (fp16 ? 0u : 1u << 7 | 1u << 10) | (form == FORM_MM ? 1u << 15 : 0u) |
-            (form != FORM_KK ? 1u << 16 : 0u) | (uint32_t)(p.bn >> 3) << 17 | 16u << 24;
+            (form == FORM_KM || form == FORM_MM ? 1u << 16 : 0u) | (uint32_t)(p.bn >> 3) << 17 | 16u << 24;
   const bool ok_a = make_map(&l.a, a.ptr, a.pitch, a.cols, a.rows, form == FORM_MM ? 64 : a_rows);
-  const bool ok_b = swiglu ? make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows / 2, p.bn / 2, 2, b.pitch * (b.rows / 2))
-                           : make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows, form == FORM_KK ? p.bn / 2 : 64);
+  const bool ok_b = swiglu ? make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows / 2, p.bn / 2, 2, b.pitch * (b.rows / 2), false, codes)
+                           : make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows, form == FORM_KK || codes ? p.bn / 2 : 64, 1, 0, false, codes);
   l.e = l.g = l.a;
-  p.box_off = std::max(p.stages * p.stage_bytes, p.split > 1 ? p.bn * 512 : 0);
-  return ok_a && ok_b && p.stages >= 2 && p.box_off + p.ewarps * p.bufs * kStageBox <= d.smem - 2048;
+  p.box_off = std::max(p.stages * p.stage_bytes + p.raw_slots * p.bn * 64, p.split > 1 ? p.bn * 512 : 0);
+  return ok_a && ok_b && p.stages >= 2 && (!codes || p.raw_slots >= 2) && p.box_off + p.ewarps * p.bufs * kStageBox <= d.smem - 2048;
 }
 
 // Results [M, N] of 2 bytes, or fp32 (as pairs of 2 bytes where nothing is added), and their addends.
@@ -124,7 +132,7 @@ bool prepare_out(PairLaunch& l, const void* out, bool f32) {
 
 cudaError_t launch(PairLaunch& l, const Device& d, bool pdl, cudaStream_t s) {
   const void* k = pair_kernel(l.form, l.epi);
-  static std::atomic<uint64_t> ready[3][5];  // per kernel: devices whose limit is set
+  static std::atomic<uint64_t> ready[4][5];  // per kernel: devices whose limit is set
   if (d.id >= 64 || !(ready[l.form][l.epi].load() >> d.id & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem - 1024);
     if (e != cudaSuccess) return e;
@@ -134,7 +142,7 @@ cudaError_t launch(PairLaunch& l, const Device& d, bool pdl, cudaStream_t s) {
   const int64_t tiles = (int64_t)l.p.tiles_m * l.p.tiles_n;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(2 * l.p.split * (l.p.split > 1 ? tiles : std::min<int64_t>(tiles, d.sms / 2))));
-  c.blockDim = dim3(kPairThreads);
+  c.blockDim = dim3(pair_threads(l.form));
   // All of the SM's shared memory: a CTA takes all tensor memory, and a pair's CTAs wait for one
   // another, so none may wait for tensor memory that a CTA of another launch on its SM holds.
   c.dynamicSmemBytes = d.smem - 1024;
@@ -161,16 +169,12 @@ struct Places {
   }
 };
 
-// Which kernel a product of `rows` rows with `bytes` of weights goes to. Few rows: a stream of the weights.
+// Few rows: a stream of the weights, else the pair product. From 9 rows on the pair product is as fast for
+// bf16 weights of more than 16 MB (16 rows of the 4096 x 8192 block: 51 and 50 us, of 1024 x 2048
+// 9 and 19), and for int8 from 33 on.
 constexpr int64_t kStreamBytes = 16 << 20;
 bool few(int64_t rows, int64_t bytes) { return rows <= 8 || (rows <= kStreamRows && bytes <= kStreamBytes); }
-// int8, more rows: weights widened as they come (the grouped product), or fp16 copies of them for the
-// pair product.
-constexpr int64_t kWidenRows = 512;
-enum Int8Way { INT8_STREAM, INT8_ROWS, INT8_PAIR };
-Int8Way int8_way(int64_t rows, int64_t weights) {
-  return few(rows, weights) ? INT8_STREAM : rows <= kWidenRows ? INT8_ROWS : INT8_PAIR;
-}
+bool few_codes(int64_t rows) { return rows <= kStreamRows; }
 
 // ------------------------------------------------------------------ int8
 moe_status check_int8(const moe_int8_config* c) {
@@ -182,22 +186,18 @@ moe_status check_int8(const moe_int8_config* c) {
   return MOE_OK;
 }
 
-int64_t int8_weights(const moe_int8_config& c) { return (int64_t)c.outer * (c.swiglu ? 2 : 1) * c.inner; }
-
 struct Int8Plan {
-  size_t status, codes, scale, w, bytes;
+  size_t status, codes, scale, bytes;
 };
-// A stream takes the codes as they are, the others fp16 copies.
+// A stream takes the codes as they are, the pair product fp16 copies.
 Int8Plan int8_plan(const moe_int8_config& c, int64_t rows) {
   Places pl;
   Int8Plan p = {};
-  const Int8Way way = int8_way(rows, int8_weights(c));
   const bool made = c.x_dtype != MOE_I8;
-  if (way == INT8_STREAM && !made) return p;  // nothing is kept, and nothing waits
+  if (few_codes(rows) && !made) return p;  // nothing is kept, and nothing waits
   p.status = pl.take(kStatusBytes);
-  if (made || way != INT8_STREAM) p.codes = pl.take((size_t)rows * c.inner * (way == INT8_STREAM ? 1 : 2));
+  p.codes = pl.take((size_t)rows * c.inner * (few_codes(rows) ? 1 : 2));
   if (made) p.scale = pl.take((size_t)rows * 4);
-  if (way == INT8_PAIR) p.w = pl.take((size_t)int8_weights(c) * 2);
   p.bytes = pl.at;
   return p;
 }
@@ -218,68 +218,38 @@ struct Int8Product {
   bool status_keep;
   uint8_t* codes;
   float* scale;
-  __half* w16;
-  Int8Way way;
   PairLaunch l;
-  RowsInt8 r;
 };
 
 moe_status prepare_int8(Int8Product& a, const Device& d) {
-  a.way = int8_way(a.rows, int8_weights(a.c));
+  if (few_codes(a.rows)) return MOE_OK;
   const bool f32 = a.c.out_dtype == MOE_F32;
-  const float* scale = a.c.x_dtype == MOE_I8 ? a.x_scale : a.scale;
-  const int64_t k = a.c.inner;
-  if (a.way == INT8_ROWS) {
-    GemmParams& p = a.r.p;
-    p.R = a.c.outer;
-    p.K = a.c.inner;
-    p.rows = (int)a.rows;
-    p.row_scale = scale;
-    p.wscale = a.w_scale;
-    p.addend = static_cast<const __nv_bfloat16*>(a.addend);
-    p.out = a.out;
-    p.status = a.status;
-    p.status_clear = a.status_keep ? nullptr : a.status + kMaxSms;
-    p.status_keep = a.status_keep;
-    a.r.epi = a.c.swiglu ? (f32 ? EPI_SWIGLU_F32 : EPI_SWIGLU) : f32 ? EPI_F32 : EPI_BF16;
-    a.r.weight = a.w;
-    a.r.x16 = a.codes;
-    return prepare_rows_int8(&a.r, d) ? MOE_OK : MOE_ERR_CUDA;
-  }
-  if (a.way == INT8_PAIR) {
-    const int epi = a.c.swiglu ? (f32 ? PAIR_SWIGLU_F32 : PAIR_SWIGLU) : f32 ? PAIR_F32 : PAIR_BF16;
-    PairParams& p = a.l.p;
-    p.M = (int)a.rows;
-    p.N = a.c.outer;
-    p.K = a.c.inner;
-    p.row_scale = scale;
-    p.col_scale = a.w_scale;
-    p.addend = static_cast<const __nv_bfloat16*>(a.addend);
-    p.status = a.status;
-    p.status_keep = a.status_keep;
-    if (!prepare(a.l, FORM_KK, epi, {a.codes, k * 2, a.rows, k}, {a.w16, k * 2, int8_weights(a.c) / k, k}, true, d) ||
-        !prepare_out(a.l, a.out, f32))
-      return MOE_ERR_CUDA;
-  }
-  return MOE_OK;
+  PairParams& p = a.l.p;
+  p.M = (int)a.rows;
+  p.N = a.c.outer;
+  p.K = a.c.inner;
+  p.row_scale = a.c.x_dtype == MOE_I8 ? a.x_scale : a.scale;
+  p.col_scale = a.w_scale;
+  p.addend = static_cast<const __nv_bfloat16*>(a.addend);
+  p.status = a.status;
+  p.status_keep = a.status_keep;
+  const int64_t k = a.c.inner, w_rows = (int64_t)a.c.outer * (a.c.swiglu ? 2 : 1);
+  const int epi = a.c.swiglu ? (f32 ? PAIR_SWIGLU_F32 : PAIR_SWIGLU) : f32 ? PAIR_F32 : PAIR_BF16;
+  return prepare(a.l, FORM_KK8, epi, {a.codes, k * 2, a.rows, k}, {a.w, k, w_rows, k}, true, d) && prepare_out(a.l, a.out, f32)
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 cudaError_t launch_int8(Int8Product& a, const Device& d, bool pdl, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  const bool made = a.c.x_dtype != MOE_I8, small = a.way == INT8_STREAM;
-  if (made) {
+  const bool made = a.c.x_dtype != MOE_I8, small = few_codes(a.rows);
+  if (made)
     e = launch_quantise(a.c.x_dtype, a.x, a.x_stride, a.rows, a.c.inner, a.codes, !small, a.scale, pdl, s);
-    pdl = true;
-  } else if (!small) {
+  else if (!small)
     e = launch_widen(static_cast<const int8_t*>(a.x), a.x_stride, a.rows, a.c.inner, reinterpret_cast<__half*>(a.codes), pdl, s);
-    pdl = true;
-  }
   if (e != cudaSuccess) return e;
-  if (a.way == INT8_ROWS) return launch_rows_int8(a.r, d, pdl, s);
-  if (a.way == INT8_PAIR) {
-    e = launch_widen(a.w, a.c.inner, int8_weights(a.c) / a.c.inner, a.c.inner, a.w16, pdl, s);
-    return e == cudaSuccess ? launch(a.l, d, true, s) : e;
-  }
+  pdl = pdl || made || !small;
+  if (!small) return launch(a.l, d, pdl, s);
   StreamParams p = {};
   p.w = a.w;
   p.x = made ? static_cast<const void*>(a.codes) : a.x;
@@ -308,7 +278,7 @@ moe_status check_ff(const moe_ff_config* c) {
 }
 
 struct FfPlan {
-  size_t status, h, codes, scale, w, bytes;
+  size_t status, h, codes, scale, bytes;
 };
 FfPlan ff_plan(const moe_ff_config& c, int64_t rows) {
   Places pl;
@@ -320,7 +290,6 @@ FfPlan ff_plan(const moe_ff_config& c, int64_t rows) {
     // (both products' rows in turn; a stream takes a byte each)
     p.codes = pl.take((size_t)rows * std::max(c.hidden, c.inter) * 2);
     p.scale = pl.take((size_t)rows * 4);
-    if (rows > kWidenRows) p.w = pl.take((size_t)c.hidden * c.inter * 4);  // W13 in fp16, then W2
   }
   p.bytes = pl.at;
   return p;
@@ -405,7 +374,7 @@ moe_status moe_decode_project_int8(const moe_int8_config* c, const int8_t* w, co
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Int8Product a = {*c,  w,    w_scale, x, x_scale, x_stride, addend, out, rows,
                    workspace && workspace_bytes >= kStatusBytes ? reinterpret_cast<int*>(ws + p.status) : nullptr, false,
-                   ws + p.codes, reinterpret_cast<float*>(ws + p.scale), reinterpret_cast<__half*>(ws + p.w), INT8_STREAM, {}, {}};
+                   ws + p.codes, reinterpret_cast<float*>(ws + p.scale), {}};
   st = prepare_int8(a, d);
   if (st != MOE_OK) return st;
   return cuda_status(launch_int8(a, d, false, reinterpret_cast<cudaStream_t>(stream)));
@@ -457,11 +426,10 @@ moe_status moe_decode_ff(const moe_ff_config* c, const moe_ff_weights* wt, const
   if (int8) {
     uint8_t* codes = ws + p.codes;
     float* scale = reinterpret_cast<float*>(ws + p.scale);
-    __half* w16 = reinterpret_cast<__half*>(ws + p.w);
     Int8Product one = {{c->hidden, c->inter, 1, MOE_BF16, MOE_F32}, static_cast<const int8_t*>(wt->w13), wt->s13, x, nullptr,
-                       x_stride, nullptr, h, rows, status, false, codes, scale, w16, INT8_STREAM, {}, {}};
+                       x_stride, nullptr, h, rows, status, false, codes, scale, {}};
     Int8Product two = {{c->inter, c->hidden, 0, MOE_F32, MOE_BF16}, static_cast<const int8_t*>(wt->w2), wt->s2, h, nullptr,
-                       in, residual, out, rows, status, true, codes, scale, w16, INT8_STREAM, {}, {}};
+                       in, residual, out, rows, status, true, codes, scale, {}};
     if ((st = prepare_int8(one, d)) != MOE_OK || (st = prepare_int8(two, d)) != MOE_OK) return st;
     const cudaError_t e = launch_int8(one, d, false, s);
     return cuda_status(e == cudaSuccess ? launch_int8(two, d, true, s) : e);

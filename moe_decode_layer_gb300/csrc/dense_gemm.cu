@@ -5,8 +5,10 @@ namespace moe {
 namespace dense {
 
 const void* pair_kernel_backward(int form, int epi);
+const void* pair_kernel_int8(int epi);
 
 const void* pair_kernel(int form, int epi) {
+  if (form == FORM_KK8) return pair_kernel_int8(epi);
   if (form != FORM_KK) return pair_kernel_backward(form, epi);
   switch (epi) {
     case PAIR_SWIGLU: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_SWIGLU>);

@@ -15,6 +15,9 @@
 // Few tiles: the pairs of a cluster (2 or 4) take parts of K of one tile, and their sums are
 // joined through distributed shared memory, in the order of the parts.
 //
+// int8 weights (FORM_KK8) come as codes: eight warps widen them into the stage, and the epilogue has four. (A pass that widens the whole matrix first costs its 3 bytes a weight: 36 us for
+// 67 million, as long as the product of 400 rows.)
+//
 // Warps: 0 copies (both CTAs), 1 tensor core (the pair's first CTA), 4..11 epilogue. All
 // copies are TMA with the operands' 128-byte swizzle; results leave through shared memory by
 // TMA stores, which clip what lies past the matrix.
@@ -99,8 +102,8 @@ __device__ __forceinline__ void mma_pair_commit(uint32_t bar, uint16_t mask) {
       "h"(mask)
       : "memory");
 }
-// (Nothing in memory is handed over with it: the tensor-memory loads before it are done. A release
-// over the cluster waits for the thread's stores as well, 2200 clocks a tile.)
+// (What is handed over is this CTA's own tensor and shared memory, which is in order by the fences before
+// it. A release over the cluster waits for the thread's global stores as well, 2200 clocks a tile.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mapped_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
@@ -192,15 +195,17 @@ __device__ __forceinline__ PairTile pair_tile(const PairParams& p, int t, int co
 }
 
 template <int FORM, int EPI>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(pair_threads(FORM), 1)
     pair_gemm_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d,
                      const __grid_constant__ CUtensorMap map_e, const __grid_constant__ CUtensorMap map_g) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  // full, empty [kPairStages], tmem full / empty [2], an epilogue warp's loads [8][2], drain
-  __shared__ __align__(8) uint64_t s_bar[2 * kPairStages + 4 + 16 + 1];
+  // full, empty [kPairStages], tmem full / empty [2], an epilogue warp's loads [8][2], drain, codes full / empty
+  __shared__ __align__(8) uint64_t s_bar[2 * kPairStages + 4 + 16 + 1 + 2 * kRawSlots];
+  constexpr bool kI8 = FORM == FORM_KK8, kKK = FORM == FORM_KK || kI8;
+  constexpr int kThreads = pair_threads(FORM);
   constexpr bool kSwiglu = EPI == PAIR_SWIGLU || EPI == PAIR_SWIGLU_F32;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -212,6 +217,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   auto tempty = [&](int b) { return bar0 + 8u * (2 * kPairStages + 2 + b); };
   auto loads = [&](int w, int i) { return bar0 + 8u * (2 * kPairStages + 4 + 2 * w + i); };
   const uint32_t drain = bar0 + 8u * (2 * kPairStages + 20);
+  auto rfull = [&](int s) { return bar0 + 8u * (2 * kPairStages + 21 + s); };
+  auto rempty = [&](int s) { return bar0 + 8u * (2 * kPairStages + 21 + kRawSlots + s); };
   const uint32_t crank = cluster_rank();
   const int rank = crank & 1, part = crank >> 1;
   const uint32_t first_cta = crank & ~1u;  // of the pair
@@ -219,9 +226,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (tid == 0) {
     s_abort = 0;
     for (int s = 0; s < p.stages; s++) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), kI8 ? 1 + 8 : 1);  // copies; both CTAs' widening warps
       mbar_init(empty(s), 1);
     }
+    if (kI8)
+      for (int s = 0; s < p.raw_slots; s++) {
+        mbar_init(rfull(s), 1);
+        mbar_init(rempty(s), 8);
+      }
     for (int b = 0; b < 2; b++) {
       mbar_init(tfull(b), 1);
       mbar_init(tempty(b), 2 * p.ewarps);  // the epilogue warps of both CTAs
@@ -253,8 +265,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int ntiles = p.tiles_m * p.tiles_n;
   const int step = gridDim.x / (2 * p.split);
   const int t_first = blockIdx.x / (2 * p.split);
-  const int ksteps = (p.K + 63) / 64;
-  const int k_first = ksteps * part / p.split, k_last = ksteps * (part + 1) / p.split;
+  // (codes come 128 k at a time; what lies past K is zero)
+  constexpr int kCut = kI8 ? 2 : 1;
+  const int ksteps = (p.K + 64 * kCut - 1) / (64 * kCut);
+  const int k_first = ksteps * part / p.split * kCut, k_last = ksteps * (part + 1) / p.split * kCut;
   const int b_rows = p.bn / 2;  // of B in this CTA
 
   if (warp == 0) {
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       // Few rows: the ring holds less of B than HBM's latency asks for; L2 takes the rest.
       auto fetch_b = [&](int n, int half, int k) {
-        if (FORM == FORM_KK) {
+        if (kKK) {
           tma_prefetch_3d(&map_b, k * 64, n, half);
         } else {
           tma_prefetch_3d(&map_b, n, k * 64, 0);
@@ -276,13 +290,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const PairTile tl = pair_tile(p, t, cols);
         const int m = tl.m0 + rank * 128;
         const int n = kSwiglu ? tl.n0 : tl.n0 + rank * b_rows, half = kSwiglu ? rank : 0;
-        for (int k = k_first; k < min(k_first + p.ahead, k_last); k++) fetch_b(n, half, k);
+        if (!kI8)
+          for (int k = k_first; k < min(k_first + p.ahead, k_last); k++) fetch_b(n, half, k);
         for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
           const uint32_t s = it.slot;
           if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
           const uint32_t bar = bars + 8u * s;
           const uint32_t a = base + s * p.stage_bytes, b = a + p.a_bytes;
-          if (p.ahead && k + p.ahead < k_last) fetch_b(n, half, k + p.ahead);
+          if (!kI8 && p.ahead && k + p.ahead < k_last) fetch_b(n, half, k + p.ahead);
           // (the other CTA's bytes may be counted before this; the phase ends with the arrival)
           if (rank == 0) mbar_arrive_expect_tx(full(s), p.step_bytes);
           if (FORM == FORM_MM) {
@@ -293,7 +308,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
           if (FORM == FORM_KK) {
             tma_pair_3d(b, &map_b, k * 64, n, half, bar);
-          } else {
+          } else if (!kI8) {
             tma_pair_3d(b, &map_b, n, k * 64, 0, bar);
             if (b_rows > 64) tma_pair_3d(b + 8192, &map_b, n + 64, k * 64, 0, bar);
           }
@@ -304,6 +319,69 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (!ok) {  // let the copies in flight land before the shared memory goes
         const uint64_t t0 = global_ns();
         while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
+      }
+    }
+  } else if (kI8 && warp == 2) {
+    // ---------------------------------------------------------------- codes
+    if (lane == 0) {
+      Ring it;
+      bool ok = true;
+      for (int t = t_first; ok && t < ntiles; t += step) {
+        const PairTile tl = pair_tile(p, t, cols);
+        const int n = kSwiglu ? tl.n0 : tl.n0 + rank * b_rows, half = kSwiglu ? rank : 0;
+        for (int i = 0; i < p.ahead && k_first + 2 * i < k_last; i++) tma_prefetch_3d(&map_b, (k_first + 2 * i) * 64, n, half);
+        for (int k = k_first; k < k_last; k += 2, it.next(p.raw_slots)) {
+          const uint32_t s = it.slot;
+          if (!(ok = wait_phase(rempty(s), it.parity ^ 1, &s_abort))) break;
+          if (p.ahead && k + 2 * p.ahead < k_last) tma_prefetch_3d(&map_b, (k + 2 * p.ahead) * 64, n, half);
+          mbar_arrive_expect_tx(rfull(s), b_rows * 128);
+          tma_load_3d(base + p.raw_off + s * (b_rows * 128), &map_b, k * 64, n, half, rfull(s));
+        }
+      }
+      if (!ok) {
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
+      }
+    }
+  } else if (kI8 && warp >= 8) {
+    // ---------------------------------------------------------------- widening
+    // A thread has a row of this CTA's half of B: 64 codes a step become 128 bytes of fp16, exactly, where the
+    // operand's swizzle has them; the scales multiply the sums.
+    // Four warps take the first 64 k of a slot, four the others: one thread's wait, loads, conversions, stores
+    // and fence take about 1000 clocks, twice the tensor core's for a step.
+    const int row = (warp & 3) * 32 + lane, h = (warp - 8) >> 2;
+    const uint32_t bars = map_rank(bar0, first_cta);
+    const bool mine = row < b_rows;
+    Ring it, rit;
+    if (h) it.next(p.stages);
+    bool ok = true;
+    for (int t = t_first; ok && t < ntiles; t += step) {
+      for (int k = k_first; ok && k < k_last; k += 2, rit.next(p.raw_slots)) {
+        const uint32_t rs = rit.slot, raw = base + p.raw_off + rs * (b_rows * 128) + row * 128;
+        if (!(ok = warp_wait(rfull(rs), rit.parity, &s_abort))) break;
+        const uint32_t s = it.slot, to = base + s * p.stage_bytes + p.a_bytes + row * 128;
+        uint32_t o[32];
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            const uint4 q = ld_shared4(raw + (((h * 4 + c) ^ (row & 7)) << 4));
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) int8x4_f16x4(w[j], o[8 * c + 2 * j], o[8 * c + 2 * j + 1]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rempty(rs), 1);
+        if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < 8; c++) st_shared4(to + ((c ^ (row & 7)) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(bars + 8u * s);
+        it.next(p.stages);
+        it.next(p.stages);
       }
     }
   } else if (warp == 1 && rank == 0) {
@@ -323,8 +401,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t at = base + s * p.stage_bytes;
         const uint64_t da = FORM == FORM_MM ? smem_desc_mn(at) : smem_desc(at);
-        const uint64_t db = FORM == FORM_KK ? smem_desc(at + p.a_bytes) : smem_desc_mn(at + p.a_bytes);
-        constexpr int kA = FORM == FORM_MM ? 2048 >> 4 : 2, kB = FORM == FORM_KK ? 2 : 2048 >> 4;
+        const uint64_t db = kKK ? smem_desc(at + p.a_bytes) : smem_desc_mn(at + p.a_bytes);
+        constexpr int kA = FORM == FORM_MM ? 2048 >> 4 : 2, kB = kKK ? 2 : 2048 >> 4;
         if (leader) {
 #pragma unroll
           for (int j = 0; j < 4; j++) mma_pair(d, da + kA * j, db + kB * j, p.idesc, k != k_first || j != 0);
@@ -548,11 +626,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       return base + (uint32_t)(c * 128 + q * 32 + (r & 7) * 4) * 4u;
     };
     constexpr int kAtOnce = 3;  // (a load takes most of a microsecond)
-    for (int i0 = tid; i0 < all; i0 += kAtOnce * kPairThreads) {
+    for (int i0 = tid; i0 < all; i0 += kAtOnce * kThreads) {
       float4 v[kAtOnce][kSplitMost];
 #pragma unroll
       for (int k = 0; k < kAtOnce; k++) {
-        const uint32_t at = place(min(i0 + k * kPairThreads, all - 1));
+        const uint32_t at = place(min(i0 + k * kThreads, all - 1));
 #pragma unroll
         for (int s = 0; s < kSplitMost; s++)
           if (s < p.split) v[k][s] = ld_cluster4(at, 2 * s + rank);
@@ -563,7 +641,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int s = 1; s < kSplitMost; s++)
           if (s < p.split) sum.x += v[k][s].x, sum.y += v[k][s].y, sum.z += v[k][s].z, sum.w += v[k][s].w;
-        const int i = i0 + k * kPairThreads;
+        const int i = i0 + k * kThreads;
         if (i < all)
           st_shared4(place(i), __float_as_uint(sum.x), __float_as_uint(sum.y), __float_as_uint(sum.z), __float_as_uint(sum.w));
       }
@@ -589,7 +667,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   // the status words: this CTA's, and from CTA 0 those that no CTA has, and the second launch's
   if (tid == 0 && (s_abort || !p.status_keep)) p.status[blockIdx.x] = s_abort;
   if (blockIdx.x == 0 && !p.status_keep)
-    for (int i = gridDim.x + tid; i < 2 * kMaxSms; i += kPairThreads) p.status[i] = 0;
+    for (int i = gridDim.x + tid; i < 2 * kMaxSms; i += kThreads) p.status[i] = 0;
 }
 
 }  // namespace dense

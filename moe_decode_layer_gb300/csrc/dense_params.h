@@ -12,8 +12,8 @@ namespace moe {
 namespace dense {
 
 constexpr int kPairStages = 16;      // operand stages at most
-constexpr int kPairThreads = 384;    // copies, tensor core, two idle warps, eight epilogue warps
 constexpr int kTileM = 256;          // rows of a pair's tile
+constexpr int kRawSlots = 6;         // slots of codes at most
 constexpr int kStageBox = 4096;      // an epilogue warp's box in shared memory: 32 rows of 128 bytes
 constexpr int kSplitMost = 4;        // pairs of a cluster of 8
 constexpr int kGroupM = 8;           // row tiles that go round the columns together
@@ -22,8 +22,11 @@ constexpr int kGroupM = 8;           // row tiles that go round the columns toge
 enum Form {
   FORM_KK = 0,  // A [M, K], B [N, K]
   FORM_KM = 1,  // A [M, K], B [K, N]
-  FORM_MM = 2   // A [K, M], B [K, N]
+  FORM_MM = 2,  // A [K, M], B [K, N]
+  FORM_KK8 = 3  // FORM_KK, fp16 A and int8 B, which is widened to fp16 in shared memory
 };
+// Copies, tensor core, copies of codes, an idle warp; eight epilogue warps, or (FORM_KK8) four and eight that widen.
+__host__ __device__ constexpr int pair_threads(int form) { return form == FORM_KK8 ? 512 : 384; }
 enum PairEpi {
   PAIR_BF16 = 0,
   PAIR_F32 = 1,
@@ -38,6 +41,7 @@ struct PairParams {
   int tiles_m, tiles_n;
   int split;     // pairs of a cluster that share a tile's K
   int stages, stage_bytes;
+  int raw_off, raw_slots;  // FORM_KK8: slots of 128 codes of each row of B
   // A's part of a stage: 128 rows, or of few rows (M <= 128, no FORM_MM) those in the first CTA alone.
   // The tensor core reads 128 all the same; what lies behind them becomes rows that nothing reads.
   int a_bytes;
@@ -74,7 +78,7 @@ struct StreamParams {
   __nv_bfloat16* keep;   // SWIGLU: [T, 2 R], or NULL
   int* status;           // the workspace's status words, to be cleared, or NULL
 };
-constexpr int kStreamRows = 16;  // rows at most
+constexpr int kStreamRows = 32;  // rows at most
 cudaError_t launch_stream(const StreamParams& p, bool int8, bool pdl, int sms, cudaStream_t s);
 
 // codes of rows, as int8 or (half) as fp16 numbers

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
           p.keep[o + (int64_t)t * p.R] = __float2bfloat16_rn(v);
           p.keep[o + (int64_t)(t + 1) * p.R] = __float2bfloat16_rn(u);
         }
-        v = v / (1.0f + expf(-v)) * u;
+        v = rows::silu_mul_f32(v, u);
       }
       if (p.addend) v += __bfloat162float(p.addend[o]);
       if (p.out_f32) static_cast<float*>(p.out)[o] = v;
@@ -269,11 +269,13 @@ cudaError_t launch(const StreamParams& p, int per_sm, bool pdl, int sms, cudaStr
 }
 
 // Stages and CTAs an SM: of 1 to 4 CTAs and 2 to 6 stages of 64 or 128 bytes a row, the fastest for
-// matrices of 17 to 134 MB.
+// matrices of 17 to 134 MB. (More rows of x take two blocks of weight rows a CTA, which read
+// them half as often.)
 template <bool I8>
 cudaError_t choose(const StreamParams& p, bool pdl, int sms, cudaStream_t s) {
   if (p.T <= 8) return launch<I8, 1, 1, 2, 4>(p, 2, pdl, sms, s);
-  return launch<I8, 1, 2, 1, 4>(p, 3, pdl, sms, s);
+  if (p.T <= 16) return launch<I8, 2, 2, 1, 4>(p, 2, pdl, sms, s);
+  return launch<I8, 2, 4, 1, 4>(p, 1, pdl, sms, s);
 }
 
 }  // namespace

@@ -28,7 +28,7 @@ constexpr int kMinN = 32;  // rows of a tile of experts' rows at least
 bool make_map(CUtensorMap* m, const void* ptr, int fmt, int64_t cols, int64_t rows, int halves, int64_t groups, int rt) {
   EncodeTiled enc = encode_tiled();
   if (!enc) return false;
-  const int64_t row_bytes = fmt == FMT_BF16 ? cols * 2 : fmt == FMT_NVFP4 ? cols / 2 : cols;
+  const int64_t row_bytes = fmt == FMT_BF16 ? cols * 2 : fmt == FMT_FP8 ? cols : cols / 2;
   const cuuint64_t dims[4] = {(cuuint64_t)(fmt == FMT_BF16 ? cols : row_bytes), (cuuint64_t)rows, (cuuint64_t)halves,
                               (cuuint64_t)groups};
   const cuuint64_t strides[3] = {(cuuint64_t)row_bytes, (cuuint64_t)(row_bytes * rows),
@@ -101,7 +101,7 @@ int choose_rt(int64_t R, bool swiglu, double entries, double reuse, int n, int f
               const Device& d, double* cost_out = nullptr) {
   int best = 128;
   double least = 1e300;
-  const double bytes = fmt == FMT_BF16 ? 256.0 : fmt == FMT_NVFP4 ? 72.0 : 128.0;
+  const double bytes = fmt == FMT_BF16 ? 256.0 : fmt == FMT_FP8 ? 128.0 : 72.0;
   for (int rt = 128; rt >= 8; rt -= rt > 16 ? 16 : 8) {
     Layout l;
     if (!layout(rt, nmax, fmt, ksteps, ad_mode, d.smem, &l)) continue;
@@ -122,19 +122,19 @@ int choose_rt(int64_t R, bool swiglu, double entries, double reuse, int n, int f
 // For few rows: the CTAs that share a tile's K (1: none) and the rows of a sub-tile.
 // All tiles run at once (clusters do not fill every SM: 7 of 8 are counted on); joining
 // the sums costs about 1800 clocks.
-int choose_split(int64_t R, bool swiglu, int entries, int fmt, int nmax, int ksteps, int ad_mode, const Device& d, int* rt) {
+int choose_split(int64_t R, bool swiglu, int entries, int nmax, int ksteps, int ad_mode, const Device& d, int* rt) {
   double least = 0.0;
-  *rt = choose_rt(R, swiglu, entries, entries, nmax, fmt, nmax, ksteps, ad_mode, d, &least);
+  *rt = choose_rt(R, swiglu, entries, entries, nmax, FMT_BF16, nmax, ksteps, ad_mode, d, &least);
   int split = 1;
   for (int s = 2; s <= 8; s *= 2) {
     if (ksteps < 2 * s) break;
     for (int t = 128; t >= 16; t -= 16) {
       const int64_t ctas = entries * cdiv(R, swiglu ? t : 2 * t) * s;
       Layout l;
-      if (ctas > d.sms * 7 / 8 || !layout(t, nmax, fmt, (int)cdiv(ksteps, s), ad_mode, d.smem, &l)) continue;
-      if (l.raw_off + l.raw_slots * 2 * t * 128 < nmax * 2 * t * 4) continue;
+      if (ctas > d.sms * 7 / 8 || !layout(t, nmax, FMT_BF16, (int)cdiv(ksteps, s), ad_mode, d.smem, &l)) continue;
+      if (l.stages * l.stage_bytes < nmax * 2 * t * 4) continue;
       const double rate = std::min(45.0, 23.0 * d.sms / ctas);
-      const double cost = cdiv(ksteps, s) * std::max({t * (fmt == FMT_BF16 ? 256.0 : 128.0) / rate, kSmallStep, 4.0 * nmax}) + 2500.0 + 1800.0;
+      const double cost = cdiv(ksteps, s) * std::max({t * 256.0 / rate, kSmallStep, 4.0 * nmax}) + 2500.0 + 1800.0;
       if (cost < least * 0.98) {
         least = cost;
         split = s;
@@ -151,7 +151,7 @@ struct Maps {
 
 cudaError_t launch_gemm(GemmParams& p, int epi, int fmt, Maps& m, int64_t tiles, const Layout& l, const Device& d, bool pdl, cudaStream_t st) {
   const void* k = gemm_kernel(epi, fmt);
-  static std::atomic<uint64_t> ready[5][4];  // per kernel: devices whose limit is set
+  static std::atomic<uint64_t> ready[4][3];  // per kernel: devices whose limit is set
   if (d.id >= 64 || !(ready[epi][fmt].load() >> d.id & 1)) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem - 4096);
     if (e != cudaSuccess) return e;
@@ -441,51 +441,6 @@ moe_status check_project(const moe_project_config* c) {
 
 }  // namespace
 
-namespace moe {
-namespace rows {
-
-bool prepare_rows_int8(RowsInt8* r, const Device& d) {
-  GemmParams& g = r->p;
-  const bool swiglu = r->epi == EPI_SWIGLU || r->epi == EPI_SWIGLU_F32;
-  const int ksteps = (int)cdiv(g.K, 128) * 2;
-  // a tile holds 128 rows at most, and the blocks of rows are about as wide
-  g.nmax = std::max(16, round16((double)g.rows / cdiv(g.rows, 128)));
-  const double entries = (double)cdiv(g.rows, g.nmax);
-  if (g.rows <= 128)
-    g.split = choose_split(g.R, swiglu, (int)entries, FMT_INT8, g.nmax, ksteps, AD_NONE, d, &g.rt);
-  else
-    g.rt = choose_rt(g.R, swiglu, entries, entries, g.nmax, FMT_INT8, g.nmax, ksteps, AD_NONE, d);
-  g.nrb = (int)cdiv(g.R, swiglu ? g.rt : 2 * g.rt);
-  g.groups_main = 1;
-  g.box_rows = g.nmax % 32 ? 16 : 32;
-  g.out_stride = g.R;
-  Layout l;
-  if (!layout(g.rt, g.nmax, FMT_INT8, (int)cdiv(ksteps, std::max(1, g.split)), AD_NONE, d.smem, &l)) return false;
-  g.stages = l.stages;
-  g.stage_bytes = l.stage_bytes;
-  g.raw_off = l.raw_off;
-  g.raw_slots = l.raw_slots;
-  g.ad_off = l.ad_off;
-  return make_map(&r->w, r->weight, FMT_INT8, g.K, g.R, swiglu ? 2 : 1, 1, g.rt) &&
-         make_rows_map(&r->x, r->x16, g.K, g.rows, g.K, g.box_rows);
-}
-
-cudaError_t launch_rows_int8(RowsInt8& r, const Device& d, bool pdl, cudaStream_t s) {
-  Layout l;
-  l.stages = r.p.stages;
-  l.stage_bytes = r.p.stage_bytes;
-  l.raw_off = r.p.raw_off;
-  l.raw_slots = r.p.raw_slots;
-  l.ad_off = r.p.ad_off;
-  Maps m;
-  m.w = m.s = m.u = r.w;
-  m.x = r.x;
-  return launch_gemm(r.p, r.epi, FMT_INT8, m, cdiv(r.p.rows, r.p.nmax) * r.p.nrb, l, d, pdl, s);
-}
-
-}  // namespace rows
-}  // namespace moe
-
 extern "C" {
 
 moe_status moe_decode_route_check(const moe_route_config* c) {
@@ -663,7 +618,7 @@ moe_status moe_decode_project(const moe_project_config* c, const moe_project_wei
   }
   const double entries = (double)cdiv(p.positions, p.nmax);
   if (fmt == FMT_BF16 && p.mode != AD_STEPS && rows <= 64)
-    g.split = choose_split(c->outer, swiglu, (int)entries, fmt, p.nmax, ksteps, p.mode, d, &g.rt);
+    g.split = choose_split(c->outer, swiglu, (int)entries, p.nmax, ksteps, p.mode, d, &g.rt);
   else
     g.rt = choose_rt(c->outer, swiglu, entries, entries, p.nmax, fmt, p.nmax, ksteps, p.mode, d);
   g.nrb = (int)cdiv(c->outer, swiglu ? g.rt : 2 * g.rt);

@@ -6,12 +6,10 @@ namespace rows {
 
 const void* gemm_kernel_fp8(int epi);
 const void* gemm_kernel_nvfp4(int epi);
-const void* gemm_kernel_int8(int epi);
 
 const void* gemm_kernel(int epi, int fmt) {
   if (fmt == FMT_FP8) return gemm_kernel_fp8(epi);
   if (fmt == FMT_NVFP4) return gemm_kernel_nvfp4(epi);
-  if (fmt == FMT_INT8) return gemm_kernel_int8(epi);
   switch (epi) {
     case EPI_SWIGLU: return reinterpret_cast<const void*>(&rows_gemm_kernel<EPI_SWIGLU, FMT_BF16>);
     case EPI_F32: return reinterpret_cast<const void*>(&rows_gemm_kernel<EPI_F32, FMT_BF16>);

@@ -219,18 +219,14 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   pdl_launch_dependents();
 
   const int ntiles = num_tiles(p);
-  // (int8: K is cut at slots of 128 codes; what lies past K is zero)
-  const int main_steps = FMT == FMT_INT8 ? (p.K + 127) / 128 * 2 : (p.K + 63) / 64;
+  const int main_steps = (p.K + 63) / 64;
   // Few rows: the CTAs of a cluster take parts of K of one tile, and the sums are
   // joined through distributed shared memory. (A step costs 200 to 400 clocks however
   // few rows there are: 40 of them one after another were most of a decoding
   // projection's time. 32 rows, K = 2560, 2 x 768 columns: 54 -> 46 us for a call alone.)
-  constexpr bool kSplits = FMT == FMT_BF16 || FMT == FMT_INT8;
-  constexpr int kCut = FMT == FMT_INT8 ? 2 : 1;
-  const int split = kSplits ? p.split : 1;
+  const int split = FMT == FMT_BF16 ? p.split : 1;
   const int part_of = split > 1 ? blockIdx.x % split : 0;
-  const int k_first = main_steps / kCut * part_of / split * kCut;
-  const int k_last = main_steps / kCut * (part_of + 1) / split * kCut;
+  const int k_first = main_steps * part_of / split, k_last = main_steps * (part_of + 1) / split;
   const int t_first = split > 1 ? blockIdx.x / split : blockIdx.x;
   const int t_step = split > 1 ? ntiles : gridDim.x;
   const int a_half = p.rt * 128;  // bytes of a sub-tile of a stage
@@ -249,8 +245,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
   constexpr int kHalves = stage_steps(FMT);
   const int half_bytes = p.nmax * 128;  // the rows of x of one step
   const int b_off = FMT == FMT_BF16 || ad_steps ? 2 * a_half : 0;  // the rows of x in a stage
-  constexpr bool kSwiglu = EPI == EPI_SWIGLU || EPI == EPI_SWIGLU_F32;
-  const int sub_rows = kSwiglu ? p.rt : 2 * p.rt;  // output rows per tile
+  const int sub_rows = EPI == EPI_SWIGLU ? p.rt : 2 * p.rt;  // output rows per tile
 
   if (warp == 0) {
     // ---------------------------------------------------------------- weights
@@ -263,7 +258,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         const CUtensorMap* m = sh ? &map_s : &map_w;
         const int g = sh ? tl.g - p.groups_main : tl.g;
         const int y0 = tl.rb * sub_rows;
-        const int y1 = kSwiglu ? y0 : y0 + p.rt, z1 = kSwiglu ? 1 : 0;
+        const int y1 = EPI == EPI_SWIGLU ? y0 : y0 + p.rt, z1 = EPI == EPI_SWIGLU ? 1 : 0;
         if (FMT == FMT_BF16) {
           for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
             const uint32_t s = it.slot;
@@ -275,8 +270,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           }
         } else {
           // raw slots: 128 bytes of codes per row
-          const int first = FMT == FMT_INT8 ? k_first / 2 : 0, last = FMT == FMT_INT8 ? k_last / 2 : p.K / kmath(FMT);
-          for (int k = first; k < last; k++, rit.next(p.raw_slots)) {
+          const int nraw = p.K / kmath(FMT);
+          for (int k = 0; k < nraw; k++, rit.next(p.raw_slots)) {
             const uint32_t s = rit.slot;
             if (!(ok = wait_phase(rempty(s), rit.parity ^ 1, &s_abort))) break;
             const uint32_t dst = base + p.raw_off + s * (2 * a_half);
@@ -320,8 +315,8 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       const int b = acc.slot;
       if (!(ok = warp_wait(tempty(b), acc.parity ^ 1, &s_abort))) break;
       tc_fence_after();
-      // fp32 accumulators, bf16 x bf16 (int8: fp16 x fp16), both K-major, M = 128
-      constexpr uint32_t kDesc = (1u << 4) | (FMT == FMT_INT8 ? 0u : (1u << 7) | (1u << 10)) | (8u << 24);
+      // fp32 accumulators, bf16 x bf16, both K-major, M = 128
+      constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
       const uint32_t d0 = tmem + b * 2 * p.nmax, d1 = d0 + p.nmax;
       // one stage into the accumulators of n rows from the tile's row c on
       auto step = [&](int c, int n, bool first, bool main) {
@@ -458,11 +453,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           const int c = i / (2 * p.rt), wr = i % (2 * p.rt);
           if (split > 1 && c % split != part_of) continue;  // another CTA joins that column
           const int sub = wr >= p.rt;
-          const int y = tl.rb * sub_rows + (kSwiglu ? wr - sub * p.rt : wr);
+          const int y = tl.rb * sub_rows + (EPI == EPI_SWIGLU ? wr - sub * p.rt : wr);
           const int a = __ldg(p.ids + tl.p0 + c);
           float v = 0.0f;
           if ((unsigned)a < (unsigned)p.num_adapters && y < p.R) {
-            const size_t brow = kSwiglu ? ((size_t)a * 2 + sub) * p.R + y : (size_t)a * p.R + y;
+            const size_t brow = EPI == EPI_SWIGLU ? ((size_t)a * 2 + sub) * p.R + y : (size_t)a * p.R + y;
             const uint4* bp = reinterpret_cast<const uint4*>(p.b + brow * p.rank);
             const float* up = p.u32 + (size_t)(tl.p0 + c) * p.rank;
             // four chunks' loads at a time: one by one they were most of the launch
@@ -477,7 +472,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           s_ad[i] = v;
         }
       }
-      if (!kSwiglu && p.addend && split == 1) {  // the tile's addends on their way to L2
+      if (EPI != EPI_SWIGLU && p.addend && split == 1) {  // the tile's addends on their way to L2
         const int first = tl.rb * sub_rows, cols = min(2 * p.rt, p.R - first);
         const int lines = (cols * 2 + 127) / 128 + 1;
         for (int i = tid - 128; i < tl.n * lines; i += 32 * epilogue_warps(FMT)) {
@@ -504,7 +499,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       if (FMT == FMT_NVFP4 && !ad_steps) {
         const float* gs = sh ? p.gscale_s : p.gscale;
         const int g = sh ? tl.g - p.groups_main : tl.g;
-        if (kSwiglu) {
+        if (EPI == EPI_SWIGLU) {
           g0 = __ldg(gs + 2 * g);
           g1 = __ldg(gs + 2 * g + 1);
         } else {
@@ -512,11 +507,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         }
       } else if (EPI == EPI_TWO && p.gscale) {
         g0 = g1 = __ldg(p.gscale + tl.g);
-      } else if (FMT == FMT_INT8) {
-        const float* ws = static_cast<const float*>(p.wscale);
-        const int y0 = min(tl.rb * sub_rows + min(r, p.rt - 1), p.R - 1);
-        g0 = __ldg(ws + y0);
-        g1 = __ldg(ws + (kSwiglu ? p.R + y0 : min(y0 + p.rt, p.R - 1)));
       }
       if (split > 1 && q * 32 < p.rt) {
         // the partial sums, [column][weight row], where the stages were: all are used
@@ -538,7 +528,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       } else if (q * 32 < p.rt) {
         const int y0 = tl.rb * sub_rows + r;
         const int y1 = y0 + p.rt;
-        const bool ok0 = r < p.rt && y0 < p.R, ok1 = !kSwiglu && r < p.rt && y1 < p.R;
+        const bool ok0 = r < p.rt && y0 < p.R, ok1 = EPI != EPI_SWIGLU && r < p.rt && y1 < p.R;
         // Two lanes exchange a value of each pair of columns, so that a store takes two
         // neighbouring results of one column: lane 2 i those of the even column.
         const bool odd = lane & 1;
@@ -547,17 +537,15 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
         // meanwhile. No branches between columns: with them each column waited for the
         // one before (225 clocks).
         constexpr int kStep = 2 * epilogue_warps(FMT);
-        const bool add = !kSwiglu && p.addend;
+        const bool add = EPI != EPI_SWIGLU && p.addend;
         uint32_t n0[8], n1[8];
         __nv_bfloat16 q0[8], q1[8];
         int row_n = -1;
-        float rs_n = 1.0f;  // int8: lane j: the scale of column j's row of x
         auto fetch = [&](int c) {
           __syncwarp();
           tmem_ld8(d0 + c, n0);
           tmem_ld8(d1 + c, n1);
           row_n = tl.p0 + min(c + (lane & 7), tl.n - 1);  // lane j: the row of out of column j
-          if (FMT == FMT_INT8) rs_n = p.row_scale[row_n];
           if (p.out_row) row_n = p.out_row[row_n];
           if (add) {
 #pragma unroll
@@ -574,7 +562,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
           tmem_ld_wait();
           const int m = min(8, tl.n - c);
           const int row_l = row_n;
-          const float rs_l = rs_n;
 #pragma unroll
           for (int j = 0; j < 8; j++) {
             a0[j] = __uint_as_float(n0[j]);
@@ -582,11 +569,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             if (FMT == FMT_NVFP4 || EPI == EPI_TWO) {
               a0[j] *= g0;
               a1[j] *= g1;
-            }
-            if (FMT == FMT_INT8) {
-              const float rs = __shfl_sync(0xffffffffu, rs_l, j);
-              a0[j] *= rs * g0;
-              a1[j] *= rs * g1;
             }
             if (add) {
               a0[j] += __bfloat162float(q0[j]);
@@ -603,9 +585,9 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
               a1[j] += ad[at + p.rt];
             }
           }
-          if (kSwiglu) {
+          if (EPI == EPI_SWIGLU) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) a0[j] = EPI == EPI_SWIGLU_F32 ? silu_mul_f32(a0[j], a1[j]) : silu_mul(a0[j], a1[j]);
+            for (int j = 0; j < 8; j++) a0[j] = silu_mul(a0[j], a1[j]);
           }
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
@@ -615,11 +597,11 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
             const float x0 = __shfl_xor_sync(0xffffffffu, odd ? a0[j] : a0[j + 1], 1);
             const float2 f0 = odd ? make_float2(x0, a0[j + 1]) : make_float2(a0[j], x0);
             float2 f1 = f0;
-            if (!kSwiglu) {
+            if (EPI != EPI_SWIGLU) {
               const float x1 = __shfl_xor_sync(0xffffffffu, odd ? a1[j] : a1[j + 1], 1);
               f1 = odd ? make_float2(x1, a1[j + 1]) : make_float2(a1[j], x1);
             }
-            if (EPI == EPI_F32 || EPI == EPI_SWIGLU_F32) {
+            if (EPI == EPI_F32) {
               float* out = reinterpret_cast<float*>(p.out) + o;
               if (ok0 && there) *reinterpret_cast<float2*>(out + yp0) = f0;
               if (ok1 && there) *reinterpret_cast<float2*>(out + yp1) = f1;
@@ -629,7 +611,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
               const __nv_bfloat162 h0 = kTwo ? __floats2bfloat162_rn(high(f0.x), high(f0.y)) : __floats2bfloat162_rn(f0.x, f0.y);
               const __nv_bfloat162 h1 = kTwo ? __floats2bfloat162_rn(high(f1.x), high(f1.y)) : __floats2bfloat162_rn(f1.x, f1.y);
               if (ok0 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp0) = h0;
-              if (!kSwiglu && ok1 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp1) = h1;
+              if (EPI != EPI_SWIGLU && ok1 && there) *reinterpret_cast<__nv_bfloat162*>(out + yp1) = h1;
               if (kTwo) {  // what the rounding left
                 const float2 r0 = __bfloat1622float2(h0), r1 = __bfloat1622float2(h1);
                 out += p.lo_off;
@@ -650,7 +632,6 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     }
   } else if (FMT != FMT_BF16 && warp >= 4 + epilogue_warps(FMT)) {
     // ---------------------------------------------------------------- widening
-    // (int8: to fp16, exact; the scales of rows and columns multiply the sum)
     const int wt = tid - (128 + 32 * epilogue_warps(FMT));  // 0..kWidenThreads - 1
     // A thread has one row of one sub-tile, its warp's tensor-memory lane. Lanes with
     // neighbouring rows read one chunk each: the swizzle spreads them over all banks.
@@ -665,31 +646,29 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       const bool sh = tl.g >= p.groups_main;
       const int g = sh ? tl.g - p.groups_main : tl.g;
       const int y0 = tl.rb * sub_rows;
-      const int raw_first = FMT == FMT_INT8 ? k_first / 2 : 0, nraw = FMT == FMT_INT8 ? k_last / 2 : p.K / kmath(FMT);
+      const int nraw = p.K / kmath(FMT);
       constexpr int kParts = kmath(FMT) / 64;          // stages per raw slot
-      constexpr int kChunks = FMT == FMT_NVFP4 ? 2 : 4;  // 16-byte chunks of codes per row and stage
+      constexpr int kChunks = FMT == FMT_FP8 ? 4 : 2;  // 16-byte chunks of codes per row and stage
       constexpr int kOut = 32 / kChunks;               // columns made of one
       // The matrix row of this thread's sub-tile row (rows past the matrix hold zero
       // codes) and where its scales are. The scales of a slot are loaded while the
       // one before is widened.
-      const int y = min(y0 + (kSwiglu ? rr : row), p.R - 1);
-      const int yy = kSwiglu ? sub * p.R + y : y;
-      const int rows_all = kSwiglu ? 2 * p.R : p.R;
+      const int y = min(y0 + (EPI == EPI_SWIGLU ? rr : row), p.R - 1);
+      const int yy = EPI == EPI_SWIGLU ? sub * p.R + y : y;
+      const int rows_all = EPI == EPI_SWIGLU ? 2 * p.R : p.R;
       const float* sc8 = reinterpret_cast<const float*>(sh ? p.wscale_s : p.wscale) +
                          ((size_t)g * (rows_all / 128) + yy / 128) * (p.K / 128);
       const uint4* sc4 = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(sh ? p.wscale_s : p.wscale) +
                                                         ((size_t)g * rows_all + yy) * (p.K / 16));
       float next8 = 0.0f, ts = 1.0f;
       uint4 next4 = make_uint4(0, 0, 0, 0);
-      if (FMT == FMT_FP8) next8 = __ldg(sc8);
-      if (FMT == FMT_NVFP4) next4 = __ldg(sc4);
-      if (FMT == FMT_NVFP4 && ad_steps) ts = __ldg((sh ? p.gscale_s : p.gscale) + (kSwiglu ? 2 * g + sub : g));
-      for (int k = raw_first; ok && k < nraw; k++, rit.next(p.raw_slots)) {
+      if (FMT == FMT_FP8) next8 = __ldg(sc8); else next4 = __ldg(sc4);
+      if (FMT == FMT_NVFP4 && ad_steps) ts = __ldg((sh ? p.gscale_s : p.gscale) + (EPI == EPI_SWIGLU ? 2 * g + sub : g));
+      for (int k = 0; ok && k < nraw; k++, rit.next(p.raw_slots)) {
         const float f8 = next8;
         const uint32_t f4[4] = {next4.x, next4.y, next4.z, next4.w};
         if (k + 1 < nraw) {
-          if (FMT == FMT_FP8) next8 = __ldg(sc8 + k + 1);
-          if (FMT == FMT_NVFP4) next4 = __ldg(sc4 + k + 1);
+          if (FMT == FMT_FP8) next8 = __ldg(sc8 + k + 1); else next4 = __ldg(sc4 + k + 1);
         }
         const uint32_t rs = rit.slot;
         if (!(ok = warp_wait(rfull(rs), rit.parity, &s_abort))) break;
@@ -711,11 +690,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
 #pragma unroll
           for (int q = 0; q < kChunks; q++) {
             const uint32_t w[4] = {codes[q].x, codes[q].y, codes[q].z, codes[q].w};
-            if (FMT == FMT_INT8) {
-#pragma unroll
-              for (int j = 0; j < 4; j++)
-                int8x4_f16x4(w[j], o[(kOut * q + 2 * j) & 31], o[(kOut * q + 2 * j + 1) & 31]);
-            } else if (FMT == FMT_FP8) {
+            if (FMT == FMT_FP8) {
 #pragma unroll
               for (int j = 0; j < 4; j++)
                 fp8x4_bf16x4(w[j], f8, o[(kOut * q + 2 * j) & 31], o[(kOut * q + 2 * j + 1) & 31]);
@@ -746,7 +721,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       }
       // adapter steps: their weights come by TMA, loaded here; every widening thread arrives
       if (ok && ad_steps) {
-        const int y1 = kSwiglu ? y0 : y0 + p.rt, z1 = kSwiglu ? 1 : 0;
+        const int y1 = EPI == EPI_SWIGLU ? y0 : y0 + p.rt, z1 = EPI == EPI_SWIGLU ? 1 : 0;
         for (int a = adapter_next(p, adapter_of(p, tl.p0), tl.p0, tl.n); ok && a < p.num_adapters;
              a = adapter_next(p, a + 1, tl.p0, tl.n)) {
           for (int k = 0; k < per_adapter; k++, it.next(p.stages)) {
@@ -777,7 +752,7 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
     cluster_sync();
     if (p.pdl) pdl_wait();  // (addends may be of the launch before)
     const Tile tl = tile_at(p, min(t_first, ntiles - 1));
-    const int rows_out = kSwiglu ? p.rt : 2 * p.rt;
+    const int rows_out = EPI == EPI_SWIGLU ? p.rt : 2 * p.rt;
     const int cols = (tl.n - part_of + split - 1) / split;
     const float* s_ad = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + p.ad_off);
     for (int i = tid; i < cols * rows_out; i += threads_of(FMT)) {
@@ -788,22 +763,16 @@ __global__ void __launch_bounds__(threads_of(FMT), 1)
       float a0 = 0.0f, a1 = 0.0f;
       for (int k = 0; k < split; k++) {
         a0 += ld_cluster(base + at * 4u, k);
-        if (kSwiglu) a1 += ld_cluster(base + (at + p.rt) * 4u, k);
+        if (EPI == EPI_SWIGLU) a1 += ld_cluster(base + (at + p.rt) * 4u, k);
       }
       if (p.ad_mode == AD_EPILOGUE) {
         a0 += s_ad[at];
-        if (kSwiglu) a1 += s_ad[at + p.rt];
-      }
-      if (FMT == FMT_INT8) {
-        const float* ws = static_cast<const float*>(p.wscale);
-        const float rs = p.row_scale[tl.p0 + c];
-        a0 *= rs * __ldg(ws + y);
-        if (kSwiglu) a1 *= rs * __ldg(ws + p.R + y);
+        if (EPI == EPI_SWIGLU) a1 += s_ad[at + p.rt];
       }
       const size_t o = (size_t)(tl.p0 + c) * p.out_stride + y;
-      if (!kSwiglu && p.addend) a0 += __bfloat162float(p.addend[o]);
-      if (kSwiglu) a0 = EPI == EPI_SWIGLU_F32 ? silu_mul_f32(a0, a1) : silu_mul(a0, a1);
-      if (EPI == EPI_F32 || EPI == EPI_SWIGLU_F32) reinterpret_cast<float*>(p.out)[o] = a0;
+      if (EPI != EPI_SWIGLU && p.addend) a0 += __bfloat162float(p.addend[o]);
+      if (EPI == EPI_SWIGLU) a0 = silu_mul(a0, a1);
+      if (EPI == EPI_F32) reinterpret_cast<float*>(p.out)[o] = a0;
       else reinterpret_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(a0);
     }
     cluster_sync();  // no CTA leaves while another reads its sums

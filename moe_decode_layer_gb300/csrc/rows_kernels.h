@@ -40,19 +40,6 @@ cudaError_t launch_combine(const float* y, const int* pos, const float* w, const
 cudaError_t launch_shrink(const __nv_bfloat16* x, int64_t x_stride, const __nv_bfloat16* a, const float* scale,
                           const int* ids, float* u, int rows, int inner, int rank, int adapters, cudaStream_t s);
 
-// The grouped product with one int8 matrix, for any number of rows: x as fp16 copies of the codes. Set by the
-// caller: p.R, p.K, p.rows, p.out, p.addend, p.row_scale, p.wscale, p.status, p.status_keep, epi, weight, x16.
-struct RowsInt8 {
-  GemmParams p = {};
-  int epi = 0;
-  const void* weight = nullptr;  // [R, K], or [2, R, K] with swiglu
-  const void* x16 = nullptr;     // [rows, K]
-  CUtensorMap w, x;
-};
-struct Device;
-bool prepare_rows_int8(RowsInt8* r, const Device& d);  // descriptors and launch shape; nothing is launched
-cudaError_t launch_rows_int8(RowsInt8& r, const Device& d, bool pdl, cudaStream_t s);
-
 cudaError_t launch_route(const moe_route_config& c, const void* logits, int64_t stride, const float* bias,
                          int64_t rows, int32_t* idx, float* w, cudaStream_t s);
 

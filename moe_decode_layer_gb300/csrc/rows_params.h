@@ -21,17 +21,12 @@ constexpr int kMaxSms = 512;      // status words of a launch (two launches': th
 constexpr uint32_t kWaitLimit = 1u << 21;
 constexpr unsigned long long kDrainNs = 1000000ull;
 
-// Beside WFmt: 8-bit integers with a scale for each weight row (wscale) and for each row of x
-// (row_scale); x holds fp16 numbers then.
-constexpr int FMT_INT8 = 3;
-
 // What the epilogue makes of the accumulators.
 enum Epi {
   EPI_SWIGLU = 0,  // bf16 silu(gate) * up
   EPI_F32 = 1,     // fp32
   EPI_BF16 = 2,    // bf16
-  EPI_TWO = 3,     // the sum of two bf16 numbers, with a scale per group (bf16 weights)
-  EPI_SWIGLU_F32 = 4  // fp32 silu(gate) * up (int8)
+  EPI_TWO = 3      // the sum of two bf16 numbers, with a scale per group (bf16 weights)
 };
 
 // How the rows' adapters join the sum.
@@ -53,7 +48,7 @@ constexpr int threads_of(int fmt) {
   return 128 + 32 * epilogue_warps(fmt) + (fmt == FMT_BF16 ? 0 : kWidenThreads);
 }
 // k's in 128 bytes of codes
-constexpr int kmath(int fmt) { return fmt == FMT_NVFP4 ? 256 : 128; }
+constexpr int kmath(int fmt) { return fmt == FMT_FP8 ? 128 : 256; }
 
 // A tile of a launch with grouped rows: `n` rows of `group` from position p0 on, the
 // block-th of the group's `blocks` tiles. Block and count have a word each (a group of
@@ -76,12 +71,11 @@ struct GemmParams {
   int rt;           // weight rows per sub-tile (multiple of 8, <= 128)
   int nrb;          // tiles along R
   int groups_main;  // groups of map_w; later ones are map_s's
-  const void* wscale;    // FP8 / NVFP4 block scales; int8: fp32, one a row
+  const void* wscale;    // FP8 / NVFP4 block scales
   const void* wscale_s;
   const float* gscale;   // NVFP4 tensor scales; EPI_TWO: a scale per group
   const float* gscale_s;
   // rows of x (map_x)
-  const float* row_scale;  // int8: one a row of x
   const int* src_row;  // row at each sorted position (NULL: the position)
   int box_rows;        // without a list: rows of a copy (map_x's box)
   int all_rows;        // rows of each group from groups_main on, read through map_u; 0: as the others
@@ -118,7 +112,7 @@ struct GemmParams {
   int raw_off;
   int raw_slots;
   int pdl;
-  int split;  // CTAs of a cluster that share a tile's K (bf16 or int8 weights, uniform tiles, no AD_STEPS)
+  int split;  // CTAs of a cluster that share a tile's K (bf16 weights, uniform tiles, no AD_STEPS)
 };
 
 const void* gemm_kernel(int epi, int fmt);

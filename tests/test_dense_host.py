@@ -110,7 +110,7 @@ def _names(lib):
     found = []
     for i in range(lib.fake_launches()):
         name = lib.fake_name(i).decode()
-        found.append(next(n for n in ("quantise", "widen", "zero", "stream", "rows_gemm", "pair_gemm") if n + "_kernel" in name))
+        found.append(next(n for n in ("quantise", "widen", "zero", "stream", "pair_gemm") if n + "_kernel" in name))
     return found
 
 
@@ -118,12 +118,11 @@ def test_launches(lib):
     assert _quantise(lib) == OK and _names(lib) == ["quantise"]
     assert _project(lib) == OK and _names(lib) == ["stream"]
     assert _project(lib, x_dtype=0) == OK and _names(lib) == ["quantise", "stream"]
-    assert _project(lib, rows=100) == OK and _names(lib) == ["widen", "rows_gemm"]
-    assert _project(lib, rows=1000) == OK and _names(lib) == ["widen", "widen", "pair_gemm"]
-    assert _project(lib, rows=1000, x_dtype=1) == OK and _names(lib) == ["quantise", "widen", "pair_gemm"]
+    assert _project(lib, rows=100) == OK and _names(lib) == ["widen", "pair_gemm"]
+    assert _project(lib, rows=1000, x_dtype=1) == OK and _names(lib) == ["quantise", "pair_gemm"]
     assert _ff(lib) == OK and _names(lib) == ["stream"] * 2
     assert _ff(lib, rows=100) == OK and _names(lib) == ["pair_gemm"] * 2
-    assert _ff(lib, rows=1000, wdtype=3) == OK and _names(lib) == ["quantise", "widen", "pair_gemm"] * 2
+    assert _ff(lib, rows=1000, wdtype=3) == OK and _names(lib) == ["quantise", "pair_gemm"] * 2
     assert _backward(lib) == OK and _names(lib) == ["pair_gemm"] * 4
     assert _backward(lib, d13=None, d2=None) == OK and _names(lib) == ["pair_gemm"] * 2
     assert _backward(lib, rows=0) == OK and _names(lib) == ["zero"] * 2
@@ -189,7 +188,7 @@ def test_project_refuses(lib, rows):
     bad = [dict(w=None), dict(ws=None), dict(x=None), dict(xs=None), dict(out=None), dict(w=_at(W, 8)), dict(ws=_at(S, 8)), dict(x=_at(X, 8)), dict(xs=_at(S, 2)),
            dict(out=_at(OUT, 8)), dict(addend=_at(RES, 8)), dict(work=_at(WS, 8)), dict(stride=240), dict(stride=264), dict(addend=RES, swiglu=1), dict(out=X),
            dict(out=_at(X, 256)), dict(addend=_at(OUT, 256)), dict(addend=OUT, out_dtype=1), dict(xs=_at(OUT, 64))]
-    if rows > 8:
+    if rows > 32:
         bad += [dict(work=None), dict(short=1)]
     for kw in bad:
         assert _project(lib, rows=rows, **kw) == BAD and lib.fake_launches() == 0, kw
