@@ -96,10 +96,13 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   p.a_bytes = a_rows * 128;
   p.stage_bytes = p.a_bytes + b_bytes;
   p.step_bytes = (a_rows < 128 ? 1 : 2) * p.a_bytes + (codes ? 0 : 2 * b_bytes);
-  // Three boxes a warp leave four stages of 256 columns; with four warps there are five. Where a tile's
-  // product is long enough for its epilogue, that is faster.
-  p.ewarps = codes || (p.bufs == 3 && p.split == 1 && p.K >= kFewWarpsK) ? 4 : 8;
-  int room = d.smem - 2048 - p.ewarps * p.bufs * kStageBox;
+  // The boxes of eight warps leave four or five stages of 256 columns, those of four one more. Where a
+  // tile's product is long enough for its epilogue, that is faster (the round of a stage's barriers and
+  // copies takes about 2600 clocks).
+  p.ewarps = codes || (p.split == 1 && p.K >= kFewWarpsK) ? 4 : 8;
+  const int end = d.smem - 2048;
+  p.scale_off = end - 4096;
+  int room = end - p.ewarps * p.bufs * kStageBox - (codes ? 4096 : 0);
   p.raw_slots = 0;
   if (codes) {
     // the copies in flight are the slots of codes: four at least, and up to six stages
@@ -118,7 +121,7 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
                            : make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows, form == FORM_KK || codes ? p.bn / 2 : 64, 1, 0, false, codes);
   l.e = l.g = l.a;
   p.box_off = std::max(p.stages * p.stage_bytes + p.raw_slots * p.bn * 64, p.split > 1 ? p.bn * 512 : 0);
-  return ok_a && ok_b && p.stages >= 2 && (!codes || p.raw_slots >= 2) && p.box_off + p.ewarps * p.bufs * kStageBox <= d.smem - 2048;
+  return ok_a && ok_b && p.stages >= 2 && (!codes || p.raw_slots >= 2) && p.box_off + p.ewarps * p.bufs * kStageBox <= (codes ? p.scale_off : end);
 }
 
 // Results [M, N] of 2 bytes, or fp32 (as pairs of 2 bytes where nothing is added), and their addends.

@@ -429,9 +429,27 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   constexpr bool kThree = EPI == PAIR_SWIGLU || EPI == PAIR_DSWIGLU;  // three boxes at once, else two in turn
   const int nbox = cols / kBox;
   const bool asks = EPI == PAIR_DSWIGLU || (EPI == PAIR_BF16 && p.addend);  // a unit's inputs come by TMA
-  uint32_t asked = 0, units = 0;
+  uint32_t asked = 0, landed = 0, units = 0;
   auto there = [&](const PairTile& tl, int box, int q) {
     return tl.m0 + rank * 128 + q * 32 < p.M && tl.n0 + box * kBox < p.N;
+  };
+  // int8: the scales of this lane's row, and of a tile's columns, in shared memory (each warp's own): on their
+  // way while the sums are made. (Loaded where they are used, they took 8 us of a tile's epilogue.)
+  const uint32_t scales = base + p.scale_off + max(ew, 0) * 1024;
+  auto row_scale = [&](const PairTile& tl, int q) {
+    return kI8 ? p.row_scale[min(tl.m0 + rank * 128 + q * 32 + lane, p.M - 1)] : 1.0f;
+  };
+  auto column_scales = [&](const PairTile& tl) {
+    if constexpr (kI8) {
+      __syncwarp();
+#pragma unroll 4
+      for (int c = lane; c < p.bn; c += 32) {
+        const int half = kSwiglu && c >= p.bn / 2, n = tl.n0 + c - half * (p.bn / 2);  // (past N: the last one's, not used)
+        const float v = __ldg(p.col_scale + half * p.N + min(n, p.N - 1));
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + c * 4), "f"(v) : "memory");
+      }
+      __syncwarp();
+    }
   };
   // Asks for the next unit's inputs into its boxes, which the store before the last one has left.
   auto ask = [&](const PairTile& tl, int box, int q) {
@@ -452,21 +470,25 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   };
   // One box: 32 rows of the quadrant q. get(c, v): accumulator columns c .. c + 15 of this lane's row, there
   // after wait(v).
-  auto unit = [&](const PairTile& tl, int box, int q, auto get, auto wait) {
+  auto unit = [&](const PairTile& tl, int box, int q, float rs, auto get, auto wait) {
     const int row0 = tl.m0 + rank * 128 + q * 32, col0 = tl.n0 + box * kBox;
     const int row = min(row0 + lane, p.M - 1);
-    const float rs = p.row_scale ? p.row_scale[row] : 1.0f;
     const uint32_t n = units++, at = kThree ? boxes : boxes + (n & 1) * kStageBox;
-    // (columns past N are not stored; their scales are those of the last ones)
-    auto scaled = [&](uint32_t (&v)[16], int c, int half) {
-      if (!p.row_scale) return;
+    auto scaled = [&](uint32_t (&v)[16], int c) {  // accumulator columns c .. c + 15
+      if constexpr (kI8) {
 #pragma unroll
-      for (int j = 0; j < 16; j++)
-        v[j] = __float_as_uint(__uint_as_float(v[j]) * (rs * __ldg(p.col_scale + half * p.N + min(c + j, p.N - 1))));
+        for (int j = 0; j < 4; j++) {
+          const uint4 w = ld_shared4(scales + (c + 4 * j) * 4);
+          const uint32_t f[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; i++) v[4 * j + i] = __float_as_uint(__uint_as_float(v[4 * j + i]) * (rs * __uint_as_float(f[i])));
+        }
+      }
     };
     if (asks) {
       ok = ok && warp_wait(loads(ew, n & 1), (n >> 1) & 1, &s_abort);
       if (!ok) return;
+      landed++;
     } else {
       if (lane == 0) {
         if (kThree) store_wait_read<0>();
@@ -486,8 +508,8 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
         get(p.bn / 2 + box * kBox + h * 16, u);
         wait(v);
         wait(u);
-        scaled(v, c0, 0);
-        scaled(u, c0, 1);
+        scaled(v, box * kBox + h * 16);
+        scaled(u, p.bn / 2 + box * kBox + h * 16);
         if (EPI == PAIR_SWIGLU && p.keep) {
           box_bf16(at + kStageBox, lane, 2 * h, v);
           box_bf16(at + 2 * kStageBox, lane, 2 * h, u);
@@ -530,7 +552,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
       } else if (EPI == PAIR_SWIGLU) {
         box_bf16(at, lane, 2 * h, v);
       } else {
-        if (EPI != PAIR_SWIGLU_F32) scaled(v, c0, 0);
+        if (EPI != PAIR_SWIGLU_F32) scaled(v, box * kBox + h * 16);
         if (p.addend) {
 #pragma unroll
           for (int j = 0; j < 2; j++) {
@@ -579,7 +601,13 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
     for (int t = t_first; ok && t < ntiles; t += step, acc.next(2)) {
       const PairTile tl = pair_tile(p, t, cols);
       const int b = acc.slot;
+      column_scales(tl);
+      const float rs = row_scale(tl, q);
       const bool first = p.split == 1 && which < nbox && there(tl, which, q);
+      if (asks && p.split > 1 && ew < 4 / p.split * nbox) {  // the first box that this warp joins
+        const int mine = 4 / p.split, jq = part + p.split * (ew % mine), box = ew / mine;
+        if (there(tl, box, jq)) ask(tl, box, jq);
+      }
       if (asks && first) {
         ask(tl, which, q);
         if (EPI == PAIR_DSWIGLU && lane == 0)  // the others' on their way to L2
@@ -593,7 +621,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
         for (int box = which; box < nbox && there(tl, box, q); box += per_q) {
           const bool more = asks && box + per_q < nbox && there(tl, box + per_q, q);
           if (EPI == PAIR_BF16 && more) ask(tl, box + per_q, q);
-          unit(tl, box, q, [&](int c, uint32_t (&v)[16]) { tmem_ld16(d + c, v); }, [](uint32_t (&v)[16]) { tmem_wait16(v); });
+          unit(tl, box, q, rs, [&](int c, uint32_t (&v)[16]) { tmem_ld16(d + c, v); }, [](uint32_t (&v)[16]) { tmem_wait16(v); });
           if (EPI == PAIR_DSWIGLU && more) ask(tl, box + per_q, q);
         }
       } else {
@@ -652,11 +680,15 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
       for (int i = ew; i < mine * nbox; i += p.ewarps) {
         const int q = part + p.split * (i % mine), box = i / mine;
         if (!there(tl, box, q)) continue;
-        if (asks) ask(tl, box, q);
-        unit(tl, box, q, [&](int c, uint32_t (&v)[16]) { smem_ld16(base + (uint32_t)(c * 128 + q * 32 + lane) * 4u, v); }, [](uint32_t (&)[16]) {});
+        if (asks && i != ew) ask(tl, box, q);
+        unit(tl, box, q, row_scale(tl, q), [&](int c, uint32_t (&v)[16]) { smem_ld16(base + (uint32_t)(c * 128 + q * 32 + lane) * 4u, v); }, [](uint32_t (&)[16]) {});
       }
     }
   }
+  // (where a wait ended early, copies in flight land before the shared memory goes)
+  for (; landed != asked; landed++)
+    for (int i = 0; i < 1000 && !mbar_try_wait(loads(ew, landed & 1), (landed >> 1) & 1); i++) {
+      }
   if (warp >= 4 && lane == 0) store_wait_all();  // shared memory is read and the results are written
   __syncwarp();
   tc_fence_before();

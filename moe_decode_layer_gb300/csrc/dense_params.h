@@ -51,8 +51,9 @@ struct PairParams {
   int box_off;   // where they are: behind the stages, and behind a split tile's sums
   int ahead;     // steps of B that are fetched to L2 before their copies, or 0
   uint32_t idesc;
-  const float* row_scale;  // int8: a scale for each row and each column (gate columns first), or NULL
+  const float* row_scale;  // FORM_KK8: a scale for each row and each column (gate columns first)
   const float* col_scale;
+  int scale_off;           // the scales of a tile's columns, for each epilogue warp
   const __nv_bfloat16* addend;  // [M, N], or NULL
   int keep;      // SWIGLU: store gate and up; DSWIGLU: store h
   int reduce;    // F32: add to what is there
