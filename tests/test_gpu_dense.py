@@ -33,7 +33,8 @@ def _int8(g, rows, cols):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("rows,inner", [(1, 8), (2, 16), (7, 1016), (9, 1024), (8, 1032), (33, 2048), (5, 2056), (3, 8200), (2, 65536)])
+@pytest.mark.parametrize("rows,inner", [(1, 8), (2, 16), (7, 1016), (9, 1024), (8, 1032), (33, 2048), (5, 2056), (3, 8200), (2, 65536),
+                                        (512, 8), (600, 264), (513, 1032), (515, 2048), (520, 4096), (512, 4104)])
 def test_quantise(dtype, rows, inner):
     x = (_normal(_gen(rows + inner), rows, inner) * torch.exp(_normal(_gen(1), inner))).to(dtype)
     q, s = batch.quantise(x)
