@@ -44,7 +44,7 @@ struct Matrix {
 
 struct PairLaunch {
   PairParams p = {};
-  CUtensorMap a, b, d, e, g;
+  CUtensorMap a, b, d, e, g, d2;
   int form = 0, epi = 0;
 };
 
@@ -59,11 +59,13 @@ void shape_of(PairParams& p, bool swiglu, const Device& d) {
   const int pairs = d.sms / 2, ksteps = (p.K + 63) / 64;
   double least = 1e300;
   p.tiles_m = (int)cdiv(p.M, kTileM);
+  p.tiles_m2 = (int)cdiv(p.M2, kTileM);
   for (int bn : {256, 192, 128})
     for (int split : {1, 2, 4}) {
       if (swiglu && bn == 192) continue;
       const int tiles_n = (int)cdiv(p.N, swiglu ? bn / 2 : bn);
-      const int64_t tiles = (int64_t)p.tiles_m * tiles_n;
+      const int tiles_n2 = (int)cdiv(p.N2, bn);
+      const int64_t tiles = (int64_t)p.tiles_m * tiles_n + (int64_t)p.tiles_m2 * tiles_n2;
       if (split > 1 && (tiles > (split == 2 ? d.sms * 9 / 38 : d.sms / 10) || ksteps < 4 * split)) continue;
       const double waves = split > 1 ? 1 : (double)cdiv(tiles, pairs);
       const double ctas = 2.0 * std::min<double>((double)tiles * split, pairs);
@@ -76,11 +78,12 @@ void shape_of(PairParams& p, bool swiglu, const Device& d) {
         p.bn = bn;
         p.split = split;
         p.tiles_n = tiles_n;
+        p.tiles_n2 = tiles_n2;
       }
     }
 }
 
-constexpr int kFewWarpsK = 2048;
+constexpr int kFewWarpsK = 512;
 
 // Operands a and b, and results: map d at `out` (and e, g as the epilogue has them). Descriptors only.
 bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b, bool fp16, const Device& d) {
@@ -119,18 +122,28 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   const bool ok_a = make_map(&l.a, a.ptr, a.pitch, a.cols, a.rows, form == FORM_MM ? 64 : a_rows);
   const bool ok_b = swiglu ? make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows / 2, p.bn / 2, 2, b.pitch * (b.rows / 2), false, codes)
                            : make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows, form == FORM_KK || codes ? p.bn / 2 : 64, 1, 0, false, codes);
-  l.e = l.g = l.a;
+  l.e = l.g = l.d2 = l.a;
   p.box_off = std::max(p.stages * p.stage_bytes + p.raw_slots * p.bn * 64, p.split > 1 ? p.bn * 512 : 0);
   return ok_a && ok_b && p.stages >= 2 && (!codes || p.raw_slots >= 2) && p.box_off + p.ewarps * p.bufs * kStageBox <= (codes ? p.scale_off : end);
+}
+
+bool out_map(CUtensorMap* m, const void* out, int64_t M, int64_t N, bool f32, bool reduce) {
+  if (f32 && reduce) return make_map(m, out, N * 4, N, M, 32, 1, 0, true);
+  // an fp32 column counts as two
+  return make_map(m, out, N * (f32 ? 4 : 2), N * (f32 ? 2 : 1), M, 32);
+}
+
+// A second product of FORM_MM, which p.M2 and p.N2 have announced.
+bool prepare_second(PairLaunch& l, const Matrix& a, const Matrix& b, const void* out, bool f32) {
+  return make_map(&l.e, a.ptr, a.pitch, a.cols, a.rows, 64) && make_map(&l.g, b.ptr, b.pitch, b.cols, b.rows, 64) &&
+         out_map(&l.d2, out, l.p.M2, l.p.N2, f32, l.p.reduce);
 }
 
 // Results [M, N] of 2 bytes, or fp32 (as pairs of 2 bytes where nothing is added), and their addends.
 bool prepare_out(PairLaunch& l, const void* out, bool f32) {
   const PairParams& p = l.p;
   if (p.addend && l.epi == PAIR_BF16 && !make_map(&l.g, p.addend, (int64_t)p.N * 2, p.N, p.M, 32)) return false;
-  if (f32 && p.reduce) return make_map(&l.d, out, (int64_t)p.N * 4, p.N, p.M, 32, 1, 0, true);
-  // an fp32 column counts as two
-  return make_map(&l.d, out, (int64_t)p.N * (f32 ? 4 : 2), p.N * (f32 ? 2 : 1), p.M, 32);
+  return out_map(&l.d, out, p.M, p.N, f32, p.reduce);
 }
 
 cudaError_t launch(PairLaunch& l, const Device& d, bool pdl, cudaStream_t s) {
@@ -142,7 +155,7 @@ cudaError_t launch(PairLaunch& l, const Device& d, bool pdl, cudaStream_t s) {
     if (d.id < 64) ready[l.form][l.epi].fetch_or(1ull << d.id);
   }
   l.p.pdl = pdl;
-  const int64_t tiles = (int64_t)l.p.tiles_m * l.p.tiles_n;
+  const int64_t tiles = (int64_t)l.p.tiles_m * l.p.tiles_n + (int64_t)l.p.tiles_m2 * l.p.tiles_n2;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(2 * l.p.split * (l.p.split > 1 ? tiles : std::min<int64_t>(tiles, d.sms / 2))));
   c.blockDim = dim3(pair_threads(l.form));
@@ -158,7 +171,7 @@ cudaError_t launch(PairLaunch& l, const Device& d, bool pdl, cudaStream_t s) {
   a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
   c.attrs = a;
   c.numAttrs = 2;
-  void* args[] = {&l.p, &l.a, &l.b, &l.d, &l.e, &l.g};
+  void* args[] = {&l.p, &l.a, &l.b, &l.d, &l.e, &l.g, &l.d2};
   return cudaLaunchKernelExC(&c, k, args);
 }
 
@@ -527,9 +540,9 @@ moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* 
   void *both = ws + p.both, *h = ws + p.h;
   int* status = reinterpret_cast<int*>(ws + p.status);
 
-  // dh, and from it dg, du and h
-  PairLaunch one, up, down, inputs;
-  for (PairLaunch* l : {&one, &up, &down, &inputs}) {
+  // dh, and from it dg, du and h; the weights' gradients in one launch; dx
+  PairLaunch one, both_w, inputs;
+  for (PairLaunch* l : {&one, &both_w, &inputs}) {
     l->p.status = status;
     l->p.status_keep = l != &one;
     l->p.reduce = accumulate != 0;
@@ -541,19 +554,21 @@ moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* 
   bool ok = prepare(one, FORM_KM, PAIR_DSWIGLU, {grad, grad_stride * 2, rows, hid}, {wt->w2, in * 2, hid, in}, false, d) &&
             prepare_out(one, h, false) && make_map(&one.e, both, in * 4, in, rows, 32, 2, in * 2) &&
             make_map(&one.g, gate_up, in * 4, in, rows, 32, 2, in * 2);
+  const Matrix up_a = {both, in * 4, rows, 2 * in}, up_b = {x, x_stride * 2, rows, hid};
+  const Matrix down_a = {grad, grad_stride * 2, rows, hid}, down_b = {h, in * 2, rows, in};
+  const int epi = f32 ? PAIR_F32 : PAIR_BF16;
+  both_w.p.K = (int)rows;
   if (ok && dw13) {
-    up.p.M = 2 * c->inter;
-    up.p.N = c->hidden;
-    up.p.K = (int)rows;
-    ok = prepare(up, FORM_MM, f32 ? PAIR_F32 : PAIR_BF16, {both, in * 4, rows, 2 * in}, {x, x_stride * 2, rows, hid}, false, d) &&
-         prepare_out(up, dw13, f32);
-  }
-  if (ok && dw2) {
-    down.p.M = c->hidden;
-    down.p.N = c->inter;
-    down.p.K = (int)rows;
-    ok = prepare(down, FORM_MM, f32 ? PAIR_F32 : PAIR_BF16, {grad, grad_stride * 2, rows, hid}, {h, in * 2, rows, in}, false, d) &&
-         prepare_out(down, dw2, f32);
+    both_w.p.M = 2 * c->inter;
+    both_w.p.N = c->hidden;
+    both_w.p.M2 = dw2 ? c->hidden : 0;
+    both_w.p.N2 = dw2 ? c->inter : 0;
+    ok = prepare(both_w, FORM_MM, epi, up_a, up_b, false, d) && prepare_out(both_w, dw13, f32) &&
+         (!dw2 || prepare_second(both_w, down_a, down_b, dw2, f32));
+  } else if (ok && dw2) {
+    both_w.p.M = c->hidden;
+    both_w.p.N = c->inter;
+    ok = prepare(both_w, FORM_MM, epi, down_a, down_b, false, d) && prepare_out(both_w, dw2, f32);
   }
   if (ok && dx) {
     inputs.p.M = (int)rows;
@@ -564,8 +579,7 @@ moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* 
   }
   if (!ok) return MOE_ERR_CUDA;
   cudaError_t e = launch(one, d, false, s);
-  if (e == cudaSuccess && dw2) e = launch(down, d, true, s);
-  if (e == cudaSuccess && dw13) e = launch(up, d, true, s);
+  if (e == cudaSuccess && (dw13 || dw2)) e = launch(both_w, d, true, s);
   if (e == cudaSuccess && dx) e = launch(inputs, d, true, s);
   return cuda_status(e);
 }

@@ -185,20 +185,27 @@ __device__ __forceinline__ void box_f32(uint32_t box, int r, int first, const ui
 // ------------------------------------------------------------------ the kernel
 struct PairTile {
   int m0, n0;
+  bool second;  // of the second product
 };
 // Row tiles go round in groups of kGroupM, the columns outside: the pairs that run at one time
 // read about as much of A as of B, and most of it from L2.
+template <bool TWO>
 __device__ __forceinline__ PairTile pair_tile(const PairParams& p, int t, int cols) {
-  const int per = kGroupM * p.tiles_n, group = t / per;
-  const int gm = min(kGroupM, p.tiles_m - group * kGroupM), r = t - group * per;
-  return {(group * kGroupM + r % gm) * kTileM, r / gm * cols};
+  const int first = p.tiles_m * p.tiles_n;
+  const bool second = TWO && t >= first;
+  const int tiles_m = second ? p.tiles_m2 : p.tiles_m, tiles_n = second ? p.tiles_n2 : p.tiles_n;
+  if (second) t -= first;
+  const int per = kGroupM * tiles_n, group = t / per;
+  const int gm = min(kGroupM, tiles_m - group * kGroupM), r = t - group * per;
+  return {(group * kGroupM + r % gm) * kTileM, r / gm * cols, second};
 }
 
 template <int FORM, int EPI>
 __global__ void __launch_bounds__(pair_threads(FORM), 1)
     pair_gemm_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d,
-                     const __grid_constant__ CUtensorMap map_e, const __grid_constant__ CUtensorMap map_g) {
+                     const __grid_constant__ CUtensorMap map_e, const __grid_constant__ CUtensorMap map_g,
+                     const __grid_constant__ CUtensorMap map_d2) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
@@ -206,6 +213,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   __shared__ __align__(8) uint64_t s_bar[2 * kPairStages + 4 + 16 + 1 + 2 * kRawSlots];
   constexpr bool kI8 = FORM == FORM_KK8, kKK = FORM == FORM_KK || kI8;
   constexpr int kThreads = pair_threads(FORM);
+  constexpr bool kTwo = FORM == FORM_MM;  // (the second product's operands are map_e and map_g)
   constexpr bool kSwiglu = EPI == PAIR_SWIGLU || EPI == PAIR_SWIGLU_F32;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -262,7 +270,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   pdl_launch_dependents();
 
   const int cols = kSwiglu ? p.bn / 2 : p.bn;  // result columns of a tile
-  const int ntiles = p.tiles_m * p.tiles_n;
+  const int ntiles = p.tiles_m * p.tiles_n + (kTwo ? p.tiles_m2 * p.tiles_n2 : 0);
   const int step = gridDim.x / (2 * p.split);
   const int t_first = blockIdx.x / (2 * p.split);
   // (codes come 128 k at a time; what lies past K is zero)
@@ -287,9 +295,10 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
         }
       };
       for (int t = t_first; ok && t < ntiles; t += step) {
-        const PairTile tl = pair_tile(p, t, cols);
+        const PairTile tl = pair_tile<kTwo>(p, t, cols);
         const int m = tl.m0 + rank * 128;
         const int n = kSwiglu ? tl.n0 : tl.n0 + rank * b_rows, half = kSwiglu ? rank : 0;
+        const CUtensorMap *ma = kTwo && tl.second ? &map_e : &map_a, *mb = kTwo && tl.second ? &map_g : &map_b;
         if (!kI8)
           for (int k = k_first; k < min(k_first + p.ahead, k_last); k++) fetch_b(n, half, k);
         for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
@@ -301,16 +310,16 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
           // (the other CTA's bytes may be counted before this; the phase ends with the arrival)
           if (rank == 0) mbar_arrive_expect_tx(full(s), p.step_bytes);
           if (FORM == FORM_MM) {
-            tma_pair_3d(a, &map_a, m, k * 64, 0, bar);
-            tma_pair_3d(a + 8192, &map_a, m + 64, k * 64, 0, bar);
+            tma_pair_3d(a, ma, m, k * 64, 0, bar);
+            tma_pair_3d(a + 8192, ma, m + 64, k * 64, 0, bar);
           } else if (rank == 0 || p.a_bytes == 128 * 128) {  // (few rows are all the first CTA's)
             tma_pair_3d(a, &map_a, k * 64, m, 0, bar);
           }
           if (FORM == FORM_KK) {
             tma_pair_3d(b, &map_b, k * 64, n, half, bar);
           } else if (!kI8) {
-            tma_pair_3d(b, &map_b, n, k * 64, 0, bar);
-            if (b_rows > 64) tma_pair_3d(b + 8192, &map_b, n + 64, k * 64, 0, bar);
+            tma_pair_3d(b, mb, n, k * 64, 0, bar);
+            if (b_rows > 64) tma_pair_3d(b + 8192, mb, n + 64, k * 64, 0, bar);
           }
         }
       }
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
       Ring it;
       bool ok = true;
       for (int t = t_first; ok && t < ntiles; t += step) {
-        const PairTile tl = pair_tile(p, t, cols);
+        const PairTile tl = pair_tile<kTwo>(p, t, cols);
         const int n = kSwiglu ? tl.n0 : tl.n0 + rank * b_rows, half = kSwiglu ? rank : 0;
         for (int i = 0; i < p.ahead && k_first + 2 * i < k_last; i++) tma_prefetch_3d(&map_b, (k_first + 2 * i) * 64, n, half);
         for (int k = k_first; k < k_last; k += 2, it.next(p.raw_slots)) {
@@ -431,7 +440,8 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   const bool asks = EPI == PAIR_DSWIGLU || (EPI == PAIR_BF16 && p.addend);  // a unit's inputs come by TMA
   uint32_t asked = 0, landed = 0, units = 0;
   auto there = [&](const PairTile& tl, int box, int q) {
-    return tl.m0 + rank * 128 + q * 32 < p.M && tl.n0 + box * kBox < p.N;
+    const bool two = kTwo && tl.second;
+    return tl.m0 + rank * 128 + q * 32 < (two ? p.M2 : p.M) && tl.n0 + box * kBox < (two ? p.N2 : p.N);
   };
   // int8: the scales of this lane's row, and of a tile's columns, in shared memory (each warp's own): on their
   // way while the sums are made. (Loaded where they are used, they took 8 us of a tile's epilogue.)
@@ -584,10 +594,10 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
         tma_store_3d(&map_e, col0, row0, 0, at);
         tma_store_3d(&map_e, col0, row0, 1, at + kStageBox);
         if (p.keep) tma_store_3d(&map_d, col0, row0, 0, at + 2 * kStageBox);
-      } else if (EPI == PAIR_F32 && p.reduce) {
-        tma_add_3d(&map_d, col0, row0, 0, at);
       } else {
-        tma_store_3d(&map_d, kBox == 32 ? 2 * col0 : col0, row0, 0, at);  // (an fp32 column is two of 2 bytes)
+        const CUtensorMap* md = kTwo && tl.second ? &map_d2 : &map_d;
+        if (EPI == PAIR_F32 && p.reduce) tma_add_3d(md, col0, row0, 0, at);
+        else tma_store_3d(md, kBox == 32 ? 2 * col0 : col0, row0, 0, at);  // (an fp32 column is two of 2 bytes)
       }
       store_commit();
     }
@@ -599,7 +609,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     Ring acc;
     for (int t = t_first; ok && t < ntiles; t += step, acc.next(2)) {
-      const PairTile tl = pair_tile(p, t, cols);
+      const PairTile tl = pair_tile<kTwo>(p, t, cols);
       const int b = acc.slot;
       column_scales(tl);
       const float rs = row_scale(tl, q);
@@ -676,7 +686,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
     }
     __syncthreads();
     if (warp >= 4 && ew < p.ewarps) {
-      const PairTile tl = pair_tile(p, min(t_first, ntiles - 1), cols);
+      const PairTile tl = pair_tile<kTwo>(p, min(t_first, ntiles - 1), cols);
       for (int i = ew; i < mine * nbox; i += p.ewarps) {
         const int q = part + p.split * (i % mine), box = i / mine;
         if (!there(tl, box, q)) continue;

@@ -39,6 +39,7 @@ struct PairParams {
   int M, N, K;   // SWIGLU: N columns of h, 2 N rows of B
   int bn;        // accumulator columns of a tile, 256, 192 or 128 (SWIGLU: half gate, half up; not 192)
   int tiles_m, tiles_n;
+  int M2, N2, tiles_m2, tiles_n2;  // FORM_MM: a second product over the same K, behind the first's tiles (tiles_m2 0: none)
   int split;     // pairs of a cluster that share a tile's K
   int stages, stage_bytes;
   int raw_off, raw_slots;  // FORM_KK8: slots of 128 codes of each row of B

@@ -289,6 +289,23 @@ def test_backward_strides_places_and_parts(rows):
     assert none is None and torch.equal(d13, want[1]) and torch.equal(d2, want[2])
 
 
+@pytest.mark.parametrize("rows", [5, 300])
+def test_one_weight_gradient(rows):
+    """A call that asks for one matrix's gradient alone gives the bits of the whole one."""
+    g = _gen(rows)
+    w13, w2 = _block(g, 136, 72)
+    x, grad, kept = _bf16(g, rows, 136), _bf16(g, rows, 136), _bf16(g, rows, 144)
+    _, want13, want2 = batch.feed_forward_backward(grad, x, w13, w2, kept)
+    ws = torch.empty(batch.feed_forward_backward_workspace(136, 72, rows), dtype=torch.uint8, device="cuda")
+    weights = _lib.FfWeights(w13.data_ptr(), w2.data_ptr(), None, None)
+    for want, places in ((want13, lambda d: (None, d.data_ptr(), None)), (want2, lambda d: (None, None, d.data_ptr()))):
+        d = torch.full_like(want, 7.0)
+        assert _lib.load().moe_decode_ff_backward(
+            _lib.FfConfig(136, 72, 0), weights, grad.data_ptr(), 136, x.data_ptr(), 136, kept.data_ptr(), *places(d), 0, 0, rows,
+            ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream) == _lib.MOE_OK
+        assert torch.equal(d, want)
+
+
 def test_backward_without_rows():
     w13, w2 = _block(_gen(1), 64, 72)
     x, kept = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 144, dtype=torch.bfloat16, device="cuda")
