@@ -540,7 +540,7 @@ moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* 
   void *both = ws + p.both, *h = ws + p.h;
   int* status = reinterpret_cast<int*>(ws + p.status);
 
-  // dh, and from it dg, du and h; the weights' gradients in one launch; dx
+  // dh, and from it dg, du and h; dx; the weights' gradients in one launch
   PairLaunch one, both_w, inputs;
   for (PairLaunch* l : {&one, &both_w, &inputs}) {
     l->p.status = status;
@@ -579,8 +579,9 @@ moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* 
   }
   if (!ok) return MOE_ERR_CUDA;
   cudaError_t e = launch(one, d, false, s);
-  if (e == cudaSuccess && (dw13 || dw2)) e = launch(both_w, d, true, s);
+  // (dx first: what it reads of dg and du is still in L2)
   if (e == cudaSuccess && dx) e = launch(inputs, d, true, s);
+  if (e == cudaSuccess && (dw13 || dw2)) e = launch(both_w, d, true, s);
   return cuda_status(e);
 }
 
