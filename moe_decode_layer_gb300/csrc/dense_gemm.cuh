@@ -3,9 +3,9 @@
 //
 // Two CTAs of a cluster (a pair of SMs) work on one tile of 256 rows x bn columns with
 // cta_group::2 instructions: each holds 128 rows of A and half of B's columns in shared
-// memory, so that a step of 64 k moves 32 KB into each SM for 2.1 M multiplications -- half
-// of what two separate CTAs would move. Both accumulators (2 x 256 columns) fill tensor memory:
-// the epilogue of one tile runs beside the product of the next.
+// memory, so that a step of 64 k moves 32 KB into each SM for 2.1 M multiplications; a CTA by
+// itself would move 48 KB for a tile of 128 x 256. Both accumulators (2 x 256 columns) fill tensor
+// memory: the epilogue of one tile runs beside the product of the next.
 //
 // The gradients contract over rows of matrices that are stored by rows, so operands come in two
 // orders: k innermost (rows of x, weights of the forward pass) or the operand's own index
@@ -15,12 +15,25 @@
 // Few tiles: the pairs of a cluster (2 or 4) take parts of K of one tile, and their sums are
 // joined through distributed shared memory, in the order of the parts.
 //
-// int8 weights (FORM_KK8) come as codes: eight warps widen them into the stage, and the epilogue has four. (A pass that widens the whole matrix first costs its 3 bytes a weight: 36 us for
-// 67 million, as long as the product of 400 rows.)
+// int8 weights (FORM_KK8) come as codes: eight warps widen them into the stage, and the epilogue
+// has four. (A pass that widened the whole matrix first cost its 3 bytes a weight: 36 us for 67
+// million; 1024 rows, 4096 to 2 x 8192, 123 us with it and 91 us without.)
 //
-// Warps: 0 copies (both CTAs), 1 tensor core (the pair's first CTA), 4..11 epilogue. All
-// copies are TMA with the operands' 128-byte swizzle; results leave through shared memory by
-// TMA stores, which clip what lies past the matrix.
+// What bounds it: with many rows the tensor core. 8192 rows, 4096 x 8192: gate/up 549 us, dx 555
+// us for 1.1 TFLOP each, 2.0 PFLOP/s in short runs; in long ones the power limit (1.6 to 1.7). A step
+// takes 530 clocks where its products take 512. With narrower tiles a step's copies bound it: an
+// SM takes in about 64 bytes a clock from L2, so that a step of bn columns needs 256 + bn clocks
+// (and the ring, 5 or 6 stages, covers a copy's latency of 2600). dh's epilogue (three results for each
+// of its sums, and two inputs) runs beside the product at 1.57 PFLOP/s. With few rows the weights'
+// bytes: gate/up of 64 rows, 134 MB, streams at 6.4 TB/s for 21 us, and start, first copies,
+// epilogue and end take 5.
+// (A warp each for A's and B's copies was slower, 562 -> 634 us for dW13; so were stages of 128 k,
+// half as many, 264 -> 307 us for a backward pass of 1024 rows.)
+//
+// Warps: 0 copies (both CTAs), 1 tensor core (the pair's first CTA), 2 copies of codes, 4..11
+// epilogue (int8: 4..7, and 8..15 widen). All copies are TMA with the operands' 128-byte swizzle;
+// results leave through shared memory by TMA stores, which clip what lies past the matrix.
+// Every wait is bounded; who gives up sets a flag that the others look at, and the CTA's status word.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
