@@ -92,7 +92,7 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   l.form = form;
   l.epi = epi;
   shape_of(p, swiglu, d);
-  p.bufs = epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU ? 1 : 2;
+  p.bufs = epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU || codes ? 1 : 2;
   // (A copy takes the TMA unit about two clocks a row of 128 bytes, also of rows that it fills with zeros.)
   const int a_rows = form != FORM_MM && p.M <= 128 ? (int)up(p.M, 8) : 128;
   const int b_bytes = form == FORM_KK || codes ? p.bn * 64 : (int)cdiv(p.bn, 128) * 8192;
@@ -110,7 +110,7 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   if (codes) {
     // the copies in flight are the slots of codes: four at least, and up to six stages
     p.stages = std::min(6, (room - 4 * p.bn * 64) / p.stage_bytes);
-    p.raw_slots = std::min(kRawSlots, (room - p.stages * p.stage_bytes) / (p.bn * 64));
+    p.raw_slots = std::min(kRawSlots, (room - p.stages * p.stage_bytes) / (p.bn * 64)) & ~1;
     p.raw_off = p.stages * p.stage_bytes;
   } else {
     p.stages = std::min(kPairStages, room / p.stage_bytes);
@@ -124,7 +124,7 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
                            : make_map(&l.b, b.ptr, b.pitch, b.cols, b.rows, form == FORM_KK || codes ? p.bn / 2 : 64, 1, 0, false, codes);
   l.e = l.g = l.d2 = l.a;
   p.box_off = std::max(p.stages * p.stage_bytes + p.raw_slots * p.bn * 64, p.split > 1 ? p.bn * 512 : 0);
-  return ok_a && ok_b && p.stages >= 2 && (!codes || p.raw_slots >= 2) && p.box_off + p.ewarps * p.bufs * kStageBox <= (codes ? p.scale_off : end);
+  return ok_a && ok_b && p.stages >= 2 && (!codes || (p.raw_slots >= 2 && p.stages >= 3)) && p.box_off + p.ewarps * p.bufs * kStageBox <= (codes ? p.scale_off : end);
 }
 
 bool out_map(CUtensorMap* m, const void* out, int64_t M, int64_t N, bool f32, bool reduce) {

@@ -247,13 +247,13 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   if (tid == 0) {
     s_abort = 0;
     for (int s = 0; s < p.stages; s++) {
-      mbar_init(full(s), kI8 ? 1 + 8 : 1);  // copies; both CTAs' widening warps
+      mbar_init(full(s), kI8 ? 1 + 8 : 1);  // copies; four widening warps of each CTA
       mbar_init(empty(s), 1);
     }
     if (kI8)
       for (int s = 0; s < p.raw_slots; s++) {
         mbar_init(rfull(s), 1);
-        mbar_init(rempty(s), 8);
+        mbar_init(rempty(s), 4);
       }
     for (int b = 0; b < 2; b++) {
       mbar_init(tfull(b), 1);
@@ -369,41 +369,53 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
     // ---------------------------------------------------------------- widening
     // A thread has a row of this CTA's half of B: 64 codes a step become 128 bytes of fp16, exactly, where the
     // operand's swizzle has them; the scales multiply the sums.
-    // Four warps take the first 64 k of a slot, four the others: one thread's wait, loads, conversions, stores
-    // and fence take about 1000 clocks, twice the tensor core's for a step.
-    const int row = (warp & 3) * 32 + lane, h = (warp - 8) >> 2;
+    // Four warps take a slot, two steps, and four the next one: a slot's waits, loads, conversions, stores and
+    // fence take about 1300 clocks of a thread, the tensor core's two steps 1024. (An even number of slots: each
+    // slot is one group's, which so waits for its every use. Steps are released in order, and a group has waited
+    // for a later one than the stage's use before last: three stages at least.)
+    const int row = (warp & 3) * 32 + lane, group = (warp - 8) >> 2;
     const uint32_t bars = map_rank(bar0, first_cta);
     const bool mine = row < b_rows;
     Ring it, rit;
-    if (h) it.next(p.stages);
+    uint32_t turn = 0;
     bool ok = true;
     for (int t = t_first; ok && t < ntiles; t += step) {
       for (int k = k_first; ok && k < k_last; k += 2, rit.next(p.raw_slots)) {
+        if ((turn++ & 1) != group) {
+          it.next(p.stages);
+          it.next(p.stages);
+          continue;
+        }
         const uint32_t rs = rit.slot, raw = base + p.raw_off + rs * (b_rows * 128) + row * 128;
         if (!(ok = warp_wait(rfull(rs), rit.parity, &s_abort))) break;
-        const uint32_t s = it.slot, to = base + s * p.stage_bytes + p.a_bytes + row * 128;
-        uint32_t o[32];
+        uint32_t o[2][32];
         if (mine) {
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            const uint4 q = ld_shared4(raw + (((h * 4 + c) ^ (row & 7)) << 4));
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+          for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) int8x4_f16x4(w[j], o[8 * c + 2 * j], o[8 * c + 2 * j + 1]);
-          }
+            for (int c = 0; c < 4; c++) {
+              const uint4 q = ld_shared4(raw + (((h * 4 + c) ^ (row & 7)) << 4));
+              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int j = 0; j < 4; j++) int8x4_f16x4(w[j], o[h][8 * c + 2 * j], o[h][8 * c + 2 * j + 1]);
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(rempty(rs), 1);
-        if (!(ok = warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
-        if (mine) {
 #pragma unroll
-          for (int c = 0; c < 8; c++) st_shared4(to + ((c ^ (row & 7)) << 4), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        for (int h = 0; h < 2; h++) {
+          const uint32_t s = it.slot, to = base + s * p.stage_bytes + p.a_bytes + row * 128;
+          if (!(ok = ok && warp_wait(empty(s), it.parity ^ 1, &s_abort))) break;
+          if (mine) {
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+              st_shared4(to + ((c ^ (row & 7)) << 4), o[h][4 * c], o[h][4 * c + 1], o[h][4 * c + 2], o[h][4 * c + 3]);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(bars + 8u * s);
+          it.next(p.stages);
         }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(bars + 8u * s);
-        it.next(p.stages);
-        it.next(p.stages);
       }
     }
   } else if (warp == 1 && rank == 0) {
@@ -449,6 +461,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   // Columns of a box: a row of it is 128 bytes.
   constexpr int kBox = EPI == PAIR_F32 || EPI == PAIR_SWIGLU_F32 ? 32 : 64;
   constexpr bool kThree = EPI == PAIR_SWIGLU || EPI == PAIR_DSWIGLU;  // three boxes at once, else two in turn
+  constexpr bool kTurns = !kThree && !kI8;  // (int8: one box, and another stage)
   const int nbox = cols / kBox;
   const bool asks = EPI == PAIR_DSWIGLU || (EPI == PAIR_BF16 && p.addend);  // a unit's inputs come by TMA
   uint32_t asked = 0, landed = 0, units = 0;
@@ -486,7 +499,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
         tma_load_3d(boxes + kStageBox, &map_g, col, row, 1, bar);
       } else {
         mbar_arrive_expect_tx(bar, kStageBox);
-        tma_load_3d(boxes + (i & 1) * kStageBox, &map_g, col, row, 0, bar);
+        tma_load_3d(boxes + (kTurns ? i & 1 : 0) * kStageBox, &map_g, col, row, 0, bar);
       }
     }
     __syncwarp();
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   auto unit = [&](const PairTile& tl, int box, int q, float rs, auto get, auto wait) {
     const int row0 = tl.m0 + rank * 128 + q * 32, col0 = tl.n0 + box * kBox;
     const int row = min(row0 + lane, p.M - 1);
-    const uint32_t n = units++, at = kThree ? boxes : boxes + (n & 1) * kStageBox;
+    const uint32_t n = units++, at = kTurns ? boxes + (n & 1) * kStageBox : boxes;
     auto scaled = [&](uint32_t (&v)[16], int c) {  // accumulator columns c .. c + 15
       if constexpr (kI8) {
 #pragma unroll
@@ -514,8 +527,8 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
       landed++;
     } else {
       if (lane == 0) {
-        if (kThree) store_wait_read<0>();
-        else store_wait_read<1>();
+        if (kTurns) store_wait_read<1>();
+        else store_wait_read<0>();
       }
       __syncwarp();
     }
@@ -643,9 +656,9 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
       if (p.split == 1) {
         for (int box = which; box < nbox && there(tl, box, q); box += per_q) {
           const bool more = asks && box + per_q < nbox && there(tl, box + per_q, q);
-          if (EPI == PAIR_BF16 && more) ask(tl, box + per_q, q);
+          if (kTurns && more) ask(tl, box + per_q, q);
           unit(tl, box, q, rs, [&](int c, uint32_t (&v)[16]) { tmem_ld16(d + c, v); }, [](uint32_t (&v)[16]) { tmem_wait16(v); });
-          if (EPI == PAIR_DSWIGLU && more) ask(tl, box + per_q, q);
+          if (!kTurns && more) ask(tl, box + per_q, q);
         }
       } else {
         // the partial sums, [column][row], where the stages were: all are used
