@@ -70,6 +70,7 @@ struct StreamParams {
   const void* w;   // bf16 or int8 [R, K], SWIGLU: [2 R, K]
   const void* x;   // bf16 or int8 codes, row t at x + t * x_stride elements
   int64_t x_stride;
+  const __nv_bfloat16* x_lo;  // bf16: what x's rounding left, laid out as x, or NULL (not for more than kExactRows rows)
   int T, K, R;
   int swiglu;
   const float* x_scale;  // int8
@@ -77,10 +78,12 @@ struct StreamParams {
   const __nv_bfloat16* addend;
   void* out;
   int out_f32;
+  __nv_bfloat16* out_lo;  // bf16 results: what their rounding leaves, or NULL
   __nv_bfloat16* keep;   // SWIGLU: [T, 2 R], or NULL
   int* status;           // the workspace's status words, to be cleared, or NULL
 };
 constexpr int kStreamRows = 32;  // rows at most
+constexpr int kExactRows = 16;
 cudaError_t launch_stream(const StreamParams& p, bool int8, bool pdl, int sms, cudaStream_t s);
 
 // codes of rows, as int8 or (half) as fp16 numbers

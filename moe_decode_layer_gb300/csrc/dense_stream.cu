@@ -58,17 +58,18 @@ __device__ __forceinline__ void mma_bf16x(float (&c)[4], uint32_t a0, uint32_t a
 }
 
 constexpr int kWarps = 8;
-constexpr int pieces(int mt, int nt, int halves) { return (2 * mt + nt) * halves; }
+constexpr int pieces(int mt, int nt, int halves, bool lo) { return (2 * mt + (lo ? 2 : 1) * nt) * halves; }
 constexpr int sums_floats(int mt, int nt) { return kWarps * 8 * nt * (16 * mt + 4); }
-constexpr int stream_smem(int mt, int nt, int halves, int stages) {
-  return kWarps * stages * pieces(mt, nt, halves) * 512 + 2 * sums_floats(mt, nt) * 4;
+constexpr int stream_smem(int mt, int nt, int halves, int stages, bool lo) {
+  return kWarps * stages * pieces(mt, nt, halves, lo) * 512 + 2 * sums_floats(mt, nt) * 4;
 }
 
-// MT: 16-row blocks of weights, NT: 8-row blocks of x, HALVES: 64-byte pieces of a row in a stage.
-template <bool I8, int MT, int NT, int HALVES, int STAGES>
+// MT: 16-row blocks of weights, NT: 8-row blocks of x, HALVES: 64-byte pieces of a row in a stage, LO: x is
+// the sum of two bf16 numbers.
+template <bool I8, int MT, int NT, int HALVES, int STAGES, bool LO>
 __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams p) {
   extern __shared__ __align__(16) uint8_t s_raw[];
-  constexpr int kPieces = pieces(MT, NT, HALVES), kPitch = 16 * MT + 4, kChunk = 64 * HALVES;
+  constexpr int kPieces = pieces(MT, NT, HALVES, LO), kPitch = 16 * MT + 4, kChunk = 64 * HALVES;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, i = lane & 3;
   const int64_t row_bytes = (int64_t)p.K * (I8 ? 1 : 2);
@@ -103,6 +104,9 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
           const bool there = in && n * 8 + g < p.T;
           copy_rows(dst + (2 * MT * HALVES + h * NT + n) * 512,
                     static_cast<const uint8_t*>(p.x) + (there ? (int64_t)(n * 8 + g) * p.x_stride * (I8 ? 1 : 2) + at + h * 64 : 0), there);
+          if (LO)
+            copy_rows(dst + ((2 * MT + NT) * HALVES + h * NT + n) * 512,
+                      reinterpret_cast<const uint8_t*>(p.x_lo) + (there ? (int64_t)(n * 8 + g) * p.x_stride * 2 + at + h * 64 : 0), there);
         }
       }
     }
@@ -184,6 +188,17 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
               mma_bf16x(acc[m][n], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, x[n].x, x[n].y);
               mma_bf16x(acc[m][n], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, x[n].z, x[n].w);
             }
+          if (LO) {
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+              const uint4 l = ld_shared4(src + ((2 * MT + NT) * HALVES + h * NT + n) * 512);
+#pragma unroll
+              for (int m = 0; m < MT; m++) {
+                mma_bf16x(acc[m][n], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, l.x, l.y);
+                mma_bf16x(acc[m][n], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, l.z, l.w);
+              }
+            }
+          }
         }
       }
       if (ib < blocks) copy(ib, ic, is, true, true);
@@ -231,7 +246,13 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
       }
       if (p.addend) v += __bfloat162float(p.addend[o]);
       if (p.out_f32) static_cast<float*>(p.out)[o] = v;
-      else static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+      else if (p.out_lo) {
+        const __nv_bfloat16 hi = __float2bfloat16_rn(rows::high(v));
+        static_cast<__nv_bfloat16*>(p.out)[o] = hi;
+        p.out_lo[o] = __float2bfloat16_rn(rows::low(v, __bfloat162float(hi)));
+      } else {
+        static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+      }
     }
   }
   copies_wait<0>();
@@ -239,10 +260,10 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
     for (int j = tid; j < 2 * rows::kMaxSms; j += 32 * kWarps) p.status[j] = 0;
 }
 
-template <bool I8, int MT, int NT, int HALVES, int STAGES>
+template <bool I8, int MT, int NT, int HALVES, int STAGES, bool LO = false>
 cudaError_t launch(const StreamParams& p, int per_sm, bool pdl, int sms, cudaStream_t s) {
-  const void* f = reinterpret_cast<const void*>(&stream_kernel<I8, MT, NT, HALVES, STAGES>);
-  constexpr int smem = stream_smem(MT, NT, HALVES, STAGES);
+  const void* f = reinterpret_cast<const void*>(&stream_kernel<I8, MT, NT, HALVES, STAGES, LO>);
+  constexpr int smem = stream_smem(MT, NT, HALVES, STAGES, LO);
   static std::atomic<uint64_t> ready{0};  // devices whose limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -281,6 +302,9 @@ cudaError_t choose(const StreamParams& p, bool pdl, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_stream(const StreamParams& p, bool int8, bool pdl, int sms, cudaStream_t s) {
+  if (p.x_lo) {  // (bf16, at most kExactRows)
+    return p.T <= 8 ? launch<false, 1, 1, 1, 5, true>(p, 2, pdl, sms, s) : launch<false, 2, 2, 1, 4, true>(p, 1, pdl, sms, s);
+  }
   return int8 ? choose<true>(p, pdl, sms, s) : choose<false>(p, pdl, sms, s);
 }
 

@@ -110,15 +110,6 @@ __device__ __forceinline__ int adapter_next(const GemmParams& p, int a, int p0, 
   return p.num_adapters;
 }
 
-// A number as hi + lo, two bf16 numbers: hi = bf16(high(v)), lo = low(v, hi). A finite one
-// above bf16's largest gives that and the rest; an infinity or NaN is hi's alone, so that
-// the products' sum is what the number itself would make it, and not inf - inf.
-__device__ __forceinline__ float high(float v) {
-  constexpr float kMost = 0x1.fep+127f;  // bf16's largest
-  return fabsf(v) < INFINITY ? fminf(fmaxf(v, -kMost), kMost) : v;
-}
-__device__ __forceinline__ float low(float v, float hi) { return fabsf(v) < INFINITY ? v - hi : 0.0f; }
-
 // Widening of quantised codes to the bf16 operand.
 // FP8: w = bf16(e4m3 * block scale): one rounding of the product (at most 2^-8 of it,
 // 1/16 of the codes' own rounding); the tensor core takes bf16 operands with the bf16

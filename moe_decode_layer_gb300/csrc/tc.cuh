@@ -158,6 +158,15 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(
 // after another, took 20 us of a tile's epilogue.
 __device__ __forceinline__ float silu_mul_f32(float g, float u) { return __fdividef(g, 1.0f + expf(-g)) * u; }
 
+// A number as hi + lo, two bf16 numbers: hi = bf16(high(v)), lo = low(v, hi). A finite one
+// above bf16's largest gives that and the rest; an infinity or NaN is hi's alone, so that
+// the products' sum is what the number itself would make it, and not inf - inf.
+__device__ __forceinline__ float high(float v) {
+  constexpr float kMost = 0x1.fep+127f;  // bf16's largest
+  return fabsf(v) < INFINITY ? fminf(fmaxf(v, -kMost), kMost) : v;
+}
+__device__ __forceinline__ float low(float v, float hi) { return fabsf(v) < INFINITY ? v - hi : 0.0f; }
+
 // Four int8 -> four fp16, exact: the byte v + 128 under the exponent of 1024 is 1152 + v.
 __device__ __forceinline__ uint32_t sub_1152(uint32_t v) {
   const __half2 k = __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
