@@ -120,7 +120,9 @@ moe_status moe_decode_ff(const moe_ff_config* cfg, const moe_ff_weights* weights
  * The block's backward pass (MOE_W_BF16), from grad = d loss / d out and the kept gate_up:
  *   dh = W2^T grad,  dg = dh * u * silu'(g),  du = dh * silu(g),  h = silu(g) * u
  *   dx = W13^T [dg; du],  dW13 = sum_t [dg; du]_t x_t^T,  dW2 = sum_t grad_t h_t^T
- * with fp32 sums; dg, du and h are rounded to bf16 (operands of the tensor cores), dx to bf16. The
+ * with fp32 sums; dg, du and h are rounded to bf16 (operands of the tensor cores; of few rows of
+ * a narrow block, up to 4096 values, they are the sums of two bf16 numbers, of which the second
+ * makes NaN of an infinity that it meets in grad, x or a weight), dx to bf16. The
  * residual's gradient is grad itself. dx, dw13 and dw2 may be NULL: what is not wanted is not
  * computed. dw_dtype is the weight gradients' type; with MOE_F32 and accumulate they are added
  * to what dw13 and dw2 hold (gradients of several batches). With rows 0 dw13 and dw2 become zero

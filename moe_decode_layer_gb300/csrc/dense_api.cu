@@ -42,8 +42,14 @@ struct Matrix {
   int64_t rows, cols;
 };
 
-struct PairLaunch {
+PairParams one_pass() {
   PairParams p = {};
+  p.passes = 1;
+  return p;
+}
+
+struct PairLaunch {
+  PairParams p = one_pass();
   CUtensorMap a, b, d, e, g, d2;
   int form = 0, epi = 0;
 };
@@ -56,7 +62,7 @@ struct PairLaunch {
 // are resident at once (a 16th of eight waited for another's end: 34 us for a product of 256 rows
 // that takes 12).
 void shape_of(PairParams& p, bool swiglu, const Device& d) {
-  const int pairs = d.sms / 2, ksteps = (p.K + 63) / 64;
+  const int pairs = d.sms / 2, ksteps = (p.K + 63) / 64 * p.passes;
   double least = 1e300;
   p.tiles_m = (int)cdiv(p.M, kTileM);
   p.tiles_m2 = (int)cdiv(p.M2, kTileM);
@@ -92,7 +98,7 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   l.form = form;
   l.epi = epi;
   shape_of(p, swiglu, d);
-  p.bufs = epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU || codes ? 1 : 2;
+  p.bufs = epi == PAIR_DSWIGLU && p.lo ? 6 : epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU || codes ? 1 : 2;
   // (A copy takes the TMA unit about two clocks a row of 128 bytes, also of rows that it fills with zeros.)
   const int a_rows = form != FORM_MM && p.M <= 128 ? (int)up(p.M, 8) : 128;
   const int b_bytes = form == FORM_KK || codes ? p.bn * 64 : (int)cdiv(p.bn, 128) * 8192;
@@ -102,7 +108,7 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   // The boxes of eight warps leave four or five stages of 256 columns, those of four one more. Where a
   // tile's product is long enough for its epilogue, that is faster (the round of a stage's barriers and
   // copies takes about 2600 clocks).
-  p.ewarps = codes || (p.split == 1 && p.K >= kFewWarpsK) ? 4 : 8;
+  p.ewarps = codes || p.bufs == 6 || (p.split == 1 && p.K >= kFewWarpsK) ? 4 : 8;
   const int end = d.smem - 2048;
   p.scale_off = end - 4096;
   int room = end - p.ewarps * p.bufs * kStageBox - (codes ? 4096 : 0);
@@ -322,12 +328,21 @@ FfPlan ff_plan(const moe_ff_config& c, int64_t rows) {
 struct BackwardPlan {
   size_t status, both, h, bytes;
 };
+// A few rows of a narrow block: dg, du and h as two bf16 numbers each, side by side in a row. The roundings of so few
+// values do not even out (a gradient's error was up to 1.9 times its own rounding, where that of many is 1.41). dx's
+// product is then twice as long and the weight gradients have a step more: one row, 1024 x 2048, 38 us and 32 without.
+constexpr int64_t kExactValues = 4096;
+int64_t exact_backward_rows(const moe_ff_config& c) {
+  return (int64_t)c.hidden * c.inter * 4 <= kStreamBytes ? kExactValues / std::min(c.hidden, c.inter) : 0;
+}
+bool exact_backward(int64_t rows, const moe_ff_config& c) { return rows <= exact_backward_rows(c); }
 BackwardPlan backward_plan(const moe_ff_config& c, int64_t rows) {
   Places pl;
   BackwardPlan p = {};
+  const size_t each = exact_backward(rows, c) ? 2 : 1;
   p.status = pl.take(kStatusBytes);
-  p.both = pl.take((size_t)rows * c.inter * 4);
-  p.h = pl.take((size_t)rows * c.inter * 2);
+  p.both = pl.take((size_t)rows * c.inter * 4 * each);
+  p.h = pl.take((size_t)rows * c.inter * 2 * each);
   p.bytes = pl.at;
   return p;
 }
@@ -509,7 +524,9 @@ moe_status moe_decode_ff_backward_workspace(const moe_ff_config* c, int64_t rows
   if (st != MOE_OK) return st;
   if (c->wdtype != MOE_W_BF16) return MOE_ERR_UNSUPPORTED;
   if (!bytes || rows < 0 || rows > kMaxRows) return MOE_ERR_INVALID_ARG;
-  *bytes = rows ? backward_plan(*c, rows).bytes : 0;
+  *bytes = 0;  // (fewer rows may need more)
+  for (int64_t r : {rows, std::min(rows, exact_backward_rows(*c))})
+    if (r) *bytes = std::max(*bytes, backward_plan(*c, r).bytes);
   return MOE_OK;
 }
 
@@ -565,30 +582,35 @@ moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* 
   one.p.N = c->inter;
   one.p.K = c->hidden;
   one.p.keep = dw2 != nullptr;
+  const int each = exact_backward(rows, *c) ? 2 : 1;  // numbers that each of dg, du and h is the sum of
+  one.p.lo = each == 2;
   bool ok = prepare(one, FORM_KM, PAIR_DSWIGLU, {grad, grad_stride * 2, rows, hid}, {wt->w2, in * 2, hid, in}, false, d) &&
-            prepare_out(one, h, false) && make_map(&one.e, both, in * 4, in, rows, 32, 2, in * 2) &&
+            make_map(&one.d, h, in * 2 * each, in, rows, 32, each, in * 2) &&
+            make_map(&one.e, both, in * 4 * each, in, rows, 32, 2 * each, in * 2) &&
             make_map(&one.g, gate_up, in * 4, in, rows, 32, 2, in * 2);
-  const Matrix up_a = {both, in * 4, rows, 2 * in}, up_b = {x, x_stride * 2, rows, hid};
-  const Matrix down_a = {grad, grad_stride * 2, rows, hid}, down_b = {h, in * 2, rows, in};
+  const Matrix up_a = {both, in * 4 * each, rows, 2 * in * each}, up_b = {x, x_stride * 2, rows, hid};
+  const Matrix down_a = {grad, grad_stride * 2, rows, hid}, down_b = {h, in * 2 * each, rows, in * each};
   const int epi = f32 ? PAIR_F32 : PAIR_BF16;
   both_w.p.K = (int)rows;
+  both_w.p.passes = inputs.p.passes = each;
   if (ok && dw13) {
-    both_w.p.M = 2 * c->inter;
+    both_w.p.M = both_w.p.pass_a = 2 * c->inter;
     both_w.p.N = c->hidden;
+    both_w.p.pass_b2 = c->inter;
     both_w.p.M2 = dw2 ? c->hidden : 0;
     both_w.p.N2 = dw2 ? c->inter : 0;
     ok = prepare(both_w, FORM_MM, epi, up_a, up_b, false, d) && prepare_out(both_w, dw13, f32) &&
          (!dw2 || prepare_second(both_w, down_a, down_b, dw2, f32));
   } else if (ok && dw2) {
     both_w.p.M = c->hidden;
-    both_w.p.N = c->inter;
+    both_w.p.N = both_w.p.pass_b = c->inter;
     ok = prepare(both_w, FORM_MM, epi, down_a, down_b, false, d) && prepare_out(both_w, dw2, f32);
   }
   if (ok && dx) {
     inputs.p.M = (int)rows;
     inputs.p.N = c->hidden;
-    inputs.p.K = 2 * c->inter;
-    ok = prepare(inputs, FORM_KM, PAIR_BF16, {both, in * 4, rows, 2 * in}, {wt->w13, hid * 2, 2 * in, hid}, false, d) &&
+    inputs.p.K = inputs.p.pass_a = 2 * c->inter;
+    ok = prepare(inputs, FORM_KM, PAIR_BF16, up_a, {wt->w13, hid * 2, 2 * in, hid}, false, d) &&
          prepare_out(inputs, dx, false);
   }
   if (!ok) return MOE_ERR_CUDA;

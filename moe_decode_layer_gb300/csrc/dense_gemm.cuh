@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   const int t_first = blockIdx.x / (2 * p.split);
   // (codes come 128 k at a time; what lies past K is zero)
   constexpr int kCut = kI8 ? 2 : 1;
-  const int ksteps = (p.K + 64 * kCut - 1) / (64 * kCut);
+  constexpr bool kPasses = FORM == FORM_KM || FORM == FORM_MM;
+  const int once = (p.K + 64 * kCut - 1) / (64 * kCut), ksteps = kPasses ? once * p.passes : once;
   const int k_first = ksteps * part / p.split * kCut, k_last = ksteps * (part + 1) / p.split * kCut;
   const int b_rows = p.bn / 2;  // of B in this CTA
 
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
       auto fetch_b = [&](int n, int half, int k) {
         if (kKK) {
           tma_prefetch_3d(&map_b, k * 64, n, half);
-        } else {
+        } else if (k < once) {
           tma_prefetch_3d(&map_b, n, k * 64, 0);
           if (b_rows > 64) tma_prefetch_3d(&map_b, n + 64, k * 64, 0);
         }
@@ -322,17 +323,20 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
           if (!kI8 && p.ahead && k + p.ahead < k_last) fetch_b(n, half, k + p.ahead);
           // (the other CTA's bytes may be counted before this; the phase ends with the arrival)
           if (rank == 0) mbar_arrive_expect_tx(full(s), p.step_bytes);
+          const bool again = kPasses && k >= once;
+          const int kx = (again ? k - once : k) * 64;
+          const int oa = !again ? 0 : kTwo && tl.second ? p.pass_a2 : p.pass_a, ob = !again ? 0 : kTwo && tl.second ? p.pass_b2 : p.pass_b;
           if (FORM == FORM_MM) {
-            tma_pair_3d(a, ma, m, k * 64, 0, bar);
-            tma_pair_3d(a + 8192, ma, m + 64, k * 64, 0, bar);
+            tma_pair_3d(a, ma, m + oa, kx, 0, bar);
+            tma_pair_3d(a + 8192, ma, m + oa + 64, kx, 0, bar);
           } else if (rank == 0 || p.a_bytes == 128 * 128) {  // (few rows are all the first CTA's)
-            tma_pair_3d(a, &map_a, k * 64, m, 0, bar);
+            tma_pair_3d(a, &map_a, kx + oa, m, 0, bar);
           }
           if (FORM == FORM_KK) {
-            tma_pair_3d(b, &map_b, k * 64, n, half, bar);
+            tma_pair_3d(b, &map_b, kx, n, half, bar);
           } else if (!kI8) {
-            tma_pair_3d(b, mb, n, k * 64, 0, bar);
-            if (b_rows > 64) tma_pair_3d(b + 8192, mb, n + 64, k * 64, 0, bar);
+            tma_pair_3d(b, mb, n + ob, kx, 0, bar);
+            if (b_rows > 64) tma_pair_3d(b + 8192, mb, n + ob + 64, kx, 0, bar);
           }
         }
       }
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
           const uint32_t ag = box_at(at, lane, 2 * h + c), au = ag + kStageBox;
           const uint4 g4 = ld_shared4(ag), u4 = ld_shared4(au);
           const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
-          uint32_t dg[4], du[4], hh[4];
+          uint32_t dg[4], du[4], hh[4], l[3][4];
 #pragma unroll
           for (int j = 0; j < 4; j++) {
             float a[2], b[2], w[2];
@@ -577,13 +581,25 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
               b[e] = dh * s;
               a[e] = dh * u * (sig + s * (1.0f - sig));
             }
-            dg[j] = pack_bf16(a[0], a[1]);
-            du[j] = pack_bf16(b[0], b[1]);
-            hh[j] = pack_bf16(w[0], w[1]);
+            if (p.lo) {
+              dg[j] = pack_bf16(high(a[0]), high(a[1]));
+              du[j] = pack_bf16(high(b[0]), high(b[1]));
+              hh[j] = pack_bf16(high(w[0]), high(w[1]));
+              l[0][j] = pack_bf16(low(a[0], bf16lo(dg[j])), low(a[1], bf16hi(dg[j])));
+              l[1][j] = pack_bf16(low(b[0], bf16lo(du[j])), low(b[1], bf16hi(du[j])));
+              l[2][j] = pack_bf16(low(w[0], bf16lo(hh[j])), low(w[1], bf16hi(hh[j])));
+            } else {
+              dg[j] = pack_bf16(a[0], a[1]);
+              du[j] = pack_bf16(b[0], b[1]);
+              hh[j] = pack_bf16(w[0], w[1]);
+            }
           }
           st_shared4(ag, dg[0], dg[1], dg[2], dg[3]);
           st_shared4(au, du[0], du[1], du[2], du[3]);
           st_shared4(ag + 2 * kStageBox, hh[0], hh[1], hh[2], hh[3]);
+          if (p.lo)
+#pragma unroll
+            for (int i = 0; i < 3; i++) st_shared4(ag + (3 + i) * kStageBox, l[i][0], l[i][1], l[i][2], l[i][3]);
         }
       } else if (EPI == PAIR_SWIGLU) {
         box_bf16(at, lane, 2 * h, v);
@@ -620,6 +636,11 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
         tma_store_3d(&map_e, col0, row0, 0, at);
         tma_store_3d(&map_e, col0, row0, 1, at + kStageBox);
         if (p.keep) tma_store_3d(&map_d, col0, row0, 0, at + 2 * kStageBox);
+        if (p.lo) {
+          tma_store_3d(&map_e, col0, row0, 2, at + 3 * kStageBox);
+          tma_store_3d(&map_e, col0, row0, 3, at + 4 * kStageBox);
+          if (p.keep) tma_store_3d(&map_d, col0, row0, 1, at + 5 * kStageBox);
+        }
       } else {
         const CUtensorMap* md = kTwo && tl.second ? &map_d2 : &map_d;
         if (EPI == PAIR_F32 && p.reduce) tma_add_3d(md, col0, row0, 0, at);

@@ -56,6 +56,10 @@ struct PairParams {
   const float* col_scale;
   int scale_off;           // the scales of a tile's columns, for each epilogue warp
   const __nv_bfloat16* addend;  // [M, N], or NULL
+  // An operand that is the sum of two bf16 numbers: K is gone through twice (passes 2), the second time this many
+  // columns further on in A and in B (and in the second product's).
+  int passes, pass_a, pass_b, pass_a2, pass_b2;
+  int lo;        // DSWIGLU: results are two bf16 numbers each, the second ones in maps e's and d's later halves
   int keep;      // SWIGLU: store gate and up; DSWIGLU: store h
   int reduce;    // F32: add to what is there
   int pdl;

@@ -74,8 +74,9 @@ def block_int8(x, w13, s13, w2, s2, residual=None):
     return y, bound + BF16 * (y.abs() + bound)
 
 
-def gradients(grad, x, w13, w2, gate_up, bf16_weights=True):
-    """((dx, bound), (dw13, bound), (dw2, bound)); the bounds count dg, du and h rounded to bf16."""
+def gradients(grad, x, w13, w2, gate_up, bf16_weights=True, operand=BF16):
+    """((dx, bound), (dw13, bound), (dw2, bound)); the bounds count dg, du and h rounded by `operand` (two bf16
+    numbers: BF16 of what BF16 leaves)."""
     grad, x, w13, w2 = grad.double(), x.double(), w13.double(), w2.double()
     g, u = gate_up.double().chunk(2, 1)
     dh, e = grad @ w2, grad.shape[1] * FP32 * (grad.abs() @ w2.abs())
@@ -89,7 +90,7 @@ def gradients(grad, x, w13, w2, gate_up, bf16_weights=True):
     eu = (dh.abs() * (r + 2 * FP32) + e * (1 + r)) * s.abs()
     eh = (r + 2 * FP32) * h.abs()
     both, eb = torch.cat((dg, du), 1), torch.cat((eg, eu), 1)
-    eb, eh = eb + BF16 * (both.abs() + eb), eh + BF16 * (h.abs() + eh)
+    eb, eh = eb + operand * (both.abs() + eb), eh + operand * (h.abs() + eh)
     last = BF16 if bf16_weights else FP32
 
     def product(a, ea, b, n, rounding):

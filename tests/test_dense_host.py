@@ -66,7 +66,7 @@ def test_workspaces_grow_with_rows():
     rows = [*range(0, 40), *range(40, 1200, 13), 5000, 100000]
     for f in (lambda t: batch.feed_forward_workspace(264, 136, t), lambda t: batch.feed_forward_workspace(4096, 8192, t),
               lambda t: batch.feed_forward_workspace(272, 144, t, wdtype="int8"), lambda t: batch.feed_forward_workspace(4096, 8192, t, wdtype="int8"),
-              lambda t: batch.feed_forward_backward_workspace(264, 136, t), lambda t: batch.project_int8_workspace(272, 136, t),
+              lambda t: batch.feed_forward_backward_workspace(264, 136, t), lambda t: batch.feed_forward_backward_workspace(8, 72, t), lambda t: batch.project_int8_workspace(272, 136, t),
               lambda t: batch.project_int8_workspace(8192, 8192, t), lambda t: batch.project_int8_workspace(272, 136, t, x_dtype=torch.float32)):
         sizes = [f(t) for t in rows]
         assert sizes[0] == 0 and sizes == sorted(sizes)

@@ -242,6 +242,24 @@ def test_backward(rows, hidden, inter):
     assert batch.status(ws) == _lib.MOE_OK
 
 
+@pytest.mark.parametrize("rows,hidden,inter", [(1, 64, 8), (3, 1032, 136), (7, 264, 136), (15, 64, 2056), (17, 8, 72), (200, 8, 264), (512, 8, 8)])
+def test_backward_of_few_rows_keeps_two_numbers(rows, hidden, inter):
+    """dg, du and h as two bf16 numbers each: the gradients' errors are those of rounding by 2^-16 and of fp32 sums
+    of twice the products."""
+    g = _gen(rows)
+    w13, w2 = _block(g, hidden, inter)
+    x, grad, kept = _bf16(g, rows, hidden), _bf16(g, rows, hidden), _bf16(g, rows, 2 * inter)
+    d13, d2 = torch.empty(2 * inter, hidden, device="cuda"), torch.empty(hidden, inter, device="cuda")
+    dx, _, _ = batch.feed_forward_backward(grad, x, w13, w2, kept, dw13=d13, dw2=d2)
+    want = ref.gradients(grad, x, w13, w2, kept, bf16_weights=False, operand=ref.BF16 ** 2 + 2 * max(rows, 2 * inter) * ref.FP32)
+    assert all(ref.within(d, *w) for d, w in zip((dx, d13, d2), want))
+    # an infinite dh stays one (no inf - inf in its second number); an infinite grad meets h's second number, of either sign
+    grad[0], grad[0, 0] = 0, float("inf")
+    w2[0], kept[0], x[0] = w2[0].abs() + 0.125, kept[0].abs() + 0.125, x[0].abs() + 0.125
+    batch.feed_forward_backward(grad, x, w13, w2, kept, dw13=d13, dw2=d2)
+    assert bool((d13 == float("inf")).all()) and bool(torch.isfinite(d2[1:]).all()) and not bool(torch.isfinite(d2[0]).any())
+
+
 def test_gradients_against_differences():
     """The loss along random directions of x, W13 and W2, in 64 bits, against the gradients' products with them."""
     g = _gen(5)
