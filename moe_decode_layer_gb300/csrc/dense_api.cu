@@ -98,7 +98,7 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   l.form = form;
   l.epi = epi;
   shape_of(p, swiglu, d);
-  p.bufs = epi == PAIR_DSWIGLU && p.lo ? 6 : epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU || codes ? 1 : 2;
+  p.bufs = epi == PAIR_DSWIGLU_LO ? 6 : epi == PAIR_DSWIGLU || (epi == PAIR_SWIGLU && p.keep) ? 3 : epi == PAIR_SWIGLU || codes ? 1 : 2;
   // (A copy takes the TMA unit about two clocks a row of 128 bytes, also of rows that it fills with zeros.)
   const int a_rows = form != FORM_MM && p.M <= 128 ? (int)up(p.M, 8) : 128;
   const int b_bytes = form == FORM_KK || codes ? p.bn * 64 : (int)cdiv(p.bn, 128) * 8192;
@@ -108,7 +108,7 @@ bool prepare(PairLaunch& l, int form, int epi, const Matrix& a, const Matrix& b,
   // The boxes of eight warps leave four or five stages of 256 columns, those of four one more. Where a
   // tile's product is long enough for its epilogue, that is faster (the round of a stage's barriers and
   // copies takes about 2600 clocks).
-  p.ewarps = codes || p.bufs == 6 || (p.split == 1 && p.K >= kFewWarpsK) ? 4 : 8;
+  p.ewarps = codes || epi == PAIR_DSWIGLU_LO || (p.split == 1 && p.K >= kFewWarpsK) ? 4 : 8;
   const int end = d.smem - 2048;
   p.scale_off = end - 4096;
   int room = end - p.ewarps * p.bufs * kStageBox - (codes ? 4096 : 0);
@@ -154,7 +154,7 @@ bool prepare_out(PairLaunch& l, const void* out, bool f32) {
 
 cudaError_t launch(PairLaunch& l, const Device& d, bool pdl, cudaStream_t s) {
   const void* k = pair_kernel(l.form, l.epi);
-  static std::atomic<uint64_t> ready[4][5];  // per kernel: devices whose limit is set
+  static std::atomic<uint64_t> ready[4][PAIR_DSWIGLU_LO + 1];  // per kernel: devices whose limit is set
   if (d.id >= 64 || !(ready[l.form][l.epi].load() >> d.id & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem - 1024);
     if (e != cudaSuccess) return e;
@@ -583,8 +583,7 @@ moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* 
   one.p.K = c->hidden;
   one.p.keep = dw2 != nullptr;
   const int each = exact_backward(rows, *c) ? 2 : 1;  // numbers that each of dg, du and h is the sum of
-  one.p.lo = each == 2;
-  bool ok = prepare(one, FORM_KM, PAIR_DSWIGLU, {grad, grad_stride * 2, rows, hid}, {wt->w2, in * 2, hid, in}, false, d) &&
+  bool ok = prepare(one, FORM_KM, each == 2 ? PAIR_DSWIGLU_LO : PAIR_DSWIGLU, {grad, grad_stride * 2, rows, hid}, {wt->w2, in * 2, hid, in}, false, d) &&
             make_map(&one.d, h, in * 2 * each, in, rows, 32, each, in * 2) &&
             make_map(&one.e, both, in * 4 * each, in, rows, 32, 2 * each, in * 2) &&
             make_map(&one.g, gate_up, in * 4, in, rows, 32, 2, in * 2);

@@ -315,28 +315,33 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
         const CUtensorMap *ma = kTwo && tl.second ? &map_e : &map_a, *mb = kTwo && tl.second ? &map_g : &map_b;
         if (!kI8)
           for (int k = k_first; k < min(k_first + p.ahead, k_last); k++) fetch_b(n, half, k);
-        for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
-          const uint32_t s = it.slot;
-          if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
-          const uint32_t bar = bars + 8u * s;
-          const uint32_t a = base + s * p.stage_bytes, b = a + p.a_bytes;
-          if (!kI8 && p.ahead && k + p.ahead < k_last) fetch_b(n, half, k + p.ahead);
-          // (the other CTA's bytes may be counted before this; the phase ends with the arrival)
-          if (rank == 0) mbar_arrive_expect_tx(full(s), p.step_bytes);
-          const bool again = kPasses && k >= once;
-          const int kx = (again ? k - once : k) * 64;
-          const int oa = !again ? 0 : kTwo && tl.second ? p.pass_a2 : p.pass_a, ob = !again ? 0 : kTwo && tl.second ? p.pass_b2 : p.pass_b;
-          if (FORM == FORM_MM) {
-            tma_pair_3d(a, ma, m + oa, kx, 0, bar);
-            tma_pair_3d(a + 8192, ma, m + oa + 64, kx, 0, bar);
-          } else if (rank == 0 || p.a_bytes == 128 * 128) {  // (few rows are all the first CTA's)
-            tma_pair_3d(a, &map_a, kx + oa, m, 0, bar);
-          }
-          if (FORM == FORM_KK) {
-            tma_pair_3d(b, &map_b, kx, n, half, bar);
-          } else if (!kI8) {
-            tma_pair_3d(b, mb, n + ob, kx, 0, bar);
-            if (b_rows > 64) tma_pair_3d(b + 8192, mb, n + ob + 64, kx, 0, bar);
+        // (once through K, or twice: with the second numbers of operands that are sums of two)
+        for (int turn = 0; ok && turn < (kPasses ? p.passes : 1); turn++) {
+          const int from = turn ? max(once, k_first) : k_first, to = kPasses && !turn && p.passes > 1 ? min(once, k_last) : k_last;
+          const int x = turn * once * 64;  // K of step 0
+          const int am = m + (turn && FORM == FORM_MM ? kTwo && tl.second ? p.pass_a2 : p.pass_a : 0);
+          const int ax = x - (turn && FORM == FORM_KM ? p.pass_a : 0);
+          const int bn = n + (turn ? kTwo && tl.second ? p.pass_b2 : p.pass_b : 0);
+          for (int k = from; k < to; k++, it.next(p.stages)) {
+            const uint32_t s = it.slot;
+            if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
+            const uint32_t bar = bars + 8u * s;
+            const uint32_t a = base + s * p.stage_bytes, b = a + p.a_bytes;
+            if (!kI8 && p.ahead && k + p.ahead < k_last) fetch_b(n, half, k + p.ahead);
+            // (the other CTA's bytes may be counted before this; the phase ends with the arrival)
+            if (rank == 0) mbar_arrive_expect_tx(full(s), p.step_bytes);
+            if (FORM == FORM_MM) {
+              tma_pair_3d(a, ma, am, k * 64 - x, 0, bar);
+              tma_pair_3d(a + 8192, ma, am + 64, k * 64 - x, 0, bar);
+            } else if (rank == 0 || p.a_bytes == 128 * 128) {  // (few rows are all the first CTA's)
+              tma_pair_3d(a, &map_a, k * 64 - ax, m, 0, bar);
+            }
+            if (FORM == FORM_KK) {
+              tma_pair_3d(b, &map_b, k * 64, n, half, bar);
+            } else if (!kI8) {
+              tma_pair_3d(b, mb, bn, k * 64 - x, 0, bar);
+              if (b_rows > 64) tma_pair_3d(b + 8192, mb, bn + 64, k * 64 - x, 0, bar);
+            }
           }
         }
       }
@@ -464,10 +469,11 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
   bool ok = true;
   // Columns of a box: a row of it is 128 bytes.
   constexpr int kBox = EPI == PAIR_F32 || EPI == PAIR_SWIGLU_F32 ? 32 : 64;
-  constexpr bool kThree = EPI == PAIR_SWIGLU || EPI == PAIR_DSWIGLU;  // three boxes at once, else two in turn
+  constexpr bool kLo = EPI == PAIR_DSWIGLU_LO, kGrad = EPI == PAIR_DSWIGLU || kLo;
+  constexpr bool kThree = EPI == PAIR_SWIGLU || kGrad;  // three boxes at once, else two in turn
   constexpr bool kTurns = !kThree && !kI8;  // (int8: one box, and another stage)
   const int nbox = cols / kBox;
-  const bool asks = EPI == PAIR_DSWIGLU || (EPI == PAIR_BF16 && p.addend);  // a unit's inputs come by TMA
+  const bool asks = kGrad || (EPI == PAIR_BF16 && p.addend);  // a unit's inputs come by TMA
   uint32_t asked = 0, landed = 0, units = 0;
   auto there = [&](const PairTile& tl, int box, int q) {
     const bool two = kTwo && tl.second;
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
     if (lane == 0) {
       const int row = tl.m0 + rank * 128 + q * 32, col = tl.n0 + box * 64;
       store_wait_read<0>();
-      if (EPI == PAIR_DSWIGLU) {
+      if (kGrad) {
         mbar_arrive_expect_tx(bar, 2 * kStageBox);
         tma_load_3d(boxes, &map_g, col, row, 0, bar);
         tma_load_3d(boxes + kStageBox, &map_g, col, row, 1, bar);
@@ -562,7 +568,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
       } else {
         wait(v);
       }
-      if (EPI == PAIR_DSWIGLU) {
+      if (kGrad) {
 #pragma unroll
         for (int c = 0; c < 2; c++) {
           const uint32_t ag = box_at(at, lane, 2 * h + c), au = ag + kStageBox;
@@ -581,7 +587,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
               b[e] = dh * s;
               a[e] = dh * u * (sig + s * (1.0f - sig));
             }
-            if (p.lo) {
+            if (kLo) {
               dg[j] = pack_bf16(high(a[0]), high(a[1]));
               du[j] = pack_bf16(high(b[0]), high(b[1]));
               hh[j] = pack_bf16(high(w[0]), high(w[1]));
@@ -597,7 +603,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
           st_shared4(ag, dg[0], dg[1], dg[2], dg[3]);
           st_shared4(au, du[0], du[1], du[2], du[3]);
           st_shared4(ag + 2 * kStageBox, hh[0], hh[1], hh[2], hh[3]);
-          if (p.lo)
+          if (kLo)
 #pragma unroll
             for (int i = 0; i < 3; i++) st_shared4(ag + (3 + i) * kStageBox, l[i][0], l[i][1], l[i][2], l[i][3]);
         }
@@ -632,11 +638,11 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
           tma_store_3d(&map_e, col0, row0, 0, at + kStageBox);
           tma_store_3d(&map_e, col0, row0, 1, at + 2 * kStageBox);
         }
-      } else if (EPI == PAIR_DSWIGLU) {
+      } else if (kGrad) {
         tma_store_3d(&map_e, col0, row0, 0, at);
         tma_store_3d(&map_e, col0, row0, 1, at + kStageBox);
         if (p.keep) tma_store_3d(&map_d, col0, row0, 0, at + 2 * kStageBox);
-        if (p.lo) {
+        if (kLo) {
           tma_store_3d(&map_e, col0, row0, 2, at + 3 * kStageBox);
           tma_store_3d(&map_e, col0, row0, 3, at + 4 * kStageBox);
           if (p.keep) tma_store_3d(&map_d, col0, row0, 1, at + 5 * kStageBox);
@@ -667,7 +673,7 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
       }
       if (asks && first) {
         ask(tl, which, q);
-        if (EPI == PAIR_DSWIGLU && lane == 0)  // the others' on their way to L2
+        if (kGrad && lane == 0)  // the others' on their way to L2
           for (int box = which + per_q; box < nbox && there(tl, box, q); box += per_q)
             for (int z = 0; z < 2; z++) tma_prefetch_3d(&map_g, tl.n0 + box * 64, tl.m0 + rank * 128 + q * 32, z);
       }

@@ -32,7 +32,8 @@ enum PairEpi {
   PAIR_F32 = 1,
   PAIR_SWIGLU = 2,      // bf16 silu(gate) * up, and (map_e) gate and up themselves
   PAIR_SWIGLU_F32 = 3,  // the same in fp32, without them
-  PAIR_DSWIGLU = 4      // from dh, gate and up: bf16 dg, du (map_e) and h
+  PAIR_DSWIGLU = 4,     // from dh, gate and up: bf16 dg, du (map_e) and h
+  PAIR_DSWIGLU_LO = 5   // each as two bf16 numbers, the second ones in the maps' later halves
 };
 
 struct PairParams {
@@ -59,8 +60,7 @@ struct PairParams {
   // An operand that is the sum of two bf16 numbers: K is gone through twice (passes 2), the second time this many
   // columns further on in A and in B (and in the second product's).
   int passes, pass_a, pass_b, pass_a2, pass_b2;
-  int lo;        // DSWIGLU: results are two bf16 numbers each, the second ones in maps e's and d's later halves
-  int keep;      // SWIGLU: store gate and up; DSWIGLU: store h
+  int keep;      // SWIGLU: store gate and up; DSWIGLU, DSWIGLU_LO: store h
   int reduce;    // F32: add to what is there
   int pdl;
   int* status;   // one word a CTA; 1 = a wait ran into its limit
