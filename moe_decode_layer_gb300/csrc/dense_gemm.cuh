@@ -17,7 +17,7 @@
 //
 // int8 weights (FORM_KK8) come as codes: eight warps widen them into the stage, and the epilogue
 // has four. (A pass that widened the whole matrix first cost its 3 bytes a weight: 36 us for 67
-// million; 1024 rows, 4096 to 2 x 8192, 123 us with it and 91 us without.)
+// million; 1024 rows, 4096 to 2 x 8192, 123 us with it and 84 us without.)
 //
 // What bounds it: with many rows the tensor core. 8192 rows, 4096 x 8192: gate/up 549 us, dx 555
 // us for 1.1 TFLOP each, 2.0 PFLOP/s in short runs; in long ones the power limit (1.6 to 1.7). A step
