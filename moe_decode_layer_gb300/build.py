@@ -31,7 +31,7 @@ DECODE_SOURCES = ["api.cu", "kernels_bf16.cu", "kernels_nvfp4.cu", "kernels_fp8.
 ROWS_SOURCES = ["rows_api.cu", "rows_kernels.cu", "rows_route.cu", "rows_gemm.cu", "rows_gemm_fp8.cu",
                 "rows_gemm_nvfp4.cu", "dense_api.cu", "dense_quantise.cu",
                 "dense_stream.cu", "dense_gemm.cu",
-                "dense_gemm_backward.cu", "dense_gemm_int8.cu"]
+                "dense_gemm_backward.cu", "dense_gemm_int8.cu", "dense_lanes.cu"]
 SOURCES = DECODE_SOURCES + ROWS_SOURCES
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,

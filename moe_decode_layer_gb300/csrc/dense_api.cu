@@ -193,10 +193,19 @@ struct Places {
 
 // Few rows: a stream of the weights, else the pair product. From 9 rows on the pair product is as fast for
 // bf16 weights of more than 16 MB (16 rows of the 4096 x 8192 block: 51 and 50 us, of 1024 x 2048
-// 9 and 19), and for int8 from 33 on.
+// 9 and 19).
 constexpr int64_t kStreamBytes = 16 << 20;
 bool few(int64_t rows, int64_t bytes) { return rows <= 8 || (rows <= kStreamRows && bytes <= kStreamBytes); }
-bool few_codes(int64_t rows) { return rows <= kStreamRows; }
+// Codes: a stream up to 8 rows, or 16 where the weights on the lanes are few tiles and their start and end count (16 rows,
+// 4096 to 2 x 8192: 23.6 us and 19.0, 8192 to 4096: 12.4 and 13.3). These up to 128 rows, or 192 where the
+// pair product has few tiles as well (160 rows, 8192 to 4096: 21.5 us and 29.8 in pairs, 224: 23.8 and 30;
+// 4096 to 2 x 8192: 29.5 and 30.2, 256: 45 and 31).
+constexpr int kFewTiles = 76, kLanesAlways = 128;
+bool few_tiles(const moe_int8_config& c) { return lanes_tiles(c.outer, c.swiglu) <= kFewTiles; }
+bool few_codes(int64_t rows, const moe_int8_config& c) {
+  return rows <= 8 || (rows <= 16 && few_tiles(c));
+}
+bool on_lanes(int64_t rows, const moe_int8_config& c) { return !few_codes(rows, c) && rows <= (few_tiles(c) ? kLaneRows : kLanesAlways); }
 
 // ------------------------------------------------------------------ int8
 moe_status check_int8(const moe_int8_config* c) {
@@ -216,9 +225,9 @@ Int8Plan int8_plan(const moe_int8_config& c, int64_t rows) {
   Places pl;
   Int8Plan p = {};
   const bool made = c.x_dtype != MOE_I8;
-  if (few_codes(rows) && !made) return p;  // nothing is kept, and nothing waits
+  if (few_codes(rows, c) && !made) return p;  // nothing is kept, and nothing waits
   p.status = pl.take(kStatusBytes);
-  p.codes = pl.take((size_t)rows * c.inner * (few_codes(rows) ? 1 : 2));
+  p.codes = pl.take((size_t)rows * c.inner * (few_codes(rows, c) ? 1 : 2));
   if (made) p.scale = pl.take((size_t)rows * 4);
   p.bytes = pl.at;
   return p;
@@ -244,7 +253,7 @@ struct Int8Product {
 };
 
 moe_status prepare_int8(Int8Product& a, const Device& d) {
-  if (few_codes(a.rows)) return MOE_OK;
+  if (few_codes(a.rows, a.c)) return MOE_OK;
   const bool f32 = a.c.out_dtype == MOE_F32;
   PairParams& p = a.l.p;
   p.M = (int)a.rows;
@@ -256,6 +265,13 @@ moe_status prepare_int8(Int8Product& a, const Device& d) {
   p.status = a.status;
   p.status_keep = a.status_keep;
   const int64_t k = a.c.inner, w_rows = (int64_t)a.c.outer * (a.c.swiglu ? 2 : 1);
+  if (on_lanes(a.rows, a.c)) {
+    const int64_t halves = a.c.swiglu ? 2 : 1;
+    return make_map(&a.l.b, a.w, k, k, a.c.outer, 64, (int)halves, k * a.c.outer, false, true) &&
+                   make_map(&a.l.a, a.codes, k * 2, k, a.rows, (int)up(a.rows, 16))
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+  }
   const int epi = a.c.swiglu ? (f32 ? PAIR_SWIGLU_F32 : PAIR_SWIGLU) : f32 ? PAIR_F32 : PAIR_BF16;
   return prepare(a.l, FORM_KK8, epi, {a.codes, k * 2, a.rows, k}, {a.w, k, w_rows, k}, true, d) && prepare_out(a.l, a.out, f32)
              ? MOE_OK
@@ -264,13 +280,29 @@ moe_status prepare_int8(Int8Product& a, const Device& d) {
 
 cudaError_t launch_int8(Int8Product& a, const Device& d, bool pdl, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  const bool made = a.c.x_dtype != MOE_I8, small = few_codes(a.rows);
+  const bool made = a.c.x_dtype != MOE_I8, small = few_codes(a.rows, a.c);
   if (made)
     e = launch_quantise(a.c.x_dtype, a.x, a.x_stride, a.rows, a.c.inner, a.codes, !small, a.scale, pdl, s);
   else if (!small)
     e = launch_widen(static_cast<const int8_t*>(a.x), a.x_stride, a.rows, a.c.inner, reinterpret_cast<__half*>(a.codes), pdl, s);
   if (e != cudaSuccess) return e;
   pdl = pdl || made || !small;
+  if (on_lanes(a.rows, a.c)) {
+    LaneParams p = {};
+    p.T = (int)a.rows;
+    p.K = a.c.inner;
+    p.R = a.c.outer;
+    p.swiglu = a.c.swiglu;
+    p.cols = (int)up(a.rows, 16);
+    p.x_scale = a.l.p.row_scale;
+    p.w_scale = a.w_scale;
+    p.addend = a.l.p.addend;
+    p.out = a.out;
+    p.out_f32 = a.c.out_dtype == MOE_F32;
+    p.status = a.status;
+    p.status_keep = a.status_keep;
+    return launch_lanes(p, a.l.b, a.l.a, d.id, d.smem, d.sms, s);
+  }
   if (!small) return launch(a.l, d, pdl, s);
   StreamParams p = {};
   p.w = a.w;

@@ -110,7 +110,7 @@ def _names(lib):
     found = []
     for i in range(lib.fake_launches()):
         name = lib.fake_name(i).decode()
-        found.append(next(n for n in ("quantise", "widen", "zero", "stream", "pair_gemm") if n + "_kernel" in name))
+        found.append(next(n for n in ("quantise", "widen", "zero", "stream", "lanes", "pair_gemm") if n + "_kernel" in name))
     return found
 
 
@@ -118,10 +118,12 @@ def test_launches(lib):
     assert _quantise(lib) == OK and _names(lib) == ["quantise"]
     assert _project(lib) == OK and _names(lib) == ["stream"]
     assert _project(lib, x_dtype=0) == OK and _names(lib) == ["quantise", "stream"]
-    assert _project(lib, rows=100) == OK and _names(lib) == ["widen", "pair_gemm"]
+    assert _project(lib, rows=100) == OK and _names(lib) == ["widen", "lanes"]
+    assert _project(lib, rows=300) == OK and _names(lib) == ["widen", "pair_gemm"]
     assert _project(lib, rows=1000, x_dtype=1) == OK and _names(lib) == ["quantise", "pair_gemm"]
     assert _ff(lib) == OK and _names(lib) == ["stream"] * 2
     assert _ff(lib, rows=100) == OK and _names(lib) == ["pair_gemm"] * 2
+    assert _ff(lib, rows=20, wdtype=3) == OK and _names(lib) == ["quantise", "lanes"] * 2
     assert _ff(lib, rows=1000, wdtype=3) == OK and _names(lib) == ["quantise", "pair_gemm"] * 2
     assert _backward(lib) == OK and _names(lib) == ["pair_gemm"] * 3
     assert _backward(lib, d13=None, d2=None) == OK and _names(lib) == ["pair_gemm"] * 2
@@ -139,7 +141,7 @@ def test_first_launch_is_ordered_behind_the_stream(lib):
         assert [lib.fake_pdl(i) for i in range(lib.fake_launches())] == [0] + [1] * (lib.fake_launches() - 1)
 
 
-@pytest.mark.parametrize("rows", [1, 9, 33, 129, 300, 1000, 20000, 1 << 24])
+@pytest.mark.parametrize("rows", [1, 9, 17, 33, 64, 65, 128, 129, 192, 300, 1000, 20000, 1 << 24])
 def test_every_size_can_be_launched(lib, rows):
     """Descriptors by the documented rules, grids in whole clusters and shared memory within the limit, for odd sizes."""
     for hidden, inter in ((8, 8), (256, 128), (2560, 6912), (65536, 8), (8, 65536), (4096, 16384), (65536, 65536)):
@@ -168,7 +170,7 @@ def test_without_descriptors_nothing_is_enqueued(lib, call):
 
 
 @pytest.mark.parametrize("call", [lambda lib, n: _ff(lib, rows=4, fail_launch=n), lambda lib, n: _ff(lib, rows=100, fail_launch=n), lambda lib, n: _backward(lib, rows=100, fail_launch=n),
-                                  lambda lib, n: _project(lib, rows=1000, fail_launch=n), lambda lib, n: _ff(lib, rows=4, wdtype=3, fail_launch=n)])
+                                  lambda lib, n: _project(lib, rows=1000, fail_launch=n), lambda lib, n: _project(lib, rows=100, fail_launch=n), lambda lib, n: _ff(lib, rows=4, wdtype=3, fail_launch=n)])
 def test_failed_launches_are_reported_once(lib, call):
     assert call(lib, -1) == OK
     for n in range(lib.fake_launches()):

@@ -81,7 +81,10 @@ def test_quantise_strides_places_and_rows_behind():
 
 INT8 = [(1, 16, 8), (2, 128, 72), (5, 4096, 264), (8, 48, 4104), (9, 144, 200), (16, 1040, 136), (17, 16, 8), (31, 2048, 96),
         (64, 640, 1000), (100, 4096, 512), (128, 272, 264), (129, 1024, 72), (300, 208, 776), (512, 512, 256), (513, 16, 8),
-        (700, 1008, 520), (1100, 256, 264)]
+        (700, 1008, 520), (1100, 256, 264),
+        # rows on the weights' other side: one CTA a tile, and clusters of 2, 4 and 8
+        (12, 400, 10008), (40, 1040, 6000), (33, 2064, 4008), (63, 3088, 1000), (96, 2064, 984), (127, 1168, 4504), (160, 784, 9736),
+        (192, 2064, 3000), (250, 2320, 1032), (256, 16, 9800)]
 
 
 @pytest.mark.parametrize("rows,inner,outer", INT8)
