@@ -301,7 +301,8 @@ cudaError_t launch_int8(Int8Product& a, const Device& d, bool pdl, cudaStream_t 
     p.out_f32 = a.c.out_dtype == MOE_F32;
     p.status = a.status;
     p.status_keep = a.status_keep;
-    return launch_lanes(p, a.l.b, a.l.a, d.id, d.smem, d.sms, s);
+    p.pdl = 1;
+    return launch_lanes(p, true, a.l.b, a.l.a, d.id, d.smem, d.sms, s);
   }
   if (!small) return launch(a.l, d, pdl, s);
   StreamParams p = {};
@@ -531,6 +532,26 @@ moe_status moe_decode_ff(const moe_ff_config* c, const moe_ff_weights* wt, const
     two.out = out;
     const cudaError_t e = launch_stream(one, false, false, d.sms, s);
     return cuda_status(e == cudaSuccess ? launch_stream(two, false, true, d.sms, s) : e);
+  }
+
+  if (rows <= kLanesAlways) {
+    LaneParams one = {}, two = {};
+    CUtensorMap w1, x1, w2, x2;
+    one.T = two.T = (int)rows;
+    one.cols = two.cols = (int)up(rows, 16);
+    one.K = two.R = c->hidden;
+    one.R = two.K = c->inter;
+    one.swiglu = two.pdl = two.status_keep = 1;
+    one.out = h;
+    one.keep = static_cast<__nv_bfloat16*>(gate_up);
+    two.addend = static_cast<const __nv_bfloat16*>(residual);
+    two.out = out;
+    one.status = two.status = status;
+    if (!make_map(&w1, wt->w13, hid * 2, hid, in, 64, 2, in * hid * 2) || !make_map(&x1, x, x_stride * 2, hid, rows, one.cols) ||
+        !make_map(&w2, wt->w2, in * 2, in, hid, 64) || !make_map(&x2, h, in * 2, in, rows, one.cols))
+      return MOE_ERR_CUDA;
+    const cudaError_t e = launch_lanes(one, false, w1, x1, d.id, d.smem, d.sms, s);
+    return cuda_status(e == cudaSuccess ? launch_lanes(two, false, w2, x2, d.id, d.smem, d.sms, s) : e);
   }
 
   PairLaunch one, two;

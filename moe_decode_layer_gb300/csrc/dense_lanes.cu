@@ -28,8 +28,9 @@ namespace dense {
 namespace {
 
 constexpr int kThreads = 384, kSlots = 12, kStages = 6;
-constexpr int kWeightBytes = 16384;  // of a slot: 128 rows of 128 codes
+constexpr int kWeightBytes = 16384;  // of a slot: 128 rows of 128 bytes
 
+template <bool I8>
 __global__ void __launch_bounds__(kThreads, 1)
     lanes_kernel(const __grid_constant__ LaneParams p, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x) {
   extern __shared__ uint8_t smem_raw[];
@@ -50,9 +51,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto rows = [&](int s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + s); };
   const uint32_t done = bar0 + 8u * (3 * kSlots + 2 * kStages), drain = done + 8u;
   const int part = cluster_rank(), tile = blockIdx.x / p.split;
-  const int ksteps = (p.K + 127) / 128, k0 = ksteps * part / p.split, n = ksteps * (part + 1) / p.split - k0;
+  constexpr int kStep = I8 ? 128 : 64, kBoxes = I8 ? 2 : 1;  // k of a step; boxes of rows of x
+  const int ksteps = (p.K + kStep - 1) / kStep, k0 = ksteps * part / p.split, n = ksteps * (part + 1) / p.split - k0;
   const int x_box = p.cols * 128;
-  const uint32_t slot_bytes = kWeightBytes + 2 * x_box;
+  const uint32_t slot_bytes = kWeightBytes + kBoxes * x_box;
 
   if (tid == 0) {
     s_abort = 0;
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   auto weights = [&](int i, int s) {
     mbar_arrive_expect_tx(full(s), kWeightBytes);
-    const int k = (k0 + i) * 128;
+    const int k = (k0 + i) * kStep;
     for (int h = 0; h < 2; h++)
       tma_load_3d(base + s * slot_bytes + h * 8192, &map_w, k, p.swiglu ? tile * 64 : tile * 128 + h * 64, p.swiglu ? h : 0, full(s));
   };
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_global();
     pdl_launch_dependents();
   };
-  if (warp < 4) behind();
+  if (!I8 || warp < 4) behind();
 
   bool ok = true;
   if (warp == 0) {
@@ -103,9 +105,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_phase(empty(s), it.parity ^ 1, &s_abort))) break;
           weights(i, s);
         }
-        mbar_arrive_expect_tx(rows(s), 2 * x_box);
-        for (int h = 0; h < 2; h++)
-          tma_load_3d(base + s * slot_bytes + kWeightBytes + h * x_box, &map_x, (k0 + i) * 128 + h * 64, 0, 0, rows(s));
+        mbar_arrive_expect_tx(rows(s), kBoxes * x_box);
+        for (int h = 0; h < kBoxes; h++)
+          tma_load_3d(base + s * slot_bytes + kWeightBytes + h * x_box, &map_x, (k0 + i) * kStep + h * 64, 0, 0, rows(s));
       }
       ok = ok && wait_phase(done, 0, &s_abort);  // then all have landed
       if (!ok) {  // let the copies in flight land before the shared memory goes
@@ -118,15 +120,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = elect_one();
     Ring it, at;
     for (int i = 0; i < n; i++, it.next(p.slots), at.next(p.stages)) {
-      if (!(ok = warp_wait(ready(at.slot), at.parity, &s_abort) && warp_wait(rows(it.slot), it.parity, &s_abort))) break;
+      if (!(ok = warp_wait(I8 ? ready(at.slot) : full(it.slot), I8 ? at.parity : it.parity, &s_abort) && warp_wait(rows(it.slot), it.parity, &s_abort))) break;
       tc_fence_after();
-      const uint32_t a = tmem + p.stage_at + at.slot * 64, x = base + it.slot * slot_bytes + kWeightBytes;
+      const uint32_t w = base + it.slot * slot_bytes, x = w + kWeightBytes;
       if (leader) {
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-          mma_bf16_ta(tmem, a + 8 * j, smem_desc(x + (j >> 2) * x_box) + 2 * (j & 3), p.idesc, i != 0 || j != 0);
+        for (int j = 0; j < kStep / 16; j++) {
+          const uint64_t rows_of_x = smem_desc(x + (j >> 2) * x_box) + 2 * (j & 3);
+          if (I8) mma_bf16_ta(tmem, tmem + p.stage_at + at.slot * 64 + 8 * j, rows_of_x, p.idesc, i != 0 || j != 0);
+          else mma_bf16(tmem, smem_desc(w) + 2 * j, rows_of_x, p.idesc, i != 0 || j != 0);
+        }
         mma_commit(empty(it.slot));
-        mma_commit(used(at.slot));
+        if (I8) mma_commit(used(at.slot));
       }
       __syncwarp();
     }
@@ -142,11 +147,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 4) {
     // ---------------------------------------------------------------- scales, and addends on their way
     const int me = tid - 64;
-    for (int j = me; j < 128; j += 64) {
+    for (int j = me; I8 && j < 128; j += 64) {
       const int h = p.swiglu && j >= 64, r = p.swiglu ? tile * 64 + (j & 63) : tile * 128 + j;
       s_weights[j] = r < p.R ? __ldg(p.w_scale + h * p.R + r) : 0.0f;
     }
-    for (int j = me; j < p.T; j += 64) s_rows[j] = p.x_scale[j];
+    for (int j = me; I8 && j < p.T; j += 64) s_rows[j] = p.x_scale[j];
     if (p.addend)
       for (int t = part + p.split * me; t < p.T; t += p.split * 64)
         for (int r = tile * 128; r < min(tile * 128 + 128, p.R); r += 64)
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane, group = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     Ring it, at;
-    for (int i = 0; i < n; i++, it.next(p.slots), at.next(p.stages)) {
+    for (int i = 0; I8 && i < n; i++, it.next(p.slots), at.next(p.stages)) {
       if ((i & 1) != group) continue;
       if (!(ok = warp_wait(full(it.slot), it.parity, &s_abort))) break;
       const uint32_t src = base + it.slot * slot_bytes + row * 128;
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ready(at.slot), 1);
     }
-    if (n <= p.stages + group) behind();
+    if (I8 && n <= p.stages + group) behind();
     if (p.split > 1 && early) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     ok = ok && warp_wait(done, 0, &s_abort);  // all slots are used
     if (p.split > 1 && !early) {
@@ -227,13 +232,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
       }
     }
-    const float xs = s_rows[t];
+    const int64_t to = (int64_t)t * p.R + o;
+    if (!I8 && p.keep) {
+      __nv_bfloat16* keep = p.keep + to + (int64_t)t * p.R;
+      *reinterpret_cast<uint2*>(keep) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      *reinterpret_cast<uint2*>(keep + p.R) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+    }
+    const float xs = I8 ? s_rows[t] : 1.0f;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      v[j] *= xs * s_weights[g * 4 + j];
-      if (p.swiglu) v[j] = silu_mul_f32(v[j], u[j] * (xs * s_weights[64 + g * 4 + j]));
+      if (I8) v[j] *= xs * s_weights[g * 4 + j];
+      if (I8) u[j] *= xs * s_weights[(64 + g * 4 + j) & 127];
+      if (p.swiglu) v[j] = silu_mul_f32(v[j], u[j]);
     }
-    const int64_t to = (int64_t)t * p.R + o;
     if (p.addend) {
       const uint2 a = *reinterpret_cast<const uint2*>(p.addend + to);
       v[0] += bf16lo(a.x), v[1] += bf16hi(a.x), v[2] += bf16lo(a.y), v[3] += bf16hi(a.y);
@@ -249,30 +260,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 // CTAs of a cluster: as many as fill the SMs, where clusters of that size fit (of 152 SMs 76, 36 and 15).
-int lanes_split(int tiles, int K, int sms) {
-  const int ksteps = (K + 127) / 128;
+int lanes_split(int tiles, int ksteps, int sms) {
   return tiles <= sms / 10 && ksteps >= 16 ? 8 : tiles <= sms * 9 / 38 && ksteps >= 8 ? 4 : tiles <= sms / 2 && ksteps >= 4 ? 2 : 1;
 }
 
-cudaError_t launch_lanes(LaneParams p, const CUtensorMap& w, const CUtensorMap& x, int dev, int smem, int sms, cudaStream_t s) {
-  const void* k = reinterpret_cast<const void*>(&lanes_kernel);
-  static std::atomic<uint64_t> ready{0};  // devices whose limit is set
+cudaError_t launch_lanes(LaneParams p, bool int8, const CUtensorMap& w, const CUtensorMap& x, int dev, int smem, int sms, cudaStream_t s) {
+  const void* k = int8 ? reinterpret_cast<const void*>(&lanes_kernel<true>) : reinterpret_cast<const void*>(&lanes_kernel<false>);
+  static std::atomic<uint64_t> known[2];  // devices whose limit is set
+  std::atomic<uint64_t>& ready = known[int8];
   if (dev >= 64 || !(ready.load() >> dev & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem - 1024);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
   const int tiles = lanes_tiles(p.R, p.swiglu);
-  p.split = lanes_split(tiles, p.K, sms);
+  p.split = lanes_split(tiles, (p.K + (int8 ? 127 : 63)) / (int8 ? 128 : 64), sms);
   p.scale_off = smem - 4 * 1024;
   // (Sums of few rows have a place of their own: they are handed over a microsecond earlier, without a
   // wait for the other CTAs' slots. Of many, that would cost a slot or two.)
   p.sums_off = p.split > 1 && p.cols <= 64 ? p.scale_off - p.cols * 512 : 0;
-  p.slots = std::min(kSlots, (p.sums_off ? p.sums_off : p.scale_off) / (kWeightBytes + 2 * p.cols * 128));
+  p.slots = std::min(kSlots, (p.sums_off ? p.sums_off : p.scale_off) / (kWeightBytes + (int8 ? 2 : 1) * p.cols * 128));
   p.stage_at = (p.cols + 63) / 64 * 64;
   p.stages = std::min(kStages, (512 - p.stage_at) / 64);
-  // fp32 accumulators, fp16 operands, M = 128
-  p.idesc = 1u << 4 | (uint32_t)(p.cols >> 3) << 17 | 8u << 24;
+  // fp32 accumulators, fp16 or bf16 operands, M = 128
+  p.idesc = 1u << 4 | (int8 ? 0u : 1u << 7 | 1u << 10) | (uint32_t)(p.cols >> 3) << 17 | 8u << 24;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(tiles * p.split));
   c.blockDim = dim3(kThreads);
@@ -282,7 +293,7 @@ cudaError_t launch_lanes(LaneParams p, const CUtensorMap& w, const CUtensorMap& 
   c.stream = s;
   cudaLaunchAttribute a[2];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[0].val.programmaticStreamSerializationAllowed = p.pdl;
   a[1].id = cudaLaunchAttributeClusterDimension;
   a[1].val.clusterDim.x = p.split;
   a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;

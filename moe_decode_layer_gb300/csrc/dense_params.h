@@ -91,29 +91,31 @@ constexpr int kStreamRows = 32;  // rows at most
 constexpr int kExactRows = 16;
 cudaError_t launch_stream(const StreamParams& p, bool int8, bool pdl, int sms, cudaStream_t s);
 
-// Some rows of codes, as fp16 numbers: the weights on the tensor core's lanes.
+// Some rows, bf16 or codes as fp16 numbers: the weights on the tensor core's lanes.
 struct LaneParams {
   int T, K, R, swiglu;  // as for the stream
   int cols;             // accumulator columns: T, rounded up to 16s
   int split;            // CTAs of a cluster that share a tile's K
-  int slots;            // of weights and rows of x, 128 k each
+  int slots;            // of weights and rows of x, 64 k each or (codes) 128
   int sums_off;         // a tile's sums: behind them, or (0) where they were
   int scale_off;        // the scales
   int stages;           // of widened weights in tensor memory, from this column on
   int stage_at;
   uint32_t idesc;
-  const float* x_scale;
+  const float* x_scale;  // codes
   const float* w_scale;
   const __nv_bfloat16* addend;
   void* out;
   int out_f32;
+  __nv_bfloat16* keep;  // bf16 with SWIGLU: [T, 2 R], or NULL
+  int pdl;
   int* status;
   int status_keep;
 };
 constexpr int kLaneRows = 192;  // rows at most
 constexpr int lanes_tiles(int R, bool swiglu) { return swiglu ? (R + 63) / 64 : (R + 127) / 128; }
-// Behind a launch that writes no weights and lets this one start when all before it have ended.
-cudaError_t launch_lanes(LaneParams p, const CUtensorMap& w, const CUtensorMap& x, int dev, int smem, int sms, cudaStream_t s);
+// pdl: behind a launch that writes no weights and lets this one start when all before it have ended.
+cudaError_t launch_lanes(LaneParams p, bool int8, const CUtensorMap& w, const CUtensorMap& x, int dev, int smem, int sms, cudaStream_t s);
 
 // codes of rows, as int8 or (half) as fp16 numbers
 cudaError_t launch_quantise(int dtype, const void* x, int64_t x_stride, int64_t rows, int inner, void* codes, bool half,

@@ -122,7 +122,8 @@ def test_launches(lib):
     assert _project(lib, rows=300) == OK and _names(lib) == ["widen", "pair_gemm"]
     assert _project(lib, rows=1000, x_dtype=1) == OK and _names(lib) == ["quantise", "pair_gemm"]
     assert _ff(lib) == OK and _names(lib) == ["stream"] * 2
-    assert _ff(lib, rows=100) == OK and _names(lib) == ["pair_gemm"] * 2
+    assert _ff(lib, rows=100) == OK and _names(lib) == ["lanes"] * 2
+    assert _ff(lib, rows=300) == OK and _names(lib) == ["pair_gemm"] * 2
     assert _ff(lib, rows=20, wdtype=3) == OK and _names(lib) == ["quantise", "lanes"] * 2
     assert _ff(lib, rows=1000, wdtype=3) == OK and _names(lib) == ["quantise", "pair_gemm"] * 2
     assert _backward(lib) == OK and _names(lib) == ["pair_gemm"] * 3
@@ -160,7 +161,7 @@ def test_every_size_can_be_launched(lib, rows):
                 assert lib.fake_bad_maps() == 0
 
 
-@pytest.mark.parametrize("call", [lambda lib, n: _ff(lib, rows=100, kept=KEPT, fail_encode=n), lambda lib, n: _backward(lib, rows=100, fail_encode=n),
+@pytest.mark.parametrize("call", [lambda lib, n: _ff(lib, rows=100, kept=KEPT, fail_encode=n), lambda lib, n: _ff(lib, rows=300, kept=KEPT, fail_encode=n), lambda lib, n: _backward(lib, rows=100, fail_encode=n),
                                   lambda lib, n: _project(lib, rows=100, fail_encode=n), lambda lib, n: _project(lib, rows=1000, fail_encode=n, addend=RES),
                                   lambda lib, n: _ff(lib, rows=100, wdtype=3, fail_encode=n), lambda lib, n: _ff(lib, rows=1000, wdtype=3, fail_encode=n)])
 def test_without_descriptors_nothing_is_enqueued(lib, call):
@@ -169,7 +170,7 @@ def test_without_descriptors_nothing_is_enqueued(lib, call):
         assert call(lib, n) == CUDA and lib.fake_launches() == 0
 
 
-@pytest.mark.parametrize("call", [lambda lib, n: _ff(lib, rows=4, fail_launch=n), lambda lib, n: _ff(lib, rows=100, fail_launch=n), lambda lib, n: _backward(lib, rows=100, fail_launch=n),
+@pytest.mark.parametrize("call", [lambda lib, n: _ff(lib, rows=4, fail_launch=n), lambda lib, n: _ff(lib, rows=100, fail_launch=n), lambda lib, n: _ff(lib, rows=300, fail_launch=n), lambda lib, n: _backward(lib, rows=100, fail_launch=n),
                                   lambda lib, n: _project(lib, rows=1000, fail_launch=n), lambda lib, n: _project(lib, rows=100, fail_launch=n), lambda lib, n: _ff(lib, rows=4, wdtype=3, fail_launch=n)])
 def test_failed_launches_are_reported_once(lib, call):
     assert call(lib, -1) == OK

@@ -142,7 +142,9 @@ def test_project_int8_rows_are_their_own(rows):
 
 BLOCKS = [(1, 64, 8), (2, 8, 8), (7, 264, 136), (8, 1000, 520), (9, 128, 64), (15, 64, 2056), (16, 520, 1032), (17, 8, 8), (33, 72, 200),
           (64, 512, 264), (127, 256, 384), (128, 1032, 136), (129, 64, 64), (200, 328, 776), (256, 512, 512), (257, 128, 1000),
-          (400, 2560, 768), (700, 200, 264), (1100, 136, 328)]
+          (400, 2560, 768), (700, 200, 264), (1100, 136, 328),
+          # a CTA a tile, and clusters of 2, 4 and 8; a second wave of CTAs
+          (33, 9800, 40), (40, 1032, 5000), (70, 2056, 1040), (96, 4104, 520), (120, 72, 10008)]
 
 
 def _block(g, hidden, inter):
