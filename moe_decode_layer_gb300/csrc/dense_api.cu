@@ -191,9 +191,9 @@ struct Places {
   }
 };
 
-// Few rows: a stream of the weights, else the pair product. From 9 rows on the pair product is as fast for
-// bf16 weights of more than 16 MB (16 rows of the 4096 x 8192 block: 51 and 50 us, of 1024 x 2048
-// 9 and 19).
+// Rows of bf16: few take a stream of the weights, 8 or, where these are small, 16 (16 rows of the 1024 x 2048 block
+// 10.1 us; 4096 x 8192 51, and 38.7 with the weights on the lanes); up to 128 have the weights on the lanes (64 rows, 4096 x
+// 8192 and 2560 x 6912: 42 and 30 us, 50 and 34 in pairs; 128: 48 and 35, 53 and 37); more take the pair product.
 constexpr int64_t kStreamBytes = 16 << 20;
 bool few(int64_t rows, int64_t bytes) { return rows <= 8 || (rows <= kStreamRows && bytes <= kStreamBytes); }
 // Codes: a stream up to 8 rows, or 16 where the weights on the lanes are few tiles and their start and end count (16 rows,

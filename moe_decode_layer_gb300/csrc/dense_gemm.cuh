@@ -24,9 +24,8 @@
 // takes 530 clocks where its products take 512. With narrower tiles a step's copies bound it: an
 // SM takes in about 64 bytes a clock from L2, so that a step of bn columns needs 256 + bn clocks
 // (and the ring, 5 or 6 stages, covers a copy's latency of 2600). dh's epilogue (three results for each
-// of its sums, and two inputs) runs beside the product at 1.57 PFLOP/s. With few rows the weights'
-// bytes: gate/up of 64 rows, 134 MB, streams at 6.4 TB/s for 21 us, and start, first copies,
-// epilogue and end take 5.
+// of its sums, and two inputs) runs beside the product at 1.57 PFLOP/s. With few rows (the
+// backward pass) the weights' bytes.
 // (A warp each for A's and B's copies was slower, 562 -> 634 us for dW13; so were stages of 128 k,
 // half as many, 264 -> 307 us for a backward pass of 1024 rows.)
 //

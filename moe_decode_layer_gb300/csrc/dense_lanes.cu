@@ -1,22 +1,23 @@
-// Some rows of codes times int8 weights (tcgen05, sm_103a): D [R, T] = W X^T, fp16 operands, fp32
-// accumulators, and out = D^T with its scales.
+// Some rows times bf16 or int8 weights (tcgen05, sm_103a): D [R, T] = W X^T, bf16 or fp16 operands, fp32
+// accumulators, and out = D^T, with scales, as the block has them.
 //
 // The weights take the tensor core's lanes and the rows of x its columns, so that a step costs what
 // the rows are (the pair product's tile of 256 rows costs the same for 32). A CTA has 128 rows of
-// weights (gate and up: 64 and 64) and all of x: TMA brings 128 codes of each weight row and the
+// weights (gate and up: 64 and 64) and all of x. Codes: TMA brings 128 of each weight row and the
 // same k of x as fp16; a thread widens a weight row, exactly, and puts it into tensor memory, from where the
 // tensor core takes it: what shared memory moves for a weight are its byte in and its byte out.
 // Few tiles: the CTAs of a cluster take parts of K, and their sums are joined through distributed
 // shared memory, in the order of the parts.
 //
-// What bounds it: the weights' bytes, 0.30 us for a step of 128 k in 128 CTAs (7 TB/s), behind 8 us of start and end
+// What bounds it: the weights' bytes; int8 0.30 us for a step of 128 k in 128 CTAs (7 TB/s), behind 8 us of start and end
 // with the rows' codes: 32 rows, 4096 to 2 x 8192 (67 MB), 19.7 us (with both operands widened in
 // registers for mma.sync 32, as a pair product 30), 8192 to 4096 14.4 (17 and 29), 128 rows 26.5 and 19.
+// bf16: the 4096 x 8192 block of 16 rows in 38.7 us (201 MB, 5.2 TB/s; 50 as a pair product), of 128 in 47.6 (53).
 // (Joined by loads from the other CTAs and another barrier, instead of stores to them: 1 to 2 us more.)
 //
 // Warps: 0 copies, 1 tensor core, 2 tensor memory, 4..11 widen (four take a step, four the next one)
 // and read the sums; all write results. The weights' first copies are under way before the launch that
-// makes the codes has ended: it does not write weights, and all before it have ended. Every wait is
+// makes x has ended: it does not write weights, and all before it have ended. Every wait is
 // bounded; who gives up sets a flag that the others look at, and the CTA's status word.
 #include <algorithm>
 #include <atomic>

@@ -87,7 +87,7 @@ struct StreamParams {
   __nv_bfloat16* keep;   // SWIGLU: [T, 2 R], or NULL
   int* status;           // the workspace's status words, to be cleared, or NULL
 };
-constexpr int kStreamRows = 32;  // rows at most
+constexpr int kStreamRows = 16;  // rows at most
 constexpr int kExactRows = 16;
 cudaError_t launch_stream(const StreamParams& p, bool int8, bool pdl, int sms, cudaStream_t s);
 

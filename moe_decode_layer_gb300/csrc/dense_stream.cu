@@ -295,8 +295,7 @@ cudaError_t launch(const StreamParams& p, int per_sm, bool pdl, int sms, cudaStr
 template <bool I8>
 cudaError_t choose(const StreamParams& p, bool pdl, int sms, cudaStream_t s) {
   if (p.T <= 8) return launch<I8, 1, 1, 2, 4>(p, 2, pdl, sms, s);
-  if (I8 || p.T <= 16) return launch<I8, 2, 2, 1, 4>(p, 2, pdl, sms, s);  // (codes: 16 rows at most)
-  return launch<false, 2, 4, 1, 4>(p, 1, pdl, sms, s);
+  return launch<I8, 2, 2, 1, 4>(p, 2, pdl, sms, s);
 }
 
 }  // namespace
