@@ -10,12 +10,8 @@ const void* pair_kernel_int8(int epi);
 const void* pair_kernel(int form, int epi) {
   if (form == FORM_KK8) return pair_kernel_int8(epi);
   if (form != FORM_KK) return pair_kernel_backward(form, epi);
-  switch (epi) {
-    case PAIR_SWIGLU: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_SWIGLU>);
-    case PAIR_SWIGLU_F32: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_SWIGLU_F32>);
-    case PAIR_F32: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_F32>);
-    default: return reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_BF16>);
-  }
+  return epi == PAIR_SWIGLU ? reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_SWIGLU>)
+                            : reinterpret_cast<const void*>(&pair_gemm_kernel<FORM_KK, PAIR_BF16>);
 }
 
 }  // namespace dense
