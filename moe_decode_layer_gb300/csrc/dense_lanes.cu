@@ -162,9 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane, group = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     Ring it, at;
+    auto wait = [&](LaneWait what, uint32_t s, uint32_t parity) { return warp_wait(what == LANE_FULL ? full(s) : empty(s), parity, &s_abort); };
     for (int i = 0; I8 && i < n; i++, it.next(p.slots), at.next(p.stages)) {
       if ((i & 1) != group) continue;
-      if (!(ok = warp_wait(full(it.slot), it.parity, &s_abort))) break;
+      if (!(ok = landed(it, p.slots, p.stages, wait))) break;
       const uint32_t src = base + it.slot * slot_bytes + row * 128;
       uint32_t o[2][32];
 #pragma unroll

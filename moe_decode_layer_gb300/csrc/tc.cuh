@@ -1,11 +1,12 @@
 // Tensor-core, TMA and tensor-memory instructions of the many-row and the dense kernels
-// (sm_103a), bounded waits, and places in rings of barriers.
+// (sm_103a), and bounded waits.
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
+#include "rings.h"
 #include "rows_params.h"
 
 namespace moe {
@@ -135,18 +136,6 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, wait_phase(bar, parity, abort));
 }
-
-// A place in a ring of n barriers: the slot, and the parity of its use. (Divisions
-// by the number of slots took a quarter of a widening warp's step.)
-struct Ring {
-  uint32_t slot = 0, parity = 0;
-  __device__ __forceinline__ void next(uint32_t n) {
-    if (++slot == n) {
-      slot = 0;
-      parity ^= 1;
-    }
-  }
-};
 
 // CUDA's fast exp and division: at most 105 + 2 steps of fp32 (2^-16 of the value) at g = -88,
 // a few near 0; the result is rounded to bf16 (2^-8) next. exp(-g) past fp32's range makes
