@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; j++) int8x4_f16x4(w[j], o[h][8 * c + 2 * j], o[h][8 * c + 2 * j + 1]);
         }
-      if (i == p.stages + group) behind();
+      if (i == behind_at(p.stages, group)) behind();
       if (!(ok = warp_wait(used(at.slot), at.parity ^ 1, &s_abort))) break;
       tc_fence_after();
       const uint32_t to = tmem + lanes + p.stage_at + at.slot * 64;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ready(at.slot), 1);
     }
-    if (I8 && n <= p.stages + group) behind();
+    if (I8 && n <= behind_at(p.stages, group)) behind();
     if (p.split > 1 && early) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     ok = ok && warp_wait(done, 0, &s_abort);  // all slots are used
     if (p.split > 1 && !early) {

@@ -42,5 +42,9 @@ __host__ __device__ __forceinline__ bool landed(const rows::Ring& it, int slots,
   return (slots >= stages + 2 || wait(LANE_EMPTY, it.slot, it.parity ^ 1)) && wait(LANE_FULL, it.slot, it.parity);
 }
 
+// The step at which a widening group waits for the launch before, or the end where it has no such step: its first that has to
+// wait for a place in tensor memory. (Nothing that it does before touches what that launch writes.)
+__host__ __device__ __forceinline__ int behind_at(int stages, int group) { return stages + ((stages ^ group) & 1); }
+
 }  // namespace dense
 }  // namespace moe

@@ -120,20 +120,28 @@ extern "C" void all(int slots, int stages, int n, int only_full, int* early, int
 }
 """
 
+BEHIND = r"""
+#include "rings.h"
+extern "C" int behind(int stages, int group) { return moe::dense::behind_at(stages, group); }
+"""
+
 # a launch of lanes_kernel leaves its parameters' first words
 KEPT = "cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void** args) {\n" \
        "  if (g_names[f].find(\"lanes_kernel\") != std::string::npos) memcpy(g_lanes, args[0], sizeof(g_lanes));"
 
 
-@pytest.fixture(scope="module")
-def model(tmp_path_factory):
-    folder = str(tmp_path_factory.mktemp("rings"))
+def _compiled(folder, text):
     src, out = os.path.join(folder, "model.cpp"), os.path.join(folder, "librings.so")
     with open(src, "w") as f:
-        f.write(MODEL)
+        f.write(text)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
     subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-O2", "-w", "-I", cuda, "-I", build.CSRC, src, "-o", out], check=True)
-    lib = ctypes.CDLL(out)
+    return ctypes.CDLL(out)
+
+
+@pytest.fixture(scope="module")
+def model(tmp_path_factory):
+    lib = _compiled(str(tmp_path_factory.mktemp("rings")), MODEL)
 
     def run(slots, stages, n, only_full=False):
         early, stuck = ctypes.c_int(), ctypes.c_int()
@@ -189,3 +197,14 @@ def test_launches_are_within_the_model(lib):
                     assert split in (1, 2, 4, 8) and 2 <= slots <= 12 and 2 <= stages <= 6
                     seen.add((slots, stages))
     assert {(3, 5), (5, 6), (7, 6)} <= seen  # the ones where the copies' barriers alone would not do
+
+
+def test_each_group_waits_once_for_the_launch_before(tmp_path):
+    """At a step of its own (the groups take steps in turn), or after its last one; odd numbers of stages too."""
+    behind = _compiled(str(tmp_path), BEHIND).behind
+    for stages in range(2, 7):
+        for group in (0, 1):
+            at = behind(stages, group)
+            assert at >= stages
+            for n in range(1, 40):
+                assert sum(i == at for i in range(n) if i % 2 == group) + (n <= at) == 1, (stages, group, n)
