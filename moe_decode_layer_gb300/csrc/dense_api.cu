@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kMostWidth = 65536;
 constexpr size_t kStatusBytes = kStatusKernels * kMaxSms * 4;
+static_assert(lanes_tiles(kMostWidth, true) <= kStatusKernels * kMaxSms, "a CTA of the widest product has a status word");
 
 // [halves][rows][cols] of 2-byte numbers (or fp32, or codes), copied in boxes of 128 bytes x box_rows rows;
 // what lies past the matrix reads as zero and is not written.

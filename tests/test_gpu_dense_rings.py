@@ -44,3 +44,20 @@ def test_feed_forward_int8_wide(rows, hidden, inter):
     out = batch.feed_forward(x, w13, w2, wdtype="int8", residual=residual, workspace=ws)
     assert batch.status(ws) == _lib.MOE_OK
     assert ref.within(out, *ref.block_int8(x, *w13, *w2, residual))
+
+
+@pytest.mark.parametrize("rows,wdtype", [(4, "bf16"), (100, "bf16"), (300, "bf16"), (12, "int8"), (100, "int8"), (300, "int8")])
+def test_status_words_are_cleared(rows, wdtype):
+    """All of them, also those that no block of the call has."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    w13, w2, x = n(528, 272), n(272, 264 if wdtype == "bf16" else 272), n(rows, 272)
+    w13 = w13 if wdtype == "bf16" else n(544, 272)
+    if wdtype == "int8":
+        w13, w2 = batch.quantise(w13), batch.quantise(w2)
+    inter = 264 if wdtype == "bf16" else 272
+    ws = torch.full((batch.feed_forward_workspace(272, inter, rows, wdtype=wdtype),), 255, dtype=torch.uint8, device="cuda")
+    batch.feed_forward(x, w13, w2, wdtype=wdtype, workspace=ws)
+    assert not bool(ws[:_lib.ROWS_STATUS_BYTES].any()) and batch.status(ws) == _lib.MOE_OK
+    ws[4 * 700:4 * 701] = 1  # a word that a block past the SMs' number would set
+    assert batch.status(ws) == _lib.MOE_ERR_DEVICE_TIMEOUT
