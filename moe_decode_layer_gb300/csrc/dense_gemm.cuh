@@ -114,11 +114,37 @@ __device__ __forceinline__ void mma_pair_commit(uint32_t bar, uint16_t mask) {
       "h"(mask)
       : "memory");
 }
-// (What is handed over is this CTA's own tensor and shared memory, which is in order by the fences before
-// it. A release over the cluster waits for the thread's global stores as well, 2200 clocks a tile.)
+// Arrivals at another CTA's barrier, and waits for them. The order of what is handed over is left to fences: those of
+// tcgen05 for tensor memory, and for shared memory the two below. (A release over the cluster by the arrival itself
+// waits for global memory as well: 2200 clocks a tile of the epilogue, and 4096 rows, 4096 to 2 x 8192 in int8, take 797 us for 296.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mapped_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+// warp_wait for such arrivals.
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
+  bool ok = false;
+  for (uint32_t i = 0; !ok && i < kWaitLimit; i++) {
+    ok = mbar_try_wait_cluster(bar, parity);
+    if (!ok && (i & 63) == 63 && *abort) break;
+  }
+  if (!ok) *abort = 1;
+  return __all_sync(0xffffffffu, ok);
+}
+// What was written to this CTA's shared memory, before an arrival; what has arrived from shared memory of the
+// cluster's CTAs, after a wait. Shared memory alone.
+__device__ __forceinline__ void fence_release_shared() { asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory"); }
+__device__ __forceinline__ void fence_acquire_shared() { asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory"); }
 // 16 accumulator columns of this thread's TMEM lane; they are there after tmem_wait16.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
@@ -377,8 +403,8 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
     // ---------------------------------------------------------------- widening
     // A thread has a row of this CTA's half of B: 64 codes a step become 128 bytes of fp16, exactly, where the
     // operand's swizzle has them; the scales multiply the sums.
-    // Four warps take a slot, two steps, and four the next one: a slot's waits, loads, conversions, stores and
-    // fence take about 1300 clocks of a thread, the tensor core's two steps 1024. (An even number of slots: each
+    // Four warps take a slot, two steps, and four the next one: a slot's waits, loads, conversions and stores take
+    // about 1300 clocks of a thread and its fences more, the tensor core's two steps 1024. (An even number of slots: each
     // slot is one group's, which so waits for its every use. Steps are released in order, and a group has waited
     // for a later one than the stage's use before last: three stages at least.)
     const int row = (warp & 3) * 32 + lane, group = (warp - 8) >> 2;
@@ -410,6 +436,8 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(rempty(rs), 1);
+        // (Both steps are told at once, behind one pair of fences. The second's stage does not wait for the first's product.)
+        uint32_t told[2];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           const uint32_t s = it.slot, to = base + s * p.stage_bytes + p.a_bytes + row * 128;
@@ -419,10 +447,16 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
             for (int c = 0; c < 8; c++)
               st_shared4(to + ((c ^ (row & 7)) << 4), o[h][4 * c], o[h][4 * c + 1], o[h][4 * c + 2], o[h][4 * c + 3]);
           }
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(bars + 8u * s);
+          told[h] = bars + 8u * s;
           it.next(p.stages);
+        }
+        if (!ok) break;
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          fence_release_shared();
+          mbar_arrive_cluster(told[0]);
+          mbar_arrive_cluster(told[1]);
         }
       }
     }
@@ -434,12 +468,13 @@ __global__ void __launch_bounds__(pair_threads(FORM), 1)
     bool ok = true;
     for (int t = t_first; ok && t < ntiles; t += step, acc.next(2)) {
       const int b = acc.slot;
-      if (!(ok = warp_wait(tempty(b), acc.parity ^ 1, &s_abort))) break;
+      if (!(ok = warp_wait_cluster(tempty(b), acc.parity ^ 1, &s_abort))) break;
       tc_fence_after();
       const uint32_t d = tmem + b * 256;
       for (int k = k_first; k < k_last; k++, it.next(p.stages)) {
         const uint32_t s = it.slot;
-        if (!(ok = warp_wait(full(s), it.parity, &s_abort))) break;
+        if (!(ok = kI8 ? warp_wait_cluster(full(s), it.parity, &s_abort) : warp_wait(full(s), it.parity, &s_abort))) break;
+        if (kI8) fence_acquire_shared();
         tc_fence_after();
         const uint32_t at = base + s * p.stage_bytes;
         const uint64_t da = FORM == FORM_MM ? smem_desc_mn(at) : smem_desc(at);
