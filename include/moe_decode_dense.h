@@ -73,8 +73,8 @@ moe_status moe_decode_project_int8_workspace(const moe_int8_config* cfg, int64_t
  *   x       row r at x + r * x_stride elements; x_stride * element size a multiple of 16
  *   addend  bf16 [rows, O] or NULL; not with swiglu. May be out (out_dtype MOE_BF16)
  *   out     [rows, O] of out_dtype
- * x, w, w_scale, addend, out and workspace 16-byte aligned. Other overlaps of out with x or
- * addend are refused.
+ * x, w, w_scale, addend, out and workspace 16-byte aligned. Other overlaps of out with an input,
+ * the weights among them, are refused.
  */
 moe_status moe_decode_project_int8(const moe_int8_config* cfg, const int8_t* w, const float* w_scale, const void* x,
                                    const float* x_scale, int64_t x_stride, const void* addend, void* out,
@@ -109,8 +109,8 @@ moe_status moe_decode_ff_workspace(const moe_ff_config* cfg, int64_t rows, size_
  *   residual  bf16 [rows, H] or NULL; gate_up bf16 [rows, 2 I] or NULL: receives [g; u], rounded,
  *             for moe_decode_ff_backward (MOE_W_BF16 only)
  *   out       bf16 [rows, H]; may be the residual, and x (rows without gaps, x_stride H)
- * All addresses 16-byte aligned. Other overlaps of out or gate_up with an input or with each
- * other are refused.
+ * All addresses 16-byte aligned. Other overlaps of out or gate_up with an input (the weights among
+ * them) or with each other are refused.
  */
 moe_status moe_decode_ff(const moe_ff_config* cfg, const moe_ff_weights* weights, const void* x, int64_t x_stride,
                          const void* residual, void* gate_up, void* out, int64_t rows, void* workspace,

@@ -440,6 +440,8 @@ moe_status moe_decode_project_int8(const moe_int8_config* c, const int8_t* w, co
   if (rows_overlap(x, x_stride * size, c->inner * size, rows, out, out_bytes)) return MOE_ERR_INVALID_ARG;
   if (codes && overlap(x_scale, rows * 4, out, out_bytes)) return MOE_ERR_INVALID_ARG;
   if ((addend != out || f32) && overlap(addend, add_bytes, out, out_bytes)) return MOE_ERR_INVALID_ARG;
+  const int64_t w_rows = (int64_t)c->outer * (c->swiglu ? 2 : 1);
+  if (any_overlap({out, out_bytes}, {{w, w_rows * c->inner}, {w_scale, w_rows * 4}})) return MOE_ERR_INVALID_ARG;
   const Int8Plan p = int8_plan(*c, rows);
   if (workspace_bytes < p.bytes || (p.bytes && !workspace)) return MOE_ERR_INVALID_ARG;
   Device d;
@@ -485,6 +487,11 @@ moe_status moe_decode_ff(const moe_ff_config* c, const moe_ff_weights* wt, const
   if (residual != out && overlap(residual, out_bytes, out, out_bytes)) return MOE_ERR_INVALID_ARG;
   if ((x != out || (x_stride != c->hidden && rows > 1)) && rows_overlap(x, x_stride * 2, c->hidden * 2, rows, out, out_bytes))
     return MOE_ERR_INVALID_ARG;
+  const int64_t size = int8 ? 1 : 2, halves = 2 * (int64_t)c->inter;
+  for (const Range& o : {Range{out, out_bytes}, Range{gate_up, kept_bytes}})
+    if (any_overlap(o, {{wt->w13, halves * c->hidden * size}, {wt->w2, (int64_t)c->hidden * c->inter * size},
+                        {int8 ? wt->s13 : nullptr, halves * 4}, {int8 ? wt->s2 : nullptr, (int64_t)c->hidden * 4}}))
+      return MOE_ERR_INVALID_ARG;
   if (gate_up && (rows_overlap(x, x_stride * 2, c->hidden * 2, rows, gate_up, kept_bytes) ||
                   any_overlap({gate_up, kept_bytes}, {{residual, out_bytes}, {out, out_bytes}})))
     return MOE_ERR_INVALID_ARG;
