@@ -598,7 +598,8 @@ moe_status moe_decode_ff_backward(const moe_ff_config* c, const moe_ff_weights* 
   moe_status st = check_ff(c);
   if (st != MOE_OK) return st;
   if (c->wdtype != MOE_W_BF16) return MOE_ERR_UNSUPPORTED;
-  if (rows < 0 || rows > kMaxRows || (!dx && !dw13 && !dw2)) return MOE_ERR_INVALID_ARG;
+  // (of no rows dx has no address)
+  if (rows < 0 || rows > kMaxRows || (rows && !dx && !dw13 && !dw2)) return MOE_ERR_INVALID_ARG;
   if (dw_dtype != MOE_BF16 && dw_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
   const bool f32 = dw_dtype == MOE_F32;
   if (accumulate && !f32) return MOE_ERR_UNSUPPORTED;
