@@ -260,10 +260,12 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
     for (int j = tid; j < 2 * rows::kMaxSms; j += 32 * kWarps) p.status[j] = 0;
 }
 
-template <bool I8, int MT, int NT, int HALVES, int STAGES, bool LO = false>
-cudaError_t launch(const StreamParams& p, int per_sm, bool pdl, int sms, cudaStream_t s) {
+// PER_SM: CTAs of an SM. All are resident at once: one that started behind another would find its ring empty.
+template <bool I8, int MT, int NT, int HALVES, int STAGES, int PER_SM, bool LO = false>
+cudaError_t launch(const StreamParams& p, bool pdl, int sms, cudaStream_t s) {
   const void* f = reinterpret_cast<const void*>(&stream_kernel<I8, MT, NT, HALVES, STAGES, LO>);
   constexpr int smem = stream_smem(MT, NT, HALVES, STAGES, LO);
+  static_assert(PER_SM * (smem + 1024) <= 228 * 1024, "the SM's shared memory, 1 KB of it for the system in each CTA");
   static std::atomic<uint64_t> ready{0};  // devices whose limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -276,7 +278,7 @@ cudaError_t launch(const StreamParams& p, int per_sm, bool pdl, int sms, cudaStr
   StreamParams q = p;
   cudaLaunchConfig_t c = {};
   const int rows_out = (p.swiglu ? 8 : 16) * MT, blocks = (p.R + rows_out - 1) / rows_out;
-  c.gridDim = dim3((unsigned)(blocks < sms * per_sm ? blocks : sms * per_sm));
+  c.gridDim = dim3((unsigned)(blocks < sms * PER_SM ? blocks : sms * PER_SM));
   c.blockDim = dim3(32 * kWarps);
   c.dynamicSmemBytes = smem;
   c.stream = s;
@@ -289,20 +291,21 @@ cudaError_t launch(const StreamParams& p, int per_sm, bool pdl, int sms, cudaStr
   return cudaLaunchKernelExC(&c, f, args);
 }
 
-// Stages and CTAs an SM: of 1 to 4 CTAs and 2 to 6 stages of 64 or 128 bytes a row, the fastest for
-// matrices of 17 to 134 MB. (More rows of x take two blocks of weight rows a CTA, which read
-// them half as often.)
+// Stages and CTAs an SM: up to 8 rows the fastest for matrices of 17 to 134 MB, of 1 to 4 CTAs and 2 to 6 stages of 64 or
+// 128 bytes a row. More rows of x take two blocks of weight rows a CTA, which read them half as often; the ring
+// and the sums of one such CTA fill an SM. (16 rows, int8, 4096 to 2 x 4800: 12.6 us; with CTAs that waited for one another's
+// end 13.9; two CTAs of three stages 11.3, but 13.0 for 11.4 from 8192 to 4096.)
 template <bool I8>
 cudaError_t choose(const StreamParams& p, bool pdl, int sms, cudaStream_t s) {
-  if (p.T <= 8) return launch<I8, 1, 1, 2, 4>(p, 2, pdl, sms, s);
-  return launch<I8, 2, 2, 1, 4>(p, 2, pdl, sms, s);
+  if (p.T <= 8) return launch<I8, 1, 1, 2, 4, 2>(p, pdl, sms, s);
+  return launch<I8, 2, 2, 1, 4, 1>(p, pdl, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_stream(const StreamParams& p, bool int8, bool pdl, int sms, cudaStream_t s) {
   if (p.x_lo) {  // (bf16, at most kExactRows)
-    return p.T <= 8 ? launch<false, 1, 1, 1, 5, true>(p, 2, pdl, sms, s) : launch<false, 2, 2, 1, 4, true>(p, 1, pdl, sms, s);
+    return p.T <= 8 ? launch<false, 1, 1, 1, 5, 2, true>(p, pdl, sms, s) : launch<false, 2, 2, 1, 4, 1, true>(p, pdl, sms, s);
   }
   return int8 ? choose<true>(p, pdl, sms, s) : choose<false>(p, pdl, sms, s);
 }
