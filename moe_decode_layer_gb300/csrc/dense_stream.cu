@@ -142,12 +142,13 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
   int stage = 0, buf = 0;
   for (int b = blockIdx.x; b < blocks; b += gridDim.x, buf ^= 1) {
     float acc[MT][NT][4];
+    float rest[MT][NT][4];  // LO: the products of the second numbers
 #pragma unroll
     for (int m = 0; m < MT; m++)
 #pragma unroll
       for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[m][n][j] = 0.0f;
+        for (int j = 0; j < 4; j++) acc[m][n][j] = rest[m][n][j] = 0.0f;
     for (int c = warp; c < chunks; c += kWarps) {
       copies_wait<STAGES - 2>();
       const uint32_t src = ring + stage * (kPieces * 512);
@@ -194,8 +195,8 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
               const uint4 l = ld_shared4(src + ((2 * MT + NT) * HALVES + h * NT + n) * 512);
 #pragma unroll
               for (int m = 0; m < MT; m++) {
-                mma_bf16x(acc[m][n], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, l.x, l.y);
-                mma_bf16x(acc[m][n], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, l.z, l.w);
+                mma_bf16x(rest[m][n], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, l.x, l.y);
+                mma_bf16x(rest[m][n], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, l.z, l.w);
               }
             }
           }
@@ -206,6 +207,16 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const StreamParams 
       next();
     }
 
+    // (where the first numbers' products are infinite, the second ones', of any sign, would make NaN of them)
+    if (LO) {
+#pragma unroll
+      for (int m = 0; m < MT; m++)
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            if (fabsf(acc[m][n][j]) < INFINITY) acc[m][n][j] += rest[m][n][j];
+    }
     // [warp][row of x][weight row], rows of x 16 MT + 4 apart: no bank twice. Two buffers in turn: one
     // barrier a block.
     float* mine = sums + buf * sums_floats(MT, NT) + warp * (8 * NT * kPitch);
