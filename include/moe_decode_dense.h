@@ -85,8 +85,8 @@ moe_status moe_decode_project_int8(const moe_int8_config* cfg, const int8_t* w, 
  *   [g; u]_t = W13 x_t,  h_t = silu(g_t) * u_t,  out_t = W2 h_t (+ residual_t)
  * with fp32 sums and one rounding to bf16. MOE_W_BF16: h is rounded to bf16 (it is an operand of
  * the tensor cores; of up to 4 rows, and of up to 16 where W13 has 16 MB at most, it is the sum of two
- * bf16 numbers). MOE_W_INT8: the codes of x_t and of h_t (in fp32) are those of
- * moe_decode_quantise.
+ * bf16 numbers: a row's last bits may depend on how many come with it). MOE_W_INT8: the codes of
+ * x_t and of h_t (in fp32) are those of moe_decode_quantise.
  * Supported: hidden, inter % 8 == 0 (MOE_W_INT8: % 16), <= 65536.
  */
 typedef struct moe_ff_config {

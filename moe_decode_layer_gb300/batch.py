@@ -6,7 +6,8 @@ include/moe_decode_rows.h, and ``quantise``, ``project_int8``, ``feed_forward`` 
 computed. They check shapes,
 types and devices, allocate results (and a workspace, unless one is given) with
 torch's allocator on the stream they run on, and enqueue their work on the current
-stream (or ``stream``) without waiting. No arithmetic happens here.
+stream (or ``stream``) without waiting. No arithmetic happens here, and no autograd graph
+is recorded: results require no gradient, whatever their inputs do.
 
 A workspace that is handed in must not be in use by another call at the same time,
 and must stay alive while a CUDA graph that captured a call with it is replayed.
@@ -510,7 +511,8 @@ def feed_forward(x: torch.Tensor, w13, w2, *, wdtype: str = "bf16", residual: to
     documents. ``x`` bf16 [T, H], any row stride of a multiple of 8; ``w13`` = [Wg; Wu] bf16 [2 I, H] and ``w2``
     bf16 [H, I], or for ``wdtype`` "int8" (codes, scale) of each, a scale a row. ``gate_up``: a bf16
     [T, 2 I] tensor that receives the sums which :func:`feed_forward_backward` needs (bf16 weights).
-    ``out`` may be the residual, and x."""
+    ``out`` may be the residual, and x. Autograd does not see the call: its gradients are
+    :func:`feed_forward_backward`'s."""
     int8 = wdtype == "int8"
     if int8:
         _need(all(isinstance(w, (tuple, list)) and len(w) == 2 for w in (w13, w2)), "int8 weights come as (codes, scale)")

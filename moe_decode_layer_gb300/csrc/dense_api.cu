@@ -193,14 +193,14 @@ struct Places {
 };
 
 // Rows of bf16: few take a stream of the weights, 8 or, where these are small, 16 (16 rows of the 1024 x 2048 block
-// 10.1 us; 4096 x 8192 51, and 38.7 with the weights on the lanes); up to 128 have the weights on the lanes (64 rows, 4096 x
-// 8192 and 2560 x 6912: 42 and 30 us, 50 and 34 in pairs; 128: 48 and 35, 53 and 37); more take the pair product.
+// 10.1 us, on the lanes 11.2; 4096 x 8192 45.0, and 37.8 on the lanes); up to 128 have the weights on the lanes (64 rows, 4096 x
+// 8192 and 2560 x 6912: 41.7 and 30.6 us, 49.3 and 34.8 in pairs; 128: 47.0 and 35.0, 52.6 and 37.2); more take the pair product.
 constexpr int64_t kStreamBytes = 16 << 20;
 bool few(int64_t rows, int64_t bytes) { return rows <= 8 || (rows <= kStreamRows && bytes <= kStreamBytes); }
 // Codes: a stream up to 8 rows, or 16 where the weights on the lanes are few tiles and their start and end count (16 rows,
-// 4096 to 2 x 8192: 23.6 us and 19.0, 8192 to 4096: 12.4 and 13.3). These up to 128 rows, or 192 where the
-// pair product has few tiles as well (160 rows, 8192 to 4096: 21.5 us and 29.8 in pairs, 224: 23.8 and 30;
-// 4096 to 2 x 8192: 29.5 and 30.2, 256: 45 and 31).
+// 4096 to 2 x 8192: 21.4 us and 18.9, 8192 to 4096: 11.4 and 14.3). These up to 128 rows, or 192 where the
+// pair product has few tiles as well (160 rows, 8192 to 4096: 22.2 us and 30.4 in pairs, 192: 23.0 and 30.4;
+// 4096 to 2 x 8192: 128 rows 27.1 and 31.5, 160 30.7 and 31.7).
 constexpr int kFewTiles = 76, kLanesAlways = 128;
 bool few_tiles(const moe_int8_config& c) { return lanes_tiles(c.outer, c.swiglu) <= kFewTiles; }
 bool few_codes(int64_t rows, const moe_int8_config& c) {
@@ -334,8 +334,9 @@ moe_status check_ff(const moe_ff_config* c) {
 }
 
 // A handful of rows in bf16: h as the sum of two bf16 numbers. It costs a stream little (one row, 4096 x 8192:
-// 33.3 -> 34.6 us), and so the result has its own rounding alone. More rows of large matrices read
-// twice the rows of h for every weight (8 rows: 35 -> 40 us) and do without.
+// 33.3 -> 34.6 us), and so the result has its own rounding alone. h's rounding counts as much in many rows: the
+// limit is where the cost shows. More rows of large matrices read twice the rows of h for every weight (8 rows: 35 -> 40 us)
+// and do without.
 constexpr int64_t kAlwaysExact = 4;
 bool exact(int64_t rows, const moe_ff_config& c) {
   return c.wdtype == MOE_W_BF16 && (rows <= kAlwaysExact || (rows <= kExactRows && (int64_t)c.hidden * c.inter * 4 <= kStreamBytes));
@@ -362,9 +363,10 @@ FfPlan ff_plan(const moe_ff_config& c, int64_t rows) {
 struct BackwardPlan {
   size_t status, both, h, bytes;
 };
-// A few rows of a narrow block: dg, du and h as two bf16 numbers each, side by side in a row. The roundings of so few
-// values do not even out (a gradient's error was up to 1.9 times its own rounding, where that of many is 1.41). dx's
-// product is then twice as long and the weight gradients have a step more: one row, 1024 x 2048, 38 us and 32 without.
+// A few rows of a narrow block: dg, du and h as two bf16 numbers each, side by side in a row. With one number a gradient
+// of many values is 1.41 times its own rounding off (root mean square); that of few varies from input to input (1.9 times in
+// the largest seen, which is no bound). dx's product is then twice as long and the weight gradients have a step more: one
+// row, 1024 x 2048, 38 us and 32 without. The limit is where that cost is a fixed few microseconds.
 constexpr int64_t kExactValues = 4096;
 int64_t exact_backward_rows(const moe_ff_config& c) {
   return (int64_t)c.hidden * c.inter * 4 <= kStreamBytes ? kExactValues / std::min(c.hidden, c.inter) : 0;

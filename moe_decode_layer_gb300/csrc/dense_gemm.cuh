@@ -17,14 +17,14 @@
 //
 // int8 weights (FORM_KK8) come as codes: eight warps widen them into the stage, and the epilogue
 // has four. (A pass that widened the whole matrix first cost its 3 bytes a weight: 36 us for 67
-// million; 1024 rows, 4096 to 2 x 8192, 123 us with it and 84 us without.)
+// million; 1024 rows, 4096 to 2 x 8192, 123 us with it and 89 us without.)
 //
-// What bounds it: with many rows the tensor core. 8192 rows, 4096 x 8192: gate/up 549 us, dx 555
-// us for 1.1 TFLOP each, 2.0 PFLOP/s in short runs; in long ones the power limit (1.6 to 1.7). A step
-// takes 530 clocks where its products take 512. With narrower tiles a step's copies bound it: an
+// What bounds it: with many rows the tensor core, and the power limit. 8192 rows, 4096 x 8192: the forward pass 985
+// us and the backward pass 2050 us one after another, 1.68 and 1.61 PFLOP/s; the forward pass in runs of some ms 903 to 940 us
+// (1.75 to 1.83). A step takes 530 clocks where its products take 512. With narrower tiles a step's copies bound it: an
 // SM takes in about 64 bytes a clock from L2, so that a step of bn columns needs 256 + bn clocks
 // (and the ring, 5 or 6 stages, covers a copy's latency of 2600). dh's epilogue (three results for each
-// of its sums, and two inputs) runs beside the product at 1.57 PFLOP/s. With few rows (the
+// of its sums, and two inputs) runs beside the product. With few rows (the
 // backward pass) the weights' bytes.
 // (A warp each for A's and B's copies was slower, 562 -> 634 us for dW13; so were stages of 128 k,
 // half as many, 264 -> 307 us for a backward pass of 1024 rows.)

@@ -10,9 +10,9 @@
 // shared memory, in the order of the parts.
 //
 // What bounds it: the weights' bytes; int8 0.30 us for a step of 128 k in 128 CTAs (7 TB/s), behind 8 us of start and end
-// with the rows' codes: 32 rows, 4096 to 2 x 8192 (67 MB), 19.7 us (with both operands widened in
-// registers for mma.sync 32, as a pair product 30), 8192 to 4096 14.4 (17 and 29), 128 rows 26.5 and 19.
-// bf16: the 4096 x 8192 block of 16 rows in 38.7 us (201 MB, 5.2 TB/s; 50 as a pair product), of 128 in 47.6 (53).
+// with the rows' codes: 32 rows, 4096 to 2 x 8192 (67 MB), 20.1 us (with both operands widened in
+// registers for mma.sync 32, as a pair product 30), 8192 to 4096 14.3 (17 and 29), 128 rows 27.1 and 19.5 (pairs 31.5 and 30.3).
+// bf16: the 4096 x 8192 block of 16 rows in 37.8 us (201 MB, 5.3 TB/s), of 128 in 47.0 (52.6 as a pair product).
 // (Joined by loads from the other CTAs and another barrier, instead of stores to them: 1 to 2 us more.)
 //
 // Warps: 0 copies, 1 tensor core, 2 tensor memory, 4..11 widen (four take a step, four the next one)

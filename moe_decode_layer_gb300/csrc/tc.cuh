@@ -139,7 +139,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 
 // CUDA's fast exp and division: at most 105 + 2 steps of fp32 (2^-16 of the value) at g = -88,
 // a few near 0; the result is rounded to bf16 (2^-8) next. exp(-g) past fp32's range makes
-// the quotient 0, as it should be.
+// the quotient 0, as it should be. (The fast division gives 0 from 2^126 on already: below g = -87.3 silu
+// is 0 instead of 88 x 2^-126 at most.)
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // The same with the accurate exp, a few steps of fp32 (results that are quantised next: at 2^-16 codes
